@@ -6,6 +6,13 @@ The names and argument order are those of ``include/gemv.h``:
     gemv_f16 (A, x, bias, y, M, K, B, stream=None)
     gemv_bf16(A, x, bias, y, M, K, B, stream=None)
     gemv_w8  (A, row_scale, x, bias, y, M, K, B, stream=None)
+    gemv_f8  (A, a_scale, x, x_scale, bias, y, M, K, B, y_dtype="bf16", stream=None)
+    gemv_f8_quantize(dtype, x, q, scale, K, B, stream=None)
+    gemv_kv8_append(dtype, *cache, k, v, lens, starts, S, N, stream=None)
+    gemv_kv8_attention(dtype, *cache, q, lens, out, lse, S, T, q_heads, scale,
+                       window=0, sinks=0, stream=None)
+
+(``cache``: k, v, k_scale, v_scale, table, whose shapes give the sizes).
 
 Buffers may be torch CUDA tensors (checked for device, contiguity, element size
 and minimum length before the call) or raw device addresses (ints, unchecked).
@@ -25,6 +32,7 @@ __all__ = [
     "gemv_f32", "gemv_f16", "gemv_bf16", "gemv_w8", "gemv_w4", "gemv_bf16_splitk_noalloc", "gemv_ex",
     "gemv_swiglu", "gemv_host", "set_launch_overlap", "ACT_NONE", "ACT_SILU", "GemvError", "Plan", "plan_for",
     "status_string", "launch_count", "last_cuda_error", "force_kernel", "last_plan",
+    "gemv_f8", "gemv_f8_quantize", "gemv_kv8_append", "gemv_kv8_attention", "F8_GROUP", "KV8_BLOCK",
     "KERNELS", "DTYPE_CODES", "lib", "build", "LIB_PATH", "device_status", "test_stall",
 ]
 
@@ -33,6 +41,8 @@ MAX_BATCH, MAX_BATCH_TC = 16, 256
 ACT_NONE, ACT_SILU = 0, 1
 DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2, "w8": 3, "w4": 4}
 W4_GROUP = 128  # elements of a row that share one int4 scale
+F8_GROUP = 128  # columns (and weight rows) that share one scale of an 8-bit floating point matrix
+KV8_BLOCK = 64  # tokens of the 8-bit cache that share one scale (per head)
 KERNELS = {"auto": 0, "rows_per_warp": 1, "warp_per_row": 2, "block_per_row": 3,
            "split_k": 4, "batched": 5, "scalar": 6, "stream": 7, "xsplit": 8, "tc": 9}
 X_STAGING = {0: "global", 1: "smem", 2: "smem_fp32", 3: "regs"}
@@ -52,6 +62,12 @@ class Plan(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel_name"] = KERNEL_NAMES.get(self.kernel, "?")
         return d
+
+
+class Kv8CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("blocks", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
 
 
 class GemvError(RuntimeError):
@@ -91,6 +107,14 @@ def lib() -> ctypes.CDLL:
         L.gemv_swiglu.restype = ci
         L.gemv_host.argtypes = [ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, ci, vp]
         L.gemv_host.restype = ci
+        L.gemv_f8_quantize.argtypes = [ci, vp, vp, vp, i64, ci, vp]
+        L.gemv_f8_quantize.restype = ci
+        L.gemv_f8.argtypes = [vp, vp, vp, vp, vp, vp, ci, i64, i64, ci, vp]
+        L.gemv_f8.restype = ci
+        L.gemv_kv8_append.argtypes = [ci, vp, vp, i64, vp, i64, vp, vp, ci, i64, vp]
+        L.gemv_kv8_append.restype = ci
+        L.gemv_kv8_attention.argtypes = [ci, vp, vp, i64, vp, vp, vp, ci, ci, ci, ctypes.c_float, i64, i64, vp]
+        L.gemv_kv8_attention.restype = ci
         L.gemv_set_launch_overlap.argtypes = [ci]
         L.gemv_set_launch_overlap.restype = ci
         L.gemv_status_string.argtypes = [ci]
@@ -136,11 +160,12 @@ def plan_for(dtype: str, M: int, K: int, B: int, aligned16: bool = True, num_sms
 
 def device_status(stream=None) -> tuple:
     """Synchronise `stream` and read (then clear) the device status word of the
-    kernels with bounded waits: (status, bits), status SUCCESS or
-    ERR_DEVICE_TIMEOUT; raises GemvError on a CUDA failure."""
+    kernels with bounded waits and of the 8-bit cache: (status, bits), status SUCCESS,
+    ERR_DEVICE_TIMEOUT or ERR_INVALID_VALUE (a block that the cache's pool or table does
+    not have); raises GemvError on a CUDA failure."""
     bits = ctypes.c_int(0)
     st = lib().gemv_get_device_status(_stream(stream), ctypes.byref(bits))
-    if st not in (SUCCESS, ERR_DEVICE_TIMEOUT):
+    if st not in (SUCCESS, ERR_DEVICE_TIMEOUT, ERR_INVALID_VALUE):
         _check(st)
     return st, int(bits.value)
 
@@ -358,3 +383,97 @@ def gemv_swiglu(dtype, A, row_scale, x, bias, y, I, K, B, stream=None) -> None:
             _addr(x, sx, max(0, B * K), "x"), _addr(bias, sx, M2 if bias is not None else 0, "bias"),
             _addr(y, sx, max(0, B * I), "y"))
     _check(_fn("gemv_swiglu")(DTYPE_CODES[dtype], *args, I, K, B, _stream(stream)))
+
+
+# ------------------------------------------------------ 8-bit floating point layers
+def gemv_f8_quantize(dtype, x, q, scale, K, B, stream=None) -> None:
+    """x (B, K) of `dtype` ("f32", "f16", "bf16") to e4m3 values q and fp32 scales
+    (B, ceil(K / F8_GROUP)), one for each group of F8_GROUP elements of a vector."""
+    K, B = int(K), int(B)
+    n, g = max(0, B * K), max(0, B * -(-K // F8_GROUP))
+    args = (_addr(x, _ESIZE[dtype][1], n, "x"), _addr(q, 1, n, "q"), _addr(scale, 4, g, "scale"))
+    _check(_fn("gemv_f8_quantize")(DTYPE_CODES[dtype], *args, K, B, _stream(stream)))
+
+
+def gemv_f8(A, a_scale, x, x_scale, bias, y, M, K, B, y_dtype="bf16", stream=None) -> None:
+    """y[b, m] = sum_k (a_scale A)[m, k] (x_scale x)[b, k] (+ bias[m]): e4m3 A (M, K)
+    with a scale for each block of F8_GROUP x F8_GROUP, e4m3 x (B, K) with one for each
+    F8_GROUP elements of a vector; y and bias of `y_dtype`."""
+    M, K, B, na, nx, ny = _sizes(M, K, B)
+    G, sy = -(-max(K, 0) // F8_GROUP), _ESIZE[y_dtype][1]
+    args = (_addr(A, 1, na, "A"), _addr(a_scale, 4, -(-max(M, 0) // F8_GROUP) * G, "a_scale"), _addr(x, 1, nx, "x"),
+            _addr(x_scale, 4, max(0, B * G), "x_scale"), _addr(bias, sy, M if bias is not None else 0, "bias"),
+            _addr(y, sy, ny, "y"))
+    _check(_fn("gemv_f8")(*args, DTYPE_CODES[y_dtype], M, K, B, _stream(stream)))
+
+
+def _kv8_cache(k, v, k_scale, v_scale, table, S):
+    """The cache as the library takes it; sizes from the tensors' shapes."""
+    if k.dim() != 4 or k.shape[2] != KV8_BLOCK or tuple(v.shape) != (k.shape[0], k.shape[1], k.shape[3], KV8_BLOCK):
+        raise ValueError(f"k must be (blocks, heads, {KV8_BLOCK}, dim) and v (blocks, heads, dim, {KV8_BLOCK}): "
+                         f"got {tuple(k.shape)} and {tuple(v.shape)}")
+    if table.dim() != 2 or table.shape[0] < S:
+        raise ValueError(f"table must be ({S}, width): got {tuple(table.shape)}")
+    blocks, heads, _, dim = k.shape
+    n = blocks * heads
+    return Kv8CacheStruct(_addr(k, 1, 0, "k"), _addr(v, 1, 0, "v"), _addr(k_scale, 4, n, "k_scale"),
+                          _addr(v_scale, 4, n, "v_scale"), _addr(table, 4, 0, "table"), blocks, table.shape[1], heads, dim)
+
+
+def _rows(t, elem_size, rows, row, what):
+    """Address and row stride of a tensor whose last dimensions, flattened, are rows of
+    `row` consecutive elements and whose first ones are `rows` evenly spaced rows."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.element_size() != elem_size:
+        raise ValueError(f"{what}: element size {t.element_size()} != {elem_size}")
+    if t.numel() != rows * row:
+        raise ValueError(f"{what}: {t.numel()} elements, {rows} rows of {row} are needed")
+    if t.is_contiguous() or rows == 0:
+        return t.data_ptr(), row
+    if rows == 1:  # one row: its own dimensions alone have to be consecutive
+        stride = row
+    else:
+        stride = None
+    want, n = 1, 1  # expected stride, elements covered so far
+    for size, st in zip(reversed(t.shape), reversed(t.stride())):
+        if size == 1:
+            continue
+        if n == row:  # the innermost of the row dimensions
+            if stride is None:
+                stride = want = st
+        if st != want:
+            raise ValueError(f"{what}: strides {t.stride()} are no evenly spaced rows of {row} consecutive elements")
+        want *= size
+        n *= size
+    return t.data_ptr(), stride
+
+
+def gemv_kv8_append(dtype, k_cache, v_cache, k_scale, v_scale, table, k, v, lens, starts, S, N, stream=None) -> None:
+    """Writes N new tokens (rows of k and v, each heads x dim of `dtype`, columns of a
+    wider tensor as well) to the 8-bit cache: those of sequence s are the rows
+    starts[s] .. starts[s + 1] (int32, S + 1 values; None: N / S each) and take the last
+    positions of its lens[s] tokens (int32)."""
+    S, N = int(S), int(N)
+    c = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, row = _ESIZE[dtype][1], c.heads * c.dim
+    ka, ks = _rows(k, size, max(N, 0), row, "k")
+    va, vs = _rows(v, size, max(N, 0), row, "v")
+    _check(_fn("gemv_kv8_append")(DTYPE_CODES[dtype], ctypes.addressof(c), ka, ks, va, vs, _addr(lens, 4, max(S, 0), "lens"),
+                                  _addr(starts, 4, S + 1, "starts"), S, N, _stream(stream)))
+
+
+def gemv_kv8_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, q, lens, out, lse, S, T, q_heads, scale,
+                       window=0, sinks=0, stream=None) -> None:
+    """Attention of the newest T tokens of S sequences over the 8-bit cache: q and out
+    (S, T, q_heads, dim) of `dtype` ("f16", "bf16"; q also as columns of a wider
+    tensor), lens (S) int32, lse (S, T, q_heads) fp32 or None.  window > 0: a query sees
+    the `window` latest tokens, itself among them, and the first `sinks`."""
+    S, T, q_heads = int(S), int(T), int(q_heads)
+    c = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, rows, row = _ESIZE[dtype][1], max(0, S * T), max(0, q_heads * c.dim)
+    qa, qs = _rows(q, size, rows, row, "q")
+    _check(_fn("gemv_kv8_attention")(DTYPE_CODES[dtype], ctypes.addressof(c), qa, qs, _addr(lens, 4, max(S, 0), "lens"),
+                                     _addr(out, size, rows * row, "out"),
+                                     _addr(lse, 4, rows * max(q_heads, 0), "lse"), S, T, q_heads, float(scale),
+                                     int(window), int(sinks), _stream(stream)))

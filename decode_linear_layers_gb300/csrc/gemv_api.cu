@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "../../include/gemv.h"
+#include "gemv_internal.h"
 #include "gemv_launch.cuh"
 #include "gemv_plan.h"
 
@@ -243,6 +244,47 @@ bool tc_tensor_maps(int dtype, const void *A, const void *x, int64_t M, int64_t 
 void record_cuda_error(int e) { t_last_cuda_error = e; }
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 int launch_overlap() { return t_overlap; }
+gemv_status_t fail(int e) { return cuda_fail((cudaError_t)e); }
+gemv_status_t device_sms(int *out) { return sm_count(out); }
+gemv_status_t device_status_word(int **out) { return status_word(out); }
+int64_t wait_limit(int *stall) {
+  *stall = g_test_stall;
+  return g_test_stall && g_test_timeout_ns > 0 ? g_test_timeout_ns : kDefaultTimeoutNs;
+}
+bool overlaps(const void *p, int64_t n, const void *q, int64_t m) { return ::overlaps(p, n, q, m); }
+
+cudaError_t workspace(void **p, size_t bytes, cudaStream_t s) {
+  static std::atomic<cudaMemPool_t> pools[kMaxDevices];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  cudaMemPool_t pool = pools[dev].load(std::memory_order_acquire);
+  if (pool == nullptr) {
+    std::lock_guard<std::mutex> lk(mu);
+    pool = pools[dev].load(std::memory_order_relaxed);
+    if (pool == nullptr) {
+      // a first call may come while its stream is captured: the pool is no part of that
+      cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+      if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+      cudaMemPoolProps props = {};
+      props.allocType = cudaMemAllocationTypePinned;
+      props.location.type = cudaMemLocationTypeDevice;
+      props.location.id = dev;
+      e = cudaMemPoolCreate(&pool, &props);
+      if (e == cudaSuccess) {
+        uint64_t keep = UINT64_MAX;
+        e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+      }
+      const cudaError_t e2 = cudaThreadExchangeStreamCaptureMode(&mode);
+      if (e == cudaSuccess) e = e2;
+      if (e != cudaSuccess) return e;
+      pools[dev].store(pool, std::memory_order_release);
+    }
+  }
+  return cudaMallocFromPoolAsync(p, bytes, pool, s);
+}
 }  // namespace gemv
 
 extern "C" {
@@ -377,7 +419,7 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits) {
   e = cudaMemset(p, 0, sizeof v);
   if (e != cudaSuccess) return cuda_fail(e);
   if (bits != nullptr) *bits = v;
-  return GEMV_ERR_DEVICE_TIMEOUT;
+  return (v & (gemv::kTcStatusMma | gemv::kTcStatusDrain)) != 0 ? GEMV_ERR_DEVICE_TIMEOUT : GEMV_ERR_INVALID_VALUE;
 }
 
 gemv_status_t gemv_test_stall(int stall, int64_t timeout_ns) {

@@ -1,0 +1,174 @@
+// gemv_f8 and gemv_f8_quantize: argument checks, the choice of the form, launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gemv.h"
+#include "gemv_f8.cuh"
+#include "gemv_internal.h"
+#include "gemv_launch.cuh"
+
+namespace gemv {
+namespace {
+
+// 8-bit matrix (rows x K, row-major) in boxes of 128 columns x box_rows, 128-byte
+// swizzle, zeros outside.
+bool f8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {(cuuint32_t)kF8Group, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N, bool kPrompt>
+gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int sms, cudaStream_t s) {
+  using F = F8Form<N, kPrompt>;
+  a.tm = (int)((a.M + (kPrompt ? N : kF8Rows) - 1) / (kPrompt ? N : kF8Rows));
+  a.tn = kPrompt ? (a.B + kF8Rows - 1) / kF8Rows : 1;
+  a.tiles = (int64_t)a.tm * a.tn;
+  const int64_t blocks = a.tiles * a.groups;
+  const int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
+  a.shared = a.tiles % W;
+  CUtensorMap map_a, map_x;
+  if (!f8_map(&map_a, A, a.M, K, kPrompt ? N : kF8Rows) || !f8_map(&map_x, x, a.B, K, kPrompt ? kF8Rows : N))
+    return fail((int)cudaErrorInvalidValue);
+  cudaError_t e = cudaSuccess;
+  void *ws = nullptr;
+  if (a.shared > 0) {
+    e = workspace(&ws, (size_t)(W * 2 * F::kPartial * 4), s);
+    if (e != cudaSuccess) return fail((int)e);
+    a.ws = static_cast<float *>(ws);
+  }
+  const int pdl = launch_overlap();
+  e = allow_smem(k_f8<N, kPrompt>, F::kSmem);
+  if (e == cudaSuccess)
+    e = launch_k(k_f8<N, kPrompt>, dim3((unsigned)W), dim3(F::kThreads), (size_t)F::kSmem, s, pdl,
+                 kPrompt ? map_x : map_a, kPrompt ? map_a : map_x, a);
+  int n = 1;
+  if (e == cudaSuccess && a.shared > 0) {
+    e = launch_k(k_f8_join<N, kPrompt>, dim3((unsigned)a.shared, (unsigned)(F::kPartial / kF8JoinPiece)),
+                 dim3(kF8JoinThreads), 0, s, pdl, a, (int)W);
+    n = 2;
+  }
+  if (ws != nullptr) {
+    const cudaError_t e2 = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = e2;
+  }
+  if (e != cudaSuccess) return fail((int)e);
+  count_launches(n);
+  return GEMV_SUCCESS;
+}
+
+bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
+bool aligned(const void *p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
+
+template <int DT>
+cudaError_t quantize(const void *x, uint8_t *q, float *scale, int64_t K, int64_t G, int64_t groups, int sms, cudaStream_t s) {
+  const bool vec = K % 8 == 0 && aligned(x, 16) && aligned(q, 8);
+  constexpr int kTeams = kF8QThreads / 16;
+  // several groups of a team in flight once every SM's threads have one
+  const bool many = groups > (int64_t)sms * (2048 / 16) * 2;
+  auto go = [&](auto kern, int u) {
+    const int64_t grid = (groups + kTeams * u - 1) / (kTeams * u);
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_k(kern, dim3((unsigned)grid), dim3(kF8QThreads), 0, s, launch_overlap(), x, q, scale, K, (int)G, groups);
+  };
+  if (vec) return many ? go(k_f8_quantize<DT, true, 4>, 4) : go(k_f8_quantize<DT, true, 1>, 1);
+  return many ? go(k_f8_quantize<DT, false, 2>, 2) : go(k_f8_quantize<DT, false, 1>, 1);
+}
+
+}  // namespace
+}  // namespace gemv
+
+using namespace gemv;
+
+extern "C" {
+
+gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, float *scale, int64_t K, int B,
+                               gemv_stream_t stream) {
+  if (K < 0 || B < 0 || dtype < GEMV_DTYPE_F32 || dtype > GEMV_DTYPE_BF16) return GEMV_ERR_INVALID_VALUE;
+  if (K == 0 || B == 0) return GEMV_SUCCESS;
+  const int sx = dtype == GEMV_DTYPE_F32 ? 4 : 2;
+  const int64_t G = (K + GEMV_F8_GROUP - 1) / GEMV_F8_GROUP;
+  int64_t bk, xb, groups, sb;
+  if (K > 0x7fffffff || !mul_ok(B, K, &bk) || !mul_ok(bk, sx, &xb) || !mul_ok(B, G, &groups) || !mul_ok(groups, 4, &sb))
+    return GEMV_ERR_INVALID_VALUE;
+  if (x == nullptr || q == nullptr || scale == nullptr || !aligned(x, sx) || !aligned(scale, 4)) return GEMV_ERR_INVALID_VALUE;
+  if (overlaps(q, bk, x, xb) || overlaps(scale, sb, x, xb) || overlaps(scale, sb, q, bk)) return GEMV_ERR_INVALID_VALUE;
+  int sms = 0;
+  gemv_status_t st = device_sms(&sms);
+  if (st != GEMV_SUCCESS) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == GEMV_DTYPE_F32   ? quantize<GEMV_DTYPE_F32>(x, q, scale, K, G, groups, sms, s)
+                        : dtype == GEMV_DTYPE_F16 ? quantize<GEMV_DTYPE_F16>(x, q, scale, K, G, groups, sms, s)
+                                                  : quantize<GEMV_DTYPE_BF16>(x, q, scale, K, G, groups, sms, s);
+  if (e != cudaSuccess) return fail((int)e);
+  count_launches(1);
+  return GEMV_SUCCESS;
+}
+
+gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
+                      void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream) {
+  if (M < 0 || K < 0 || B < 0 || y_dtype < GEMV_DTYPE_F32 || y_dtype > GEMV_DTYPE_BF16) return GEMV_ERR_INVALID_VALUE;
+  if (K % GEMV_F8_ALIGN != 0) return GEMV_ERR_INVALID_VALUE;
+  if (M == 0 || B == 0) return GEMV_SUCCESS;
+  const int sy = y_dtype == GEMV_DTYPE_F32 ? 4 : 2;
+  const int64_t G = (K + GEMV_F8_GROUP - 1) / GEMV_F8_GROUP;
+  int64_t mk, bk, bm, yb, bg, t;
+  // sizes and row numbers are 32-bit coordinates of the copies
+  if (M > 0x7fffff00 || K > 0x7fffff00 || B > 0x7fffff00 || !mul_ok(M, K, &mk) || !mul_ok(B, K, &bk) || !mul_ok(B, M, &bm) ||
+      !mul_ok(bm, sy, &yb) || !mul_ok(B, G * 4, &bg) || !mul_ok((M / 128 + 1) * ((int64_t)B / 128 + 1), G, &t) ||
+      t > ((int64_t)1 << 50))
+    return GEMV_ERR_INVALID_VALUE;
+  const int64_t ag = (M + GEMV_F8_GROUP - 1) / GEMV_F8_GROUP * G * 4;
+  if (y == nullptr || (K > 0 && (A == nullptr || a_scale == nullptr || x == nullptr || x_scale == nullptr)))
+    return GEMV_ERR_INVALID_VALUE;
+  if (!aligned(A, GEMV_F8_ALIGN) || !aligned(x, GEMV_F8_ALIGN) || !aligned(a_scale, 4) || !aligned(x_scale, 4) ||
+      !aligned(y, sy) || !aligned(bias, sy))
+    return GEMV_ERR_INVALID_VALUE;
+  if (overlaps(y, yb, A, mk) || overlaps(y, yb, x, bk) || overlaps(y, yb, a_scale, ag) || overlaps(y, yb, x_scale, bg) ||
+      overlaps(y, yb, bias, M * sy))
+    return GEMV_ERR_INVALID_VALUE;
+  int sms = 0;
+  gemv_status_t st = device_sms(&sms);
+  if (st != GEMV_SUCCESS) return st;
+  F8Args a;
+  a.a_scale = a_scale;
+  a.x_scale = x_scale;
+  a.bias = bias;
+  a.y = y;
+  a.y_dtype = (int)y_dtype;
+  a.M = M;
+  a.B = B;
+  a.groups = (int)G;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (K == 0) {
+    const int64_t grid = (bm + 255) / 256;
+    const cudaError_t e = launch_k(k_f8_empty, dim3((unsigned)(grid < sms * 8 ? grid : sms * 8)), dim3(256), 0, s, launch_overlap(), a);
+    if (e != cudaSuccess) return fail((int)e);
+    count_launches(1);
+    return GEMV_SUCCESS;
+  }
+  st = device_status_word(&a.status);
+  if (st != GEMV_SUCCESS) return st;
+  a.timeout_ns = wait_limit(&a.test_stall);
+  if (B <= 16) return f8_launch<16, false>(a, A, x, K, sms, s);
+  if (B <= 32) return f8_launch<32, false>(a, A, x, K, sms, s);
+  if (B <= 64) return f8_launch<64, false>(a, A, x, K, sms, s);
+  if (B <= 128) return f8_launch<128, false>(a, A, x, K, sms, s);
+  return f8_launch<256, true>(a, A, x, K, sms, s);
+}
+
+}  // extern "C"

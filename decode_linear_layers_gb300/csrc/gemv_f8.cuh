@@ -1,0 +1,664 @@
+// Kernels of the block-scaled 8-bit floating point product (gemv_f8) and of the
+// quantiser of its vectors (gemv_f8_quantize).
+//
+//     y[b][m] = sum_g sa[m / 128][g] sx[b][g] P_g[b][m] + bias[m],
+//     P_g[b][m] = sum_{k in group g} A[m][k] x[b][k]
+//
+// A and x hold e4m3 values; g runs over the groups of 128 columns.  The tensor cores
+// (tcgen05 kind::f8f6f4) compute P_g, a tile of 128 x N values for each k-block of 128
+// columns, into one of a few accumulators in tensor memory.  The scales are any fp32
+// numbers, so P_g cannot stay there: the scaling warps read it (tcgen05.ld), and
+// add sa sx P_g to the tile's fp32 sums in their registers, while the next k-blocks'
+// products fill the other accumulators.
+#pragma once
+
+#include "gemv_tc.cuh"
+
+namespace gemv {
+
+constexpr int kF8Group = 128;    // columns per scale, and per k-block: one 128-byte swizzle atom
+constexpr int kF8Rows = 128;     // rows of a tile: the MMA's M
+constexpr int kF8RoleThreads = 128;  // warps 0 (copies) and 1 (MMAs), two idle
+constexpr int kF8MaxStages = 12;
+constexpr int kF8TileM = 256;    // weight rows of a tile of the prompt form
+
+struct F8Args {
+  const float *a_scale = nullptr, *x_scale = nullptr;
+  const void *bias = nullptr;
+  void *y = nullptr;
+  float *ws = nullptr;   // partial sums of tiles that several CTAs share
+  int *status = nullptr;
+  int64_t timeout_ns = 0, M = 0;
+  int64_t tiles = 0;     // row tiles x column tiles
+  int64_t shared = 0;    // tiles 0 .. shared - 1 are split over all CTAs, the rest go whole
+  int B = 0, groups = 0; // groups = k-blocks
+  int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
+  int y_dtype = 0, stages = 0, test_stall = 0;
+};
+
+// ------------------------------------------------------------------ output types
+__device__ __forceinline__ unsigned short f8_round16(float v, int dt) {
+  return dt == GEMV_DTYPE_F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ float f8_bias(const F8Args &a, int64_t m) {
+  if (a.y_dtype == GEMV_DTYPE_F32) return __ldg(reinterpret_cast<const float *>(a.bias) + m);
+  const unsigned short h = __ldg(reinterpret_cast<const unsigned short *>(a.bias) + m);
+  return a.y_dtype == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half(h)) : __uint_as_float((uint32_t)h << 16);
+}
+__device__ __forceinline__ void f8_store(const F8Args &a, int64_t i, float v) {
+  if (a.y_dtype == GEMV_DTYPE_F32)
+    reinterpret_cast<float *>(a.y)[i] = v;
+  else
+    reinterpret_cast<unsigned short *>(a.y)[i] = f8_round16(v, a.y_dtype);
+}
+
+// ------------------------------------------------------------------ work of a CTA
+// The k-blocks of the `shared` first tiles, R = shared x groups of them, are cut into
+// gridDim.x equal ranges (range w: [w R / W, (w + 1) R / W)), so that a few tiles keep
+// every SM busy; at most one range more than a tile's worth, so it meets two tiles at
+// most.  The other tiles, a multiple of W, go round whole.  Each role of a CTA walks
+// the same segments.
+struct F8Seg {
+  int64_t tile;
+  int k0, k1;
+  int slot;  // which of the CTA's two partial sums it fills; -1: the whole tile
+};
+struct F8Walk {
+  int64_t lo, hi, next_tile, tiles;
+  int groups, step, part;
+  __device__ F8Walk(const F8Args &a) {
+    const int64_t R = a.shared * a.groups, w = blockIdx.x, W = gridDim.x;
+    lo = w * R / W;
+    hi = (w + 1) * R / W;
+    next_tile = a.shared + w;
+    tiles = a.tiles;
+    groups = a.groups;
+    step = (int)W;
+    part = 0;
+  }
+  __device__ bool next(F8Seg &s) {
+    if (lo < hi) {
+      s.tile = lo / groups;
+      s.k0 = (int)(lo - s.tile * groups);
+      s.k1 = (int)(hi - lo < groups - s.k0 ? s.k0 + (hi - lo) : groups);
+      s.slot = s.k0 == 0 && s.k1 == groups ? -1 : part;
+      ++part;
+      lo += s.k1 - s.k0;
+      return true;
+    }
+    if (next_tile >= tiles) return false;
+    s.tile = next_tile;
+    s.k0 = 0;
+    s.k1 = groups;
+    s.slot = -1;
+    next_tile += step;
+    return true;
+  }
+};
+// The CTA whose range holds k-block u of the shared tiles: the last w with w R / W <= u.
+__host__ __device__ inline int64_t f8_owner(int64_t u, int64_t R, int64_t W) { return ((u + 1) * W - 1) / R; }
+
+// Tile -> (tile of weight rows, tile of vectors).  Whole bands of 16 weight tiles, their
+// weights read once into L2, meet every tile of vectors before the next band.
+__device__ __forceinline__ void f8_tile(const F8Args &a, int64_t t, int &im, int &in) {
+  constexpr int kBand = 16;
+  const int64_t per = (int64_t)kBand * a.tn;
+  const int64_t band = t / per;
+  const int64_t r = t - band * per;
+  const int w = (int)(a.tm - band * kBand < kBand ? a.tm - band * kBand : kBand);
+  in = (int)(r / w);
+  im = (int)(band * kBand + (r - (int64_t)in * w));
+}
+
+// ------------------------------------------------------------------ instructions
+// kind::f8f6f4, both operands e4m3 (format 0), fp32 accumulator, both K-major; 32
+// columns of k.
+__device__ __forceinline__ uint32_t f8_idesc(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kF8Rows >> 4) << 24);
+}
+__device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// C accumulator columns of this warp's 32 tensor-memory lanes; the values are there
+// after f8_ld_wait, which names them so that no use moves above it.
+template <int C>
+__device__ __forceinline__ void f8_ld(uint32_t addr, uint32_t (&r)[C]) {
+  static_assert(C == 16 || C == 32);
+  if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+  }
+}
+template <int C>
+__device__ __forceinline__ void f8_ld_wait(uint32_t (&r)[C]) {
+  if constexpr (C == 16) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+  }
+}
+
+// ------------------------------------------------------------------ the product
+// kPrompt = false: a tile is 128 weight rows x N vectors (one tile of vectors, B <= N);
+//   thread = weight row, column = vector.
+// kPrompt = true: a tile is 128 vectors x N = 256 weight rows; thread = vector, and the
+//   256 columns are two blocks of 128 weight rows, one per scaling warpgroup, so that a
+//   thread's factor sa sx is one number per k-block.
+template <int N, bool kPrompt>
+struct F8Form {
+  static constexpr int kGroupsOfWarps = kPrompt ? 2 : 1;                      // scaling warpgroups
+  static constexpr int kThreads = kF8RoleThreads + 128 * kGroupsOfWarps;
+  static constexpr int kCols = N / kGroupsOfWarps;                           // columns of a thread
+  static constexpr int kAcc = N == 256 ? 2 : 4;                              // accumulators in tensor memory
+  static constexpr int kTmemCols = kAcc * N < 32 ? 32 : kAcc * N;
+  static constexpr int kStage = (kF8Rows + N) * kF8Group;                    // bytes
+  // after the ring: each scaling warp's output staging (prompts) or factors (two sets)
+  static constexpr int kWarpBytes = kPrompt ? 32 * 128 : 2 * N * 4;
+  static constexpr int kTail = 4 * kGroupsOfWarps * kWarpBytes;
+  static constexpr int kStages = (226 * 1024 - kTail) / kStage < kF8MaxStages ? (226 * 1024 - kTail) / kStage : kF8MaxStages;
+  static constexpr int kSmem = 1024 + kStages * kStage + kTail;
+  static constexpr int64_t kPartial = (int64_t)kF8Rows * N;                  // floats of a partial sum
+};
+
+// map_p: the operand of the tile's 128 rows, map_q: that of its N columns; 8-bit, box
+// 128 bytes x 128 or N rows, 128-byte swizzle, zeros outside the matrix.
+template <int N, bool kPrompt>
+__global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
+    k_f8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const F8Args a) {
+  using F = F8Form<N, kPrompt>;
+  constexpr int S = F::kStages, NACC = F::kAcc, COLS = F::kCols;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ long long sh_loaded, sh_consumed, sh_committed;  // for the drain after an abort
+  pdl_trigger();
+  pdl_wait();  // every read (TMA included) after the kernel before has finished
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)),
+                 "r"((uint32_t)F::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc_mbar_init(&full[s], 1);
+      tc_mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      tc_mbar_init(&accf[b], 1);
+      tc_mbar_init(&acce[b], 4 * F::kGroupsOfWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+    sh_loaded = sh_consumed = sh_committed = -1;
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort = &abort_flag;
+  const int G = a.groups;
+
+  if (warp < 4) {
+    if constexpr (kPrompt) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {  // copies
+      int64_t i = 0;
+      int s = 0;
+      uint32_t ph = 1;  // the ring starts empty
+      F8Walk walk(a);
+      F8Seg g;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        int im, in;
+        f8_tile(a, g.tile, im, in);
+        const int32_t p0 = kPrompt ? in * kF8Rows : im * kF8Rows, q0 = kPrompt ? im * N : in * N;
+        for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
+          if (i >= S && !tc_mbar_wait_or_abort(&empty[s], ph, a.timeout_ns, abort)) {
+            ok = false;
+            break;
+          }
+          unsigned char *st = smem + (size_t)s * F::kStage;
+          tc_mbar_arrive_expect_tx(&full[s], F::kStage);
+          tc_tma_2d(st, &map_p, kb * kF8Group, p0, &full[s]);
+          tc_tma_2d(st + kF8Rows * kF8Group, &map_q, kb * kF8Group, q0, &full[s]);
+          sh_loaded = i;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 1 && lane == 0) {  // MMAs
+      const uint32_t idesc = f8_idesc(N);
+      int64_t i = 0, total = 0;
+      if (a.test_stall) {  // test: the last k-block of the first CTA never completes
+        F8Walk w(a);
+        F8Seg g;
+        while (w.next(g)) total += g.k1 - g.k0;
+      }
+      int s = 0, c = 0;
+      uint32_t ph = 0, cph = 1;
+      F8Walk walk(a);
+      F8Seg g;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
+          if ((i >= NACC && !tc_mbar_wait_or_abort(&acce[c], cph, a.timeout_ns, abort)) ||
+              !tc_mbar_wait_or_abort(&full[s], ph, a.timeout_ns, abort)) {
+            ok = false;
+            break;
+          }
+          sh_consumed = i;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (a.test_stall && blockIdx.x == 0 && i == total - 1) break;
+          const uint32_t sp = tc_smem_u32(smem + (size_t)s * F::kStage), sq = sp + kF8Rows * kF8Group;
+#pragma unroll
+          for (int kk = 0; kk < kF8Group / 32; ++kk)
+            f8_mma(tmem + (uint32_t)(c * N), tc_smem_desc(sp + kk * 32), tc_smem_desc(sq + kk * 32), idesc, kk > 0);
+          tc_commit(&empty[s]);
+          tc_commit(&accf[c]);
+          sh_committed = i;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++c == NACC) {
+            c = 0;
+            cph ^= 1;
+          }
+        }
+      }
+    }
+  } else {
+    if constexpr (kPrompt) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int wq = warp & 3, wg = (warp >> 2) - 1;     // tensor-memory lanes 32 wq .. + 31
+    const int row = wq * 32 + lane;                    // of the tile
+    const int col0 = wg * COLS;
+    unsigned char *mine = smem + (size_t)S * F::kStage + (size_t)(warp - 4) * F::kWarpBytes;
+    constexpr int CH = COLS < 32 ? COLS : 32;
+    int c = 0;
+    uint32_t cph = 0;
+    F8Walk walk(a);
+    F8Seg g;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      int im, in;
+      f8_tile(a, g.tile, im, in);
+      __syncwarp();  // the factors of the segment before are read before they are overwritten
+      float acc[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      // the factors' sources: this thread's vector and column block (prompts), or the
+      // row block and the vectors lane, lane + 32, ...
+      constexpr int NV = kPrompt ? 1 : (N + 31) / 32;
+      const float *sa, *sx[NV];
+      bool vx[NV], va = true;
+      if constexpr (kPrompt) {
+        const int64_t b = (int64_t)in * kF8Rows + row, mb = (int64_t)im * (N / kF8Group) + wg;
+        vx[0] = b < a.B;
+        sx[0] = a.x_scale + (vx[0] ? b : 0) * G;
+        va = mb * kF8Group < a.M;
+        sa = a.a_scale + (va ? mb : 0) * G;
+      } else {
+        sa = a.a_scale + (int64_t)im * G;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int b = lane + 32 * v;
+          vx[v] = b < a.B && b < N;
+          sx[v] = a.x_scale + (int64_t)(vx[v] ? b : 0) * G;
+        }
+      }
+      float fa = va ? __ldg(sa + g.k0) : 0.f, fx[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) fx[v] = vx[v] ? __ldg(sx[v] + g.k0) : 0.f;
+      for (int kb = g.k0; kb < g.k1; ++kb) {
+        float f = 0.f;
+        const float *fs = nullptr;
+        if constexpr (kPrompt) {
+          f = fa * fx[0];
+        } else {
+          float *w = reinterpret_cast<float *>(mine) + (kb & 1) * N;
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+            if (lane + 32 * v < N) w[lane + 32 * v] = fa * fx[v];
+          __syncwarp();
+          fs = w;
+        }
+        if (kb + 1 < g.k1) {  // the next k-block's factors, in flight during this one
+          fa = va ? __ldg(sa + kb + 1) : 0.f;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) fx[v] = vx[v] ? __ldg(sx[v] + kb + 1) : 0.f;
+        }
+        ok = tc_mbar_wait_or_abort(&accf[c], cph, a.timeout_ns, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * N + col0);
+        uint32_t r[2][CH];
+        f8_ld<CH>(at, r[0]);
+#pragma unroll
+        for (int h = 0; h < COLS / CH; ++h) {
+          f8_ld_wait<CH>(r[h & 1]);
+          if (h + 1 < COLS / CH) {
+            f8_ld<CH>(at + (h + 1) * CH, r[(h + 1) & 1]);
+          } else {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc_mbar_arrive(&acce[c]);
+          }
+          if constexpr (kPrompt) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) acc[h * CH + j] = fmaf(f, __uint_as_float(r[h & 1][j]), acc[h * CH + j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < CH; j += 4) {
+              const float4 q = *reinterpret_cast<const float4 *>(fs + h * CH + j);
+              acc[h * CH + j] = fmaf(q.x, __uint_as_float(r[h & 1][j]), acc[h * CH + j]);
+              acc[h * CH + j + 1] = fmaf(q.y, __uint_as_float(r[h & 1][j + 1]), acc[h * CH + j + 1]);
+              acc[h * CH + j + 2] = fmaf(q.z, __uint_as_float(r[h & 1][j + 2]), acc[h * CH + j + 2]);
+              acc[h * CH + j + 3] = fmaf(q.w, __uint_as_float(r[h & 1][j + 3]), acc[h * CH + j + 3]);
+            }
+          }
+        }
+        if (++c == NACC) {
+          c = 0;
+          cph ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (g.slot >= 0) {
+        // a part of the tile's k-blocks: k_f8_join adds the parts.  Prompts [row][column]
+        // (four columns at a time), else [column][row]: both as the join writes y
+        float *p = a.ws + ((int64_t)blockIdx.x * 2 + g.slot) * F::kPartial;
+        if constexpr (kPrompt) {
+#pragma unroll
+          for (int j = 0; j < COLS; j += 4)
+            *reinterpret_cast<float4 *>(p + row * N + col0 + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) p[j * kF8Rows + row] = acc[j];
+        }
+        continue;
+      }
+      if constexpr (!kPrompt) {
+        const int64_t m = (int64_t)im * kF8Rows + row;
+        if (m < a.M) {
+          const float bias = a.bias != nullptr ? f8_bias(a, m) : 0.f;
+#pragma unroll
+          for (int j = 0; j < COLS; ++j)
+            if (j < a.B) f8_store(a, (int64_t)j * a.M + m, acc[j] + bias);
+        }
+      } else {
+        // the warp's 32 rows leave through its staging buffer, 128 bytes of each at a
+        // time (16-byte pieces, their order rotated by the row: free of bank conflicts),
+        // so that eight lanes store 128 consecutive bytes of y
+        const int64_t b0 = (int64_t)in * kF8Rows + wq * 32, m0 = (int64_t)im * N + col0;
+        const bool f32 = a.y_dtype == GEMV_DTYPE_F32;
+        const int esz = f32 ? 4 : 2;
+        const bool vec = (a.M * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+        if (a.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) acc[j] += m0 + j < a.M ? f8_bias(a, m0 + j) : 0.f;
+        }
+#pragma unroll
+        for (int h = 0; h < COLS / 32; ++h) {
+          // 32 columns: 128 bytes of fp32, or half of the 64 columns of a 16-bit pass
+          if (f32) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4 *>(mine + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                  make_float4(acc[h * 32 + q * 4], acc[h * 32 + q * 4 + 1], acc[h * 32 + q * 4 + 2], acc[h * 32 + q * 4 + 3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = (uint32_t)f8_round16(acc[h * 32 + q * 8 + 2 * e], a.y_dtype) |
+                       ((uint32_t)f8_round16(acc[h * 32 + q * 8 + 2 * e + 1], a.y_dtype) << 16);
+              *reinterpret_cast<uint4 *>(mine + lane * 128 + ((((h & 1) * 4 + q) ^ (lane & 7)) * 16)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if ((h & 1) == 0) continue;
+          }
+          __syncwarp();
+          const int64_t c0 = m0 + (f32 ? h * 32 : (h - 1) * 32);   // first column of the pass
+          const int per = f32 ? 4 : 8;                             // columns of a piece
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = it * 4 + (lane >> 3), pc = lane & 7;
+            const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((pc ^ (rr & 7)) * 16));
+            const int64_t b = b0 + rr, m = c0 + pc * per;
+            if (b >= a.B || m >= a.M) continue;
+            char *dst = reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz;
+            if (vec) {  // M is a whole number of pieces
+              *reinterpret_cast<uint4 *>(dst) = w;
+            } else {
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (f32) {
+                  if (e < 4 && m + e < a.M) reinterpret_cast<uint32_t *>(dst)[e] = ww[e & 3];
+                } else if (m + e < a.M) {
+                  reinterpret_cast<unsigned short *>(dst)[e] = (unsigned short)(ww[e >> 1] >> (16 * (e & 1)));
+                }
+              }
+            }
+          }
+          __syncwarp();  // read before the next pass overwrites the buffer
+        }
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();  // the role threads rejoin their warps: the CTA barrier counts whole warps
+  __syncthreads();
+  if (abort_flag != 0) {
+    // nothing may be in flight when the CTA frees its tensor memory and exits: the last
+    // committed MMAs (their commit covers all earlier ones) and every copy issued but
+    // not waited for
+    if (tid == 0) {
+      if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
+      const int64_t committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
+      bool drained = committed < 0 || tc_mbar_wait(&empty[committed % S], (uint32_t)((committed / S) & 1), a.timeout_ns);
+      for (int64_t t = consumed + 1; t <= loaded && drained; ++t)
+        drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
+      if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)F::kTmemCols) : "memory");
+  }
+}
+
+// Tiles whose k-blocks several CTAs of k_f8 share: their partial sums, added in the
+// order of the k-blocks, and the epilogue.  grid (shared tiles, pieces of 2048 values),
+// 256 threads; W: k_f8's CTAs.
+constexpr int kF8JoinThreads = 256, kF8JoinPiece = 2048;
+template <int N, bool kPrompt>
+__global__ void __launch_bounds__(kF8JoinThreads) k_f8_join(const F8Args a, int W) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t R = a.shared * a.groups, u0 = (int64_t)blockIdx.x * a.groups;
+  const int64_t w0 = f8_owner(u0, R, W), w1 = f8_owner(u0 + a.groups - 1, R, W);
+  if (w0 == w1) return;  // one CTA had the whole tile and wrote it
+  int im, in;
+  f8_tile(a, blockIdx.x, im, in);
+  constexpr int V = kPrompt ? 4 : 1;
+  for (int i = threadIdx.x * V; i < kF8JoinPiece; i += kF8JoinThreads * V) {
+    const int e = blockIdx.y * kF8JoinPiece + i;
+    const int row = kPrompt ? e / N : e % kF8Rows, col = kPrompt ? e % N : e / kF8Rows;
+    const int64_t b = kPrompt ? (int64_t)in * kF8Rows + row : col;
+    const int64_t m = kPrompt ? (int64_t)im * N + col : (int64_t)im * kF8Rows + row;
+    if (b >= a.B || m >= a.M) continue;
+    float s[V] = {};
+    for (int64_t w = w0; w <= w1; ++w) {
+      const int64_t lo = w * R / W;
+      if (lo == (w + 1) * R / W) continue;  // (fewer k-blocks than CTAs: some have none)
+      // its first range of k-blocks, unless that lies in the tile before
+      const int slot = lo / a.groups == blockIdx.x ? 0 : 1;
+      const float *p = a.ws + (w * 2 + slot) * (int64_t)kF8Rows * N + e;
+      if constexpr (V == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        s[0] += q.x; s[1] += q.y; s[2] += q.z; s[3] += q.w;
+      } else {
+        s[0] += *p;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (m + j < a.M) f8_store(a, b * a.M + m + j, s[j] + (a.bias != nullptr ? f8_bias(a, m + j) : 0.f));
+  }
+}
+
+// No columns: the empty sum.
+static __global__ void k_f8_empty(const F8Args a) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t n = a.M * a.B;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    f8_store(a, i, a.bias != nullptr ? f8_bias(a, i % a.M) : 0.f);
+}
+
+// ------------------------------------------------------------------ the quantiser
+// Two values to e4m3, round to nearest even; beyond +-448, infinities too, to +-448;
+// NaN stays NaN.  `a` in the low byte.
+__device__ __forceinline__ uint32_t f8_pack2(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// |v| if v is finite, else 0.
+__device__ __forceinline__ float f8_finite_abs(float v) {
+  const float m = fabsf(v);
+  return m < __int_as_float(0x7f800000) ? m : 0.f;
+}
+template <int DT>
+__device__ __forceinline__ float f8_load1(const void *p, int64_t i) {
+  if constexpr (DT == GEMV_DTYPE_F32) return __ldg(reinterpret_cast<const float *>(p) + i);
+  const unsigned short h = __ldg(reinterpret_cast<const unsigned short *>(p) + i);
+  if constexpr (DT == GEMV_DTYPE_F16) return __half2float(__ushort_as_half(h));
+  return __uint_as_float((uint32_t)h << 16);
+}
+template <int DT>
+__device__ __forceinline__ void f8_load8(const void *p, int64_t i, float (&v)[8]) {
+  if constexpr (DT == GEMV_DTYPE_F32) {
+    const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const unsigned short *>(p) + i));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == GEMV_DTYPE_F16) {
+        const float2 f = f16x2_to_f2(w[e]);
+        v[2 * e] = f.x;
+        v[2 * e + 1] = f.y;
+      } else {
+        v[2 * e] = bf16_lo(w[e]);
+        v[2 * e + 1] = bf16_hi(w[e]);
+      }
+    }
+  }
+}
+
+// Sixteen lanes hold a group's 128 values, eight each (consecutive ones where rows are
+// whole 16-byte pieces, kVec; else every sixteenth), so the group is read once and its
+// largest value found by four shuffles.  U groups of a team are loaded before the first
+// is used.
+constexpr int kF8QThreads = 256;
+template <int DT, bool kVec, int U>
+__global__ void __launch_bounds__(kF8QThreads)
+    k_f8_quantize(const void *x, uint8_t *q, float *scale, int64_t K, int G, int64_t groups) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kTeams = kF8QThreads / 16;
+  const int lane = threadIdx.x & 15;
+  const int64_t first = (int64_t)blockIdx.x * (kTeams * U) + threadIdx.x / 16;
+  float v[U][8];
+  int64_t base[U];
+  int n[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t t = first + u * kTeams;
+    n[u] = 0;
+    base[u] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+    if (t >= groups) continue;
+    const int64_t b = groups <= 0x7fffffff ? (int64_t)((uint32_t)t / (uint32_t)G) : t / G;
+    const int64_t k0 = (t - b * G) * kF8Group;
+    base[u] = b * K + k0;
+    n[u] = K - k0 < kF8Group ? (int)(K - k0) : kF8Group;
+    if constexpr (kVec) {
+      if (lane * 8 < n[u]) f8_load8<DT>(x, base[u] + lane * 8, v[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lane + 16 * e < n[u]) v[u][e] = f8_load1<DT>(x, base[u] + lane + 16 * e);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, f8_finite_abs(v[u][e]));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (n[u] == 0) continue;
+    const float s = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f), r = __frcp_rn(s);
+    if constexpr (kVec) {
+      uint32_t o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o[h] = f8_pack2(v[u][4 * h] * r, v[u][4 * h + 1] * r) | (f8_pack2(v[u][4 * h + 2] * r, v[u][4 * h + 3] * r) << 16);
+      if (lane * 8 < n[u]) *reinterpret_cast<uint2 *>(q + base[u] + lane * 8) = make_uint2(o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lane + 16 * e < n[u]) q[base[u] + lane + 16 * e] = (uint8_t)f8_pack2(v[u][e] * r, 0.f);
+    }
+    if (lane == 0) scale[first + u * kTeams] = s;
+  }
+}
+
+}  // namespace gemv

@@ -1,0 +1,802 @@
+// Kernels of the 8-bit cache of keys and values: the append of new tokens
+// (gemv_kv8_append) and the attention over it (gemv_kv8_attention).
+//
+// A block holds kKvBlock = 64 tokens of one head: the keys as 64 rows of D e4m3 values,
+// the values as D rows of 64 (token index innermost, so that the second product finds
+// consecutive tokens, its summation index, in consecutive bytes), and one scale for
+// each, a power of two.
+#pragma once
+
+#include "gemv_f8.cuh"
+
+namespace gemv {
+
+constexpr int kKvBlock = 64;
+constexpr int kKvStatusTable = 64;  // a block needed lies outside the pool, or past the table
+
+struct KvArgs {
+  uint8_t *k = nullptr, *v = nullptr;
+  float *k_scale = nullptr, *v_scale = nullptr;
+  const int32_t *table = nullptr, *lens = nullptr;
+  int64_t blocks = 0;
+  int heads = 0, width = 0;
+  int S = 0, T = 0;
+  int *status = nullptr;
+  // append
+  const void *new_k = nullptr, *new_v = nullptr;
+  int64_t k_stride = 0, v_stride = 0;
+  const int32_t *starts = nullptr;
+  int64_t N = 0;
+  int dtype = 0;
+  // attention
+  const void *q = nullptr;
+  void *out = nullptr;
+  float *lse = nullptr;
+  float *ws = nullptr;
+  int64_t q_stride = 0;
+  int64_t timeout_ns = 0;
+  int group = 0, window = 0, sinks = 0, row_tiles = 0, test_stall = 0;
+  float scale_log2 = 0.f;  // softmax scale x log2 e
+};
+
+// ------------------------------------------------------------------ values
+// Two e4m3 values (the low, the high half of a word) as fp16, exact.
+__device__ __forceinline__ uint32_t kv_half2_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t kv_half2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+// The smallest power of two s >= 2^-126 with m <= 448 s: 448 = 1.75 x 2^8, so s = 2^(e - 8)
+// for m = f x 2^e with f <= 1.75, and twice that above.
+__device__ __forceinline__ float kv_power(float m) {
+  const int bits = __float_as_int(m);
+  int e = ((bits >> 23) & 0xff) - 8 + ((bits & 0x7fffff) > 0x600000 ? 1 : 0);
+  return __int_as_float((e < 1 ? 1 : e) << 23);
+}
+// Four e4m3 values times a power of two, rounded to e4m3 again (exact but for
+// subnormal results).
+__device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float r) {
+  const float2 a = f16x2_to_f2(kv_half2_lo(w)), b = f16x2_to_f2(kv_half2_hi(w));
+  return f8_pack2(a.x * r, a.y * r) | (f8_pack2(b.x * r, b.y * r) << 16);
+}
+__device__ __forceinline__ float kv_load(const void *p, int64_t i, int dt) {
+  if (dt == GEMV_DTYPE_F32) return __ldg(reinterpret_cast<const float *>(p) + i);
+  const unsigned short h = __ldg(reinterpret_cast<const unsigned short *>(p) + i);
+  return dt == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half(h)) : __uint_as_float((uint32_t)h << 16);
+}
+
+// ------------------------------------------------------------------ append
+// One CTA for each block that new tokens reach, head, and keys (blockIdx.z = 0) or
+// values (1): it reads the block's new tokens once (eight values of a token per load),
+// finds their largest, and so the block's scale; where that grows it moves the tokens
+// the block held to the new scale; and it writes the new ones.  No other CTA touches
+// the block's head, so nothing is atomic.  Values pass through shared memory to lie
+// token-innermost.
+constexpr int kKvAppendThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
+  constexpr int kPieces = D / 8;                               // of a token
+  constexpr int kLoads = kKvBlock * kPieces / kKvAppendThreads;
+  constexpr int kPitch = kKvBlock + 4;
+  __shared__ float part[kKvAppendThreads / 32];
+  __shared__ __align__(16) uint8_t tile[D * kPitch];           // values: [channel][token]
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const bool values = blockIdx.z != 0;
+  // the sequence, and which of its blocks
+  int s;
+  int64_t first, n, nth;  // its first new token, how many, and the block's number among those they reach
+  if (a.starts == nullptr) {
+    const int per = (a.T + kKvBlock - 2) / kKvBlock + 1;
+    s = blockIdx.x / per;
+    nth = blockIdx.x - s * per;
+    first = (int64_t)s * a.T;
+    n = a.T;
+  } else {
+    // n tokens reach at most n / 64 + 2 blocks: sequence s has the CTAs from
+    // starts[s] / 64 + 2 s on
+    int lo = 0, hi = a.S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if ((int64_t)(__ldg(a.starts + mid) / kKvBlock) + 2 * (int64_t)mid <= (int64_t)blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    s = lo;
+    const int64_t b = __ldg(a.starts + s), e = __ldg(a.starts + s + 1);
+    first = b < 0 ? 0 : b > a.N ? a.N : b;
+    n = (e > a.N ? a.N : e) - first;
+    nth = (int64_t)blockIdx.x - (b / kKvBlock + 2 * (int64_t)s);
+  }
+  const int64_t len = __ldg(a.lens + s), before = len - n;
+  if (n <= 0 || nth < 0) return;
+  if (before < 0) {  // fewer tokens than the new ones: nothing says where they go
+    if (tid == 0 && nth == 0 && h == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+    return;
+  }
+  const int64_t blk = before / kKvBlock + nth;
+  const int64_t p0 = blk * kKvBlock;
+  if (p0 >= len) return;
+  const int32_t pb = blk < a.width ? __ldg(a.table + (int64_t)s * a.width + blk) : -1;
+  if (pb < 0 || pb >= a.blocks) {
+    if (tid == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+    return;
+  }
+  const int held = before > p0 ? (int)(before - p0) : 0;             // tokens the block has
+  const int end = len - p0 < kKvBlock ? (int)(len - p0) : kKvBlock;  // and will have
+  const int64_t t0 = first + (p0 + held - before);                   // the first of its new tokens
+  const void *src = values ? a.new_v : a.new_k;
+  const int64_t stride = values ? a.v_stride : a.k_stride;
+  uint8_t *dst = (values ? a.v : a.k) + ((int64_t)pb * a.heads + h) * (kKvBlock * D);
+  float *sc = (values ? a.v_scale : a.k_scale) + (int64_t)pb * a.heads + h;
+  const float old = held > 0 ? *sc : 0.f;
+
+  const int esz = a.dtype == GEMV_DTYPE_F32 ? 4 : 2;
+  const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && (stride * esz) % 16 == 0;
+  float x[kLoads][8];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
+    if (tok < end) {
+      const int64_t at = (t0 + e / kPieces) * stride + (int64_t)h * D + ch;
+      if (vec) {
+        if (a.dtype == GEMV_DTYPE_F32) f8_load8<GEMV_DTYPE_F32>(src, at, x[i]);
+        else if (a.dtype == GEMV_DTYPE_F16) f8_load8<GEMV_DTYPE_F16>(src, at, x[i]);
+        else f8_load8<GEMV_DTYPE_BF16>(src, at, x[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = kv_load(src, at + j, a.dtype);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, f8_finite_abs(x[i][j]));
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if ((tid & 31) == 0) part[tid >> 5] = m;
+  __syncthreads();  // every thread has read the old scale, too
+#pragma unroll
+  for (int w = 0; w < kKvAppendThreads / 32; ++w) m = fmaxf(m, part[w]);
+  const float scale = fmaxf(kv_power(m), old), r = 1.f / scale;  // powers of two: exact
+  if (tid == 0) *sc = scale;
+  const bool move = held > 0 && scale != old;
+  const float ratio = old * r;
+
+  if (!values) {
+    if (move)
+      for (int i = tid; i < held * (D / 16); i += kKvAppendThreads) {
+        uint4 w = reinterpret_cast<const uint4 *>(dst)[i];
+        w.x = kv_rescale4(w.x, ratio);
+        w.y = kv_rescale4(w.y, ratio);
+        w.z = kv_rescale4(w.z, ratio);
+        w.w = kv_rescale4(w.w, ratio);
+        reinterpret_cast<uint4 *>(dst)[i] = w;
+      }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
+      if (tok < end)
+        *reinterpret_cast<uint2 *>(dst + tok * D + ch) =
+            make_uint2(f8_pack2(x[i][0] * r, x[i][1] * r) | (f8_pack2(x[i][2] * r, x[i][3] * r) << 16),
+                       f8_pack2(x[i][4] * r, x[i][5] * r) | (f8_pack2(x[i][6] * r, x[i][7] * r) << 16));
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
+    if (tok < end) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tile[(ch + j) * kPitch + tok] = (uint8_t)f8_pack2(x[i][j] * r, 0.f);
+    }
+  }
+  __syncthreads();
+  // words of four tokens: new ones from the tile, held ones moved, others as they are
+  const int w_lo = move ? 0 : held / 4, w_n = (end + 3) / 4 - w_lo;
+  for (int i = tid; i < D * w_n; i += kKvAppendThreads) {
+    const int ch = i / w_n, tok = (w_lo + i % w_n) * 4;
+    uint32_t *at = reinterpret_cast<uint32_t *>(dst + ch * kKvBlock + tok);
+    const int lo = held - tok, hi = end - tok;  // bytes [lo, hi) are new
+    uint32_t w = *reinterpret_cast<const uint32_t *>(tile + ch * kPitch + tok);
+    if (lo > 0 || hi < 4) {
+      const uint32_t was = *at;
+      const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
+      const uint32_t above = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1);                       // bytes of no token
+      w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
+    }
+    *at = w;
+  }
+}
+
+// ------------------------------------------------------------------ attention: work
+// What the T queries of a sequence see of it, in blocks: the `sink` first ones, then
+// those from `from` on.
+struct KvSeen {
+  int len, sink, from, count;
+};
+__device__ __forceinline__ KvSeen kv_seen(const KvArgs &a, int s) {
+  KvSeen v;
+  v.len = __ldg(a.lens + s);
+  v.len = v.len < 0 ? 0 : v.len;
+  if ((int64_t)v.len > (int64_t)a.width * kKvBlock) v.len = a.width * kKvBlock;
+  const int64_t lo = a.window > 0 ? (int64_t)v.len - a.T - a.window + 1 : 0;
+  v.from = lo > 0 ? (int)(lo / kKvBlock) : 0;
+  const int need = a.window > 0 ? (a.sinks + kKvBlock - 1) / kKvBlock : 0;
+  v.sink = need < v.from ? need : v.from;
+  v.count = v.sink + (v.len + kKvBlock - 1) / kKvBlock - v.from;
+  return v;
+}
+
+// The blocks of all sequences, heads and row tiles, one after the other (a sequence's
+// heads and row tiles are its items), are cut into equal ranges, one for each CTA: a
+// batch of very different lengths and a single long sequence both keep every SM busy.
+// A CTA meets the end of an item, whole items, and the start of one.
+__device__ __forceinline__ int64_t kv_warp_sum(int64_t v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+// Blocks (of one item each) of the sequences [0, s).
+__device__ __forceinline__ int64_t kv_before(const KvArgs &a, int s, int lane) {
+  int64_t n = 0;
+  for (int i = lane; i < s; i += 32) n += kv_seen(a, i).count;
+  return kv_warp_sum(n);
+}
+// CTAs that get a share, and the first block of CTA w's
+__device__ __forceinline__ int64_t kv_shares(int64_t total, int64_t W) { return total < W ? total : W; }
+
+// Position in that list: an item and the range [lo, hi) of its blocks' numbers.
+struct KvItem {
+  int64_t lo, hi;
+  int s, item;
+  KvSeen seen;
+  __device__ void load(const KvArgs &a, int s_, int64_t lo_) {
+    s = s_;
+    item = 0;
+    lo = lo_;
+    seen = kv_seen(a, s);
+    hi = lo + seen.count;
+  }
+  // the item that holds block u >= lo (u below the total)
+  __device__ void seek(const KvArgs &a, int64_t u) {
+    const int items = a.heads * a.row_tiles;
+    while (u >= hi) {
+      if (item + 1 < items && seen.count > 0) {
+        ++item;
+        lo = hi;
+        hi = lo + seen.count;
+      } else {
+        load(a, s + 1, hi);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ attention
+__device__ __forceinline__ void kv_bulk(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc_smem_u32(bar))
+               : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16
+__device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t kv_transpose(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float kv_exp2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t kv_pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D>
+struct KvForm {
+  // warps x slots x slot bytes of copies in flight or in use: about 190 KB
+  static constexpr int kWarps = D <= 128 ? 8 : 4;
+  static constexpr int kSlots = D == 64 ? 5 : 3;
+  static constexpr int kSlot = kKvBlock * D;  // the keys or the values of a block
+  static constexpr int kDepth = (kSlots + 1) / 2;  // blocks begun at a time
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kPitch = D + 4;  // of a row of the merge buffer: free of bank conflicts
+  static constexpr int kSmem = 128 + kWarps * kSlots * kSlot + kWarps * 8 * kPitch * 4;
+};
+// floats of a partial result: rows x (D sums, then largest logit and sum of weights)
+template <int D, int NT>
+__host__ __device__ constexpr int64_t kv_part() { return (int64_t)NT * 8 * (D + 2); }
+
+// The weights leave exp2 times 2^14, so that fp16 holds those down to 2^-28 of the
+// largest in full; the factor cancels against the sum of weights, which has it too.
+constexpr float kKvLift = 14.f;
+
+// A CTA's range of blocks, block by block over its warps (warp w takes every kWarps-th).
+// A warp has a ring of slots in shared memory: lane 0 has the copy engine bring each
+// block's keys, then its values (one contiguous piece each), as soon as a slot is free,
+// and a slot's mbarrier says that it is there.  For a block of 64 tokens and NT tiles of
+// eight query rows (the rows of all queries of the item's head):
+//   logits^T (tokens x rows) = K Q^T, four m16n8k16 tiles of 16 tokens.  A lane's 16-byte
+//     piece of a key row is four instructions' worth of its columns: k is a summation
+//     index, so any order will do that Q's registers follow.
+//   weights in fp32 with the running maximum and sum of each row, rounded to fp16 (11
+//     bits, against the 4 of the values they meet), transposed in registers (movmatrix)
+//     to the operand of
+//   O^T (channels x rows) += V^T weights, the tokens again in the order of a lane's
+//     16-byte piece of a value row.  Which tokens a logit tile holds is chosen so that
+//     the transposed weights come out in that order.
+// The scales join outside: the keys' in the logits' factor, the values' when a block's
+// product is added to the running sums.
+// At the end of an item (or of the range) the warps' sums are merged in shared memory
+// and written: the output, or a partial result that k_kv8_join adds up.
+template <int D, int NT>
+__global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const KvArgs a) {
+  using F = KvForm<D>;
+  constexpr int W = F::kWarps, R = F::kSlots, Q = D / 64, DT = D / 16;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[W * R];
+  __shared__ float stat_m[W][8], stat_l[W][8];
+  __shared__ int abort_flag;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  unsigned char *smem = smem_raw + ((128u - (tc_smem_u32(smem_raw) & 127u)) & 127u);
+  unsigned char *ring = smem + (size_t)warp * R * F::kSlot;
+  float *merge = reinterpret_cast<float *>(smem + (size_t)W * R * F::kSlot);
+  uint64_t *bar = bars + warp * R;
+  if (lane == 0)
+    for (int i = 0; i < R; ++i) tc_mbar_init(&bar[i], 1);
+  if (tid == 0) abort_flag = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+
+  const int items = a.heads * a.row_tiles;
+  const int64_t total = kv_before(a, a.S, lane) * items;
+  const int64_t shares = kv_shares(total, gridDim.x);
+  if ((int64_t)blockIdx.x >= shares) return;
+  const int64_t u_lo = (int64_t)blockIdx.x * total / shares, u_hi = ((int64_t)blockIdx.x + 1) * total / shares;
+
+  // the sequence of block u_lo
+  KvItem at;
+  {
+    int64_t base = 0;
+    int s0 = 0;
+    for (;;) {  // 32 sequences at a time
+      const int s = s0 + lane;
+      int64_t n = s < a.S ? (int64_t)kv_seen(a, s).count * items : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + n > u_lo);
+      if (past != 0) {
+        const int f = __ffs(past) - 1;
+        const int64_t prev = __shfl_sync(0xffffffffu, n, f > 0 ? f - 1 : 0);
+        at.load(a, s0 + f, base + (f > 0 ? prev : 0));
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, n, 31);
+      s0 += 32;
+    }
+    at.seek(a, u_lo);
+  }
+
+  // ---- copies: this warp's blocks, keys and values in turn
+  KvItem is = at;          // the item of block `iu`
+  int64_t iu = u_lo + warp;
+  int issued = 0;          // halves begun
+  int islot = 0;
+  int32_t entry = 0;       // table entry of block iu, loaded ahead
+  int64_t ipb = 0;         // pool block whose keys were begun last
+  float q_ks[F::kDepth], q_vs[F::kDepth];  // scales of the blocks begun, oldest first
+  int q_n = 0;
+  auto look = [&]() {
+    if (iu < u_hi) {
+      is.seek(a, iu);
+      const int j = (int)(iu - is.lo);
+      entry = __ldg(a.table + (int64_t)is.s * a.width + (j < is.seen.sink ? j : is.seen.from + j - is.seen.sink));
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < F::kDepth; ++i) q_ks[i] = q_vs[i] = 0.f;
+  look();
+  auto issue = [&]() {
+    const uint8_t *src;
+    if ((issued & 1) == 0) {
+      if (iu >= u_hi) return;
+      const int h = is.item / a.row_tiles;
+      const bool good = entry >= 0 && entry < a.blocks;
+      ipb = (good ? (int64_t)entry : 0) * a.heads + h;
+      const float ks = __ldg(a.k_scale + ipb), vs = __ldg(a.v_scale + ipb);
+#pragma unroll
+      for (int i = 0; i < F::kDepth; ++i)
+        if (i == q_n) {
+          q_ks[i] = ks;
+          q_vs[i] = good ? vs : -1.f;  // scales are positive: a block to leave out
+        }
+      ++q_n;
+      if (!good && lane == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+      iu += W;
+      look();
+      src = a.k;
+    } else {
+      src = a.v;
+    }
+    // (test: the last copy of the first CTA's first warp never comes)
+    const bool withheld = a.test_stall && blockIdx.x == 0 && warp == 0 && (issued & 1) != 0 && iu >= u_hi;
+    if (lane == 0 && !withheld) {
+      tc_mbar_arrive_expect_tx(&bar[islot], F::kSlot);
+      kv_bulk(ring + (size_t)islot * F::kSlot, src + ipb * F::kSlot, F::kSlot, &bar[islot]);
+    }
+    ++issued;
+    islot = islot + 1 == R ? 0 : islot + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < R; ++i) issue();
+
+  int taken = 0, slot = 0;  // halves used
+  uint32_t phase = 0;
+  bool dead = false;
+  auto arrived = [&]() {
+    if (!dead) {
+      const bool ok = tc_mbar_wait_or_abort(&bar[slot], phase, a.timeout_ns, &abort_flag);
+      dead = !__all_sync(0xffffffffu, ok);
+    }
+  };
+  auto release = [&]() {
+    __syncwarp();  // every lane has read the slot
+    if (dead) return;
+    ++taken;
+    if (++slot == R) {
+      slot = 0;
+      phase ^= 1;
+    }
+    issue();
+  };
+
+  int64_t u = u_lo + warp;
+  bool first_item = true;
+  for (int64_t seg = u_lo; seg < u_hi;) {
+    at.seek(a, seg);
+    const int64_t seg_end = at.hi < u_hi ? at.hi : u_hi;
+    const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
+    const int rows = a.T * a.group - row0;  // of this tile, at most NT * 8
+    const int len = at.seen.len;
+
+    // Q's registers: row g of each tile, in the order of the key pieces.  Each row is
+    // scaled by a power of two so that its largest value lies in [2^14, 2^15): fp16
+    // then holds what is within 2^-28 of it as the input does.
+    uint32_t qf[NT][DT][2];
+    float qs[NT][2];  // factor of the logits of rows 2 c, 2 c + 1: softmax scale x log2 e / that power
+    if (u < seg_end) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = row0 + n * 8 + g;
+        const bool has = n * 8 + g < rows;
+        const int t = row / a.group;
+        const int64_t qa = ((int64_t)at.s * a.T + t) * a.q_stride + ((int64_t)h * a.group + row - t * a.group) * D;
+        float mx = 0.f;
+        float x[DT][4];
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[i][e] = has ? kv_load(a.q, qa + (i >> 2) * 64 + 16 * c + (i & 3) * 4 + e, a.dtype) : 0.f;
+            mx = fmaxf(mx, f8_finite_abs(x[i][e]));
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = (__float_as_int(mx) >> 23) & 0xff;  // exponent field, 127 for [1, 2)
+        e = e < 16 ? 16 : e;
+        const float up = __int_as_float((127 + 14 + 127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          qf[n][i][0] = kv_pack_half(x[i][0] * up, x[i][1] * up);
+          qf[n][i][1] = kv_pack_half(x[i][2] * up, x[i][3] * up);
+        }
+        const float f = a.scale_log2 / up;
+        qs[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+        qs[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      }
+    }
+
+    float o[NT][DT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+    }
+
+    for (; u < seg_end; u += W) {
+      const int j = (int)(u - at.lo);
+      const int64_t pos0 = (int64_t)(j < at.seen.sink ? j : at.seen.from + j - at.seen.sink) * kKvBlock;
+      const float ks = q_ks[0], vs_raw = q_vs[0];
+      const bool bad = vs_raw < 0.f;
+      const float vs = bad ? 0.f : vs_raw;
+      // does every query see every token of the block?
+      const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
+                        (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
+      // token at `tok` of the block, query t
+      auto sees = [&](int tok, int t) {
+        const int64_t p = pos0 + tok, i = (int64_t)len - a.T + t;
+        return !bad && p <= i && (a.window <= 0 || i - p < a.window || p < a.sinks);
+      };
+
+      // ---- logits: tile j holds tokens 16 (r / 2) + 4 j + r % 2 (rows r = 0..7 of the
+      // tile) and those + 2 (rows 8..15)
+      float s[NT][4][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
+      arrived();
+      {
+        const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kp + (4 * t) * D + 64 * q);
+            const uint4 y = *reinterpret_cast<const uint4 *>(kp + (4 * t + 2) * D + 64 * q);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t f[4] = {kv_half2_lo(xw[i]), kv_half2_lo(yw[i]), kv_half2_hi(xw[i]), kv_half2_hi(yw[i])};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) kv_mma(s[n][t], f, qf[n][q * 4 + i][0], qf[n][q * 4 + i][1]);
+            }
+          }
+      }
+      // (the queue's oldest scales are in registers now)
+#pragma unroll
+      for (int i = 0; i + 1 < F::kDepth; ++i) {
+        q_ks[i] = q_ks[i + 1];
+        q_vs[i] = q_vs[i + 1];
+      }
+      --q_n;
+      release();
+
+      // ---- weights
+      uint32_t p[NT][4][2];
+      float keep[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float f0 = qs[n][0] * ks, f1 = qs[n][1] * ks;
+        float m0 = m[n][0], m1 = m[n][1];
+        const int r0 = row0 + n * 8 + 2 * c, ta = r0 / a.group, tb = (r0 + 1) / a.group;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          s[n][t][0] *= f0;
+          s[n][t][1] *= f1;
+          s[n][t][2] *= f0;
+          s[n][t][3] *= f1;
+          if (edge) {
+            const int tok = 16 * (g >> 1) + (g & 1) + 4 * t;
+            if (!sees(tok, ta)) s[n][t][0] = -INFINITY;
+            if (!sees(tok, tb)) s[n][t][1] = -INFINITY;
+            if (!sees(tok + 2, ta)) s[n][t][2] = -INFINITY;
+            if (!sees(tok + 2, tb)) s[n][t][3] = -INFINITY;
+          }
+          m0 = fmaxf(m0, fmaxf(s[n][t][0], s[n][t][2]));
+          m1 = fmaxf(m1, fmaxf(s[n][t][1], s[n][t][3]));
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+        }
+        // a row that has seen nothing yet: any finite reference leaves its weights 0
+        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+        keep[n][0] = kv_exp2(m[n][0] - z0);
+        keep[n][1] = kv_exp2(m[n][1] - z1);
+        m[n][0] = m0;
+        m[n][1] = m1;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float w0 = kv_exp2(s[n][t][0] - z0 + kKvLift), w1 = kv_exp2(s[n][t][1] - z1 + kKvLift);
+          const float w2 = kv_exp2(s[n][t][2] - z0 + kKvLift), w3 = kv_exp2(s[n][t][3] - z1 + kKvLift);
+          l0 += w0 + w2;
+          l1 += w1 + w3;
+          p[n][t][0] = kv_transpose(kv_pack_half(w0, w1));
+          p[n][t][1] = kv_transpose(kv_pack_half(w2, w3));
+        }
+        // (this lane's tokens; the lanes' sums meet at the end)
+        l[n][0] = l[n][0] * keep[n][0] + l0;
+        l[n][1] = l[n][1] * keep[n][1] + l1;
+      }
+
+      // ---- sums
+      arrived();
+      const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 16 * kKvBlock);
+        const uint4 y = *reinterpret_cast<const uint4 *>(vp + (i * 16 + 8) * kKvBlock);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        uint32_t f[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          f[t][0] = kv_half2_lo(xw[t]);
+          f[t][1] = kv_half2_lo(yw[t]);
+          f[t][2] = kv_half2_hi(xw[t]);
+          f[t][3] = kv_half2_hi(yw[t]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          if (!edge) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
+          } else {
+            // values that a query does not see may be anything, NaN among it: for each
+            // query of the tile, the product with those it sees, kept for its rows
+            const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
+            for (int t = r_lo / a.group; t <= r_hi / a.group; ++t) {
+              float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int tok = 16 * c + 4 * k;
+                const uint32_t k01 = (sees(tok, t) ? 0xffffu : 0u) | (sees(tok + 1, t) ? 0xffff0000u : 0u);
+                const uint32_t k23 = (sees(tok + 2, t) ? 0xffffu : 0u) | (sees(tok + 3, t) ? 0xffff0000u : 0u);
+                const uint32_t fm[4] = {f[k][0] & k01, f[k][1] & k01, f[k][2] & k23, f[k][3] & k23};
+                kv_mma(e, fm, p[n][k][0], p[n][k][1]);
+              }
+              if ((r_lo + 2 * c) / a.group == t) d[0] = e[0], d[2] = e[2];
+              if ((r_lo + 2 * c + 1) / a.group == t) d[1] = e[1], d[3] = e[3];
+            }
+          }
+          o[n][i][0] = fmaf(vs, d[0], o[n][i][0] * keep[n][0]);
+          o[n][i][1] = fmaf(vs, d[1], o[n][i][1] * keep[n][1]);
+          o[n][i][2] = fmaf(vs, d[2], o[n][i][2] * keep[n][0]);
+          o[n][i][3] = fmaf(vs, d[3], o[n][i][3] * keep[n][1]);
+        }
+      }
+      release();
+    }
+
+    // ---- the warps' sums become one, eight rows at a time
+    const bool whole = seg == at.lo && seg_end == at.hi;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float l0 = l[n][0], l1 = l[n][1];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      if (g == 0) {
+        stat_m[warp][2 * c] = m[n][0];
+        stat_m[warp][2 * c + 1] = m[n][1];
+        stat_l[warp][2 * c] = l0;
+        stat_l[warp][2 * c + 1] = l1;
+      }
+      float *mine = merge + (size_t)warp * 8 * F::kPitch;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        mine[(2 * c) * F::kPitch + i * 16 + g] = o[n][i][0];
+        mine[(2 * c + 1) * F::kPitch + i * 16 + g] = o[n][i][1];
+        mine[(2 * c) * F::kPitch + i * 16 + g + 8] = o[n][i][2];
+        mine[(2 * c + 1) * F::kPitch + i * 16 + g + 8] = o[n][i][3];
+      }
+      __syncthreads();
+      if (abort_flag == 0) {
+        float *part = a.ws + ((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
+        for (int e = tid; e < 8 * D; e += F::kThreads) {
+          const int r = e / D, d = e - r * D;
+          if (n * 8 + r >= rows) break;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < W; ++w) mx = fmaxf(mx, stat_m[w][r]);
+          const float z = mx == -INFINITY ? 0.f : mx;
+          float sum = 0.f, den = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float f = kv_exp2(stat_m[w][r] - z);
+            sum = fmaf(f, merge[(w * 8 + r) * F::kPitch + d], sum);
+            den = fmaf(f, stat_l[w][r], den);
+          }
+          if (whole) {
+            const int row = row0 + n * 8 + r, t = row / a.group;
+            const int64_t at_row = ((int64_t)at.s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
+            const float val = den == 0.f ? 0.f : sum / den;
+            reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = f8_round16(val, a.dtype);
+            if (d == 0 && a.lse != nullptr)
+              a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
+          } else {
+            part[(n * 8 + r) * D + d] = sum;
+            if (d == 0) {
+              part[NT * 8 * D + n * 8 + r] = mx;
+              part[NT * 8 * (D + 1) + n * 8 + r] = den;
+            }
+          }
+        }
+      }
+      __syncthreads();  // read before the next rows overwrite it
+    }
+    seg = seg_end;
+    first_item = false;
+  }
+  if (abort_flag != 0) {
+    // no copy may be in flight when the CTA exits
+    if (lane == 0) {
+      if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
+      bool drained = true;
+      for (; taken < issued; ++taken) {
+        if (!tc_mbar_wait(&bar[slot], phase, a.timeout_ns)) drained = false;
+        if (++slot == R) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
+    }
+  }
+}
+
+// Items that several CTAs of k_kv8_attention share: their partial results, merged in the
+// order of the blocks; and the outputs of sequences without tokens: zeros.
+// grid (S, items), 256 threads; W: the attention kernel's CTAs.
+constexpr int kKvJoinThreads = 256;
+template <int D, int NT>
+__global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int W) {
+  pdl_trigger();
+  pdl_wait();
+  const int s = blockIdx.x, item = blockIdx.y, lane = threadIdx.x & 31;
+  const int items = a.heads * a.row_tiles;
+  const int64_t before = kv_before(a, s, lane);
+  const KvSeen seen = kv_seen(a, s);
+  const int64_t u0 = before * items + (int64_t)item * seen.count, u1 = u0 + seen.count;
+  int64_t w0 = 0, w1 = -1, total = 0, shares = 0;
+  if (seen.count > 0) {
+    total = kv_before(a, a.S, lane) * items;
+    shares = kv_shares(total, W);
+    w0 = f8_owner(u0, total, shares);
+    w1 = f8_owner(u1 - 1, total, shares);
+    if (w0 == w1) return;
+  }
+  const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
+  const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
+  for (int e = threadIdx.x; e < rows * D; e += kKvJoinThreads) {
+    const int r = e / D, d = e - r * D;
+    float mx = -INFINITY, sum = 0.f, den = 0.f;
+    for (int64_t w = w0; w <= w1; ++w) {
+      const int slot = w * total / shares >= u0 ? 0 : 1;  // the CTA's first item, or its last
+      const float *part = a.ws + (w * 2 + slot) * kv_part<D, NT>();
+      const float pm = part[NT * 8 * D + r], pl = part[NT * 8 * (D + 1) + r], po = part[r * D + d];
+      const float big = fmaxf(mx, pm), z = big == -INFINITY ? 0.f : big;
+      const float f = kv_exp2(mx - z), q = kv_exp2(pm - z);
+      sum = fmaf(q, po, f * sum);
+      den = fmaf(q, pl, f * den);
+      mx = big;
+    }
+    const int row = row0 + r, t = row / a.group;
+    const int64_t at_row = ((int64_t)s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
+    reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = f8_round16(den == 0.f ? 0.f : sum / den, a.dtype);
+    if (d == 0 && a.lse != nullptr)
+      a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
+  }
+}
+
+}  // namespace gemv

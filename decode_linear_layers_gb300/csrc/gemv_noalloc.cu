@@ -28,6 +28,7 @@
 #include <mutex>
 
 #include "../../include/gemv.h"
+#include "gemv_internal.h"
 #include "gemv_launch.cuh"
 #include "gemv_plan.h"
 

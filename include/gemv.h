@@ -214,6 +214,112 @@ gemv_status_t gemv_host(gemv_dtype_t dtype, const void *h_A, const float *h_scal
                         const void *h_bias, void *h_y, void *d_A, float *d_scale, void *d_x, void *d_bias,
                         void *d_y, int64_t M, int64_t K, int B, gemv_stream_t stream);
 
+/* ------------------------------------------------- 8-bit floating point layers */
+
+/* Columns (and weight rows) that share one scale of an 8-bit floating point matrix. */
+#define GEMV_F8_GROUP 128
+/* gemv_f8: K is a multiple of this, and A and x start on such a byte boundary. */
+#define GEMV_F8_ALIGN 16
+
+/* Vectors to e4m3 with a scale for each group of GEMV_F8_GROUP consecutive elements.
+ *     a = max |x[b][k]| over the group's finite elements
+ *     scale[b][g] = max(a / 448, 2^-126)
+ *     q[b][k] = x[b][k] * (1 / scale[b][g]), to the nearest e4m3 value (ties to even),
+ *               values beyond +-448, infinities too, to +-448; NaN stays NaN
+ * x is B x K of `dtype` (GEMV_DTYPE_F32, _F16, _BF16), q B x K bytes, scale
+ * B x ceil(K / GEMV_F8_GROUP) fp32; any K.  q and scale overlap neither x nor each
+ * other.  K == 0 or B == 0 does nothing. */
+gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, float *scale, int64_t K, int B,
+                               gemv_stream_t stream);
+
+/* Product of two e4m3 matrices with block scales, for one vector up to whole prompts:
+ *     y[b][m] = sum_g a_scale[m / 128][g] x_scale[b][g] sum_{k in group g} A[m][k] x[b][k]
+ *               + bias[m]
+ * with G = ceil(K / GEMV_F8_GROUP) groups of columns (the last may be shorter):
+ *   A        M x K e4m3, row-major, 16-byte aligned; a_scale ceil(M / 128) x G fp32
+ *   x        B x K e4m3, row-major, 16-byte aligned; x_scale B x G fp32 (as
+ *            gemv_f8_quantize writes them)
+ *   bias     M of y's type, may be NULL;  y  B x M of y_dtype (F32, F16 or BF16)
+ * Each group's products are summed by the tensor cores, the groups in fp32; y is
+ * rounded once.  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
+ * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any.  A scratch buffer of a few MB
+ * comes from the library's stream-ordered pool where tiles are shared between SMs.
+ * The kernel's waits are bounded (gemv_get_device_status). */
+gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
+                      void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream);
+
+/* ------------------------------------------- 8-bit cache of keys and values */
+
+/* Tokens of a block of the cache; each block has one scale per head, for its keys and
+ * for its values. */
+#define GEMV_KV8_BLOCK 64
+/* Newest tokens of a sequence that one gemv_kv8_attention call answers. */
+#define GEMV_KV8_MAX_TOKENS 64
+
+/* A pool of blocks, and which blocks each sequence has.  All pointers are caller-owned
+ * device memory.
+ *   k        blocks x heads x GEMV_KV8_BLOCK x dim e4m3
+ *   v        blocks x heads x dim x GEMV_KV8_BLOCK e4m3 (token index innermost)
+ *   k_scale, v_scale   blocks x heads fp32, powers of two: a cached key is k * k_scale
+ *   table    sequences x width: the pool's block for each GEMV_KV8_BLOCK tokens of a
+ *            sequence; entries that a call does not need are not read
+ *   dim      channels of a head: 64, 128, 192 or 256 (GEMV_ERR_UNSUPPORTED otherwise)
+ * k and v are 16-byte aligned. */
+typedef struct gemv_kv8_cache {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *table;
+  int64_t blocks;
+  int64_t width;
+  int heads;
+  int dim;
+} gemv_kv8_cache_t;
+
+/* Writes new tokens to the cache.  N tokens in all, those of sequence s the rows
+ * starts[s] .. starts[s + 1] - 1 of k and v (starts: S + 1 values, rising from 0 to N);
+ * with starts == NULL every sequence has N / S of them.  A row is heads x dim elements
+ * of `dtype` (F32, F16, BF16), rows k_stride and v_stride elements apart (so both may
+ * be columns of one projection's output).  lens[s] counts the tokens of sequence s with
+ * the new ones: they take its last positions.
+ * A block's scale is the smallest power of two s >= 2^-126 with |x| <= 448 s for all
+ * its finite elements (of one head; keys and values apart); values are x / s to the
+ * nearest e4m3 value, beyond +-448 (infinities) to +-448, NaN stays NaN.  A block that
+ * held tokens keeps its scale or raises it; the values that it held are then moved to
+ * the new one, which is exact for powers of two but where e4m3 becomes subnormal.  A
+ * block whose first token is new takes nothing from what it held before.
+ * No two sequences may be given the same block to write to.  A sequence with fewer
+ * tokens than new ones, or whose table has no block of the pool for a position, is left
+ * out for that position, and gemv_get_device_status then returns
+ * GEMV_ERR_INVALID_VALUE with bit 64. */
+gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, const int32_t *lens, const int32_t *starts, int S,
+                              int64_t N, gemv_stream_t stream);
+
+/* Attention of the newest T tokens (T <= GEMV_KV8_MAX_TOKENS: one in plain decoding, a
+ * few drafted ones checked at once) of S sequences over the cache, which holds them
+ * already:
+ *     out[s][t][h] = sum_j w_j v_j,  w = softmax_j(scale q[s][t][h] . k_j),
+ * over the positions j that query t, at position i = lens[s] - T + t, sees: j <= i and,
+ * with window > 0, i - j < window or j < sinks (a sliding window, and first tokens that
+ * stay visible).  Query head h reads the cache's head h / (q_heads / cache->heads).
+ * A query that sees nothing gets zeros.  What a query does not see, NaN included, has
+ * no influence on it; blocks that no query of the call sees are not read, nor are their
+ * table entries.
+ *   q        S x T rows of q_heads x dim elements of `dtype` (F16 or BF16), q_stride
+ *            elements apart
+ *   out      S x T x q_heads x dim of `dtype`, contiguous
+ *   lse      S x T x q_heads fp32: log of the sum of exp(scale q . k_j), -infinity where
+ *            nothing is seen; may be NULL
+ * Sums, maxima and logits are fp32; the products' operands are fp16: q scaled by a
+ * power of two per row, the 8-bit values exactly, and the softmax weights, rounded to
+ * 11 bits.  The result does not depend on the run: partial results are merged in a
+ * fixed order.  lens beyond the table count as the table's size.  A table entry outside
+ * the pool counts as a block that no query sees, and gemv_get_device_status then
+ * returns GEMV_ERR_INVALID_VALUE with bit 64.  The kernel's waits are bounded. */
+gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
+                                 const int32_t *lens, void *out, float *lse, int S, int T, int q_heads, float scale,
+                                 int64_t window, int64_t sinks, gemv_stream_t stream);
+
 /* Launch overlap for the calling thread's later calls (initially GEMV_OVERLAP_LAUNCH).
  * Programmatic dependent launch: a GEMV's kernels may be scheduled while the kernel
  * before them on the stream is finishing, so that back-to-back GEMVs (a decode layer,
@@ -335,20 +441,23 @@ gemv_status_t gemv_test_force_kernel(int kernel, int param);
 /* TEST ONLY — the plan of this thread's last successful launch. */
 gemv_status_t gemv_test_last_plan(gemv_plan_t *plan);
 
-/* Device-side status of the kernels with bounded waits (GEMV_KERNEL_TC).
+/* Device-side status of the kernels with bounded waits (GEMV_KERNEL_TC, gemv_f8,
+ * gemv_kv8_attention) and of the 8-bit cache's own checks.
  * Synchronises `stream`, then returns GEMV_ERR_DEVICE_TIMEOUT if a wait of a kernel
  * launched on the current device since the previous call ran out (the kernel then
  * left its outputs unwritten, freed its tensor memory and returned with nothing in
- * flight), else GEMV_SUCCESS; the status word is cleared.  `bits` (may be NULL)
- * receives which wait ran out: 16 an MMA completion, 32 the final wait for work in
- * flight.  GEMV_ERR_CUDA if the synchronisation or the read fails. */
+ * flight), else GEMV_ERR_INVALID_VALUE if a kernel of the 8-bit cache met a block that
+ * its pool or table does not have, else GEMV_SUCCESS; the status word is cleared.
+ * `bits` (may be NULL) receives which: 16 a copy's or an MMA's completion, 32 the final
+ * wait for work in flight, 64 a block of the cache.  GEMV_ERR_CUDA if the synchronisation or the read fails. */
 gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits);
 
-/* TEST ONLY — not thread-safe.  With `stall` != 0 every later GEMV_KERNEL_TC launch
- * skips the last MMA of its first CTA (in the persistent form: the MMAs of that CTA's
- * last k-tile), so that CTA's wait for it runs out after
- * `timeout_ns` (<= 0: the default of 2 s) and gemv_get_device_status reports
- * GEMV_ERR_DEVICE_TIMEOUT.  stall = 0 restores normal launches. */
+/* TEST ONLY — not thread-safe.  With `stall` != 0 every later GEMV_KERNEL_TC or gemv_f8
+ * launch skips the last MMA of its first CTA (in the persistent form: the MMAs of that
+ * CTA's last k-tile), and every gemv_kv8_attention launch the last copy of its first
+ * CTA's first warp, so that the wait for it runs out after `timeout_ns` (<= 0: the
+ * default of 2 s) and gemv_get_device_status reports GEMV_ERR_DEVICE_TIMEOUT.
+ * stall = 0 restores normal launches. */
 gemv_status_t gemv_test_stall(int stall, int64_t timeout_ns);
 
 #ifdef __cplusplus
