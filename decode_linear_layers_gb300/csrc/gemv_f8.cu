@@ -41,6 +41,7 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   const int64_t blocks = a.tiles * a.groups;
   const int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
   a.shared = a.tiles % W;
+  a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
   if (!f8_map(&map_a, A, a.M, K, kPrompt ? N : kF8Rows) || !f8_map(&map_x, x, a.B, K, kPrompt ? kF8Rows : N))
     return fail((int)cudaErrorInvalidValue);
@@ -59,7 +60,7 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   int n = 1;
   if (e == cudaSuccess && a.shared > 0) {
     e = launch_k(k_f8_join<N, kPrompt>, dim3((unsigned)a.shared, (unsigned)(F::kPartial / kF8JoinPiece)),
-                 dim3(kF8JoinThreads), 0, s, pdl, a, (int)W);
+                 dim3(kF8JoinThreads), 0, s, pdl, a);
     n = 2;
   }
   if (ws != nullptr) {
@@ -77,15 +78,15 @@ bool aligned(const void *p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes
 template <int DT>
 cudaError_t quantize(const void *x, uint8_t *q, float *scale, int64_t K, int64_t G, int64_t groups, int sms, cudaStream_t s) {
   const bool vec = K % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-  constexpr int kTeams = kF8QThreads / 16;
-  // several groups of a team in flight once every SM's threads have one
-  const bool many = groups > (int64_t)sms * (2048 / 16) * 2;
+  constexpr int kTeams = kF8QThreads / kF8QTeam;
+  // two groups of a team in flight once every SM's threads have one
+  const bool many = groups > (int64_t)sms * (2048 / kF8QTeam) * 2;
   auto go = [&](auto kern, int u) {
     const int64_t grid = (groups + kTeams * u - 1) / (kTeams * u);
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     return launch_k(kern, dim3((unsigned)grid), dim3(kF8QThreads), 0, s, launch_overlap(), x, q, scale, K, (int)G, groups);
   };
-  if (vec) return many ? go(k_f8_quantize<DT, true, 4>, 4) : go(k_f8_quantize<DT, true, 1>, 1);
+  if (vec) return many ? go(k_f8_quantize<DT, true, 2>, 2) : go(k_f8_quantize<DT, true, 1>, 1);
   return many ? go(k_f8_quantize<DT, false, 2>, 2) : go(k_f8_quantize<DT, false, 1>, 1);
 }
 

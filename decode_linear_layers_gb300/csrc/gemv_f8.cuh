@@ -32,6 +32,7 @@ struct F8Args {
   int64_t tiles = 0;     // row tiles x column tiles
   int64_t shared = 0;    // tiles 0 .. shared - 1 are split over all CTAs, the rest go whole
   int B = 0, groups = 0; // groups = k-blocks
+  int sharers = 0;       // CTAs that the shared tiles are split over
   int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
   int y_dtype = 0, stages = 0, test_stall = 0;
 };
@@ -54,10 +55,10 @@ __device__ __forceinline__ void f8_store(const F8Args &a, int64_t i, float v) {
 
 // ------------------------------------------------------------------ work of a CTA
 // The k-blocks of the `shared` first tiles, R = shared x groups of them, are cut into
-// gridDim.x equal ranges (range w: [w R / W, (w + 1) R / W)), so that a few tiles keep
-// every SM busy; at most one range more than a tile's worth, so it meets two tiles at
-// most.  The other tiles, a multiple of W, go round whole.  Each role of a CTA walks
-// the same segments.
+// W = `sharers` equal ranges (range w: [w R / W, (w + 1) R / W)), one for each CTA, or for
+// each of the first R: so a few tiles keep every SM busy.  A range is no longer than a
+// tile's k-blocks, so it meets two tiles at most.  The other tiles, a multiple of the
+// CTAs, go round whole.  Each role of a CTA walks the same segments.
 struct F8Seg {
   int64_t tile;
   int k0, k1;
@@ -67,13 +68,13 @@ struct F8Walk {
   int64_t lo, hi, next_tile, tiles;
   int groups, step, part;
   __device__ F8Walk(const F8Args &a) {
-    const int64_t R = a.shared * a.groups, w = blockIdx.x, W = gridDim.x;
-    lo = w * R / W;
-    hi = (w + 1) * R / W;
+    const int64_t R = a.shared * a.groups, w = blockIdx.x;
+    lo = w < a.sharers ? w * R / a.sharers : 0;
+    hi = w < a.sharers ? (w + 1) * R / a.sharers : 0;
     next_tile = a.shared + w;
     tiles = a.tiles;
     groups = a.groups;
-    step = (int)W;
+    step = (int)gridDim.x;
     part = 0;
   }
   __device__ bool next(F8Seg &s) {
@@ -165,6 +166,14 @@ __device__ __forceinline__ void f8_ld_wait(uint32_t (&r)[C]) {
                  : "memory");
     asm volatile("" : "+r"(r[30]), "+r"(r[31]));
   }
+}
+
+// (s0, s1) += (f0, f1) * (v0, v1), one packed instruction.
+__device__ __forceinline__ void f8_fma2(float &s0, float &s1, float f0, float f1, uint32_t v0, uint32_t v1) {
+  asm("{\n\t.reg .b64 s, f, v;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "fma.rn.f32x2 s, v, f, s;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(f0), "f"(f1), "r"(v0), "r"(v1));
 }
 
 // ------------------------------------------------------------------ the product
@@ -368,30 +377,31 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * N + col0);
-        uint32_t r[2][CH];
-        f8_ld<CH>(at, r[0]);
+        // two pieces of CH columns on their way at a time
+        constexpr int P = COLS / CH, U = P < 2 ? 1 : 2;
+        uint32_t r[U][CH];
 #pragma unroll
-        for (int h = 0; h < COLS / CH; ++h) {
-          f8_ld_wait<CH>(r[h & 1]);
-          if (h + 1 < COLS / CH) {
-            f8_ld<CH>(at + (h + 1) * CH, r[(h + 1) & 1]);
-          } else {
+        for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
+#pragma unroll
+        for (int h0 = 0; h0 < P; h0 += U) {
+#pragma unroll
+          for (int h = 0; h < U; ++h) f8_ld_wait<CH>(r[h]);
+          if (h0 + U >= P) {
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc_mbar_arrive(&acce[c]);
           }
-          if constexpr (kPrompt) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) acc[h * CH + j] = fmaf(f, __uint_as_float(r[h & 1][j]), acc[h * CH + j]);
-          } else {
+          for (int h = 0; h < U; ++h) {
+            float *s = acc + (h0 + h) * CH;
 #pragma unroll
             for (int j = 0; j < CH; j += 4) {
-              const float4 q = *reinterpret_cast<const float4 *>(fs + h * CH + j);
-              acc[h * CH + j] = fmaf(q.x, __uint_as_float(r[h & 1][j]), acc[h * CH + j]);
-              acc[h * CH + j + 1] = fmaf(q.y, __uint_as_float(r[h & 1][j + 1]), acc[h * CH + j + 1]);
-              acc[h * CH + j + 2] = fmaf(q.z, __uint_as_float(r[h & 1][j + 2]), acc[h * CH + j + 2]);
-              acc[h * CH + j + 3] = fmaf(q.w, __uint_as_float(r[h & 1][j + 3]), acc[h * CH + j + 3]);
+              float4 q = make_float4(f, f, f, f);
+              if constexpr (!kPrompt) q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
+              f8_fma2(s[j], s[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
+              f8_fma2(s[j + 2], s[j + 3], q.z, q.w, r[h][j + 2], r[h][j + 3]);
             }
+            if (h0 + U + h < P) f8_ld<CH>(at + (h0 + U + h) * CH, r[h]);
           }
         }
         if (++c == NACC) {
@@ -410,7 +420,8 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
             *reinterpret_cast<float4 *>(p + row * N + col0 + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < COLS; ++j) p[j * kF8Rows + row] = acc[j];
+          for (int j = 0; j < COLS; ++j)
+            if (j < a.B) p[j * kF8Rows + row] = acc[j];
         }
         continue;
       }
@@ -509,43 +520,38 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
 }
 
 // Tiles whose k-blocks several CTAs of k_f8 share: their partial sums, added in the
-// order of the k-blocks, and the epilogue.  grid (shared tiles, pieces of 2048 values),
-// 256 threads; W: k_f8's CTAs.
-constexpr int kF8JoinThreads = 256, kF8JoinPiece = 2048;
+// order of the k-blocks, and the epilogue.  grid (shared tiles, pieces of 1024 values),
+// a thread for four consecutive outputs.
+constexpr int kF8JoinThreads = 256, kF8JoinPiece = 4 * kF8JoinThreads;
 template <int N, bool kPrompt>
-__global__ void __launch_bounds__(kF8JoinThreads) k_f8_join(const F8Args a, int W) {
+__global__ void __launch_bounds__(kF8JoinThreads) k_f8_join(const F8Args a) {
   pdl_trigger();
-  pdl_wait();
   const int64_t R = a.shared * a.groups, u0 = (int64_t)blockIdx.x * a.groups;
-  const int64_t w0 = f8_owner(u0, R, W), w1 = f8_owner(u0 + a.groups - 1, R, W);
+  const int64_t w0 = f8_owner(u0, R, a.sharers), w1 = f8_owner(u0 + a.groups - 1, R, a.sharers);
+  pdl_wait();            // by every CTA: the next kernel counts on it
   if (w0 == w1) return;  // one CTA had the whole tile and wrote it
   int im, in;
   f8_tile(a, blockIdx.x, im, in);
-  constexpr int V = kPrompt ? 4 : 1;
-  for (int i = threadIdx.x * V; i < kF8JoinPiece; i += kF8JoinThreads * V) {
-    const int e = blockIdx.y * kF8JoinPiece + i;
-    const int row = kPrompt ? e / N : e % kF8Rows, col = kPrompt ? e % N : e / kF8Rows;
-    const int64_t b = kPrompt ? (int64_t)in * kF8Rows + row : col;
-    const int64_t m = kPrompt ? (int64_t)im * N + col : (int64_t)im * kF8Rows + row;
-    if (b >= a.B || m >= a.M) continue;
-    float s[V] = {};
-    for (int64_t w = w0; w <= w1; ++w) {
-      const int64_t lo = w * R / W;
-      if (lo == (w + 1) * R / W) continue;  // (fewer k-blocks than CTAs: some have none)
-      // its first range of k-blocks, unless that lies in the tile before
-      const int slot = lo / a.groups == blockIdx.x ? 0 : 1;
-      const float *p = a.ws + (w * 2 + slot) * (int64_t)kF8Rows * N + e;
-      if constexpr (V == 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(p);
-        s[0] += q.x; s[1] += q.y; s[2] += q.z; s[3] += q.w;
-      } else {
-        s[0] += *p;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (m + j < a.M) f8_store(a, b * a.M + m + j, s[j] + (a.bias != nullptr ? f8_bias(a, m + j) : 0.f));
+  const int e = (blockIdx.y * kF8JoinThreads + threadIdx.x) * 4;
+  const int row = kPrompt ? e / N : e % kF8Rows, col = kPrompt ? e % N : e / kF8Rows;
+  const int64_t b = kPrompt ? (int64_t)in * kF8Rows + row : col;
+  const int64_t m = kPrompt ? (int64_t)im * N + col : (int64_t)im * kF8Rows + row;
+  if (b >= a.B || m >= a.M) return;
+  constexpr int64_t kStep = 2 * (int64_t)kF8Rows * N;
+  // the first CTA's range may have begun in the tile before: then this is its second part
+  const float *p = a.ws + w0 * kStep + (w0 * R / a.sharers < u0 ? kStep / 2 : 0) + e;
+  const float *const q = a.ws + w0 * kStep + e;
+  const int n = (int)(w1 - w0);
+  float4 s = *reinterpret_cast<const float4 *>(p);
+#pragma unroll 8
+  for (int i = 1; i <= n; ++i) {
+    const float4 v = *reinterpret_cast<const float4 *>(q + i * kStep);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (m + j < a.M) f8_store(a, b * a.M + m + j, v[j] + (a.bias != nullptr ? f8_bias(a, m + j) : 0.f));
 }
 
 // No columns: the empty sum.
@@ -601,61 +607,133 @@ __device__ __forceinline__ void f8_load8(const void *p, int64_t i, float (&v)[8]
   }
 }
 
-// Sixteen lanes hold a group's 128 values, eight each (consecutive ones where rows are
-// whole 16-byte pieces, kVec; else every sixteenth), so the group is read once and its
-// largest value found by four shuffles.  U groups of a team are loaded before the first
-// is used.
-constexpr int kF8QThreads = 256;
+// Eight lanes hold a group's 128 values, sixteen each (in two pieces of eight consecutive
+// ones where rows are whole 16-byte pieces, kVec; else every eighth), so the group is read
+// once and its largest value found by three shuffles.  The largest absolute value is taken
+// first over all values, infinities among them, on two 16-bit values per instruction;
+// only where it is infinite are the finite ones looked at one by one.
+constexpr int kF8QThreads = 256, kF8QTeam = 8;
+template <int DT>
+struct F8Raw {  // eight values as loaded
+  static constexpr int kWords = DT == GEMV_DTYPE_F32 ? 8 : 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) + i * (DT == GEMV_DTYPE_F32 ? 4 : 2));
+#pragma unroll
+    for (int h = 0; h < kWords / 4; ++h) {
+      const uint4 v = __ldg(q + h);
+      w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void set(int e, const void *p, int64_t i) {  // value e from element i
+    if constexpr (DT == GEMV_DTYPE_F32)
+      w[e] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+    else
+      w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p) + i) << (16 * (e & 1));
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (DT == GEMV_DTYPE_F32) return __uint_as_float(w[e]);
+    if constexpr (DT == GEMV_DTYPE_F16) {
+      const float2 f = f16x2_to_f2(w[e / 2]);
+      return (e & 1) ? f.y : f.x;
+    }
+    return (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+  }
+  // largest absolute value, NaN passed over
+  __device__ __forceinline__ float top() const {
+    if constexpr (DT == GEMV_DTYPE_F32) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(__uint_as_float(w[i])));
+      return m;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = w[i] & 0x7fff7fffu;
+        if constexpr (DT == GEMV_DTYPE_F16)
+          asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
+        else
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v));
+      }
+      if constexpr (DT == GEMV_DTYPE_F16) {
+        const float2 f = f16x2_to_f2(m);
+        return fmaxf(f.x, f.y);
+      }
+      return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
+  }
+};
 template <int DT, bool kVec, int U>
 __global__ void __launch_bounds__(kF8QThreads)
     k_f8_quantize(const void *x, uint8_t *q, float *scale, int64_t K, int G, int64_t groups) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kTeams = kF8QThreads / 16;
-  const int lane = threadIdx.x & 15;
-  const int64_t first = (int64_t)blockIdx.x * (kTeams * U) + threadIdx.x / 16;
-  float v[U][8];
+  constexpr int kTeams = kF8QThreads / kF8QTeam;
+  const int lane = threadIdx.x & (kF8QTeam - 1);
+  const int64_t first = (int64_t)blockIdx.x * (kTeams * U) + threadIdx.x / kF8QTeam;
+  F8Raw<DT> v[U][2];
   int64_t base[U];
   int n[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t t = first + u * kTeams;
     n[u] = 0;
-    base[u] = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+    v[u][0].zero();
+    v[u][1].zero();
     if (t >= groups) continue;
-    const int64_t b = groups <= 0x7fffffff ? (int64_t)((uint32_t)t / (uint32_t)G) : t / G;
-    const int64_t k0 = (t - b * G) * kF8Group;
-    base[u] = b * K + k0;
-    n[u] = K - k0 < kF8Group ? (int)(K - k0) : kF8Group;
-    if constexpr (kVec) {
-      if (lane * 8 < n[u]) f8_load8<DT>(x, base[u] + lane * 8, v[u]);
-    } else {
+    base[u] = t * kF8Group;
+    n[u] = kF8Group;
+    if (K % kF8Group != 0) {  // rows end inside a group
+      const int64_t b = groups <= 0x7fffffff ? (int64_t)((uint32_t)t / (uint32_t)G) : t / G;
+      const int64_t k0 = (t - b * G) * kF8Group;
+      base[u] = b * K + k0;
+      n[u] = K - k0 < kF8Group ? (int)(K - k0) : kF8Group;
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (lane + 16 * e < n[u]) v[u][e] = f8_load1<DT>(x, base[u] + lane + 16 * e);
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (kVec) {
+        if (h * 64 + lane * 8 < n[u]) v[u][h].load(x, base[u] + h * 64 + lane * 8);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (h * 64 + e * 8 + lane < n[u]) v[u][h].set(e, x, base[u] + h * 64 + e * 8 + lane);
+      }
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float m = 0.f;
+    float m = fmaxf(v[u][0].top(), v[u][1].top());
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, f8_finite_abs(v[u][e]));
+    for (int d = kF8QTeam / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (__any_sync(0xffffffffu, m == __int_as_float(0x7f800000))) {  // an infinity: the finite values' largest
+      float f = 0.f;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int e = 0; e < 8; ++e) f = fmaxf(f, fmaxf(f8_finite_abs(v[u][0].get(e)), f8_finite_abs(v[u][1].get(e))));
+#pragma unroll
+      for (int d = kF8QTeam / 2; d > 0; d >>= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, d));
+      m = f;
+    }
     if (n[u] == 0) continue;
     const float s = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f), r = __frcp_rn(s);
-    if constexpr (kVec) {
-      uint32_t o[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        o[h] = f8_pack2(v[u][4 * h] * r, v[u][4 * h + 1] * r) | (f8_pack2(v[u][4 * h + 2] * r, v[u][4 * h + 3] * r) << 16);
-      if (lane * 8 < n[u]) *reinterpret_cast<uint2 *>(q + base[u] + lane * 8) = make_uint2(o[0], o[1]);
-    } else {
+    for (int h = 0; h < 2; ++h) {
+      const F8Raw<DT> &w = v[u][h];
+      if constexpr (kVec) {
+        uint32_t o[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (lane + 16 * e < n[u]) q[base[u] + lane + 16 * e] = (uint8_t)f8_pack2(v[u][e] * r, 0.f);
+        for (int i = 0; i < 2; ++i)
+          o[i] = f8_pack2(w.get(4 * i) * r, w.get(4 * i + 1) * r) | (f8_pack2(w.get(4 * i + 2) * r, w.get(4 * i + 3) * r) << 16);
+        if (h * 64 + lane * 8 < n[u]) *reinterpret_cast<uint2 *>(q + base[u] + h * 64 + lane * 8) = make_uint2(o[0], o[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (h * 64 + e * 8 + lane < n[u]) q[base[u] + h * 64 + e * 8 + lane] = (uint8_t)f8_pack2(w.get(e) * r, 0.f);
+      }
     }
     if (lane == 0) scale[first + u * kTeams] = s;
   }

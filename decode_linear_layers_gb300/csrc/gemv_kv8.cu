@@ -70,7 +70,8 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   e = allow_smem(k_kv8_attention<D, NT>, F::kSmem);
   if (e == cudaSuccess) e = launch_k(k_kv8_attention<D, NT>, dim3((unsigned)W), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
   if (e == cudaSuccess)
-    e = launch_k(k_kv8_join<D, NT>, dim3((unsigned)a.S, (unsigned)(a.heads * a.row_tiles)), dim3(kKvJoinThreads), 0, s, pdl, a, W);
+    e = launch_k(k_kv8_join<D, NT>, dim3((unsigned)a.S, (unsigned)(a.heads * a.row_tiles), (unsigned)(NT * 8 * D / (4 * kKvJoinThreads))),
+                 dim3(kKvJoinThreads), 0, s, pdl, a, W);
   const cudaError_t e2 = cudaFreeAsync(ws, s);
   if (e == cudaSuccess) e = e2;
   if (e != cudaSuccess) return fail((int)e);

@@ -80,11 +80,13 @@ __device__ __forceinline__ float kv_load(const void *p, int64_t i, int dt) {
 constexpr int kKvAppendThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
-  constexpr int kPieces = D / 8;                               // of a token
-  constexpr int kLoads = kKvBlock * kPieces / kKvAppendThreads;
-  constexpr int kPitch = kKvBlock + 4;
+  constexpr int kPieces = D / 8;                          // of a token
+  constexpr int kLoads = (kKvBlock * kPieces / kKvAppendThreads + 3) / 4 * 4;
+  constexpr int kStride = kKvBlock / kLoads;              // threads along the tokens
+  constexpr int kActive = kStride * kPieces;              // threads with channels
+  static_assert(kActive <= kKvAppendThreads && kKvBlock % kLoads == 0);
   __shared__ float part[kKvAppendThreads / 32];
-  __shared__ __align__(16) uint8_t tile[D * kPitch];           // values: [channel][token]
+  __shared__ uint32_t tile[D * (kKvBlock / 4)];           // values: words of four tokens
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, h = blockIdx.y;
@@ -135,15 +137,24 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   float *sc = (values ? a.v_scale : a.k_scale) + (int64_t)pb * a.heads + h;
   const float old = held > 0 ? *sc : 0.f;
 
+  // this thread's eight channels of kLoads tokens: of every kStride-th token, or (values)
+  // of four neighbouring ones, which share the words of the block's rows
   const int esz = a.dtype == GEMV_DTYPE_F32 ? 4 : 2;
   const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && (stride * esz) % 16 == 0;
+  const int ch = (tid % kPieces) * 8;
+  auto token = [&](int i) {
+    const int j = tid / kPieces;
+    return values ? j * 4 + (i & 3) + (i >> 2) * 4 * kStride : j + i * kStride;
+  };
   float x[kLoads][8];
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
-    if (tok < end) {
-      const int64_t at = (t0 + e / kPieces) * stride + (int64_t)h * D + ch;
+    const int tok = token(i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    if (tid < kActive && tok >= held && tok < end) {
+      const int64_t at = (t0 + tok - held) * stride + (int64_t)h * D + ch;
       if (vec) {
         if (a.dtype == GEMV_DTYPE_F32) f8_load8<GEMV_DTYPE_F32>(src, at, x[i]);
         else if (a.dtype == GEMV_DTYPE_F16) f8_load8<GEMV_DTYPE_F16>(src, at, x[i]);
@@ -152,10 +163,12 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[i][j] = kv_load(src, at + j, a.dtype);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, f8_finite_abs(x[i][j]));
     }
   }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, f8_finite_abs(x[i][j]));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if ((tid & 31) == 0) part[tid >> 5] = m;
@@ -179,30 +192,34 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
       }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
-      if (tok < end)
+      const int tok = token(i);
+      if (tid < kActive && tok >= held && tok < end)
         *reinterpret_cast<uint2 *>(dst + tok * D + ch) =
             make_uint2(f8_pack2(x[i][0] * r, x[i][1] * r) | (f8_pack2(x[i][2] * r, x[i][3] * r) << 16),
                        f8_pack2(x[i][4] * r, x[i][5] * r) | (f8_pack2(x[i][6] * r, x[i][7] * r) << 16));
     }
     return;
   }
+  // word `w` (four tokens) of channel c lies at tile[c][w ^ (c / 8 mod 16)]: the lanes of a
+  // warp, which write eight channels apart, meet different banks
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int e = i * kKvAppendThreads + tid, tok = held + e / kPieces, ch = (e % kPieces) * 8;
-    if (tok < end) {
+  for (int i = 0; i < kLoads; i += 4) {
+    const int w = token(i) / 4;
+    if (tid < kActive) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) tile[(ch + j) * kPitch + tok] = (uint8_t)f8_pack2(x[i][j] * r, 0.f);
+      for (int j = 0; j < 8; ++j)
+        tile[(ch + j) * (kKvBlock / 4) + (w ^ ((ch >> 3) & 15))] =
+            f8_pack2(x[i][j] * r, x[i + 1][j] * r) | (f8_pack2(x[i + 2][j] * r, x[i + 3][j] * r) << 16);
     }
   }
   __syncthreads();
-  // words of four tokens: new ones from the tile, held ones moved, others as they are
+  // the words with new tokens, and with held ones to move; bytes of no token stay
   const int w_lo = move ? 0 : held / 4, w_n = (end + 3) / 4 - w_lo;
   for (int i = tid; i < D * w_n; i += kKvAppendThreads) {
-    const int ch = i / w_n, tok = (w_lo + i % w_n) * 4;
-    uint32_t *at = reinterpret_cast<uint32_t *>(dst + ch * kKvBlock + tok);
+    const int c = w_n == kKvBlock / 4 ? i / (kKvBlock / 4) : i / w_n, at_w = w_lo + i - c * w_n, tok = at_w * 4;
+    uint32_t *at = reinterpret_cast<uint32_t *>(dst) + c * (kKvBlock / 4) + at_w;
     const int lo = held - tok, hi = end - tok;  // bytes [lo, hi) are new
-    uint32_t w = *reinterpret_cast<const uint32_t *>(tile + ch * kPitch + tok);
+    uint32_t w = tile[c * (kKvBlock / 4) + (at_w ^ ((c >> 3) & 15))];
     if (lo > 0 || hi < 4) {
       const uint32_t was = *at;
       const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
@@ -290,6 +307,10 @@ __device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], ui
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The n lowest bits; none below 0, all from 64 on.
+__device__ __forceinline__ uint64_t kv_low_bits(int64_t n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
 __device__ __forceinline__ uint32_t kv_transpose(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -317,9 +338,10 @@ struct KvForm {
   static constexpr int kPitch = D + 4;  // of a row of the merge buffer: free of bank conflicts
   static constexpr int kSmem = 128 + kWarps * kSlots * kSlot + kWarps * 8 * kPitch * 4;
 };
-// floats of a partial result: rows x (D sums, then largest logit and sum of weights)
+// floats of a partial result: rows x (D sums, then largest logits, then sums of weights;
+// a whole number of 16 bytes)
 template <int D, int NT>
-__host__ __device__ constexpr int64_t kv_part() { return (int64_t)NT * 8 * (D + 2); }
+__host__ __device__ constexpr int64_t kv_part() { return (int64_t)NT * 8 * (D + 4); }
 
 // The weights leave exp2 times 2^14, so that fp16 holds those down to 2^-28 of the
 // largest in full; the factor cancels against the sum of weights, which has it too.
@@ -446,7 +468,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     ++issued;
     islot = islot + 1 == R ? 0 : islot + 1;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < R; ++i) issue();
 
   int taken = 0, slot = 0;  // halves used
@@ -471,6 +493,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
 
   int64_t u = u_lo + warp;
   bool first_item = true;
+  const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
   for (int64_t seg = u_lo; seg < u_hi;) {
     at.seek(a, seg);
     const int64_t seg_end = at.hi < u_hi ? at.hi : u_hi;
@@ -484,19 +507,43 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     uint32_t qf[NT][DT][2];
     float qs[NT][2];  // factor of the logits of rows 2 c, 2 c + 1: softmax scale x log2 e / that power
     if (u < seg_end) {
+      uint32_t raw[NT][DT][2];  // as stored, all loads before the first use
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = row0 + n * 8 + g;
-        const bool has = n * 8 + g < rows;
-        const int t = row / a.group;
-        const int64_t qa = ((int64_t)at.s * a.T + t) * a.q_stride + ((int64_t)h * a.group + row - t * a.group) * D;
+        const int row = row0 + n * 8 + g, t = row / a.group;
+        const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) +
+                                   ((int64_t)at.s * a.T + t) * a.q_stride + ((int64_t)h * a.group + row - t * a.group) * D + 16 * c;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) raw[n][i][0] = raw[n][i][1] = 0;
+        if (n * 8 + g < rows) {
+          if (q_vec) {
+#pragma unroll
+            for (int i = 0; i < DT; i += 2) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + (i >> 2) * 64 + (i & 3) * 4));
+              raw[n][i][0] = v.x;
+              raw[n][i][1] = v.y;
+              raw[n][i + 1][0] = v.z;
+              raw[n][i + 1][1] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                raw[n][i][e >> 1] |= (uint32_t)__ldg(qp + (i >> 2) * 64 + (i & 3) * 4 + e) << (16 * (e & 1));
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
         float mx = 0.f;
         float x[DT][4];
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[i][e] = has ? kv_load(a.q, qa + (i >> 2) * 64 + 16 * c + (i & 3) * 4 + e, a.dtype) : 0.f;
+            const unsigned short w = (unsigned short)(raw[n][i][e >> 1] >> (16 * (e & 1)));
+            x[i][e] = a.dtype == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
             mx = fmaxf(mx, f8_finite_abs(x[i][e]));
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -535,10 +582,12 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       // does every query see every token of the block?
       const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
                         (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
-      // token at `tok` of the block, query t
-      auto sees = [&](int tok, int t) {
-        const int64_t p = pos0 + tok, i = (int64_t)len - a.T + t;
-        return !bad && p <= i && (a.window <= 0 || i - p < a.window || p < a.sinks);
+      // bit `tok`: query t sees that token of the block
+      auto mask = [&](int t) {
+        const int64_t i = (int64_t)len - a.T + t - pos0;  // the query's position, from the block's start
+        uint64_t w = kv_low_bits(i + 1);
+        if (a.window > 0) w &= ~kv_low_bits(i + 1 - a.window) | kv_low_bits(a.sinks - pos0);
+        return bad ? 0ull : w;
       };
 
       // ---- logits: tile j holds tokens 16 (r / 2) + 4 j + r % 2 (rows r = 0..7 of the
@@ -584,20 +633,19 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       for (int n = 0; n < NT; ++n) {
         const float f0 = qs[n][0] * ks, f1 = qs[n][1] * ks;
         float m0 = m[n][0], m1 = m[n][1];
-        const int r0 = row0 + n * 8 + 2 * c, ta = r0 / a.group, tb = (r0 + 1) / a.group;
+        // the tokens that the queries of rows 2 c, 2 c + 1 see, from this lane's first on
+        uint32_t wa = ~0u, wb = ~0u;
+        if (edge) {
+          const int r0 = row0 + n * 8 + 2 * c, first = 16 * (g >> 1) + (g & 1);
+          wa = (uint32_t)(mask(r0 / a.group) >> first);
+          wb = (uint32_t)(mask((r0 + 1) / a.group) >> first);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          s[n][t][0] *= f0;
-          s[n][t][1] *= f1;
-          s[n][t][2] *= f0;
-          s[n][t][3] *= f1;
-          if (edge) {
-            const int tok = 16 * (g >> 1) + (g & 1) + 4 * t;
-            if (!sees(tok, ta)) s[n][t][0] = -INFINITY;
-            if (!sees(tok, tb)) s[n][t][1] = -INFINITY;
-            if (!sees(tok + 2, ta)) s[n][t][2] = -INFINITY;
-            if (!sees(tok + 2, tb)) s[n][t][3] = -INFINITY;
-          }
+          s[n][t][0] = wa >> (4 * t) & 1 ? s[n][t][0] * f0 : -INFINITY;
+          s[n][t][1] = wb >> (4 * t) & 1 ? s[n][t][1] * f1 : -INFINITY;
+          s[n][t][2] = wa >> (4 * t + 2) & 1 ? s[n][t][2] * f0 : -INFINITY;
+          s[n][t][3] = wb >> (4 * t + 2) & 1 ? s[n][t][3] * f1 : -INFINITY;
           m0 = fmaxf(m0, fmaxf(s[n][t][0], s[n][t][2]));
           m1 = fmaxf(m1, fmaxf(s[n][t][1], s[n][t][3]));
         }
@@ -630,12 +678,11 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       // ---- sums
       arrived();
       const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
+      // channels 16 i .. + 15: V^T's registers, tile t of tokens
+      auto load_v = [&](int i, uint32_t (&f)[4][4]) {
         const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 16 * kKvBlock);
         const uint4 y = *reinterpret_cast<const uint4 *>(vp + (i * 16 + 8) * kKvBlock);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-        uint32_t f[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           f[t][0] = kv_half2_lo(xw[t]);
@@ -643,34 +690,55 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
           f[t][2] = kv_half2_hi(xw[t]);
           f[t][3] = kv_half2_hi(yw[t]);
         }
+      };
+      if (!edge) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          if (!edge) {
+        for (int i = 0; i < DT; ++i) {
+          uint32_t f[4][4];
+          load_v(i, f);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
-          } else {
-            // values that a query does not see may be anything, NaN among it: for each
-            // query of the tile, the product with those it sees, kept for its rows
-            const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
-            for (int t = r_lo / a.group; t <= r_hi / a.group; ++t) {
-              float e[4] = {0.f, 0.f, 0.f, 0.f};
+            o[n][i][0] = fmaf(vs, d[0], o[n][i][0] * keep[n][0]);
+            o[n][i][1] = fmaf(vs, d[1], o[n][i][1] * keep[n][1]);
+            o[n][i][2] = fmaf(vs, d[2], o[n][i][2] * keep[n][0]);
+            o[n][i][3] = fmaf(vs, d[3], o[n][i][3] * keep[n][1]);
+          }
+        }
+      } else {
+        // values that a query does not see may be anything, NaN among it: for each query
+        // of a tile of rows, the product with the values that it sees, for its rows only
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int tok = 16 * c + 4 * k;
-                const uint32_t k01 = (sees(tok, t) ? 0xffffu : 0u) | (sees(tok + 1, t) ? 0xffff0000u : 0u);
-                const uint32_t k23 = (sees(tok + 2, t) ? 0xffffu : 0u) | (sees(tok + 3, t) ? 0xffff0000u : 0u);
-                const uint32_t fm[4] = {f[k][0] & k01, f[k][1] & k01, f[k][2] & k23, f[k][3] & k23};
-                kv_mma(e, fm, p[n][k][0], p[n][k][1]);
+        for (int n = 0; n < NT; ++n) {
+          const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
+          const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+          const int t_lo = r_lo / a.group;
+#pragma unroll 1
+          for (int q = t_lo; q <= r_hi / a.group; ++q) {
+            const uint32_t w = (uint32_t)(mask(q) >> (16 * c)) & 0xffffu;
+            const bool ra = ta == q, rb = tb == q;
+            const float ka = q == t_lo ? keep[n][0] : 1.f, kb = q == t_lo ? keep[n][1] : 1.f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+              uint32_t f[4][4];
+              load_v(i, f);
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t b = w >> (4 * t);
+                const uint32_t m01 = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
+                const uint32_t m23 = (b & 4 ? 0xffffu : 0u) | (b & 8 ? 0xffff0000u : 0u);
+                const uint32_t fm[4] = {f[t][0] & m01, f[t][1] & m01, f[t][2] & m23, f[t][3] & m23};
+                kv_mma(d, fm, p[n][t][0], p[n][t][1]);
               }
-              if ((r_lo + 2 * c) / a.group == t) d[0] = e[0], d[2] = e[2];
-              if ((r_lo + 2 * c + 1) / a.group == t) d[1] = e[1], d[3] = e[3];
+              o[n][i][0] = o[n][i][0] * ka + (ra ? vs * d[0] : 0.f);
+              o[n][i][1] = o[n][i][1] * kb + (rb ? vs * d[1] : 0.f);
+              o[n][i][2] = o[n][i][2] * ka + (ra ? vs * d[2] : 0.f);
+              o[n][i][3] = o[n][i][3] * kb + (rb ? vs * d[3] : 0.f);
             }
           }
-          o[n][i][0] = fmaf(vs, d[0], o[n][i][0] * keep[n][0]);
-          o[n][i][1] = fmaf(vs, d[1], o[n][i][1] * keep[n][1]);
-          o[n][i][2] = fmaf(vs, d[2], o[n][i][2] * keep[n][0]);
-          o[n][i][3] = fmaf(vs, d[3], o[n][i][3] * keep[n][1]);
         }
       }
       release();
@@ -757,8 +825,9 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
 
 // Items that several CTAs of k_kv8_attention share: their partial results, merged in the
 // order of the blocks; and the outputs of sequences without tokens: zeros.
-// grid (S, items), 256 threads; W: the attention kernel's CTAs.
-constexpr int kKvJoinThreads = 256;
+// grid (S, items, pieces of the item's values), a thread for four channels of a row; W:
+// the attention kernel's CTAs.
+constexpr int kKvJoinThreads = 128;
 template <int D, int NT>
 __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int W) {
   pdl_trigger();
@@ -768,35 +837,44 @@ __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int
   const int64_t before = kv_before(a, s, lane);
   const KvSeen seen = kv_seen(a, s);
   const int64_t u0 = before * items + (int64_t)item * seen.count, u1 = u0 + seen.count;
-  int64_t w0 = 0, w1 = -1, total = 0, shares = 0;
-  if (seen.count > 0) {
-    total = kv_before(a, a.S, lane) * items;
-    shares = kv_shares(total, W);
-    w0 = f8_owner(u0, total, shares);
-    w1 = f8_owner(u1 - 1, total, shares);
-    if (w0 == w1) return;
-  }
   const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
   const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
-  for (int e = threadIdx.x; e < rows * D; e += kKvJoinThreads) {
-    const int r = e / D, d = e - r * D;
-    float mx = -INFINITY, sum = 0.f, den = 0.f;
-    for (int64_t w = w0; w <= w1; ++w) {
-      const int slot = w * total / shares >= u0 ? 0 : 1;  // the CTA's first item, or its last
-      const float *part = a.ws + (w * 2 + slot) * kv_part<D, NT>();
-      const float pm = part[NT * 8 * D + r], pl = part[NT * 8 * (D + 1) + r], po = part[r * D + d];
-      const float big = fmaxf(mx, pm), z = big == -INFINITY ? 0.f : big;
-      const float f = kv_exp2(mx - z), q = kv_exp2(pm - z);
-      sum = fmaf(q, po, f * sum);
-      den = fmaf(q, pl, f * den);
-      mx = big;
+  const int e = (blockIdx.z * kKvJoinThreads + threadIdx.x) * 4, r = e / D, d = e - r * D;
+  float mx = -INFINITY, den = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (seen.count > 0) {
+    const int64_t total = kv_before(a, a.S, lane) * items, shares = kv_shares(total, W);
+    const int64_t w0 = f8_owner(u0, total, shares), w1 = f8_owner(u1 - 1, total, shares);
+    if (w0 == w1 || r >= rows) return;
+    constexpr int64_t kPart = kv_part<D, NT>();
+    // the first CTA's range may have begun in an item before: then this is its second part
+    const float *const p = a.ws + w0 * 2 * kPart;
+    const int64_t skip = w0 * total / shares < u0 ? kPart : 0;
+    const int n = (int)(w1 - w0) + 1;
+    for (int i = 0; i < n; ++i) mx = fmaxf(mx, p[(i == 0 ? skip : i * 2 * kPart) + NT * 8 * D + r]);
+    const float z = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float *q = p + (i == 0 ? skip : i * 2 * kPart);
+      const float f = kv_exp2(q[NT * 8 * D + r] - z);
+      const float4 v = *reinterpret_cast<const float4 *>(q + e);
+      den = fmaf(f, q[NT * 8 * (D + 1) + r], den);
+      sum.x = fmaf(f, v.x, sum.x);
+      sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z);
+      sum.w = fmaf(f, v.w, sum.w);
     }
-    const int row = row0 + r, t = row / a.group;
-    const int64_t at_row = ((int64_t)s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
-    reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = f8_round16(den == 0.f ? 0.f : sum / den, a.dtype);
-    if (d == 0 && a.lse != nullptr)
-      a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
+  } else if (r >= rows) {
+    return;
   }
+  const int row = row0 + r, t = row / a.group;
+  const int64_t at_row = ((int64_t)s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
+  unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = f8_round16(den == 0.f ? 0.f : v[j] / den, a.dtype);
+  if (d == 0 && a.lse != nullptr)
+    a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
 }
 
 }  // namespace gemv
