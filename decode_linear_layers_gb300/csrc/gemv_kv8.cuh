@@ -249,48 +249,68 @@ __device__ __forceinline__ KvSeen kv_seen(const KvArgs &a, int s) {
   return v;
 }
 
-// The blocks of all sequences, heads and row tiles, one after the other (a sequence's
-// heads and row tiles are its items), are cut into equal ranges, one for each CTA: a
-// batch of very different lengths and a single long sequence both keep every SM busy.
-// A CTA meets the end of an item, whole items, and the start of one.
-__device__ __forceinline__ int64_t kv_warp_sum(int64_t v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-// Blocks (of one item each) of the sequences [0, s).
+// The work list: the items (a sequence's heads and row tiles) one after the other, each
+// with kKvItemCost places for its queries and its output and one for each block.  It is
+// cut into equal ranges, one for each warp of the grid: a batch of very different lengths
+// and a single long sequence both keep every SM busy, and no warp waits for another.
+// A range holds the end of an item, whole items, and the start of one.
+constexpr int kKvItemCost = 1;
+
+__device__ __forceinline__ int kv_places(const KvSeen &v) { return v.count > 0 ? v.count + kKvItemCost : 0; }
+// Places of one item of each of the sequences [0, s).  (A sequence has at most 2^24
+// blocks: those of 32 fit 32 bits.)
 __device__ __forceinline__ int64_t kv_before(const KvArgs &a, int s, int lane) {
   int64_t n = 0;
-  for (int i = lane; i < s; i += 32) n += kv_seen(a, i).count;
-  return kv_warp_sum(n);
+  for (int i = 0; i < s; i += 32)
+    n += __reduce_add_sync(0xffffffffu, i + lane < s ? (unsigned)kv_places(kv_seen(a, i + lane)) : 0u);
+  return n;
 }
-// CTAs that get a share, and the first block of CTA w's
-__device__ __forceinline__ int64_t kv_shares(int64_t total, int64_t W) { return total < W ? total : W; }
+__device__ __forceinline__ int64_t kv_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// `total` places in ranges for W warps, the first `more` of them one longer.
+struct KvShares {
+  int64_t each, more;
+  __device__ KvShares(int64_t total, int W) {
+    each = kv_div(total, W);
+    more = total - each * W;
+  }
+  __device__ int64_t first(int64_t w) const { return w * each + (w < more ? w : more); }
+  __device__ int64_t owner(int64_t u) const {
+    const int64_t longer = more * (each + 1);
+    return u < longer ? kv_div(u, each + 1) : more + kv_div(u - longer, each);
+  }
+};
 
-// Position in that list: an item and the range [lo, hi) of its blocks' numbers.
+// An item, and the places [lo, hi) of its blocks.
 struct KvItem {
   int64_t lo, hi;
   int s, item;
   KvSeen seen;
-  __device__ void load(const KvArgs &a, int s_, int64_t lo_) {
+  __device__ void load(const KvArgs &a, int s_, int64_t at) {
     s = s_;
     item = 0;
-    lo = lo_;
     seen = kv_seen(a, s);
+    lo = at + (seen.count > 0 ? kKvItemCost : 0);
     hi = lo + seen.count;
   }
-  // the item that holds block u >= lo (u below the total)
-  __device__ void seek(const KvArgs &a, int64_t u) {
-    const int items = a.heads * a.row_tiles;
-    while (u >= hi) {
-      if (item + 1 < items && seen.count > 0) {
-        ++item;
-        lo = hi;
-        hi = lo + seen.count;
-      } else {
-        load(a, s + 1, hi);
-      }
+  __device__ void next(const KvArgs &a) {
+    if (seen.count > 0 && item + 1 < a.heads * a.row_tiles) {
+      ++item;
+      lo = hi + kKvItemCost;
+      hi = lo + seen.count;
+    } else {
+      load(a, s + 1, hi);
     }
+  }
+  __device__ void skip(int64_t n) {  // n items of the same sequence
+    item += (int)n;
+    lo += n * (seen.count + kKvItemCost);
+    hi = lo + seen.count;
+  }
+  // the item that ends past place u (u below the total)
+  __device__ void seek(const KvArgs &a, int64_t u) {
+    while (u >= hi) next(a);
   }
 };
 
@@ -299,6 +319,13 @@ __device__ __forceinline__ void kv_bulk(void *dst, const void *src, uint32_t byt
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(tc_smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(tc_smem_u32(bar))
                : "memory");
+}
+// Four bytes; kv_copy4_arrive: the mbarrier gets one arrival once this thread's have come.
+__device__ __forceinline__ void kv_copy4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void kv_copy4_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem_u32(bar)) : "memory");
 }
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16
 __device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -311,6 +338,8 @@ __device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], ui
 __device__ __forceinline__ uint64_t kv_low_bits(int64_t n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
+// Bytes of ones for the ones among the four lowest bits.
+__device__ __forceinline__ uint32_t kv_bytes(uint32_t b) { return (((b & 15u) * 0x00204081u) & 0x01010101u) * 255u; }
 __device__ __forceinline__ uint32_t kv_transpose(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -329,14 +358,12 @@ __device__ __forceinline__ uint32_t kv_pack_half(float lo, float hi) {
 
 template <int D>
 struct KvForm {
-  // warps x slots x slot bytes of copies in flight or in use: about 190 KB
+  // warps x slots x slot bytes of copies in flight or in use: 160 to 192 KB
   static constexpr int kWarps = D <= 128 ? 8 : 4;
-  static constexpr int kSlots = D == 64 ? 5 : 3;
+  static constexpr int kSlots = D == 64 ? 5 : D == 192 ? 4 : 3;
   static constexpr int kSlot = kKvBlock * D;  // the keys or the values of a block
-  static constexpr int kDepth = (kSlots + 1) / 2;  // blocks begun at a time
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kPitch = D + 4;  // of a row of the merge buffer: free of bank conflicts
-  static constexpr int kSmem = 128 + kWarps * kSlots * kSlot + kWarps * 8 * kPitch * 4;
+  static constexpr int kSmem = 128 + kWarps * kSlots * kSlot;
 };
 // floats of a partial result: rows x (D sums, then largest logits, then sums of weights;
 // a whole number of 16 bytes)
@@ -346,12 +373,20 @@ __host__ __device__ constexpr int64_t kv_part() { return (int64_t)NT * 8 * (D + 
 // The weights leave exp2 times 2^14, so that fp16 holds those down to 2^-28 of the
 // largest in full; the factor cancels against the sum of weights, which has it too.
 constexpr float kKvLift = 14.f;
+__device__ __forceinline__ float kv_lse(float m, float den) {
+  return den == 0.f ? -INFINITY : (m - kKvLift + log2f(den)) * 0.693147180559945f;
+}
+// Row of out (and of lse) of an item's query row.
+__device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int row) {
+  const int t = row / a.group;
+  return ((int64_t)s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
+}
 
-// A CTA's range of blocks, block by block over its warps (warp w takes every kWarps-th).
-// A warp has a ring of slots in shared memory: lane 0 has the copy engine bring each
-// block's keys, then its values (one contiguous piece each), as soon as a slot is free,
-// and a slot's mbarrier says that it is there.  For a block of 64 tokens and NT tiles of
-// eight query rows (the rows of all queries of the item's head):
+// Each warp works through its own range of blocks.  It has a ring of slots in shared
+// memory: lane 0 has the copy engine bring each block's keys, then its values (one
+// contiguous piece each), as soon as a slot is free, and a slot's mbarrier says that it
+// is there.  For a block of 64 tokens and NT tiles of eight query rows (the rows of all
+// queries of the item's head):
 //   logits^T (tokens x rows) = K Q^T, four m16n8k16 tiles of 16 tokens.  A lane's 16-byte
 //     piece of a key row is four instructions' worth of its columns: k is a summation
 //     index, so any order will do that Q's registers follow.
@@ -363,111 +398,148 @@ constexpr float kKvLift = 14.f;
 //     the transposed weights come out in that order.
 // The scales join outside: the keys' in the logits' factor, the values' when a block's
 // product is added to the running sums.
-// At the end of an item (or of the range) the warps' sums are merged in shared memory
-// and written: the output, or a partial result that k_kv8_join adds up.
+// At the end of an item (or of the range) the warp writes the output, or a partial
+// result that k_kv8_join adds up.
 template <int D, int NT>
 __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const KvArgs a) {
   using F = KvForm<D>;
   constexpr int W = F::kWarps, R = F::kSlots, Q = D / 64, DT = D / 16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[W * R];
-  __shared__ float stat_m[W][8], stat_l[W][8];
+  __shared__ float meta[W * R][2];  // of the slot's block: the keys' and the values' scale
+  __shared__ int meta_bad[W * R];
   __shared__ int abort_flag;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // after the wait: the join reads lens before its own
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   unsigned char *smem = smem_raw + ((128u - (tc_smem_u32(smem_raw) & 127u)) & 127u);
   unsigned char *ring = smem + (size_t)warp * R * F::kSlot;
-  float *merge = reinterpret_cast<float *>(smem + (size_t)W * R * F::kSlot);
   uint64_t *bar = bars + warp * R;
   if (lane == 0)
-    for (int i = 0; i < R; ++i) tc_mbar_init(&bar[i], 1);
+    for (int i = 0; i < R; ++i) tc_mbar_init(&bar[i], 2);  // the block's copy, and its scales'
   if (tid == 0) abort_flag = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
 
   const int items = a.heads * a.row_tiles;
   const int64_t total = kv_before(a, a.S, lane) * items;
-  const int64_t shares = kv_shares(total, gridDim.x);
-  if ((int64_t)blockIdx.x >= shares) return;
-  const int64_t u_lo = (int64_t)blockIdx.x * total / shares, u_hi = ((int64_t)blockIdx.x + 1) * total / shares;
+  const KvShares shares(total, (int)gridDim.x * W);
+  const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x;  // (few blocks: one for each SM)
+  const int64_t u_lo = shares.first(worker), u_hi = shares.first(worker + 1);
+  if (u_lo >= u_hi) return;
 
-  // the sequence of block u_lo
+  // the item of place u_lo
   KvItem at;
-  {
-    int64_t base = 0;
-    int s0 = 0;
-    for (;;) {  // 32 sequences at a time
-      const int s = s0 + lane;
-      int64_t n = s < a.S ? (int64_t)kv_seen(a, s).count * items : 0;
+  int64_t base = 0;
+  for (int s0 = 0;; s0 += 32) {  // 32 sequences at a time
+    const int s = s0 + lane;
+    unsigned n = s < a.S ? (unsigned)kv_places(kv_seen(a, s)) : 0u;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, n, d);
-        if (lane >= d) n += o;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, base + n > u_lo);
-      if (past != 0) {
-        const int f = __ffs(past) - 1;
-        const int64_t prev = __shfl_sync(0xffffffffu, n, f > 0 ? f - 1 : 0);
-        at.load(a, s0 + f, base + (f > 0 ? prev : 0));
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, n, 31);
-      s0 += 32;
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, n, d);
+      if (lane >= d) n += o;
     }
-    at.seek(a, u_lo);
+    const unsigned past = __ballot_sync(0xffffffffu, base + (int64_t)n * items > u_lo);
+    if (past != 0) {
+      const int f = __ffs(past) - 1;
+      const unsigned before = __shfl_sync(0xffffffffu, n, f > 0 ? f - 1 : 0);
+      at.load(a, s0 + f, base + (f > 0 ? (int64_t)before * items : 0));
+      at.skip(kv_div(u_lo - (at.lo - kKvItemCost), kv_places(at.seen)));
+      break;
+    }
+    base += (int64_t)__shfl_sync(0xffffffffu, n, 31) * items;
   }
 
-  // ---- copies: this warp's blocks, keys and values in turn
-  KvItem is = at;          // the item of block `iu`
-  int64_t iu = u_lo + warp;
-  int issued = 0;          // halves begun
-  int islot = 0;
-  int32_t entry = 0;       // table entry of block iu, loaded ahead
-  int64_t ipb = 0;         // pool block whose keys were begun last
-  float q_ks[F::kDepth], q_vs[F::kDepth];  // scales of the blocks begun, oldest first
-  int q_n = 0;
-  auto look = [&]() {
-    if (iu < u_hi) {
-      is.seek(a, iu);
-      const int j = (int)(iu - is.lo);
-      entry = __ldg(a.table + (int64_t)is.s * a.width + (j < is.seen.sink ? j : is.seen.from + j - is.seen.sink));
+  // An item's queries as stored: rows g of its tiles, 16 channels 16 c .. of each 64.  The
+  // first item's are on their way before the blocks are: behind those they would wait.
+  const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
+  constexpr bool kEarly = NT * DT <= 16;  // (more would not stay in registers)
+  uint32_t raw[NT][DT][2];
+  auto load_q = [&](const KvItem &it) {
+    const int h = it.item / a.row_tiles, row0 = (it.item - h * a.row_tiles) * NT * 8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row0 + n * 8 + g, t = row / a.group;
+      const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)it.s * a.T + t) * a.q_stride +
+                                 ((int64_t)h * a.group + row - t * a.group) * D + 16 * c;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) raw[n][i][0] = raw[n][i][1] = 0;
+      if (row < a.T * a.group) {
+        if (q_vec) {
+#pragma unroll
+          for (int i = 0; i < DT; i += 2) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + (i >> 2) * 64 + (i & 3) * 4));
+            raw[n][i][0] = v.x;
+            raw[n][i][1] = v.y;
+            raw[n][i + 1][0] = v.z;
+            raw[n][i + 1][1] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              raw[n][i][e >> 1] |= (uint32_t)__ldg(qp + (i >> 2) * 64 + (i & 3) * 4 + e) << (16 * (e & 1));
+        }
+      }
     }
   };
-#pragma unroll
-  for (int i = 0; i < F::kDepth; ++i) q_ks[i] = q_vs[i] = 0.f;
-  look();
+
+  // ---- copies: the keys and the values of this warp's blocks in turn
+  KvItem is = at;                          // the item of place `iu`
+  int64_t iu = u_lo > at.lo ? u_lo : at.lo;
+  int issued = 0, islot = 0;               // halves begun, and the next one's slot
+  int batch = -1;                          // first of the item's blocks whose table entries the lanes hold
+  int32_t entries = 0;
+  int64_t ipb = 0;                         // (block of the pool) x heads + head of the keys begun last
+  auto look = [&](int j) {
+    batch = j;
+    const int i = j + lane;
+    entries = -1;
+    if (i < is.seen.count)
+      entries = __ldg(a.table + (int64_t)is.s * a.width + (i < is.seen.sink ? i : is.seen.from + i - is.seen.sink));
+  };
   auto issue = [&]() {
-    const uint8_t *src;
-    if ((issued & 1) == 0) {
+    const bool keys = (issued & 1) == 0;
+    bool good = true;
+    if (keys) {
       if (iu >= u_hi) return;
-      const int h = is.item / a.row_tiles;
-      const bool good = entry >= 0 && entry < a.blocks;
-      ipb = (good ? (int64_t)entry : 0) * a.heads + h;
-      const float ks = __ldg(a.k_scale + ipb), vs = __ldg(a.v_scale + ipb);
-#pragma unroll
-      for (int i = 0; i < F::kDepth; ++i)
-        if (i == q_n) {
-          q_ks[i] = ks;
-          q_vs[i] = good ? vs : -1.f;  // scales are positive: a block to leave out
-        }
-      ++q_n;
-      if (!good && lane == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-      iu += W;
-      look();
-      src = a.k;
-    } else {
-      src = a.v;
+      const int j = (int)(iu - is.lo);
+      if (batch < 0 || j >= batch + 32) look(j);
+      const int32_t entry = __shfl_sync(0xffffffffu, entries, j - batch);
+      good = entry >= 0 && entry < a.blocks;
+      ipb = (good ? (int64_t)entry : 0) * a.heads + is.item / a.row_tiles;
+      if (++iu == is.hi && iu + kKvItemCost < u_hi) {
+        is.seek(a, iu);
+        iu = is.lo;
+        batch = -1;
+      } else if (iu == is.hi) {
+        iu = u_hi;
+      }
     }
-    // (test: the last copy of the first CTA's first warp never comes)
-    const bool withheld = a.test_stall && blockIdx.x == 0 && warp == 0 && (issued & 1) != 0 && iu >= u_hi;
-    if (lane == 0 && !withheld) {
-      tc_mbar_arrive_expect_tx(&bar[islot], F::kSlot);
-      kv_bulk(ring + (size_t)islot * F::kSlot, src + ipb * F::kSlot, F::kSlot, &bar[islot]);
+    const bool withheld = a.test_stall && !keys && iu >= u_hi;  // test: the range's last copy never comes
+    if (lane == 0) {
+      if (keys) {
+        meta_bad[warp * R + islot] = !good;
+        if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+        kv_copy4(&meta[warp * R + islot][0], a.k_scale + ipb);
+        kv_copy4(&meta[warp * R + islot][1], a.v_scale + ipb);
+        kv_copy4_arrive(&bar[islot]);
+      } else {
+        tc_mbar_arrive(&bar[islot]);
+      }
+      if (!withheld) {
+        tc_mbar_arrive_expect_tx(&bar[islot], F::kSlot);
+        kv_bulk(ring + (size_t)islot * F::kSlot, (keys ? a.k : a.v) + ipb * F::kSlot, F::kSlot, &bar[islot]);
+      }
     }
     ++issued;
     islot = islot + 1 == R ? 0 : islot + 1;
   };
+  if (iu < u_hi) {
+    look((int)(iu - is.lo));
+    if constexpr (kEarly) load_q(at);
+  }
 #pragma unroll 1
   for (int i = 0; i < R; ++i) issue();
 
@@ -475,14 +547,11 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   uint32_t phase = 0;
   bool dead = false;
   auto arrived = [&]() {
-    if (!dead) {
-      const bool ok = tc_mbar_wait_or_abort(&bar[slot], phase, a.timeout_ns, &abort_flag);
-      dead = !__all_sync(0xffffffffu, ok);
-    }
+    const bool ok = tc_mbar_wait_or_abort(&bar[slot], phase, a.timeout_ns, &abort_flag);
+    dead = !__all_sync(0xffffffffu, ok);
   };
   auto release = [&]() {
     __syncwarp();  // every lane has read the slot
-    if (dead) return;
     ++taken;
     if (++slot == R) {
       slot = 0;
@@ -491,12 +560,10 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     issue();
   };
 
-  int64_t u = u_lo + warp;
   bool first_item = true;
-  const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
-  for (int64_t seg = u_lo; seg < u_hi;) {
-    at.seek(a, seg);
-    const int64_t seg_end = at.hi < u_hi ? at.hi : u_hi;
+  int64_t u = u_lo > at.lo ? u_lo : at.lo;
+  while (u < u_hi) {
+    const int64_t seg = u, seg_end = at.hi < u_hi ? at.hi : u_hi;
     const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
     const int rows = a.T * a.group - row0;  // of this tile, at most NT * 8
     const int len = at.seen.len;
@@ -506,34 +573,8 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     // then holds what is within 2^-28 of it as the input does.
     uint32_t qf[NT][DT][2];
     float qs[NT][2];  // factor of the logits of rows 2 c, 2 c + 1: softmax scale x log2 e / that power
-    if (u < seg_end) {
-      uint32_t raw[NT][DT][2];  // as stored, all loads before the first use
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = row0 + n * 8 + g, t = row / a.group;
-        const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) +
-                                   ((int64_t)at.s * a.T + t) * a.q_stride + ((int64_t)h * a.group + row - t * a.group) * D + 16 * c;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) raw[n][i][0] = raw[n][i][1] = 0;
-        if (n * 8 + g < rows) {
-          if (q_vec) {
-#pragma unroll
-            for (int i = 0; i < DT; i += 2) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + (i >> 2) * 64 + (i & 3) * 4));
-              raw[n][i][0] = v.x;
-              raw[n][i][1] = v.y;
-              raw[n][i + 1][0] = v.z;
-              raw[n][i + 1][1] = v.w;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                raw[n][i][e >> 1] |= (uint32_t)__ldg(qp + (i >> 2) * 64 + (i & 3) * 4 + e) << (16 * (e & 1));
-          }
-        }
-      }
+    if (!kEarly || !first_item) load_q(at);
+    {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float mx = 0.f;
@@ -573,12 +614,14 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
     }
 
-    for (; u < seg_end; u += W) {
+    for (; u < seg_end; ++u) {
       const int j = (int)(u - at.lo);
       const int64_t pos0 = (int64_t)(j < at.seen.sink ? j : at.seen.from + j - at.seen.sink) * kKvBlock;
-      const float ks = q_ks[0], vs_raw = q_vs[0];
-      const bool bad = vs_raw < 0.f;
-      const float vs = bad ? 0.f : vs_raw;
+      arrived();
+      if (dead) break;
+      const float ks = meta[warp * R + slot][0];
+      const bool bad = meta_bad[warp * R + slot] != 0;  // no such block: nothing of it is seen
+      const float vs = bad ? 0.f : meta[warp * R + slot][1];
       // does every query see every token of the block?
       const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
                         (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
@@ -599,7 +642,6 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
-      arrived();
       {
         const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
 #pragma unroll
@@ -617,13 +659,6 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
             }
           }
       }
-      // (the queue's oldest scales are in registers now)
-#pragma unroll
-      for (int i = 0; i + 1 < F::kDepth; ++i) {
-        q_ks[i] = q_ks[i + 1];
-        q_vs[i] = q_vs[i + 1];
-      }
-      --q_n;
       release();
 
       // ---- weights
@@ -677,25 +712,31 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
 
       // ---- sums
       arrived();
+      if (dead) break;
       const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
-      // channels 16 i .. + 15: V^T's registers, tile t of tokens
-      auto load_v = [&](int i, uint32_t (&f)[4][4]) {
+      // channels 16 i .. + 15: V^T's registers, tile t of tokens; `keep4`: the bytes of
+      // the tokens that count
+      auto load_v = [&](int i, uint32_t (&f)[4][4], const uint32_t (*keep4)[4]) {
         const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 16 * kKvBlock);
         const uint4 y = *reinterpret_cast<const uint4 *>(vp + (i * 16 + 8) * kKvBlock);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
+          if (keep4 != nullptr) {
+            xw[t] &= (*keep4)[t];
+            yw[t] &= (*keep4)[t];
+          }
           f[t][0] = kv_half2_lo(xw[t]);
           f[t][1] = kv_half2_lo(yw[t]);
           f[t][2] = kv_half2_hi(xw[t]);
           f[t][3] = kv_half2_hi(yw[t]);
         }
       };
-      if (!edge) {
+      auto add_v = [&](const uint32_t (*keep4)[4]) {
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
           uint32_t f[4][4];
-          load_v(i, f);
+          load_v(i, f, keep4);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -707,36 +748,66 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
             o[n][i][3] = fmaf(vs, d[3], o[n][i][3] * keep[n][1]);
           }
         }
+      };
+      if (!edge) {
+        add_v(nullptr);
       } else {
-        // values that a query does not see may be anything, NaN among it: for each query
-        // of a tile of rows, the product with the values that it sees, for its rows only
+        // Values that no query of the tile sees may be anything, NaN among it: they count
+        // as 0.  So do, to a query, those that only others see: their weights are 0.
+        const int t_lo = row0 / a.group, t_hi = (row0 + (rows < NT * 8 ? rows : NT * 8) - 1) / a.group;
+        uint64_t some = 0, all = ~0ull;
+        for (int q = t_lo; q <= t_hi; ++q) {
+          some |= mask(q);
+          all &= mask(q);
+        }
+        uint32_t keep4[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
-          const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
-          const int t_lo = r_lo / a.group;
+        for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(some >> (16 * c + 4 * t)));
+        bool nan = false;
+        if (some != all) {  // ... unless they are NaN
 #pragma unroll 1
-          for (int q = t_lo; q <= r_hi / a.group; ++q) {
-            const uint32_t w = (uint32_t)(mask(q) >> (16 * c)) & 0xffffu;
-            const bool ra = ta == q, rb = tb == q;
-            const float ka = q == t_lo ? keep[n][0] : 1.f, kb = q == t_lo ? keep[n][1] : 1.f;
+          for (int i = 0; i < 2 * DT; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 8 * kKvBlock);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-              uint32_t f[4][4];
-              load_v(i, f);
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) nan |= __vcmpeq4(xw[t] & keep4[t] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+          }
+        }
+        if (!__any_sync(0xffffffffu, nan)) {
+          add_v(&keep4);
+        } else {
+          // then for each query of a tile of rows the product with the values that it
+          // sees, for its rows only
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const uint32_t b = w >> (4 * t);
-                const uint32_t m01 = (b & 1 ? 0xffffu : 0u) | (b & 2 ? 0xffff0000u : 0u);
-                const uint32_t m23 = (b & 4 ? 0xffffu : 0u) | (b & 8 ? 0xffff0000u : 0u);
-                const uint32_t fm[4] = {f[t][0] & m01, f[t][1] & m01, f[t][2] & m23, f[t][3] & m23};
-                kv_mma(d, fm, p[n][t][0], p[n][t][1]);
+          for (int n = 0; n < NT; ++n) {
+            const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
+            const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][i][e] *= keep[n][e & 1];
+#pragma unroll 1
+            for (int q = r_lo / a.group; q <= r_hi / a.group; ++q) {
+              const uint64_t w = mask(q);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(w >> (16 * c + 4 * t)));
+              const bool ra = ta == q, rb = tb == q;
+#pragma unroll
+              for (int i = 0; i < DT; ++i) {
+                uint32_t f[4][4];
+                load_v(i, f, &keep4);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
+                if (ra) {
+                  o[n][i][0] = fmaf(vs, d[0], o[n][i][0]);
+                  o[n][i][2] = fmaf(vs, d[2], o[n][i][2]);
+                }
+                if (rb) {
+                  o[n][i][1] = fmaf(vs, d[1], o[n][i][1]);
+                  o[n][i][3] = fmaf(vs, d[3], o[n][i][3]);
+                }
               }
-              o[n][i][0] = o[n][i][0] * ka + (ra ? vs * d[0] : 0.f);
-              o[n][i][1] = o[n][i][1] * kb + (rb ? vs * d[1] : 0.f);
-              o[n][i][2] = o[n][i][2] * ka + (ra ? vs * d[2] : 0.f);
-              o[n][i][3] = o[n][i][3] * kb + (rb ? vs * d[3] : 0.f);
             }
           }
         }
@@ -744,69 +815,49 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       release();
     }
 
-    // ---- the warps' sums become one, eight rows at a time
+    if (dead) break;
+
+    // ---- the item's output, or this range's part of it
     const bool whole = seg == at.lo && seg_end == at.hi;
+    float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float l0 = l[n][0], l1 = l[n][1];
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-      }
-      if (g == 0) {
-        stat_m[warp][2 * c] = m[n][0];
-        stat_m[warp][2 * c + 1] = m[n][1];
-        stat_l[warp][2 * c] = l0;
-        stat_l[warp][2 * c + 1] = l1;
-      }
-      float *mine = merge + (size_t)warp * 8 * F::kPitch;
+      for (int e = 0; e < 2; ++e) {
+        float den = l[n][e];
 #pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        mine[(2 * c) * F::kPitch + i * 16 + g] = o[n][i][0];
-        mine[(2 * c + 1) * F::kPitch + i * 16 + g] = o[n][i][1];
-        mine[(2 * c) * F::kPitch + i * 16 + g + 8] = o[n][i][2];
-        mine[(2 * c + 1) * F::kPitch + i * 16 + g + 8] = o[n][i][3];
-      }
-      __syncthreads();
-      if (abort_flag == 0) {
-        float *part = a.ws + ((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
-        for (int e = tid; e < 8 * D; e += F::kThreads) {
-          const int r = e / D, d = e - r * D;
-          if (n * 8 + r >= rows) break;
-          float mx = -INFINITY;
+        for (int d = 4; d < 32; d <<= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+        const int r = n * 8 + 2 * c + e;
+        if (r >= rows) continue;
+        if (whole) {
+          const int64_t at_row = kv_out_row(a, at.s, h, row0 + r);
+          unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + g;
+          const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-          for (int w = 0; w < W; ++w) mx = fmaxf(mx, stat_m[w][r]);
-          const float z = mx == -INFINITY ? 0.f : mx;
-          float sum = 0.f, den = 0.f;
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const float f = kv_exp2(stat_m[w][r] - z);
-            sum = fmaf(f, merge[(w * 8 + r) * F::kPitch + d], sum);
-            den = fmaf(f, stat_l[w][r], den);
+          for (int i = 0; i < DT; ++i) {
+            out[16 * i] = f8_round16(o[n][i][e] * inv, a.dtype);
+            out[16 * i + 8] = f8_round16(o[n][i][e + 2] * inv, a.dtype);
           }
-          if (whole) {
-            const int row = row0 + n * 8 + r, t = row / a.group;
-            const int64_t at_row = ((int64_t)at.s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
-            const float val = den == 0.f ? 0.f : sum / den;
-            reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = f8_round16(val, a.dtype);
-            if (d == 0 && a.lse != nullptr)
-              a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
-          } else {
-            part[(n * 8 + r) * D + d] = sum;
-            if (d == 0) {
-              part[NT * 8 * D + n * 8 + r] = mx;
-              part[NT * 8 * (D + 1) + n * 8 + r] = den;
-            }
+          if (g == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(m[n][e], den);
+        } else {
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+            part[r * D + 16 * i + g] = o[n][i][e];
+            part[r * D + 16 * i + 8 + g] = o[n][i][e + 2];
+          }
+          if (g == 0) {
+            part[NT * 8 * D + r] = m[n][e];
+            part[NT * 8 * (D + 1) + r] = den;
           }
         }
       }
-      __syncthreads();  // read before the next rows overwrite it
     }
-    seg = seg_end;
     first_item = false;
+    if (u >= u_hi) break;
+    at.seek(a, u);
+    u = at.lo;
   }
-  if (abort_flag != 0) {
+  if (dead) {
     // no copy may be in flight when the CTA exits
     if (lane == 0) {
       if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
@@ -823,58 +874,110 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   }
 }
 
-// Items that several CTAs of k_kv8_attention share: their partial results, merged in the
-// order of the blocks; and the outputs of sequences without tokens: zeros.
-// grid (S, items, pieces of the item's values), a thread for four channels of a row; W:
-// the attention kernel's CTAs.
-constexpr int kKvJoinThreads = 128;
-template <int D, int NT>
-__global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int W) {
+// Items that several warps of k_kv8_attention share: their partial results, merged in the
+// order of the blocks; and the outputs of sequences without tokens: zeros.  A thread adds
+// up four channels of a row.  Where items are few, and each may be in a hundred parts
+// (kByRow), a CTA has one row, and its warps share the parts; else it has rows for all its
+// threads, and each takes all of an item's few parts.
+// grid (S, items, pieces); workers: the attention kernel's warps.
+constexpr int kKvJoinThreads = 256;
+template <int D, int NT, bool kByRow>
+__global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int workers) {
+  constexpr int kAlong = kByRow ? D / 4 : kKvJoinThreads;       // threads along the channels
+  constexpr int kGroups = kKvJoinThreads / kAlong;              // that share the parts
+  constexpr int kStep = kByRow ? 1024 : 1;
+  __shared__ float factor[kStep];
+  __shared__ float4 sums[kByRow ? kGroups : 1][kByRow ? kAlong : 1];
+  __shared__ float red[2][kKvJoinThreads / 32];
   pdl_trigger();
-  pdl_wait();
-  const int s = blockIdx.x, item = blockIdx.y, lane = threadIdx.x & 31;
+  const int s = blockIdx.x, item = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int items = a.heads * a.row_tiles;
-  const int64_t before = kv_before(a, s, lane);
+  // (lens is older than the attention kernel, which let this one start after its own wait)
+  const int64_t total = kv_before(a, a.S, lane) * items, before = kv_before(a, s, lane) * items;
   const KvSeen seen = kv_seen(a, s);
-  const int64_t u0 = before * items + (int64_t)item * seen.count, u1 = u0 + seen.count;
+  const int64_t u0 = before + (int64_t)item * kv_places(seen) + kKvItemCost;  // the item's first block
+  int64_t w0 = 0, skip = 0;
+  int n = 0;  // parts
+  if (seen.count > 0) {
+    const KvShares shares(total, workers);
+    w0 = shares.owner(u0);
+    n = (int)(shares.owner(u0 + seen.count - 1) - w0) + 1;
+    // the first warp's range may hold blocks of an item before: then this is its second part
+    skip = shares.first(w0) < u0 - kKvItemCost ? kv_part<D, NT>() : 0;
+  }
+  pdl_wait();  // by every CTA: the next kernel counts on it
+  if (n == 1) return;  // one warp had the whole item and wrote it
   const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
   const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
-  const int e = (blockIdx.z * kKvJoinThreads + threadIdx.x) * 4, r = e / D, d = e - r * D;
+  const float *const p = a.ws + w0 * 2 * kv_part<D, NT>();
+  auto part = [&](int i) { return p + (i == 0 ? skip : i * 2 * kv_part<D, NT>()); };
+  const int along = tid % kAlong, grp = tid / kAlong;
+  const int e = (blockIdx.z * kAlong + along) * 4, r = e / D, d = e - r * D;
+  if (r >= rows) return;  // (by row: all threads alike)
   float mx = -INFINITY, den = 0.f;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (seen.count > 0) {
-    const int64_t total = kv_before(a, a.S, lane) * items, shares = kv_shares(total, W);
-    const int64_t w0 = f8_owner(u0, total, shares), w1 = f8_owner(u1 - 1, total, shares);
-    if (w0 == w1 || r >= rows) return;
-    constexpr int64_t kPart = kv_part<D, NT>();
-    // the first CTA's range may have begun in an item before: then this is its second part
-    const float *const p = a.ws + w0 * 2 * kPart;
-    const int64_t skip = w0 * total / shares < u0 ? kPart : 0;
-    const int n = (int)(w1 - w0) + 1;
-    for (int i = 0; i < n; ++i) mx = fmaxf(mx, p[(i == 0 ? skip : i * 2 * kPart) + NT * 8 * D + r]);
+  auto add = [&](const float *q, float f) {
+    const float4 v = *reinterpret_cast<const float4 *>(q + e);
+    sum.x = fmaf(f, v.x, sum.x);
+    sum.y = fmaf(f, v.y, sum.y);
+    sum.z = fmaf(f, v.z, sum.z);
+    sum.w = fmaf(f, v.w, sum.w);
+  };
+  if constexpr (!kByRow) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) mx = fmaxf(mx, part(i)[NT * 8 * D + r]);
     const float z = mx == -INFINITY ? 0.f : mx;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float *q = p + (i == 0 ? skip : i * 2 * kPart);
-      const float f = kv_exp2(q[NT * 8 * D + r] - z);
-      const float4 v = *reinterpret_cast<const float4 *>(q + e);
-      den = fmaf(f, q[NT * 8 * (D + 1) + r], den);
-      sum.x = fmaf(f, v.x, sum.x);
-      sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z);
-      sum.w = fmaf(f, v.w, sum.w);
+      const float f = kv_exp2(part(i)[NT * 8 * D + r] - z);
+      den = fmaf(f, part(i)[NT * 8 * (D + 1) + r], den);
+      add(part(i), f);
     }
-  } else if (r >= rows) {
-    return;
-  }
-  const int row = row0 + r, t = row / a.group;
-  const int64_t at_row = ((int64_t)s * a.T + t) * ((int64_t)a.heads * a.group) + (int64_t)h * a.group + (row - t * a.group);
-  unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
-  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  } else {
+    // the row's largest logit over all parts, then each part's factor, 1024 parts at a time
+    for (int i = tid; i < n; i += kKvJoinThreads) mx = fmaxf(mx, part(i)[NT * 8 * D + r]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) out[j] = f8_round16(den == 0.f ? 0.f : v[j] / den, a.dtype);
-  if (d == 0 && a.lse != nullptr)
-    a.lse[at_row] = den == 0.f ? -INFINITY : (mx - kKvLift + log2f(den)) * 0.693147180559945f;
+    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    if (lane == 0) red[0][tid >> 5] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kKvJoinThreads / 32; ++k) mx = fmaxf(mx, red[0][k]);
+    const float z = mx == -INFINITY ? 0.f : mx;
+    for (int i0 = 0; i0 < n; i0 += kStep) {
+      const int top = n - i0 < kStep ? n - i0 : kStep;
+      for (int i = tid; i < top; i += kKvJoinThreads) {
+        const float f = kv_exp2(part(i0 + i)[NT * 8 * D + r] - z);
+        factor[i] = f;
+        den = fmaf(f, part(i0 + i)[NT * 8 * (D + 1) + r], den);
+      }
+      __syncthreads();
+      if (grp < kGroups) {
+#pragma unroll 10
+        for (int i = grp; i < top; i += kGroups) add(part(i0 + i), factor[i]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) den += __shfl_xor_sync(0xffffffffu, den, k);
+    if (lane == 0) red[1][tid >> 5] = den;
+    if (grp < kGroups) sums[grp][along] = sum;
+    __syncthreads();
+    if (grp > 0) return;
+    den = 0.f;
+#pragma unroll
+    for (int k = 0; k < kKvJoinThreads / 32; ++k) den += red[1][k];
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+      const float4 v = sums[k][along];
+      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+    }
+  }
+  const int64_t at_row = kv_out_row(a, s, h, row0 + r);
+  unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w}, inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
+  if (d == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(mx, den);
 }
 
 }  // namespace gemv

@@ -454,8 +454,8 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits);
 
 /* TEST ONLY — not thread-safe.  With `stall` != 0 every later GEMV_KERNEL_TC or gemv_f8
  * launch skips the last MMA of its first CTA (in the persistent form: the MMAs of that
- * CTA's last k-tile), and every gemv_kv8_attention launch the last copy of its first
- * CTA's first warp, so that the wait for it runs out after `timeout_ns` (<= 0: the
+ * CTA's last k-tile), and every gemv_kv8_attention launch the last copy of each
+ * warp, so that the wait for it runs out after `timeout_ns` (<= 0: the
  * default of 2 s) and gemv_get_device_status reports GEMV_ERR_DEVICE_TIMEOUT.
  * stall = 0 restores normal launches. */
 gemv_status_t gemv_test_stall(int stall, int64_t timeout_ns);
