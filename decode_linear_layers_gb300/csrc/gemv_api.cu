@@ -212,11 +212,9 @@ gemv_status_t run(int dtype, const void *A, const float *scale, const void *x, c
 }  // namespace
 
 namespace gemv {
-// The tensor maps of the tcgen05 kernel.  cuTensorMapEncodeTiled is a driver
-// function: it is fetched once through the runtime, so the library needs no
-// link-time dependency on the driver library.
-bool tc_tensor_maps(int dtype, const void *A, const void *x, int64_t M, int64_t K, int B, int N, void *map_a,
-                    void *map_x) {
+// cuTensorMapEncodeTiled is a driver function: it is fetched once through the runtime,
+// so the library needs no link-time dependency on the driver library.
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -225,6 +223,23 @@ bool tc_tensor_maps(int dtype, const void *A, const void *x, int64_t M, int64_t 
       fn = nullptr;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }();
+  return encode;
+}
+
+bool map_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows, int box_cols, bool swizzle) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tensor maps of the tcgen05 kernel.
+bool tc_tensor_maps(int dtype, const void *A, const void *x, int64_t M, int64_t K, int B, int N, void *map_a,
+                    void *map_x) {
+  const auto encode = tensor_map_encoder();
   if (encode == nullptr || M <= 0 || K <= 0 || B <= 0) return false;
   const CUtensorMapDataType t = dtype == GEMV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const cuuint32_t es[2] = {1, 1};

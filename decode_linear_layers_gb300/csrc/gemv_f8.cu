@@ -1,6 +1,4 @@
 // gemv_f8 and gemv_f8_quantize: argument checks, the choice of the form, launches.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -11,26 +9,6 @@
 
 namespace gemv {
 namespace {
-
-// 8-bit matrix (rows x K, row-major) in boxes of 128 columns x box_rows, 128-byte
-// swizzle, zeros outside.
-bool f8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box_rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)K};
-  const cuuint32_t box[2] = {(cuuint32_t)kF8Group, (cuuint32_t)box_rows}, es[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int N, bool kPrompt>
 gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int sms, cudaStream_t s) {
@@ -43,7 +21,8 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   a.shared = a.tiles % W;
   a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
-  if (!f8_map(&map_a, A, a.M, K, kPrompt ? N : kF8Rows) || !f8_map(&map_x, x, a.B, K, kPrompt ? kF8Rows : N))
+  if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group, true) ||
+      !map_bytes(&map_x, x, a.B, K, kPrompt ? kF8Rows : N, kF8Group, true))
     return fail((int)cudaErrorInvalidValue);
   cudaError_t e = cudaSuccess;
   void *ws = nullptr;

@@ -338,6 +338,26 @@ __device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], ui
 __device__ __forceinline__ uint64_t kv_low_bits(int64_t n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
+// Four 16-bit values from anywhere (a call: such rows are rare, and their loads many).
+__device__ __noinline__ uint2 kv_load4(const unsigned short *p) {
+  const uint32_t a = __ldg(p), b = __ldg(p + 1), c = __ldg(p + 2), d = __ldg(p + 3);
+  return make_uint2(a | (b << 16), c | (d << 16));
+}
+// Two 16-bit values: wider, and the larger ones of two pairs (none negative, NaN passed over).
+__device__ __forceinline__ float kv_wide_lo(uint32_t w, int dt) {
+  return dt == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half((unsigned short)w)) : bf16_lo(w);
+}
+__device__ __forceinline__ float kv_wide_hi(uint32_t w, int dt) {
+  return dt == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : bf16_hi(w);
+}
+__device__ __forceinline__ uint32_t kv_max2(uint32_t a, uint32_t b, int dt) {
+  uint32_t r;
+  if (dt == GEMV_DTYPE_F16)
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Bytes of ones for the ones among the four lowest bits.
 __device__ __forceinline__ uint32_t kv_bytes(uint32_t b) { return (((b & 15u) * 0x00204081u) & 0x01010101u) * 255u; }
 __device__ __forceinline__ uint32_t kv_transpose(uint32_t v) {
@@ -358,9 +378,10 @@ __device__ __forceinline__ uint32_t kv_pack_half(float lo, float hi) {
 
 template <int D>
 struct KvForm {
-  // warps x slots x slot bytes of copies in flight or in use: 160 to 192 KB
-  static constexpr int kWarps = D <= 128 ? 8 : 4;
-  static constexpr int kSlots = D == 64 ? 5 : D == 192 ? 4 : 3;
+  // warps x slots x slot bytes of copies in flight or in use: 192 to 224 KB; an odd number
+  // of slots, so that each freed one takes the other half of a block
+  static constexpr int kWarps = D <= 128 ? 8 : D == 192 ? 6 : 4;
+  static constexpr int kSlots = D == 64 ? 7 : 3;
   static constexpr int kSlot = kKvBlock * D;  // the keys or the values of a block
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmem = 128 + kWarps * kSlots * kSlot;
@@ -384,9 +405,9 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 
 // Each warp works through its own range of blocks.  It has a ring of slots in shared
 // memory: lane 0 has the copy engine bring each block's keys, then its values (one
-// contiguous piece each), as soon as a slot is free, and a slot's mbarrier says that it
-// is there.  For a block of 64 tokens and NT tiles of eight query rows (the rows of all
-// queries of the item's head):
+// contiguous piece each), as soon as a slot is free, and a slot's mbarrier says that the
+// piece is there.  For a block of 64 tokens and NT tiles of eight query rows (the rows of
+// all queries of the item's head):
 //   logits^T (tokens x rows) = K Q^T, four m16n8k16 tiles of 16 tokens.  A lane's 16-byte
 //     piece of a key row is four instructions' worth of its columns: k is a summation
 //     index, so any order will do that Q's registers follow.
@@ -416,7 +437,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   unsigned char *ring = smem + (size_t)warp * R * F::kSlot;
   uint64_t *bar = bars + warp * R;
   if (lane == 0)
-    for (int i = 0; i < R; ++i) tc_mbar_init(&bar[i], 2);  // the block's copy, and its scales'
+    for (int i = 0; i < R; ++i) tc_mbar_init(&bar[i], 2);  // the piece, and with keys the block's scales
   if (tid == 0) abort_flag = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
@@ -476,22 +497,21 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              raw[n][i][e >> 1] |= (uint32_t)__ldg(qp + (i >> 2) * 64 + (i & 3) * 4 + e) << (16 * (e & 1));
+          for (int i = 0; i < DT; ++i) {
+            const uint2 v = kv_load4(qp + (i >> 2) * 64 + (i & 3) * 4);
+            raw[n][i][0] = v.x;
+            raw[n][i][1] = v.y;
+          }
         }
       }
     }
   };
 
-  // ---- copies: the keys and the values of this warp's blocks in turn
+  // ---- copies: the pieces of this warp's blocks
   KvItem is = at;                          // the item of place `iu`
   int64_t iu = u_lo > at.lo ? u_lo : at.lo;
-  int issued = 0, islot = 0;               // halves begun, and the next one's slot
   int batch = -1;                          // first of the item's blocks whose table entries the lanes hold
   int32_t entries = 0;
-  int64_t ipb = 0;                         // (block of the pool) x heads + head of the keys begun last
   auto look = [&](int j) {
     batch = j;
     const int i = j + lane;
@@ -499,65 +519,84 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     if (i < is.seen.count)
       entries = __ldg(a.table + (int64_t)is.s * a.width + (i < is.seen.sink ? i : is.seen.from + i - is.seen.sink));
   };
-  auto issue = [&]() {
-    const bool keys = (issued & 1) == 0;
-    bool good = true;
-    if (keys) {
-      if (iu >= u_hi) return;
-      const int j = (int)(iu - is.lo);
-      if (batch < 0 || j >= batch + 32) look(j);
-      const int32_t entry = __shfl_sync(0xffffffffu, entries, j - batch);
-      good = entry >= 0 && entry < a.blocks;
-      ipb = (good ? (int64_t)entry : 0) * a.heads + is.item / a.row_tiles;
-      if (++iu == is.hi && iu + kKvItemCost < u_hi) {
+  // the next block: its number in the pool x heads + head; -1: none is left, -2 - head:
+  // the table's entry is none of the pool
+  auto advance = [&]() -> int64_t {
+    if (iu >= u_hi) return -1;
+    const int j = (int)(iu - is.lo), h = is.item / a.row_tiles;
+    if (batch < 0 || j >= batch + 32) look(j);
+    const int32_t entry = __shfl_sync(0xffffffffu, entries, j - batch);
+    if (++iu == is.hi) {
+      if (iu + kKvItemCost < u_hi) {
         is.seek(a, iu);
         iu = is.lo;
         batch = -1;
-      } else if (iu == is.hi) {
+      } else {
         iu = u_hi;
       }
     }
-    const bool withheld = a.test_stall && !keys && iu >= u_hi;  // test: the range's last copy never comes
+    return entry >= 0 && entry < a.blocks ? (int64_t)entry * a.heads + h : -2 - (int64_t)h;
+  };
+  int issued = 0, taken = 0;               // pieces begun, pieces used
+  auto issue = [&](int64_t block, bool keys, int to) {
+    if (block == -1) return;
     if (lane == 0) {
+      const bool good = block >= 0;
+      const int64_t at_block = good ? block : -2 - block;  // (of an entry that is no block: any, unseen)
+      uint64_t *b = &bar[to];
       if (keys) {
-        meta_bad[warp * R + islot] = !good;
+        meta_bad[warp * R + to] = !good;
         if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-        kv_copy4(&meta[warp * R + islot][0], a.k_scale + ipb);
-        kv_copy4(&meta[warp * R + islot][1], a.v_scale + ipb);
-        kv_copy4_arrive(&bar[islot]);
+        kv_copy4(&meta[warp * R + to][0], a.k_scale + at_block);
+        kv_copy4(&meta[warp * R + to][1], a.v_scale + at_block);
+        kv_copy4_arrive(b);
       } else {
-        tc_mbar_arrive(&bar[islot]);
+        tc_mbar_arrive(b);
       }
-      if (!withheld) {
-        tc_mbar_arrive_expect_tx(&bar[islot], F::kSlot);
-        kv_bulk(ring + (size_t)islot * F::kSlot, (keys ? a.k : a.v) + ipb * F::kSlot, F::kSlot, &bar[islot]);
+      if (!a.test_stall || keys) {  // test: no values ever come
+        tc_mbar_arrive_expect_tx(b, F::kSlot);
+        kv_bulk(ring + (size_t)to * F::kSlot, (keys ? a.k : a.v) + at_block * F::kSlot, F::kSlot, b);
       }
     }
     ++issued;
-    islot = islot + 1 == R ? 0 : islot + 1;
   };
   if (iu < u_hi) {
     look((int)(iu - is.lo));
     if constexpr (kEarly) load_q(at);
   }
+  // While block n's keys are used, the ring holds its values and the R - 2 pieces after
+  // them; the slot of the keys takes the values of block n + R / 2 (`ahead`), that of its
+  // values the keys of the block after that.
+  static_assert(R % 2 == 1);
+  int64_t ahead;
+  {
+    ahead = advance();
 #pragma unroll 1
-  for (int i = 0; i < R; ++i) issue();
+    for (int i = 0; i + 1 < R; i += 2) {
+      issue(ahead, true, i);
+      issue(ahead, false, i + 1);
+      if (ahead != -1) ahead = advance();
+    }
+    issue(ahead, true, R - 1);
+  }
 
-  int taken = 0, slot = 0;  // halves used
+  int slot = 0;
   uint32_t phase = 0;
   bool dead = false;
   auto arrived = [&]() {
     const bool ok = tc_mbar_wait_or_abort(&bar[slot], phase, a.timeout_ns, &abort_flag);
     dead = !__all_sync(0xffffffffu, ok);
+    return !dead;
   };
-  auto release = [&]() {
+  auto release = [&](bool keys) {
     __syncwarp();  // every lane has read the slot
+    if (!keys && ahead != -1) ahead = advance();
+    issue(ahead, !keys, slot);
     ++taken;
     if (++slot == R) {
       slot = 0;
       phase ^= 1;
     }
-    issue();
   };
 
   bool first_item = true;
@@ -577,26 +616,23 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float mx = 0.f;
-        float x[DT][4];
+        // (an infinity takes the largest exponent: the row's result is NaN, or 0, with it)
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const unsigned short w = (unsigned short)(raw[n][i][e >> 1] >> (16 * (e & 1)));
-            x[i][e] = a.dtype == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
-            mx = fmaxf(mx, f8_finite_abs(x[i][e]));
-          }
+          for (int e = 0; e < 2; ++e) top = kv_max2(top, raw[n][i][e] & 0x7fff7fffu, a.dtype);
+        float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         int e = (__float_as_int(mx) >> 23) & 0xff;  // exponent field, 127 for [1, 2)
         e = e < 16 ? 16 : e;
         const float up = __int_as_float((127 + 14 + 127 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          qf[n][i][0] = kv_pack_half(x[i][0] * up, x[i][1] * up);
-          qf[n][i][1] = kv_pack_half(x[i][2] * up, x[i][3] * up);
-        }
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            qf[n][i][k] = kv_pack_half(kv_wide_lo(raw[n][i][k], a.dtype) * up, kv_wide_hi(raw[n][i][k], a.dtype) * up);
         const float f = a.scale_log2 / up;
         qs[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
         qs[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
@@ -617,8 +653,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     for (; u < seg_end; ++u) {
       const int j = (int)(u - at.lo);
       const int64_t pos0 = (int64_t)(j < at.seen.sink ? j : at.seen.from + j - at.seen.sink) * kKvBlock;
-      arrived();
-      if (dead) break;
+      if (!arrived()) break;
       const float ks = meta[warp * R + slot][0];
       const bool bad = meta_bad[warp * R + slot] != 0;  // no such block: nothing of it is seen
       const float vs = bad ? 0.f : meta[warp * R + slot][1];
@@ -642,24 +677,22 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
-      {
-        const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+      const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(kp + (4 * t) * D + 64 * q);
-            const uint4 y = *reinterpret_cast<const uint4 *>(kp + (4 * t + 2) * D + 64 * q);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        for (int t = 0; t < 4; ++t) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(kp + (4 * t) * D + 64 * q);
+          const uint4 y = *reinterpret_cast<const uint4 *>(kp + (4 * t + 2) * D + 64 * q);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t f[4] = {kv_half2_lo(xw[i]), kv_half2_lo(yw[i]), kv_half2_hi(xw[i]), kv_half2_hi(yw[i])};
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {kv_half2_lo(xw[i]), kv_half2_lo(yw[i]), kv_half2_hi(xw[i]), kv_half2_hi(yw[i])};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) kv_mma(s[n][t], f, qf[n][q * 4 + i][0], qf[n][q * 4 + i][1]);
-            }
+            for (int n = 0; n < NT; ++n) kv_mma(s[n][t], f, qf[n][q * 4 + i][0], qf[n][q * 4 + i][1]);
           }
-      }
-      release();
+        }
+      release(true);
 
       // ---- weights
       uint32_t p[NT][4][2];
@@ -711,108 +744,106 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       }
 
       // ---- sums
-      arrived();
-      if (dead) break;
-      const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
-      // channels 16 i .. + 15: V^T's registers, tile t of tokens; `keep4`: the bytes of
-      // the tokens that count
-      auto load_v = [&](int i, uint32_t (&f)[4][4], const uint32_t (*keep4)[4]) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 16 * kKvBlock);
-        const uint4 y = *reinterpret_cast<const uint4 *>(vp + (i * 16 + 8) * kKvBlock);
-        uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (keep4 != nullptr) {
-            xw[t] &= (*keep4)[t];
-            yw[t] &= (*keep4)[t];
-          }
-          f[t][0] = kv_half2_lo(xw[t]);
-          f[t][1] = kv_half2_lo(yw[t]);
-          f[t][2] = kv_half2_hi(xw[t]);
-          f[t][3] = kv_half2_hi(yw[t]);
-        }
-      };
-      auto add_v = [&](const uint32_t (*keep4)[4]) {
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          uint32_t f[4][4];
-          load_v(i, f, keep4);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
-            o[n][i][0] = fmaf(vs, d[0], o[n][i][0] * keep[n][0]);
-            o[n][i][1] = fmaf(vs, d[1], o[n][i][1] * keep[n][1]);
-            o[n][i][2] = fmaf(vs, d[2], o[n][i][2] * keep[n][0]);
-            o[n][i][3] = fmaf(vs, d[3], o[n][i][3] * keep[n][1]);
-          }
-        }
-      };
-      if (!edge) {
-        add_v(nullptr);
-      } else {
-        // Values that no query of the tile sees may be anything, NaN among it: they count
-        // as 0.  So do, to a query, those that only others see: their weights are 0.
+      // Values that no query of the tile sees may be anything, NaN among it: they count as
+      // 0.  So do, to a query, those that only others see: their weights are 0; unless
+      // they are NaN, then its product leaves them out.
+      uint32_t keep4[4] = {~0u, ~0u, ~0u, ~0u};  // the bytes that count, tile t of tokens
+      bool mixed = false;                        // some queries see what others do not
+      if (edge) {
         const int t_lo = row0 / a.group, t_hi = (row0 + (rows < NT * 8 ? rows : NT * 8) - 1) / a.group;
         uint64_t some = 0, all = ~0ull;
         for (int q = t_lo; q <= t_hi; ++q) {
           some |= mask(q);
           all &= mask(q);
         }
-        uint32_t keep4[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(some >> (16 * c + 4 * t)));
-        bool nan = false;
-        if (some != all) {  // ... unless they are NaN
-#pragma unroll 1
-          for (int i = 0; i < 2 * DT; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(vp + i * 8 * kKvBlock);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+        mixed = some != all;
+      }
+      if (!arrived()) break;
+      const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
+      // channels 16 k ..: V^T's registers, tile t of tokens
+      auto load_v = [&](int k, uint32_t (&f)[4][4]) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 16 * kKvBlock);
+        const uint4 y = *reinterpret_cast<const uint4 *>(vp + (k * 16 + 8) * kKvBlock);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) nan |= __vcmpeq4(xw[t] & keep4[t] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-          }
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t xm = xw[t] & keep4[t], ym = yw[t] & keep4[t];
+          f[t][0] = kv_half2_lo(xm);
+          f[t][1] = kv_half2_lo(ym);
+          f[t][2] = kv_half2_hi(xm);
+          f[t][3] = kv_half2_hi(ym);
         }
-        if (!__any_sync(0xffffffffu, nan)) {
-          add_v(&keep4);
-        } else {
-          // then for each query of a tile of rows the product with the values that it
-          // sees, for its rows only
+      };
+      bool nan = false;
+      if (mixed) {
+#pragma unroll 1
+        for (int k = 0; k < 2 * DT; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 8 * kKvBlock);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) nan |= __vcmpeq4(xw[t] & keep4[t] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+        }
+        nan = __any_sync(0xffffffffu, nan);
+      }
+      if (!nan) {
+#pragma unroll
+        for (int k = 0; k < DT; ++k) {
+          uint32_t f[4][4];
+          load_v(k, f);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
-            const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            float(&acc)[4] = o[n][k];
 #pragma unroll
-            for (int i = 0; i < DT; ++i)
+            for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
+            acc[0] = fmaf(vs, d[0], acc[0] * keep[n][0]);
+            acc[1] = fmaf(vs, d[1], acc[1] * keep[n][1]);
+            acc[2] = fmaf(vs, d[2], acc[2] * keep[n][0]);
+            acc[3] = fmaf(vs, d[3], acc[3] * keep[n][1]);
+          }
+        }
+      } else {
+        // for each query of a tile of rows the product with the values that it sees,
+        // for its rows only
+        const uint32_t any4[4] = {keep4[0], keep4[1], keep4[2], keep4[3]};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[n][i][e] *= keep[n][e & 1];
+        for (int n = 0; n < NT; ++n) {
+          const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
+          const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+#pragma unroll
+          for (int k = 0; k < DT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[n][e & 1];
 #pragma unroll 1
-            for (int q = r_lo / a.group; q <= r_hi / a.group; ++q) {
-              const uint64_t w = mask(q);
+          for (int t1 = r_lo / a.group; t1 <= r_hi / a.group; ++t1) {
+            const uint64_t w = mask(t1);
 #pragma unroll
-              for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(w >> (16 * c + 4 * t)));
-              const bool ra = ta == q, rb = tb == q;
+            for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(w >> (16 * c + 4 * t)));
 #pragma unroll
-              for (int i = 0; i < DT; ++i) {
-                uint32_t f[4][4];
-                load_v(i, f, &keep4);
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < DT; ++k) {
+              uint32_t f[4][4];
+              load_v(k, f);
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              float(&acc)[4] = o[n][k];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
-                if (ra) {
-                  o[n][i][0] = fmaf(vs, d[0], o[n][i][0]);
-                  o[n][i][2] = fmaf(vs, d[2], o[n][i][2]);
-                }
-                if (rb) {
-                  o[n][i][1] = fmaf(vs, d[1], o[n][i][1]);
-                  o[n][i][3] = fmaf(vs, d[3], o[n][i][3]);
-                }
+              for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
+              if (ta == t1) {
+                acc[0] = fmaf(vs, d[0], acc[0]);
+                acc[2] = fmaf(vs, d[2], acc[2]);
+              }
+              if (tb == t1) {
+                acc[1] = fmaf(vs, d[1], acc[1]);
+                acc[3] = fmaf(vs, d[3], acc[3]);
               }
             }
           }
         }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) keep4[t] = any4[t];
       }
-      release();
+      release(false);
     }
 
     if (dead) break;
