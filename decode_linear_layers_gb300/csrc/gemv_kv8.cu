@@ -61,23 +61,26 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   using F = KvForm<D>;
   a.row_tiles = (a.T * a.group + NT * 8 - 1) / (NT * 8);
   if ((int64_t)a.heads * a.row_tiles > 65535) return GEMV_ERR_UNSUPPORTED;
-  const int workers = sms * F::kWarps;  // one CTA per SM
+  const int items = a.heads * a.row_tiles;
+  const int64_t parts = (int64_t)sms * F::kWarps * 2 * kv_part<D, NT>() * 4;  // one CTA per SM
   void *ws = nullptr;
-  cudaError_t e = workspace(&ws, (size_t)(workers * 2 * kv_part<D, NT>() * 4), s);
+  cudaError_t e = workspace(&ws, (size_t)(parts + (int64_t)a.S * items * 16), s);
   if (e != cudaSuccess) return fail((int)e);
   a.ws = static_cast<float *>(ws);
+  a.parts = reinterpret_cast<int4 *>(static_cast<char *>(ws) + parts);
   const int pdl = launch_overlap();
   e = allow_smem(k_kv8_attention<D, NT>, F::kSmem);
   if (e == cudaSuccess) e = launch_k(k_kv8_attention<D, NT>, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
   if (e == cudaSuccess) {
-    const int items = a.heads * a.row_tiles;
-    auto join = [&](auto kern, int pieces) {
-      return launch_k(kern, dim3((unsigned)a.S, (unsigned)items, (unsigned)pieces), dim3(kKvJoinThreads), 0, s, pdl, a, workers);
-    };
-    // fewer items than SMs may be in many parts each: a CTA for each of their rows
     const int rows = a.T * a.group < NT * 8 ? a.T * a.group : NT * 8;
-    e = (int64_t)a.S * items < sms ? join(k_kv8_join<D, NT, true>, rows)
-                                   : join(k_kv8_join<D, NT, false>, (rows * D + 4 * kKvJoinThreads - 1) / (4 * kKvJoinThreads));
+    auto join = [&](auto kern, int along) {
+      return launch_k(kern, dim3((unsigned)a.S, (unsigned)items, (unsigned)((rows * D / 4 + along - 1) / along)),
+                      dim3(kKvJoinThreads), 0, s, pdl, a);
+    };
+    // eight warps for the parts while that makes no more CTAs than the SMs hold
+    const int64_t threads = (int64_t)a.S * items * rows * (D / 4);
+    e = threads * 8 / kKvJoinThreads <= (int64_t)sms * 8 ? join(k_kv8_join<D, NT, 8>, kKvJoinThreads / 8)
+                                                         : join(k_kv8_join<D, NT, 1>, kKvJoinThreads);
   }
   const cudaError_t e2 = cudaFreeAsync(ws, s);
   if (e == cudaSuccess) e = e2;

@@ -32,7 +32,8 @@ struct KvArgs {
   const void *q = nullptr;
   void *out = nullptr;
   float *lse = nullptr;
-  float *ws = nullptr;
+  float *ws = nullptr;    // partial results: two for each warp
+  int4 *parts = nullptr;  // of each item: the first warp with a part, parts, which of that warp's
   int64_t q_stride = 0;
   int64_t timeout_ns = 0;
   int group = 0, window = 0, sinks = 0, row_tiles = 0, test_stall = 0;
@@ -850,6 +851,9 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
 
     // ---- the item's output, or this range's part of it
     const bool whole = seg == at.lo && seg_end == at.hi;
+    if (seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
+      a.parts[(int64_t)at.s * items + at.item] =
+          make_int4((int)worker, (int)(shares.owner(at.hi - 1) - worker) + 1, first_item ? 0 : 1, 0);
     float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -907,108 +911,75 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
 
 // Items that several warps of k_kv8_attention share: their partial results, merged in the
 // order of the blocks; and the outputs of sequences without tokens: zeros.  A thread adds
-// up four channels of a row.  Where items are few, and each may be in a hundred parts
-// (kByRow), a CTA has one row, and its warps share the parts; else it has rows for all its
-// threads, and each takes all of an item's few parts.
-// grid (S, items, pieces); workers: the attention kernel's warps.
+// up four channels of a row, eight parts on their way at a time; kGroups warps share the
+// parts of the same channels, where there are few items, each perhaps in a hundred parts.
+// grid (S, items, pieces of a tile's rows).
 constexpr int kKvJoinThreads = 256;
-template <int D, int NT, bool kByRow>
-__global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a, int workers) {
-  constexpr int kAlong = kByRow ? D / 4 : kKvJoinThreads;       // threads along the channels
-  constexpr int kGroups = kKvJoinThreads / kAlong;              // that share the parts
-  constexpr int kStep = kByRow ? 1024 : 1;
-  __shared__ float factor[kStep];
-  __shared__ float4 sums[kByRow ? kGroups : 1][kByRow ? kAlong : 1];
-  __shared__ float red[2][kKvJoinThreads / 32];
-  pdl_trigger();
-  const int s = blockIdx.x, item = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  const int items = a.heads * a.row_tiles;
-  // (lens is older than the attention kernel, which let this one start after its own wait)
-  const int64_t total = kv_before(a, a.S, lane) * items, before = kv_before(a, s, lane) * items;
-  const KvSeen seen = kv_seen(a, s);
-  const int64_t u0 = before + (int64_t)item * kv_places(seen) + kKvItemCost;  // the item's first block
-  int64_t w0 = 0, skip = 0;
-  int n = 0;  // parts
-  if (seen.count > 0) {
-    const KvShares shares(total, workers);
-    w0 = shares.owner(u0);
-    n = (int)(shares.owner(u0 + seen.count - 1) - w0) + 1;
-    // the first warp's range may hold blocks of an item before: then this is its second part
-    skip = shares.first(w0) < u0 - kKvItemCost ? kv_part<D, NT>() : 0;
+struct KvSum {  // a row's (part of a) softmax: largest logit, sum of weights, weighted values
+  float m = -INFINITY, den = 0.f;
+  float4 v = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float fm, float fden, const float4 &f) {
+    const float big = fmaxf(m, fm), z = big == -INFINITY ? 0.f : big;
+    const float x = kv_exp2(m - z), y = kv_exp2(fm - z);
+    m = big;
+    den = den * x + fden * y;
+    v.x = v.x * x + f.x * y;
+    v.y = v.y * x + f.y * y;
+    v.z = v.z * x + f.z * y;
+    v.w = v.w * x + f.w * y;
   }
+};
+template <int D, int NT, int kGroups>
+__global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a) {
+  constexpr int kAlong = kKvJoinThreads / kGroups;  // threads along the channels
+  constexpr int64_t kPart = kv_part<D, NT>();
+  __shared__ KvSum sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kAlong : 1];
+  pdl_trigger();
+  const int s = blockIdx.x, item = blockIdx.y, items = a.heads * a.row_tiles;
+  // (lens is older than the attention kernel, which let this one start after its own wait)
+  const int count = kv_seen(a, s).count;
   pdl_wait();  // by every CTA: the next kernel counts on it
-  if (n == 1) return;  // one warp had the whole item and wrote it
+  const int4 of = count > 0 ? __ldcg(&a.parts[(int64_t)s * items + item]) : make_int4(0, 0, 0, 0);
+  if (of.y == 1) return;  // one warp had the whole item and wrote it
   const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
   const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
-  const float *const p = a.ws + w0 * 2 * kv_part<D, NT>();
-  auto part = [&](int i) { return p + (i == 0 ? skip : i * 2 * kv_part<D, NT>()); };
-  const int along = tid % kAlong, grp = tid / kAlong;
+  const int along = threadIdx.x % kAlong, grp = threadIdx.x / kAlong;
   const int e = (blockIdx.z * kAlong + along) * 4, r = e / D, d = e - r * D;
-  if (r >= rows) return;  // (by row: all threads alike)
-  float mx = -INFINITY, den = 0.f;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float *q, float f) {
-    const float4 v = *reinterpret_cast<const float4 *>(q + e);
-    sum.x = fmaf(f, v.x, sum.x);
-    sum.y = fmaf(f, v.y, sum.y);
-    sum.z = fmaf(f, v.z, sum.z);
-    sum.w = fmaf(f, v.w, sum.w);
-  };
-  if constexpr (!kByRow) {
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) mx = fmaxf(mx, part(i)[NT * 8 * D + r]);
-    const float z = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float f = kv_exp2(part(i)[NT * 8 * D + r] - z);
-      den = fmaf(f, part(i)[NT * 8 * (D + 1) + r], den);
-      add(part(i), f);
-    }
-  } else {
-    // the row's largest logit over all parts, then each part's factor, 1024 parts at a time
-    for (int i = tid; i < n; i += kKvJoinThreads) mx = fmaxf(mx, part(i)[NT * 8 * D + r]);
+  KvSum sum;
+  if (r < rows) {
+    const float *const p = a.ws + (int64_t)of.x * 2 * kPart;
+    for (int i0 = grp; i0 < of.y; i0 += 8 * kGroups) {
+      float m[8], den[8];
+      float4 v[8];
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    if (lane == 0) red[0][tid >> 5] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kKvJoinThreads / 32; ++k) mx = fmaxf(mx, red[0][k]);
-    const float z = mx == -INFINITY ? 0.f : mx;
-    for (int i0 = 0; i0 < n; i0 += kStep) {
-      const int top = n - i0 < kStep ? n - i0 : kStep;
-      for (int i = tid; i < top; i += kKvJoinThreads) {
-        const float f = kv_exp2(part(i0 + i)[NT * 8 * D + r] - z);
-        factor[i] = f;
-        den = fmaf(f, part(i0 + i)[NT * 8 * (D + 1) + r], den);
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kGroups;
+        if (i < of.y) {
+          const float *q = p + (i == 0 ? of.z * kPart : i * 2 * kPart);
+          m[k] = __ldcg(q + NT * 8 * D + r);
+          den[k] = __ldcg(q + NT * 8 * (D + 1) + r);
+          v[k] = __ldcg(reinterpret_cast<const float4 *>(q + e));
+        }
       }
-      __syncthreads();
-      if (grp < kGroups) {
-#pragma unroll 10
-        for (int i = grp; i < top; i += kGroups) add(part(i0 + i), factor[i]);
-      }
-      __syncthreads();
-    }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) den += __shfl_xor_sync(0xffffffffu, den, k);
-    if (lane == 0) red[1][tid >> 5] = den;
-    if (grp < kGroups) sums[grp][along] = sum;
-    __syncthreads();
-    if (grp > 0) return;
-    den = 0.f;
-#pragma unroll
-    for (int k = 0; k < kKvJoinThreads / 32; ++k) den += red[1][k];
-#pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 v = sums[k][along];
-      sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kGroups < of.y) sum.add(m[k], den[k], v[k]);
     }
   }
+  if constexpr (kGroups > 1) {
+    sums[grp][along] = sum;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) sum.add(sums[k][along].m, sums[k][along].den, sums[k][along].v);
+  }
+  if (r >= rows) return;
   const int64_t at_row = kv_out_row(a, s, h, row0 + r);
   unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
-  const float v[4] = {sum.x, sum.y, sum.z, sum.w}, inv = den == 0.f ? 0.f : 1.f / den;
+  const float inv = sum.den == 0.f ? 0.f : 1.f / sum.den, v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
-  if (d == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(mx, den);
+  if (d == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(sum.m, sum.den);
 }
 
 }  // namespace gemv
