@@ -106,11 +106,13 @@ gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, 
   if (M == 0 || B == 0) return GEMV_SUCCESS;
   const int sy = y_dtype == GEMV_DTYPE_F32 ? 4 : 2;
   const int64_t G = (K + GEMV_F8_GROUP - 1) / GEMV_F8_GROUP;
-  int64_t mk, bk, bm, yb, bg, t;
-  // sizes and row numbers are 32-bit coordinates of the copies
-  if (M > 0x7fffff00 || K > 0x7fffff00 || B > 0x7fffff00 || !mul_ok(M, K, &mk) || !mul_ok(B, K, &bk) || !mul_ok(B, M, &bm) ||
-      !mul_ok(bm, sy, &yb) || !mul_ok(B, G * 4, &bg) || !mul_ok((M / 128 + 1) * ((int64_t)B / 128 + 1), G, &t) ||
-      t > ((int64_t)1 << 50))
+  int64_t mk, bk, bm, yb, bg;
+  // row and column numbers are 32-bit coordinates of the copies; tiles, and the k-blocks of
+  // one CTA, are counted in 32 bits
+  if (M > 0x7fffff00 || B > 0x7fffff00 || K > ((int64_t)1 << 29)) return GEMV_ERR_INVALID_VALUE;
+  const int64_t tiles = (M / 128 + 1) * ((int64_t)B / 128 + 1);
+  if (tiles > ((int64_t)1 << 30) || tiles * G > ((int64_t)1 << 37) || !mul_ok(M, K, &mk) || !mul_ok(B, K, &bk) ||
+      !mul_ok(B, M, &bm) || !mul_ok(bm, sy, &yb) || !mul_ok(B, G * 4, &bg))
     return GEMV_ERR_INVALID_VALUE;
   const int64_t ag = (M + GEMV_F8_GROUP - 1) / GEMV_F8_GROUP * G * 4;
   if (y == nullptr || (K > 0 && (A == nullptr || a_scale == nullptr || x == nullptr || x_scale == nullptr)))

@@ -12,13 +12,14 @@
 // products fill the other accumulators.
 #pragma once
 
+#include "../../include/gemv.h"
 #include "gemv_tc.cuh"
 
 namespace gemv {
 
 constexpr int kF8Group = 128;    // columns per scale, and per k-block: one 128-byte swizzle atom
 constexpr int kF8Rows = 128;     // rows of a tile: the MMA's M
-constexpr int kF8RoleThreads = 128;  // warps 0 (copies) and 1 (MMAs), two idle
+constexpr int kF8RoleThreads = 128;  // warps 0 (copies), 1 (MMAs) and 2 (scales), one idle
 constexpr int kF8MaxStages = 12;
 constexpr int kF8TileM = 256;    // weight rows of a tile of the prompt form
 
@@ -36,6 +37,25 @@ struct F8Args {
   int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
   int y_dtype = 0, stages = 0, test_stall = 0;
 };
+
+// A bounded wait of one of several cooperating threads: false after timeout_ns, or once
+// another has set *abort.  The timer and the flag are looked at after every 256 failed
+// tries only.
+__device__ __forceinline__ bool f8_wait(uint64_t *b, uint32_t parity, int64_t timeout_ns, volatile int *abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (tc_mbar_try_wait(b, parity)) return true;
+    if ((i & 255) == 0) {
+      if (*abort) return false;
+      const uint64_t t = tc_global_ns();
+      if (t0 == 0) t0 = t;
+      if ((int64_t)(t - t0) > timeout_ns) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
 
 // ------------------------------------------------------------------ output types
 __device__ __forceinline__ unsigned short f8_round16(float v, int dt) {
@@ -60,28 +80,26 @@ __device__ __forceinline__ void f8_store(const F8Args &a, int64_t i, float v) {
 // tile's k-blocks, so it meets two tiles at most.  The other tiles, a multiple of the
 // CTAs, go round whole.  Each role of a CTA walks the same segments.
 struct F8Seg {
-  int64_t tile;
-  int k0, k1;
+  int tile, k0, k1;
   int slot;  // which of the CTA's two partial sums it fills; -1: the whole tile
 };
-struct F8Walk {
-  int64_t lo, hi, next_tile, tiles;
-  int groups, step, part;
+struct F8Walk {  // (the host limits tiles, and the k-blocks of a CTA, to 32 bits)
+  uint32_t lo, hi;
+  int next_tile, tiles, groups, part;
   __device__ F8Walk(const F8Args &a) {
     const int64_t R = a.shared * a.groups, w = blockIdx.x;
-    lo = w < a.sharers ? w * R / a.sharers : 0;
-    hi = w < a.sharers ? (w + 1) * R / a.sharers : 0;
-    next_tile = a.shared + w;
-    tiles = a.tiles;
+    lo = w < a.sharers ? (uint32_t)(w * R / a.sharers) : 0u;
+    hi = w < a.sharers ? (uint32_t)((w + 1) * R / a.sharers) : 0u;
+    next_tile = (int)(a.shared + w);
+    tiles = (int)a.tiles;
     groups = a.groups;
-    step = (int)gridDim.x;
     part = 0;
   }
   __device__ bool next(F8Seg &s) {
     if (lo < hi) {
-      s.tile = lo / groups;
-      s.k0 = (int)(lo - s.tile * groups);
-      s.k1 = (int)(hi - lo < groups - s.k0 ? s.k0 + (hi - lo) : groups);
+      s.tile = (int)(lo / groups);
+      s.k0 = (int)(lo - (uint32_t)s.tile * groups);
+      s.k1 = hi - lo < (uint32_t)(groups - s.k0) ? s.k0 + (int)(hi - lo) : groups;
       s.slot = s.k0 == 0 && s.k1 == groups ? -1 : part;
       ++part;
       lo += s.k1 - s.k0;
@@ -92,7 +110,7 @@ struct F8Walk {
     s.k0 = 0;
     s.k1 = groups;
     s.slot = -1;
-    next_tile += step;
+    next_tile += gridDim.x;
     return true;
   }
 };
@@ -101,14 +119,12 @@ __host__ __device__ inline int64_t f8_owner(int64_t u, int64_t R, int64_t W) { r
 
 // Tile -> (tile of weight rows, tile of vectors).  Whole bands of 16 weight tiles, their
 // weights read once into L2, meet every tile of vectors before the next band.
-__device__ __forceinline__ void f8_tile(const F8Args &a, int64_t t, int &im, int &in) {
+__device__ __forceinline__ void f8_tile(const F8Args &a, int t, int &im, int &in) {
   constexpr int kBand = 16;
-  const int64_t per = (int64_t)kBand * a.tn;
-  const int64_t band = t / per;
-  const int64_t r = t - band * per;
-  const int w = (int)(a.tm - band * kBand < kBand ? a.tm - band * kBand : kBand);
-  in = (int)(r / w);
-  im = (int)(band * kBand + (r - (int64_t)in * w));
+  const int band = t / (kBand * a.tn), r = t - band * (kBand * a.tn);
+  const int w = a.tm - band * kBand < kBand ? a.tm - band * kBand : kBand;
+  in = r / w;
+  im = band * kBand + (r - in * w);
 }
 
 // ------------------------------------------------------------------ instructions
@@ -168,6 +184,33 @@ __device__ __forceinline__ void f8_ld_wait(uint32_t (&r)[C]) {
   }
 }
 
+// One lane of a converged warp.  The copies and the MMAs are issued by a whole warp that
+// waits together, with only these instructions under its predicate: their operands stay
+// in the warp's uniform registers (issued from a branch of one lane, the four MMAs and
+// two commits of a k-block took 430 to 640 cycles, more than its product).
+__device__ __forceinline__ bool f8_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// Four bytes by an asynchronous copy, zeros unless `has`; f8_copy4_arrive: the mbarrier
+// gets one arrival once this thread's copies have come.
+__device__ __forceinline__ void f8_copy4(void *dst, const void *src, bool has) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc_smem_u32(dst)), "l"(src), "r"(has ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void f8_copy4_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void f8_copy4_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Two values of a 16-bit output type, `a` in the low half.
+__device__ __forceinline__ uint32_t f8_pack16(float a, float b, int dt) {
+  uint32_t r;
+  if (dt == GEMV_DTYPE_F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
 // (s0, s1) += (f0, f1) * (v0, v1), one packed instruction.
 __device__ __forceinline__ void f8_fma2(float &s0, float &s1, float f0, float f1, uint32_t v0, uint32_t v1) {
   asm("{\n\t.reg .b64 s, f, v;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
@@ -190,9 +233,12 @@ struct F8Form {
   static constexpr int kAcc = N == 256 ? 2 : 4;                              // accumulators in tensor memory
   static constexpr int kTmemCols = kAcc * N < 32 ? 32 : kAcc * N;
   static constexpr int kStage = (kF8Rows + N) * kF8Group;                    // bytes
-  // after the ring: each scaling warp's output staging (prompts) or factors (two sets)
-  static constexpr int kWarpBytes = kPrompt ? 32 * 128 : 2 * N * 4;
-  static constexpr int kTail = 4 * kGroupsOfWarps * kWarpBytes;
+  // after the ring: the scales of kScales k-blocks, and (prompts) each scaling warp's
+  // output staging
+  static constexpr int kScales = 8;
+  static constexpr int kScaleFloats = (kPrompt ? kF8Rows : N) + 4;  // the vectors', then the weight blocks'
+  static constexpr int kWarpBytes = kPrompt ? 32 * 64 : 0;
+  static constexpr int kTail = kScales * kScaleFloats * 4 + 4 * kGroupsOfWarps * kWarpBytes;
   static constexpr int kStages = (226 * 1024 - kTail) / kStage < kF8MaxStages ? (226 * 1024 - kTail) / kStage : kF8MaxStages;
   static constexpr int kSmem = 1024 + kStages * kStage + kTail;
   static constexpr int64_t kPartial = (int64_t)kF8Rows * N;                  // floats of a partial sum
@@ -206,10 +252,10 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   using F = F8Form<N, kPrompt>;
   constexpr int S = F::kStages, NACC = F::kAcc, COLS = F::kCols;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC];
+  __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC], facf[F::kScales], face[F::kScales];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ long long sh_loaded, sh_consumed, sh_committed;  // for the drain after an abort
+  __shared__ int sh_loaded, sh_consumed, sh_committed;  // for the drain after an abort
   pdl_trigger();
   pdl_wait();  // every read (TMA included) after the kernel before has finished
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -230,6 +276,10 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       tc_mbar_init(&accf[b], 1);
       tc_mbar_init(&acce[b], 4 * F::kGroupsOfWarps);
     }
+    for (int b = 0; b < F::kScales; ++b) {
+      tc_mbar_init(&facf[b], 32);
+      tc_mbar_init(&face[b], 4 * F::kGroupsOfWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
     sh_loaded = sh_consumed = sh_committed = -1;
@@ -241,66 +291,66 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   const uint32_t tmem = tmem_slot;
   volatile int *abort = &abort_flag;
   const int G = a.groups;
+  float *scales = reinterpret_cast<float *>(smem + (size_t)S * F::kStage);
 
   if (warp < 4) {
-    if constexpr (kPrompt) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0 && lane == 0) {  // copies
-      int64_t i = 0;
-      int s = 0;
+    if constexpr (kPrompt) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    F8Walk walk(a);
+    F8Seg g;
+    bool ok = true;
+    if (warp == 0) {  // copies
+      int i = 0, s = 0;
       uint32_t ph = 1;  // the ring starts empty
-      F8Walk walk(a);
-      F8Seg g;
-      bool ok = true;
       while (ok && walk.next(g)) {
         int im, in;
         f8_tile(a, g.tile, im, in);
         const int32_t p0 = kPrompt ? in * kF8Rows : im * kF8Rows, q0 = kPrompt ? im * N : in * N;
-        for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
-          if (i >= S && !tc_mbar_wait_or_abort(&empty[s], ph, a.timeout_ns, abort)) {
-            ok = false;
-            break;
-          }
+        for (int kb = g.k0; kb < g.k1; ++kb) {
+          ok = i < S || f8_wait(&empty[s], ph, a.timeout_ns, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           unsigned char *st = smem + (size_t)s * F::kStage;
-          tc_mbar_arrive_expect_tx(&full[s], F::kStage);
-          tc_tma_2d(st, &map_p, kb * kF8Group, p0, &full[s]);
-          tc_tma_2d(st + kF8Rows * kF8Group, &map_q, kb * kF8Group, q0, &full[s]);
-          sh_loaded = i;
+          if (f8_elect()) {
+            tc_mbar_arrive_expect_tx(&full[s], F::kStage);
+            tc_tma_2d(st, &map_p, kb * kF8Group, p0, &full[s]);
+            tc_tma_2d(st + kF8Rows * kF8Group, &map_q, kb * kF8Group, q0, &full[s]);
+          }
+          ++i;
           if (++s == S) {
             s = 0;
             ph ^= 1;
           }
         }
       }
-    } else if (warp == 1 && lane == 0) {  // MMAs
+      if (lane == 0) sh_loaded = i - 1;
+    } else if (warp == 1) {  // MMAs
       const uint32_t idesc = f8_idesc(N);
-      int64_t i = 0, total = 0;
-      if (a.test_stall) {  // test: the last k-block of the first CTA never completes
+      const uint64_t dp0 = tc_smem_desc(tc_smem_u32(smem)), dq0 = dp0 + (kF8Rows * kF8Group >> 4);
+      int i = 0, last = -1, consumed = -1;
+      if (a.test_stall && blockIdx.x == 0) {  // test: the last k-block of the first CTA never completes
         F8Walk w(a);
-        F8Seg g;
-        while (w.next(g)) total += g.k1 - g.k0;
+        while (w.next(g)) last += g.k1 - g.k0;
       }
       int s = 0, c = 0;
       uint32_t ph = 0, cph = 1;
-      F8Walk walk(a);
-      F8Seg g;
-      bool ok = true;
       while (ok && walk.next(g)) {
-        for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
-          if ((i >= NACC && !tc_mbar_wait_or_abort(&acce[c], cph, a.timeout_ns, abort)) ||
-              !tc_mbar_wait_or_abort(&full[s], ph, a.timeout_ns, abort)) {
-            ok = false;
-            break;
-          }
-          sh_consumed = i;
+        for (int kb = g.k0; kb < g.k1; ++kb) {
+          ok = (i < NACC || f8_wait(&acce[c], cph, a.timeout_ns, abort)) && f8_wait(&full[s], ph, a.timeout_ns, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          consumed = i;
+          if (a.test_stall && i == last) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (a.test_stall && blockIdx.x == 0 && i == total - 1) break;
-          const uint32_t sp = tc_smem_u32(smem + (size_t)s * F::kStage), sq = sp + kF8Rows * kF8Group;
+          // (a descriptor's address counts 16 bytes, 32 columns are two of them)
+          const uint64_t dp = dp0 + (uint64_t)(s * (F::kStage >> 4)), dq = dq0 + (uint64_t)(s * (F::kStage >> 4));
+          if (f8_elect()) {
 #pragma unroll
-          for (int kk = 0; kk < kF8Group / 32; ++kk)
-            f8_mma(tmem + (uint32_t)(c * N), tc_smem_desc(sp + kk * 32), tc_smem_desc(sq + kk * 32), idesc, kk > 0);
-          tc_commit(&empty[s]);
-          tc_commit(&accf[c]);
-          sh_committed = i;
+            for (int kk = 0; kk < kF8Group / 32; ++kk)
+              f8_mma(tmem + (uint32_t)(c * N), dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+            tc_commit(&empty[s]);
+            tc_commit(&accf[c]);
+          }
+          ++i;
           if (++s == S) {
             s = 0;
             ph ^= 1;
@@ -311,77 +361,77 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           }
         }
       }
+      if (lane == 0) {
+        sh_consumed = consumed;
+        sh_committed = i - 1;
+      }
+    } else if (warp == 2) {  // scales, as far ahead of the products as their slots go
+      constexpr int NV = kPrompt ? kF8Rows / 32 : (N + 31) / 32;
+      int i = 0, t = 0;
+      uint32_t ph = 1;
+      while (ok && walk.next(g)) {
+        int im, in;
+        f8_tile(a, g.tile, im, in);
+        const int64_t b0 = kPrompt ? (int64_t)in * kF8Rows : 0;     // the first vector
+        const int64_t mb = (kPrompt ? (int64_t)im * 2 : im) + lane;  // lane 0 (and 1): block of weight rows
+        const bool va = lane < (kPrompt ? 2 : 1) && mb * kF8Group < a.M;
+        const float *sa = a.a_scale + (va ? mb : 0) * G, *sx[NV];
+        bool vx[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int64_t b = b0 + lane + 32 * v;
+          vx[v] = b < a.B;
+          sx[v] = a.x_scale + (vx[v] ? b : 0) * G;
+        }
+        for (int kb = g.k0; kb < g.k1; ++kb) {
+          ok = i < F::kScales || f8_wait(&face[t], ph, a.timeout_ns, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float *w = scales + t * F::kScaleFloats;
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+            if (kPrompt || lane + 32 * v < N) f8_copy4(w + lane + 32 * v, sx[v] + kb, vx[v]);
+          if (lane < 2) f8_copy4(w + F::kScaleFloats - 4 + lane, sa + kb, va);
+          f8_copy4_arrive(&facf[t]);
+          ++i;
+          if (++t == F::kScales) {
+            t = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      f8_copy4_drain();  // nothing in flight when the CTA exits
     }
   } else {
-    if constexpr (kPrompt) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (kPrompt) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int wq = warp & 3, wg = (warp >> 2) - 1;     // tensor-memory lanes 32 wq .. + 31
     const int row = wq * 32 + lane;                    // of the tile
     const int col0 = wg * COLS;
-    unsigned char *mine = smem + (size_t)S * F::kStage + (size_t)(warp - 4) * F::kWarpBytes;
-    constexpr int CH = COLS < 32 ? COLS : 32;
-    int c = 0;
-    uint32_t cph = 0;
+    unsigned char *mine = smem + (size_t)S * F::kStage + F::kScales * F::kScaleFloats * 4 + (size_t)(warp - 4) * F::kWarpBytes;
+    constexpr int CH = COLS < 32 || kPrompt ? 16 : 32, P = COLS / CH, U = P < 2 ? 1 : 2;
+    int c = 0, t = 0;
+    uint32_t cph = 0, tph = 0;
     F8Walk walk(a);
     F8Seg g;
     bool ok = true;
     while (ok && walk.next(g)) {
       int im, in;
       f8_tile(a, g.tile, im, in);
-      __syncwarp();  // the factors of the segment before are read before they are overwritten
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      // the factors' sources: this thread's vector and column block (prompts), or the
-      // row block and the vectors lane, lane + 32, ...
-      constexpr int NV = kPrompt ? 1 : (N + 31) / 32;
-      const float *sa, *sx[NV];
-      bool vx[NV], va = true;
-      if constexpr (kPrompt) {
-        const int64_t b = (int64_t)in * kF8Rows + row, mb = (int64_t)im * (N / kF8Group) + wg;
-        vx[0] = b < a.B;
-        sx[0] = a.x_scale + (vx[0] ? b : 0) * G;
-        va = mb * kF8Group < a.M;
-        sa = a.a_scale + (va ? mb : 0) * G;
-      } else {
-        sa = a.a_scale + (int64_t)im * G;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int b = lane + 32 * v;
-          vx[v] = b < a.B && b < N;
-          sx[v] = a.x_scale + (int64_t)(vx[v] ? b : 0) * G;
-        }
-      }
-      float fa = va ? __ldg(sa + g.k0) : 0.f, fx[NV];
-#pragma unroll
-      for (int v = 0; v < NV; ++v) fx[v] = vx[v] ? __ldg(sx[v] + g.k0) : 0.f;
       for (int kb = g.k0; kb < g.k1; ++kb) {
-        float f = 0.f;
-        const float *fs = nullptr;
-        if constexpr (kPrompt) {
-          f = fa * fx[0];
-        } else {
-          float *w = reinterpret_cast<float *>(mine) + (kb & 1) * N;
-#pragma unroll
-          for (int v = 0; v < NV; ++v)
-            if (lane + 32 * v < N) w[lane + 32 * v] = fa * fx[v];
-          __syncwarp();
-          fs = w;
-        }
-        if (kb + 1 < g.k1) {  // the next k-block's factors, in flight during this one
-          fa = va ? __ldg(sa + kb + 1) : 0.f;
-#pragma unroll
-          for (int v = 0; v < NV; ++v) fx[v] = vx[v] ? __ldg(sx[v] + kb + 1) : 0.f;
-        }
-        ok = tc_mbar_wait_or_abort(&accf[c], cph, a.timeout_ns, abort);
+        ok = f8_wait(&facf[t], tph, a.timeout_ns, abort) && f8_wait(&accf[c], cph, a.timeout_ns, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * N + col0);
         // two pieces of CH columns on their way at a time
-        constexpr int P = COLS / CH, U = P < 2 ? 1 : 2;
         uint32_t r[U][CH];
 #pragma unroll
         for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
+        const float *fs = scales + t * F::kScaleFloats;
+        const float fa = fs[F::kScaleFloats - 4 + wg], f = kPrompt ? fs[row] * fa : 0.f;
 #pragma unroll
         for (int h0 = 0; h0 < P; h0 += U) {
 #pragma unroll
@@ -393,20 +443,29 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           }
 #pragma unroll
           for (int h = 0; h < U; ++h) {
-            float *s = acc + (h0 + h) * CH;
+            float *sum = acc + (h0 + h) * CH;
 #pragma unroll
             for (int j = 0; j < CH; j += 4) {
               float4 q = make_float4(f, f, f, f);
-              if constexpr (!kPrompt) q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
-              f8_fma2(s[j], s[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
-              f8_fma2(s[j + 2], s[j + 3], q.z, q.w, r[h][j + 2], r[h][j + 3]);
+              if constexpr (!kPrompt) {
+                q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
+                q = make_float4(q.x * fa, q.y * fa, q.z * fa, q.w * fa);
+              }
+              f8_fma2(sum[j], sum[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
+              f8_fma2(sum[j + 2], sum[j + 3], q.z, q.w, r[h][j + 2], r[h][j + 3]);
             }
             if (h0 + U + h < P) f8_ld<CH>(at + (h0 + U + h) * CH, r[h]);
           }
         }
+        __syncwarp();  // every lane has read the scales
+        if (lane == 0) tc_mbar_arrive(&face[t]);
         if (++c == NACC) {
           c = 0;
           cph ^= 1;
+        }
+        if (++t == F::kScales) {
+          t = 0;
+          tph ^= 1;
         }
       }
       if (!ok) break;
@@ -434,45 +493,35 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
             if (j < a.B) f8_store(a, (int64_t)j * a.M + m, acc[j] + bias);
         }
       } else {
-        // the warp's 32 rows leave through its staging buffer, 128 bytes of each at a
-        // time (16-byte pieces, their order rotated by the row: free of bank conflicts),
-        // so that eight lanes store 128 consecutive bytes of y
+        // the warp's 32 rows leave through its staging buffer, 64 bytes of each at a time
+        // (16-byte pieces, their order rotated by the row: free of bank conflicts), so that
+        // four lanes store 64 consecutive bytes of y
         const int64_t b0 = (int64_t)in * kF8Rows + wq * 32, m0 = (int64_t)im * N + col0;
         const bool f32 = a.y_dtype == GEMV_DTYPE_F32;
         const int esz = f32 ? 4 : 2;
         const bool vec = (a.M * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-        if (a.bias != nullptr) {
+        if (a.bias != nullptr) {  // through the staging buffer, four columns a lane
+          float *sb = reinterpret_cast<float *>(mine);
 #pragma unroll
-          for (int j = 0; j < COLS; ++j) acc[j] += m0 + j < a.M ? f8_bias(a, m0 + j) : 0.f;
-        }
+          for (int j = 0; j < COLS; j += 32) sb[j + lane] = m0 + j + lane < a.M ? f8_bias(a, m0 + j + lane) : 0.f;
+          __syncwarp();
 #pragma unroll
-        for (int h = 0; h < COLS / 32; ++h) {
-          // 32 columns: 128 bytes of fp32, or half of the 64 columns of a 16-bit pass
-          if (f32) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4 *>(mine + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                  make_float4(acc[h * 32 + q * 4], acc[h * 32 + q * 4 + 1], acc[h * 32 + q * 4 + 2], acc[h * 32 + q * 4 + 3]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[e] = (uint32_t)f8_round16(acc[h * 32 + q * 8 + 2 * e], a.y_dtype) |
-                       ((uint32_t)f8_round16(acc[h * 32 + q * 8 + 2 * e + 1], a.y_dtype) << 16);
-              *reinterpret_cast<uint4 *>(mine + lane * 128 + ((((h & 1) * 4 + q) ^ (lane & 7)) * 16)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            if ((h & 1) == 0) continue;
+          for (int j = 0; j < COLS; j += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(sb + j);
+            acc[j] += q.x;
+            acc[j + 1] += q.y;
+            acc[j + 2] += q.z;
+            acc[j + 3] += q.w;
           }
           __syncwarp();
-          const int64_t c0 = m0 + (f32 ? h * 32 : (h - 1) * 32);   // first column of the pass
-          const int per = f32 ? 4 : 8;                             // columns of a piece
+        }
+        // columns c0 .. of the tile's COLS, `per` to a piece, lie staged: store them
+        auto pass = [&](int64_t c0, int per) {
+          __syncwarp();
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int rr = it * 4 + (lane >> 3), pc = lane & 7;
-            const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((pc ^ (rr & 7)) * 16));
+          for (int it = 0; it < 4; ++it) {
+            const int rr = it * 8 + (lane >> 2), pc = lane & 3;
+            const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((pc ^ ((rr >> 1) & 3)) * 16));
             const int64_t b = b0 + rr, m = c0 + pc * per;
             if (b >= a.B || m >= a.M) continue;
             char *dst = reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz;
@@ -491,6 +540,30 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
             }
           }
           __syncwarp();  // read before the next pass overwrites the buffer
+        };
+        unsigned char *const my_row = mine + lane * 64;
+        const int turn = (lane >> 1) & 3;
+        if (f32) {
+#pragma unroll
+          for (int h = 0; h < COLS; h += 16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<float4 *>(my_row + ((q ^ turn) * 16)) =
+                  make_float4(acc[h + q * 4], acc[h + q * 4 + 1], acc[h + q * 4 + 2], acc[h + q * 4 + 3]);
+            pass(m0 + h, 4);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < COLS; h += 32) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float *v = acc + h + q * 8;
+              *reinterpret_cast<uint4 *>(my_row + ((q ^ turn) * 16)) =
+                  make_uint4(f8_pack16(v[0], v[1], a.y_dtype), f8_pack16(v[2], v[3], a.y_dtype),
+                             f8_pack16(v[4], v[5], a.y_dtype), f8_pack16(v[6], v[7], a.y_dtype));
+            }
+            pass(m0 + h, 8);
+          }
         }
       }
     }
@@ -504,9 +577,9 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     // not waited for
     if (tid == 0) {
       if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
-      const int64_t committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
+      const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
       bool drained = committed < 0 || tc_mbar_wait(&empty[committed % S], (uint32_t)((committed / S) & 1), a.timeout_ns);
-      for (int64_t t = consumed + 1; t <= loaded && drained; ++t)
+      for (int t = consumed + 1; t <= loaded && drained; ++t)
         drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
       if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
     }

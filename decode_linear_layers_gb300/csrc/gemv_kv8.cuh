@@ -321,13 +321,6 @@ __device__ __forceinline__ void kv_bulk(void *dst, const void *src, uint32_t byt
                "l"(src), "r"(bytes), "r"(tc_smem_u32(bar))
                : "memory");
 }
-// Four bytes; kv_copy4_arrive: the mbarrier gets one arrival once this thread's have come.
-__device__ __forceinline__ void kv_copy4(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc_smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void kv_copy4_arrive(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem_u32(bar)) : "memory");
-}
 // D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16
 __device__ __forceinline__ void kv_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -548,9 +541,9 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       if (keys) {
         meta_bad[warp * R + to] = !good;
         if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-        kv_copy4(&meta[warp * R + to][0], a.k_scale + at_block);
-        kv_copy4(&meta[warp * R + to][1], a.v_scale + at_block);
-        kv_copy4_arrive(b);
+        f8_copy4(&meta[warp * R + to][0], a.k_scale + at_block, true);
+        f8_copy4(&meta[warp * R + to][1], a.v_scale + at_block, true);
+        f8_copy4_arrive(b);
       } else {
         tc_mbar_arrive(b);
       }
@@ -585,7 +578,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   uint32_t phase = 0;
   bool dead = false;
   auto arrived = [&]() {
-    const bool ok = tc_mbar_wait_or_abort(&bar[slot], phase, a.timeout_ns, &abort_flag);
+    const bool ok = f8_wait(&bar[slot], phase, a.timeout_ns, &abort_flag);
     dead = !__all_sync(0xffffffffu, ok);
     return !dead;
   };
