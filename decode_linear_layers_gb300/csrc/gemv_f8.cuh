@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       uint32_t ph = 0, cph = 1;
       while (ok && walk.next(g)) {
         for (int kb = g.k0; kb < g.k1; ++kb) {
-          ok = (i < NACC || f8_wait(&acce[c], cph, a.timeout_ns, abort)) && f8_wait(&full[s], ph, a.timeout_ns, abort);
+          // (the copies are ahead as a rule: their wait is over before the accumulator's)
+          ok = f8_wait(&full[s], ph, a.timeout_ns, abort) && (i < NACC || f8_wait(&acce[c], cph, a.timeout_ns, abort));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           consumed = i;
@@ -347,8 +348,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kF8Group / 32; ++kk)
               f8_mma(tmem + (uint32_t)(c * N), dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
-            tc_commit(&empty[s]);
-            tc_commit(&accf[c]);
+            tc_commit(&accf[c]);  // one commit: the scaling warps pass on that the stage is free
           }
           ++i;
           if (++s == S) {
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     const int col0 = wg * COLS;
     unsigned char *mine = smem + (size_t)S * F::kStage + F::kScales * F::kScaleFloats * 4 + (size_t)(warp - 4) * F::kWarpBytes;
     constexpr int CH = COLS < 32 || kPrompt ? 16 : 32, P = COLS / CH, U = P < 2 ? 1 : 2;
-    int c = 0, t = 0;
+    int c = 0, t = 0, st = 0;
     uint32_t cph = 0, tph = 0;
     F8Walk walk(a);
     F8Seg g;
@@ -424,6 +424,8 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         ok = f8_wait(&facf[t], tph, a.timeout_ns, abort) && f8_wait(&accf[c], cph, a.timeout_ns, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (warp == 4 && lane == 0) tc_mbar_arrive(&empty[st]);  // the product is done: its stage is free
+        st = st + 1 == S ? 0 : st + 1;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * N + col0);
         // two pieces of CH columns on their way at a time
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     if (tid == 0) {
       if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
       const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
-      bool drained = committed < 0 || tc_mbar_wait(&empty[committed % S], (uint32_t)((committed / S) & 1), a.timeout_ns);
+      bool drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
       for (int t = consumed + 1; t <= loaded && drained; ++t)
         drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
       if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
