@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from .build import LIB as LIB_PATH, build
 
@@ -64,10 +65,8 @@ class Plan(ctypes.Structure):
         return d
 
 
-class Kv8CacheStruct(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("blocks", ctypes.c_int64),
-                ("width", ctypes.c_int64), ("heads", ctypes.c_int), ("dim", ctypes.c_int)]
+# gemv_kv8_cache_t: k, v, k_scale, v_scale, table, blocks, width, heads, dim
+KV8_CACHE = struct.Struct("@5P2q2i")
 
 
 class GemvError(RuntimeError):
@@ -200,6 +199,11 @@ def _addr(t, elem_size: int, min_elems: int, what: str):
         return None
     if isinstance(t, int):
         return t
+    try:  # a tensor as it should be; what is wrong with another is said below
+        if t.is_cuda and t.element_size() == elem_size and t.numel() >= min_elems and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{what} must be a CUDA tensor or a device address")
     if not t.is_contiguous():
@@ -408,16 +412,18 @@ def gemv_f8(A, a_scale, x, x_scale, bias, y, M, K, B, y_dtype="bf16", stream=Non
 
 
 def _kv8_cache(k, v, k_scale, v_scale, table, S):
-    """The cache as the library takes it; sizes from the tensors' shapes."""
-    if k.dim() != 4 or k.shape[2] != KV8_BLOCK or tuple(v.shape) != (k.shape[0], k.shape[1], k.shape[3], KV8_BLOCK):
+    """The cache as the library takes it (packed), heads and dim; sizes from the
+    tensors' shapes."""
+    ks, vs, ts = k.shape, v.shape, table.shape
+    if len(ks) != 4 or ks[2] != KV8_BLOCK or vs != (ks[0], ks[1], ks[3], KV8_BLOCK):
         raise ValueError(f"k must be (blocks, heads, {KV8_BLOCK}, dim) and v (blocks, heads, dim, {KV8_BLOCK}): "
-                         f"got {tuple(k.shape)} and {tuple(v.shape)}")
-    if table.dim() != 2 or table.shape[0] < S:
-        raise ValueError(f"table must be ({S}, width): got {tuple(table.shape)}")
-    blocks, heads, _, dim = k.shape
+                         f"got {tuple(ks)} and {tuple(vs)}")
+    if len(ts) != 2 or ts[0] < S:
+        raise ValueError(f"table must be ({S}, width): got {tuple(ts)}")
+    blocks, heads, _, dim = ks
     n = blocks * heads
-    return Kv8CacheStruct(_addr(k, 1, 0, "k"), _addr(v, 1, 0, "v"), _addr(k_scale, 4, n, "k_scale"),
-                          _addr(v_scale, 4, n, "v_scale"), _addr(table, 4, 0, "table"), blocks, table.shape[1], heads, dim)
+    return KV8_CACHE.pack(_addr(k, 1, 0, "k"), _addr(v, 1, 0, "v"), _addr(k_scale, 4, n, "k_scale"),
+                          _addr(v_scale, 4, n, "v_scale"), _addr(table, 4, 0, "table"), blocks, ts[1], heads, dim), heads, dim
 
 
 def _rows(t, elem_size, rows, row, what):
@@ -431,6 +437,9 @@ def _rows(t, elem_size, rows, row, what):
         raise ValueError(f"{what}: {t.numel()} elements, {rows} rows of {row} are needed")
     if t.is_contiguous() or rows == 0:
         return t.data_ptr(), row
+    st = t.stride()
+    if len(st) == 3 and st[2] == 1 and t.shape[0] == rows > 1 and st[1] == t.shape[2]:  # rows of heads x dim
+        return t.data_ptr(), st[0]
     if rows == 1:  # one row: its own dimensions alone have to be consecutive
         stride = row
     else:
@@ -455,11 +464,11 @@ def gemv_kv8_append(dtype, k_cache, v_cache, k_scale, v_scale, table, k, v, lens
     starts[s] .. starts[s + 1] (int32, S + 1 values; None: N / S each) and take the last
     positions of its lens[s] tokens (int32)."""
     S, N = int(S), int(N)
-    c = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
-    size, row = _ESIZE[dtype][1], c.heads * c.dim
+    cache, heads, dim = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, row = _ESIZE[dtype][1], heads * dim
     ka, ks = _rows(k, size, max(N, 0), row, "k")
     va, vs = _rows(v, size, max(N, 0), row, "v")
-    _check(_fn("gemv_kv8_append")(DTYPE_CODES[dtype], ctypes.addressof(c), ka, ks, va, vs, _addr(lens, 4, max(S, 0), "lens"),
+    _check(_fn("gemv_kv8_append")(DTYPE_CODES[dtype], cache, ka, ks, va, vs, _addr(lens, 4, max(S, 0), "lens"),
                                   _addr(starts, 4, S + 1, "starts"), S, N, _stream(stream)))
 
 
@@ -470,10 +479,10 @@ def gemv_kv8_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, q, lens
     tensor), lens (S) int32, lse (S, T, q_heads) fp32 or None.  window > 0: a query sees
     the `window` latest tokens, itself among them, and the first `sinks`."""
     S, T, q_heads = int(S), int(T), int(q_heads)
-    c = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
-    size, rows, row = _ESIZE[dtype][1], max(0, S * T), max(0, q_heads * c.dim)
+    cache, _, dim = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, rows, row = _ESIZE[dtype][1], max(0, S * T), max(0, q_heads * dim)
     qa, qs = _rows(q, size, rows, row, "q")
-    _check(_fn("gemv_kv8_attention")(DTYPE_CODES[dtype], ctypes.addressof(c), qa, qs, _addr(lens, 4, max(S, 0), "lens"),
+    _check(_fn("gemv_kv8_attention")(DTYPE_CODES[dtype], cache, qa, qs, _addr(lens, 4, max(S, 0), "lens"),
                                      _addr(out, size, rows * row, "out"),
                                      _addr(lse, 4, rows * max(q_heads, 0), "lse"), S, T, q_heads, float(scale),
                                      int(window), int(sinks), _stream(stream)))

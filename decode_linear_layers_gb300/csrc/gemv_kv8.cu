@@ -49,11 +49,19 @@ KvArgs cache_args(const gemv_kv8_cache_t *c) {
 }
 
 template <int D>
-cudaError_t append(const KvArgs &a, cudaStream_t s) {
+cudaError_t append(KvArgs a, int sms, cudaStream_t s) {
   // CTAs along x: the blocks that the new tokens can reach, at most
   const int64_t x = a.starts == nullptr ? (int64_t)a.S * ((a.T + kKvBlock - 2) / kKvBlock + 1) : a.N / kKvBlock + 2 * (int64_t)a.S;
   if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_k(k_kv8_append<D>, dim3((unsigned)x, (unsigned)a.heads, 2), dim3(kKvAppendThreads), 0, s, launch_overlap(), a);
+  // one unit for each CTA while the SMs hold all of them (four CTAs each); then more, so
+  // that finding the block is paid once for them
+  const int64_t units = 2 * (int64_t)a.heads;
+  a.per_cta = (int)((x * units + sms * 4 - 1) / (sms * 4));
+  if (a.per_cta > 4) a.per_cta = 4;
+  auto kern = a.dtype == GEMV_DTYPE_F32 ? k_kv8_append<D, GEMV_DTYPE_F32> : a.dtype == GEMV_DTYPE_F16 ? k_kv8_append<D, GEMV_DTYPE_F16>
+                                                                         : k_kv8_append<D, GEMV_DTYPE_BF16>;
+  return launch_k(kern, dim3((unsigned)x, (unsigned)((units + a.per_cta - 1) / a.per_cta)), dim3(kKvAppendThreads), 0, s,
+                  launch_overlap(), a);
 }
 
 template <int D, int NT>
@@ -134,8 +142,10 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
   a.T = (int)(N / S);
   a.dtype = (int)dtype;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dim == 64 ? append<64>(a, s) : cache->dim == 128 ? append<128>(a, s)
-                        : cache->dim == 192 ? append<192>(a, s) : append<256>(a, s);
+  int sms = 0;
+  if ((st = device_sms(&sms)) != GEMV_SUCCESS) return st;
+  const cudaError_t e = cache->dim == 64 ? append<64>(a, sms, s) : cache->dim == 128 ? append<128>(a, sms, s)
+                        : cache->dim == 192 ? append<192>(a, sms, s) : append<256>(a, sms, s);
   if (e != cudaSuccess) return fail((int)e);
   count_launches(1);
   return GEMV_SUCCESS;

@@ -27,7 +27,7 @@ struct KvArgs {
   int64_t k_stride = 0, v_stride = 0;
   const int32_t *starts = nullptr;
   int64_t N = 0;
-  int dtype = 0;
+  int dtype = 0, per_cta = 1;
   // attention
   const void *q = nullptr;
   void *out = nullptr;
@@ -65,21 +65,15 @@ __device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float r) {
   const float2 a = f16x2_to_f2(kv_half2_lo(w)), b = f16x2_to_f2(kv_half2_hi(w));
   return f8_pack2(a.x * r, a.y * r) | (f8_pack2(b.x * r, b.y * r) << 16);
 }
-__device__ __forceinline__ float kv_load(const void *p, int64_t i, int dt) {
-  if (dt == GEMV_DTYPE_F32) return __ldg(reinterpret_cast<const float *>(p) + i);
-  const unsigned short h = __ldg(reinterpret_cast<const unsigned short *>(p) + i);
-  return dt == GEMV_DTYPE_F16 ? __half2float(__ushort_as_half(h)) : __uint_as_float((uint32_t)h << 16);
-}
 
 // ------------------------------------------------------------------ append
-// One CTA for each block that new tokens reach, head, and keys (blockIdx.z = 0) or
-// values (1): it reads the block's new tokens once (eight values of a token per load),
-// finds their largest, and so the block's scale; where that grows it moves the tokens
-// the block held to the new scale; and it writes the new ones.  No other CTA touches
-// the block's head, so nothing is atomic.  Values pass through shared memory to lie
-// token-innermost.
+// A CTA has a block that new tokens reach, and of it one or more units (a head's keys, or
+// its values): it reads a unit's new tokens once (eight values of a token per load), finds
+// their largest, and so the unit's scale; where that grows it moves the tokens the block
+// held to the new scale; and it writes the new ones.  No other CTA touches the unit, so
+// nothing is atomic.  Values pass through shared memory to lie token-innermost.
 constexpr int kKvAppendThreads = 256;
-template <int D>
+template <int D, int DT>
 __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
   constexpr int kPieces = D / 8;                          // of a token
   constexpr int kLoads = (kKvBlock * kPieces / kKvAppendThreads + 3) / 4 * 4;
@@ -90,8 +84,7 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   __shared__ uint32_t tile[D * (kKvBlock / 4)];           // values: words of four tokens
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const bool values = blockIdx.z != 0;
+  const int tid = threadIdx.x, lane = tid & 31;
   // the sequence, and which of its blocks
   int s;
   int64_t first, n, nth;  // its first new token, how many, and the block's number among those they reach
@@ -104,10 +97,15 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   } else {
     // n tokens reach at most n / 64 + 2 blocks: sequence s has the CTAs from
     // starts[s] / 64 + 2 s on
-    int lo = 0, hi = a.S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if ((int64_t)(__ldg(a.starts + mid) / kKvBlock) + 2 * (int64_t)mid <= (int64_t)blockIdx.x) lo = mid; else hi = mid - 1;
+    // (each warp looks for the last such sequence in steps of 32)
+    int lo = 0, hi = a.S;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const bool from = i < hi && (int64_t)(__ldg(a.starts + i) / kKvBlock) + 2 * (int64_t)i <= (int64_t)blockIdx.x;
+      const int below = __popc(__ballot_sync(0xffffffffu, from));
+      lo += below > 0 ? (below - 1) * step : 0;
+      hi = lo + step < hi ? lo + step : hi;
+      if (below == 0) break;
     }
     s = lo;
     const int64_t b = __ldg(a.starts + s), e = __ldg(a.starts + s + 1);
@@ -118,7 +116,7 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   const int64_t len = __ldg(a.lens + s), before = len - n;
   if (n <= 0 || nth < 0) return;
   if (before < 0) {  // fewer tokens than the new ones: nothing says where they go
-    if (tid == 0 && nth == 0 && h == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+    if (tid == 0 && nth == 0 && blockIdx.y == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
     return;
   }
   const int64_t blk = before / kKvBlock + nth;
@@ -132,102 +130,109 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   const int held = before > p0 ? (int)(before - p0) : 0;             // tokens the block has
   const int end = len - p0 < kKvBlock ? (int)(len - p0) : kKvBlock;  // and will have
   const int64_t t0 = first + (p0 + held - before);                   // the first of its new tokens
-  const void *src = values ? a.new_v : a.new_k;
-  const int64_t stride = values ? a.v_stride : a.k_stride;
-  uint8_t *dst = (values ? a.v : a.k) + ((int64_t)pb * a.heads + h) * (kKvBlock * D);
-  float *sc = (values ? a.v_scale : a.k_scale) + (int64_t)pb * a.heads + h;
-  const float old = held > 0 ? *sc : 0.f;
+  const int units = 2 * a.heads;
+  for (int unit = blockIdx.y * a.per_cta; unit < units && unit < (int)(blockIdx.y + 1) * a.per_cta; ++unit) {
+    const bool values = (unit & 1) != 0;
+    const int h = unit >> 1;
+    if (unit > (int)blockIdx.y * a.per_cta) __syncthreads();  // the unit before is done with shared memory
+    const void *src = values ? a.new_v : a.new_k;
+    const int64_t stride = values ? a.v_stride : a.k_stride;
+    uint8_t *dst = (values ? a.v : a.k) + ((int64_t)pb * a.heads + h) * (kKvBlock * D);
+    float *sc = (values ? a.v_scale : a.k_scale) + (int64_t)pb * a.heads + h;
+    const float old = held > 0 ? *sc : 0.f;
 
-  // this thread's eight channels of kLoads tokens: of every kStride-th token, or (values)
-  // of four neighbouring ones, which share the words of the block's rows
-  const int esz = a.dtype == GEMV_DTYPE_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && (stride * esz) % 16 == 0;
-  const int ch = (tid % kPieces) * 8;
-  auto token = [&](int i) {
-    const int j = tid / kPieces;
-    return values ? j * 4 + (i & 3) + (i >> 2) * 4 * kStride : j + i * kStride;
-  };
-  float x[kLoads][8];
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int tok = token(i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-    if (tid < kActive && tok >= held && tok < end) {
-      const int64_t at = (t0 + tok - held) * stride + (int64_t)h * D + ch;
-      if (vec) {
-        if (a.dtype == GEMV_DTYPE_F32) f8_load8<GEMV_DTYPE_F32>(src, at, x[i]);
-        else if (a.dtype == GEMV_DTYPE_F16) f8_load8<GEMV_DTYPE_F16>(src, at, x[i]);
-        else f8_load8<GEMV_DTYPE_BF16>(src, at, x[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = kv_load(src, at + j, a.dtype);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, f8_finite_abs(x[i][j]));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((tid & 31) == 0) part[tid >> 5] = m;
-  __syncthreads();  // every thread has read the old scale, too
-#pragma unroll
-  for (int w = 0; w < kKvAppendThreads / 32; ++w) m = fmaxf(m, part[w]);
-  const float scale = fmaxf(kv_power(m), old), r = 1.f / scale;  // powers of two: exact
-  if (tid == 0) *sc = scale;
-  const bool move = held > 0 && scale != old;
-  const float ratio = old * r;
-
-  if (!values) {
-    if (move)
-      for (int i = tid; i < held * (D / 16); i += kKvAppendThreads) {
-        uint4 w = reinterpret_cast<const uint4 *>(dst)[i];
-        w.x = kv_rescale4(w.x, ratio);
-        w.y = kv_rescale4(w.y, ratio);
-        w.z = kv_rescale4(w.z, ratio);
-        w.w = kv_rescale4(w.w, ratio);
-        reinterpret_cast<uint4 *>(dst)[i] = w;
-      }
+    // this thread's eight channels of kLoads tokens: of every kStride-th token, or (values)
+    // of four neighbouring ones, which share the words of the block's rows
+    const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && (stride * (DT == GEMV_DTYPE_F32 ? 4 : 2)) % 16 == 0;
+    const int ch = (tid % kPieces) * 8;
+    auto token = [&](int i) {
+      const int j = tid / kPieces;
+      return values ? j * 4 + (i & 3) + (i >> 2) * 4 * kStride : j + i * kStride;
+    };
+    F8Raw<DT> x[kLoads];
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int tok = token(i);
-      if (tid < kActive && tok >= held && tok < end)
-        *reinterpret_cast<uint2 *>(dst + tok * D + ch) =
-            make_uint2(f8_pack2(x[i][0] * r, x[i][1] * r) | (f8_pack2(x[i][2] * r, x[i][3] * r) << 16),
-                       f8_pack2(x[i][4] * r, x[i][5] * r) | (f8_pack2(x[i][6] * r, x[i][7] * r) << 16));
-    }
-    return;
-  }
-  // word `w` (four tokens) of channel c lies at tile[c][w ^ (c / 8 mod 16)]: the lanes of a
-  // warp, which write eight channels apart, meet different banks
+      x[i].zero();
+      if (tid < kActive && tok >= held && tok < end) {
+        const int64_t at = (t0 + tok - held) * stride + (int64_t)h * D + ch;
+        if (vec) {
+          x[i].load(src, at);
+        } else {
 #pragma unroll
-  for (int i = 0; i < kLoads; i += 4) {
-    const int w = token(i) / 4;
-    if (tid < kActive) {
+          for (int j = 0; j < 8; ++j) x[i].set(j, src, at + j);
+        }
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        tile[(ch + j) * (kKvBlock / 4) + (w ^ ((ch >> 3) & 15))] =
-            f8_pack2(x[i][j] * r, x[i + 1][j] * r) | (f8_pack2(x[i + 2][j] * r, x[i + 3][j] * r) << 16);
+    for (int i = 0; i < kLoads; ++i) m = fmaxf(m, x[i].top());
+    if (m == __int_as_float(0x7f800000)) {  // an infinity: the finite values' largest
+      m = 0.f;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, f8_finite_abs(x[i].get(j)));
     }
-  }
-  __syncthreads();
-  // the words with new tokens, and with held ones to move; bytes of no token stay
-  const int w_lo = move ? 0 : held / 4, w_n = (end + 3) / 4 - w_lo;
-  for (int i = tid; i < D * w_n; i += kKvAppendThreads) {
-    const int c = w_n == kKvBlock / 4 ? i / (kKvBlock / 4) : i / w_n, at_w = w_lo + i - c * w_n, tok = at_w * 4;
-    uint32_t *at = reinterpret_cast<uint32_t *>(dst) + c * (kKvBlock / 4) + at_w;
-    const int lo = held - tok, hi = end - tok;  // bytes [lo, hi) are new
-    uint32_t w = tile[c * (kKvBlock / 4) + (at_w ^ ((c >> 3) & 15))];
-    if (lo > 0 || hi < 4) {
-      const uint32_t was = *at;
-      const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
-      const uint32_t above = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1);                       // bytes of no token
-      w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((tid & 31) == 0) part[tid >> 5] = m;
+    __syncthreads();  // every thread has read the old scale, too
+#pragma unroll
+    for (int w = 0; w < kKvAppendThreads / 32; ++w) m = fmaxf(m, part[w]);
+    const float scale = fmaxf(kv_power(m), old), r = 1.f / scale;  // powers of two: exact
+    if (tid == 0) *sc = scale;
+    const bool move = held > 0 && scale != old;
+    const float ratio = old * r;
+
+    if (!values) {
+      if (move)
+        for (int i = tid; i < held * (D / 16); i += kKvAppendThreads) {
+          uint4 w = reinterpret_cast<const uint4 *>(dst)[i];
+          w.x = kv_rescale4(w.x, ratio);
+          w.y = kv_rescale4(w.y, ratio);
+          w.z = kv_rescale4(w.z, ratio);
+          w.w = kv_rescale4(w.w, ratio);
+          reinterpret_cast<uint4 *>(dst)[i] = w;
+        }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int tok = token(i);
+        if (tid < kActive && tok >= held && tok < end)
+          *reinterpret_cast<uint2 *>(dst + tok * D + ch) =
+              make_uint2(f8_pack2(x[i].get(0) * r, x[i].get(1) * r) | (f8_pack2(x[i].get(2) * r, x[i].get(3) * r) << 16),
+                         f8_pack2(x[i].get(4) * r, x[i].get(5) * r) | (f8_pack2(x[i].get(6) * r, x[i].get(7) * r) << 16));
+      }
+      continue;
     }
-    *at = w;
+    // word `w` (four tokens) of channel c lies at tile[c][w ^ (c / 8 mod 16)]: the lanes of a
+    // warp, which write eight channels apart, meet different banks
+#pragma unroll
+    for (int i = 0; i < kLoads; i += 4) {
+      const int w = token(i) / 4;
+      if (tid < kActive) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          tile[(ch + j) * (kKvBlock / 4) + (w ^ ((ch >> 3) & 15))] =
+              f8_pack2(x[i].get(j) * r, x[i + 1].get(j) * r) | (f8_pack2(x[i + 2].get(j) * r, x[i + 3].get(j) * r) << 16);
+      }
+    }
+    __syncthreads();
+    // the words with new tokens, and with held ones to move; bytes of no token stay
+    const int w_lo = move ? 0 : held / 4, w_n = (end + 3) / 4 - w_lo;
+    for (int i = tid; i < D * w_n; i += kKvAppendThreads) {
+      const int c = w_n == kKvBlock / 4 ? i / (kKvBlock / 4) : i / w_n, at_w = w_lo + i - c * w_n, tok = at_w * 4;
+      uint32_t *at = reinterpret_cast<uint32_t *>(dst) + c * (kKvBlock / 4) + at_w;
+      const int lo = held - tok, hi = end - tok;  // bytes [lo, hi) are new
+      uint32_t w = tile[c * (kKvBlock / 4) + (at_w ^ ((c >> 3) & 15))];
+      if (lo > 0 || hi < 4) {
+        const uint32_t was = *at;
+        const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
+        const uint32_t above = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1);                       // bytes of no token
+        w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
+      }
+      *at = w;
+    }
   }
 }
 

@@ -2,8 +2,6 @@
 they refuse, without a GPU (every call here returns before any CUDA work)."""
 from __future__ import annotations
 
-import ctypes
-
 import pytest
 
 import decode_linear_layers_gb300 as g
@@ -56,17 +54,17 @@ def test_quantize_refusals():
 
 
 def cache(k=at(0), v=at(1), ks=at(2), vs=at(3), table=at(4), blocks=10, width=4, heads=2, dim=128):
-    return g.Kv8CacheStruct(k, v, ks, vs, table, blocks, width, heads, dim)
+    return g.KV8_CACHE.pack(*(p or 0 for p in (k, v, ks, vs, table)), blocks, width, heads, dim)
 
 
 def append(c=None, dt=2, k=at(5), k_stride=256, v=at(6), v_stride=256, lens=at(7), starts=at(8), S=3, N=6):
     c = cache() if c is None else c
-    return g.lib().gemv_kv8_append(dt, ctypes.addressof(c), k, k_stride, v, v_stride, lens, starts, S, N, None)
+    return g.lib().gemv_kv8_append(dt, c, k, k_stride, v, v_stride, lens, starts, S, N, None)
 
 
 def attention(c=None, dt=2, q=at(5), q_stride=1024, lens=at(6), out=at(7), lse=at(8), S=3, T=1, heads=8, window=0, sinks=0):
     c = cache() if c is None else c
-    return g.lib().gemv_kv8_attention(dt, ctypes.addressof(c), q, q_stride, lens, out, lse, S, T, heads, 0.1, window, sinks, None)
+    return g.lib().gemv_kv8_attention(dt, c, q, q_stride, lens, out, lse, S, T, heads, 0.1, window, sinks, None)
 
 
 @pytest.mark.parametrize("call", [append, attention])
