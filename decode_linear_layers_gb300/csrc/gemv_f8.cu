@@ -2,6 +2,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gemv.h"
 #include "gemv_f8.cuh"
 #include "gemv_internal.h"
@@ -10,6 +12,34 @@
 namespace gemv {
 namespace {
 
+// Clusters of n CTAs that the device holds at a time (asked once; the devices of a process
+// are taken to be alike).  A cluster's CTAs share a part of the GPU, so that clusters of
+// three, say, do not fill it: a second round of them would cost more than smaller ones.
+template <int N, bool kPrompt>
+int64_t f8_clusters(int n) {
+  using F = F8Form<N, kPrompt>;
+  static std::atomic<int> known[kTcMaxSlices + 1];
+  int v = known[n].load(std::memory_order_relaxed);
+  if (v == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n);
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&v, k_f8<N, kPrompt>, &cfg) != cudaSuccess || v < 1) {
+      (void)cudaGetLastError();
+      v = 1;
+    }
+    known[n].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
 template <int N, bool kPrompt>
 gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int sms, cudaStream_t s) {
   using F = F8Form<N, kPrompt>;
@@ -17,14 +47,22 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   a.tn = kPrompt ? (a.B + kF8Rows - 1) / kF8Rows : 1;
   a.tiles = (int64_t)a.tm * a.tn;
   const int64_t blocks = a.tiles * a.groups;
-  const int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
-  a.shared = a.tiles % W;
+  int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
+  cudaError_t e = allow_smem(k_f8<N, kPrompt>, F::kSmem);
+  if (e != cudaSuccess) return fail((int)e);
+  if (a.tiles * 2 <= sms && a.groups > 1) {  // few tiles: a cluster of up to eight for each
+    int64_t n = sms / a.tiles < kTcMaxSlices ? sms / a.tiles : kTcMaxSlices;
+    if (n > a.groups) n = a.groups;
+    while (n > 1 && f8_clusters<N, kPrompt>((int)n) < a.tiles) --n;
+    a.slices = (int)n;
+    if (n > 1) W = a.tiles * n;
+  }
+  a.shared = a.slices > 1 ? 0 : a.tiles % W;
   a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
   if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group, true) ||
       !map_bytes(&map_x, x, a.B, K, kPrompt ? kF8Rows : N, kF8Group, true))
     return fail((int)cudaErrorInvalidValue);
-  cudaError_t e = cudaSuccess;
   void *ws = nullptr;
   if (a.shared > 0) {
     e = workspace(&ws, (size_t)(W * 2 * F::kPartial * 4), s);
@@ -32,10 +70,9 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
     a.ws = static_cast<float *>(ws);
   }
   const int pdl = launch_overlap();
-  e = allow_smem(k_f8<N, kPrompt>, F::kSmem);
   if (e == cudaSuccess)
-    e = launch_k(k_f8<N, kPrompt>, dim3((unsigned)W), dim3(F::kThreads), (size_t)F::kSmem, s, pdl,
-                 kPrompt ? map_x : map_a, kPrompt ? map_a : map_x, a);
+    e = launch_k_cluster_x(k_f8<N, kPrompt>, dim3((unsigned)W), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a.slices,
+                           kPrompt ? map_x : map_a, kPrompt ? map_a : map_x, a);
   int n = 1;
   if (e == cudaSuccess && a.shared > 0) {
     e = launch_k(k_f8_join<N, kPrompt>, dim3((unsigned)a.shared, (unsigned)(F::kPartial / kF8JoinPiece)),

@@ -34,6 +34,7 @@ struct F8Args {
   int64_t shared = 0;    // tiles 0 .. shared - 1 are split over all CTAs, the rest go whole
   int B = 0, groups = 0; // groups = k-blocks
   int sharers = 0;       // CTAs that the shared tiles are split over
+  int slices = 1;        // or: CTAs of the cluster that each tile is split over
   int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
   int y_dtype = 0, stages = 0, test_stall = 0;
 };
@@ -79,6 +80,9 @@ __device__ __forceinline__ void f8_store(const F8Args &a, int64_t i, float v) {
 // each of the first R: so a few tiles keep every SM busy.  A range is no longer than a
 // tile's k-blocks, so it meets two tiles at most.  The other tiles, a multiple of the
 // CTAs, go round whole.  Each role of a CTA walks the same segments.
+// With fewer tiles than half the SMs (slices > 1) each tile is one cluster's instead, its
+// k-blocks cut among the cluster's CTAs, which add their sums in distributed shared
+// memory: one launch and no scratch buffer.
 struct F8Seg {
   int tile, k0, k1;
   int slot;  // which of the CTA's two partial sums it fills; -1: the whole tile
@@ -87,13 +91,20 @@ struct F8Walk {  // (the host limits tiles, and the k-blocks of a CTA, to 32 bit
   uint32_t lo, hi;
   int next_tile, tiles, groups, part;
   __device__ F8Walk(const F8Args &a) {
+    groups = a.groups;
+    part = 0;
+    if (a.slices > 1) {
+      const uint32_t tile = blockIdx.x / a.slices, r = blockIdx.x - tile * a.slices;
+      lo = tile * groups + r * groups / a.slices;
+      hi = tile * groups + (r + 1) * groups / a.slices;
+      next_tile = tiles = 0;
+      return;
+    }
     const int64_t R = a.shared * a.groups, w = blockIdx.x;
     lo = w < a.sharers ? (uint32_t)(w * R / a.sharers) : 0u;
     hi = w < a.sharers ? (uint32_t)((w + 1) * R / a.sharers) : 0u;
     next_tile = (int)(a.shared + w);
     tiles = (int)a.tiles;
-    groups = a.groups;
-    part = 0;
   }
   __device__ bool next(F8Seg &s) {
     if (lo < hi) {
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC], facf[F::kScales], face[F::kScales];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, abort_of[kTcMaxSlices];
   __shared__ int sh_loaded, sh_consumed, sh_committed;  // for the drain after an abort
   pdl_trigger();
   pdl_wait();  // every read (TMA included) after the kernel before has finished
@@ -292,6 +303,17 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   volatile int *abort = &abort_flag;
   const int G = a.groups;
   float *scales = reinterpret_cast<float *>(smem + (size_t)S * F::kStage);
+  // after an abort nothing may be in flight when the CTA frees its tensor memory and exits:
+  // the last committed MMAs (their commit covers all earlier ones) and every copy issued
+  // but not waited for
+  auto drain = [&]() {
+    if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
+    const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
+    bool drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
+    for (int t = consumed + 1; t <= loaded && drained; ++t)
+      drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
+    if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
+  };
 
   if (warp < 4) {
     if constexpr (kPrompt) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -402,6 +424,13 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       }
       f8_copy4_drain();  // nothing in flight when the CTA exits
     }
+    if (a.slices > 1) {  // (the scaling warps' meetings, below)
+      __syncwarp();
+      __syncthreads();
+      if (tid == 0 && abort_flag != 0) drain();
+      tc_cluster_sync();
+      tc_cluster_sync();
+    }
   } else {
     if constexpr (kPrompt) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int wq = warp & 3, wg = (warp >> 2) - 1;     // tensor-memory lanes 32 wq .. + 31
@@ -470,6 +499,52 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           tph ^= 1;
         }
       }
+      if (a.slices > 1) {
+        // Every CTA of the cluster holds the sums of its slice.  CTA q adds up rows
+        // ceil(128 q / slices) .. of the tile: all send it theirs, into its idle ring
+        // ([slice][row][column], rows padded against bank conflicts), and it adds the
+        // slices in the order of the k-blocks.
+        __syncwarp();
+        __syncthreads();
+        const int n = a.slices, rank = (int)blockIdx.x % n, most = (kF8Rows + n - 1) / n;
+        const bool aborted = abort_flag != 0;
+        constexpr int kPitch = N + 4;
+        float *parts = reinterpret_cast<float *>(smem);
+        auto first_row = [&](int q) { return (kF8Rows * q + n - 1) / n; };
+        // groups of four columns that y has
+        const int cols = kPrompt ? (a.M - (int64_t)im * N < N ? (int)(a.M - (int64_t)im * N) : N) : (a.B < N ? a.B : N);
+        const int quads = (cols + 3) / 4;
+        tc_cluster_sync();  // every ring is idle
+        const int to = row * n / kF8Rows;
+        if (tid - kF8RoleThreads < n) tc_st_dsmem_int(&abort_of[rank], (uint32_t)(tid - kF8RoleThreads), aborted ? 1 : 0);
+        if (!aborted) {
+          const float *at = parts + ((size_t)rank * most + row - first_row(to)) * kPitch + col0;
+#pragma unroll
+          for (int j = 0; j < COLS; j += 4)
+            if (col0 + j < cols) tc_st_dsmem4(at + j, (uint32_t)to, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        }
+        tc_cluster_sync();  // every slice's sums of the owned rows (and every abort flag) are here
+        bool any = false;
+        for (int q = 0; q < n; ++q) any |= abort_of[q] != 0;
+        const int r0 = first_row(rank), rows = first_row(rank + 1) - r0;
+        for (int i = tid - kF8RoleThreads; i < rows * quads && !any; i += 128 * F::kGroupsOfWarps) {
+          // neighbouring threads along y's rows: the tile's columns (prompts) or its rows
+          const int r = kPrompt ? i / quads : i % rows, cc = 4 * (kPrompt ? i % quads : i / rows);
+          float4 v = *reinterpret_cast<const float4 *>(parts + (size_t)r * kPitch + cc);
+          for (int q = 1; q < n; ++q) {
+            const float4 u = *reinterpret_cast<const float4 *>(parts + ((size_t)q * most + r) * kPitch + cc);
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+          }
+          const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t b = kPrompt ? (int64_t)in * kF8Rows + r0 + r : cc + j;
+            const int64_t m = kPrompt ? (int64_t)im * N + cc + j : (int64_t)im * kF8Rows + r0 + r;
+            if (b < a.B && m < a.M) f8_store(a, b * a.M + m, e[j] + (a.bias != nullptr ? f8_bias(a, m) : 0.f));
+          }
+        }
+        break;
+      }
       if (!ok) break;
       if (g.slot >= 0) {
         // a part of the tile's k-blocks: k_f8_join adds the parts.  Prompts [row][column]
@@ -519,26 +594,29 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         }
         // columns c0 .. of the tile's COLS, `per` to a piece, lie staged: store them
         auto pass = [&](int64_t c0, int per) {
+          if (c0 >= a.M) return;
           __syncwarp();
+          if (vec) {  // M is a whole number of pieces
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int rr = it * 8 + (lane >> 2), pc = lane & 3;
-            const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((pc ^ ((rr >> 1) & 3)) * 16));
-            const int64_t b = b0 + rr, m = c0 + pc * per;
-            if (b >= a.B || m >= a.M) continue;
-            char *dst = reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz;
-            if (vec) {  // M is a whole number of pieces
-              *reinterpret_cast<uint4 *>(dst) = w;
-            } else {
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (f32) {
-                  if (e < 4 && m + e < a.M) reinterpret_cast<uint32_t *>(dst)[e] = ww[e & 3];
-                } else if (m + e < a.M) {
-                  reinterpret_cast<unsigned short *>(dst)[e] = (unsigned short)(ww[e >> 1] >> (16 * (e & 1)));
-                }
-              }
+            for (int it = 0; it < 4; ++it) {
+              const int rr = it * 8 + (lane >> 2), pc = lane & 3;
+              const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((pc ^ ((rr >> 1) & 3)) * 16));
+              const int64_t b = b0 + rr, m = c0 + pc * per;
+              if (b < a.B && m < a.M) *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz) = w;
+            }
+          } else if (f32) {  // rows that start anywhere: neighbouring lanes store neighbouring values
+#pragma unroll 4
+            for (int rr = lane >> 4; rr < 32; rr += 2) {
+              const int j = lane & 15;
+              const uint32_t w = *reinterpret_cast<const uint32_t *>(mine + rr * 64 + (((j >> 2) ^ ((rr >> 1) & 3)) * 16) + (j & 3) * 4);
+              if (b0 + rr < a.B && c0 + j < a.M) reinterpret_cast<uint32_t *>(a.y)[(b0 + rr) * a.M + c0 + j] = w;
+            }
+          } else {
+#pragma unroll 4
+            for (int rr = 0; rr < 32; ++rr) {
+              const unsigned short w =
+                  *reinterpret_cast<const unsigned short *>(mine + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) * 16) + (lane & 7) * 2);
+              if (b0 + rr < a.B && c0 + lane < a.M) reinterpret_cast<unsigned short *>(a.y)[(b0 + rr) * a.M + c0 + lane] = w;
             }
           }
           __syncwarp();  // read before the next pass overwrites the buffer
@@ -573,18 +651,8 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();  // the role threads rejoin their warps: the CTA barrier counts whole warps
   __syncthreads();
-  if (abort_flag != 0) {
-    // nothing may be in flight when the CTA frees its tensor memory and exits: the last
-    // committed MMAs (their commit covers all earlier ones) and every copy issued but
-    // not waited for
-    if (tid == 0) {
-      if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
-      const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
-      bool drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
-      for (int t = consumed + 1; t <= loaded && drained; ++t)
-        drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
-      if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
-    }
+  if (abort_flag != 0 && a.slices == 1) {
+    if (tid == 0) drain();
     __syncwarp();
     __syncthreads();
   }

@@ -66,6 +66,27 @@ cudaError_t launch_k_cluster(void (*kern)(P...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kern, std::forward<A2>(args)...);
 }
 
+// The same, as clusters of (cx, 1, 1) CTAs (cx == 1: none).
+template <typename... P, typename... A2>
+cudaError_t launch_k_cluster_x(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int pdl, int cx,
+                               A2 &&...args) {
+  if (cx == 1) return launch_k(kern, grid, block, smem, s, pdl, std::forward<A2>(args)...);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cx;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl != 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A2>(args)...);
+}
+
 // Dynamic shared memory above 48 KB has to be allowed per kernel.
 template <typename Kern>
 cudaError_t allow_smem(Kern kern, int bytes) {
