@@ -57,7 +57,17 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
     a.slices = (int)n;
     if (n > 1) W = a.tiles * n;
   }
-  a.shared = a.slices > 1 ? 0 : a.tiles % W;
+  // Tiles that fill no whole round of the CTAs: a round of their own costs as many
+  // k-blocks as a tile has; shared among all CTAs they cost their share of it, and the
+  // join, about as long as kJoin k-blocks (us, shared / a round: 14336x3584 B=4 16.3 /
+  // 14.5, 10000x3584 B=100 20.1 / 22.1, 24000x3584 B=100 33.4 / 41.1; prompts, whose
+  // parts are 128 KB each, 11593x3584 B=1430 98.7 / 85.2, 11592x7168 130 / 115).
+  constexpr int64_t kJoin = kPrompt ? 28 : 12;
+  if (a.slices == 1) {
+    const int64_t rest = a.tiles % sms;
+    a.shared = (sms - rest) * a.groups > kJoin * sms ? rest : 0;
+    if (a.shared == 0) W = a.tiles < sms ? a.tiles : sms;
+  }
   a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
   if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group, true) ||

@@ -64,21 +64,37 @@ cudaError_t append(KvArgs a, int sms, cudaStream_t s) {
                   launch_overlap(), a);
 }
 
+// Tables of at most so many blocks per sequence: every item is one warp's, whole, in one
+// launch that needs no scratch buffer.  (us a call on the GPU, whole / shared and joined,
+// 8 heads of 128 channels: 128 tokens 6.7 / 8.2 for one sequence, 7.3 / 11.4 for 64; 256
+// tokens 9.8 / 8.3 and 10.8 / 11.9, where the host's time, 11 / 14, decides; 512 tokens
+// 16 / 8.7.)
+constexpr int kKvWhole = 4;
+
 template <int D, int NT>
 gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   using F = KvForm<D>;
   a.row_tiles = (a.T * a.group + NT * 8 - 1) / (NT * 8);
   if ((int64_t)a.heads * a.row_tiles > 65535) return GEMV_ERR_UNSUPPORTED;
   const int items = a.heads * a.row_tiles;
+  const int pdl = launch_overlap();
+  auto main = [&](auto kern) {
+    const cudaError_t e = allow_smem(kern, F::kSmem);
+    return e != cudaSuccess ? e : launch_k(kern, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
+  };
+  if (a.width <= kKvWhole) {
+    const cudaError_t e = main(k_kv8_attention<D, NT, true>);
+    if (e != cudaSuccess) return fail((int)e);
+    count_launches(1);
+    return GEMV_SUCCESS;
+  }
   const int64_t parts = (int64_t)sms * F::kWarps * 2 * kv_part<D, NT>() * 4;  // one CTA per SM
   void *ws = nullptr;
   cudaError_t e = workspace(&ws, (size_t)(parts + (int64_t)a.S * items * 16), s);
   if (e != cudaSuccess) return fail((int)e);
   a.ws = static_cast<float *>(ws);
   a.parts = reinterpret_cast<int4 *>(static_cast<char *>(ws) + parts);
-  const int pdl = launch_overlap();
-  e = allow_smem(k_kv8_attention<D, NT>, F::kSmem);
-  if (e == cudaSuccess) e = launch_k(k_kv8_attention<D, NT>, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
+  e = main(k_kv8_attention<D, NT, false>);
   if (e == cudaSuccess) {
     const int rows = a.T * a.group < NT * 8 ? a.T * a.group : NT * 8;
     auto join = [&](auto kern, int along) {

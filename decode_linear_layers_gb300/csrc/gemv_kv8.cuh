@@ -277,7 +277,7 @@ __device__ __forceinline__ int64_t kv_div(int64_t a, int64_t b) {
 // `total` places in ranges for W warps, the first `more` of them one longer.
 struct KvShares {
   int64_t each, more;
-  __device__ KvShares(int64_t total, int W) {
+  __device__ void cut(int64_t total, int64_t W) {
     each = kv_div(total, W);
     more = total - each * W;
   }
@@ -420,7 +420,7 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 // product is added to the running sums.
 // At the end of an item (or of the range) the warp writes the output, or a partial
 // result that k_kv8_join adds up.
-template <int D, int NT>
+template <int D, int NT, bool kWhole>
 __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const KvArgs a) {
   using F = KvForm<D>;
   constexpr int W = F::kWarps, R = F::kSlots, Q = D / 64, DT = D / 16;
@@ -442,14 +442,37 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   __syncthreads();
 
   const int items = a.heads * a.row_tiles;
-  const int64_t total = kv_before(a, a.S, lane) * items;
-  const KvShares shares(total, (int)gridDim.x * W);
-  const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x;  // (few blocks: one for each SM)
-  const int64_t u_lo = shares.first(worker), u_hi = shares.first(worker + 1);
-  if (u_lo >= u_hi) return;
+  const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x, workers = (int64_t)gridDim.x * W;  // (few blocks: one for each SM)
+  KvShares shares;
+  KvItem at;
+  int64_t u_lo, u_hi;
+  int slot = 0, issued = 0, taken = 0;  // the ring: slot in use, pieces begun, pieces used
+  uint32_t phase = 0;
+  bool dead = false;
+  // by shares: one round; else (kWhole, short sequences) an item, whole, each round
+  for (int64_t round = worker; !dead && (kWhole ? round < (int64_t)a.S * items : round == worker); round += workers) {
+  if constexpr (kWhole) {
+    const int s = (int)kv_div(round, items);
+    at.load(a, s, 0);
+    at.item = (int)(round - (int64_t)s * items);
+    u_lo = at.lo;
+    u_hi = at.hi;
+    if (u_lo >= u_hi) {  // no tokens
+      const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
+      for (int r = 0; r < NT * 8 && row0 + r < a.T * a.group; ++r) {
+        const int64_t at_row = kv_out_row(a, s, h, row0 + r);
+        for (int d = lane; d < D; d += 32) reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = 0;
+        if (lane == 0 && a.lse != nullptr) a.lse[at_row] = -INFINITY;
+      }
+      continue;
+    }
+  } else {
+  shares.cut(kv_before(a, a.S, lane) * items, workers);
+  u_lo = shares.first(worker);
+  u_hi = shares.first(worker + 1);
+  if (u_lo >= u_hi) break;
 
   // the item of place u_lo
-  KvItem at;
   int64_t base = 0;
   for (int s0 = 0;; s0 += 32) {  // 32 sequences at a time
     const int s = s0 + lane;
@@ -468,6 +491,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       break;
     }
     base += (int64_t)__shfl_sync(0xffffffffu, n, 31) * items;
+  }
   }
 
   // An item's queries as stored: rows g of its tiles, 16 channels 16 c .. of each 64.  The
@@ -536,7 +560,6 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     }
     return entry >= 0 && entry < a.blocks ? (int64_t)entry * a.heads + h : -2 - (int64_t)h;
   };
-  int issued = 0, taken = 0;               // pieces begun, pieces used
   auto issue = [&](int64_t block, bool keys, int to) {
     if (block == -1) return;
     if (lane == 0) {
@@ -570,18 +593,18 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
   int64_t ahead;
   {
     ahead = advance();
+    int to = slot;
+    auto next = [&]() { return to = to + 1 == R ? 0 : to + 1; };
 #pragma unroll 1
     for (int i = 0; i + 1 < R; i += 2) {
-      issue(ahead, true, i);
-      issue(ahead, false, i + 1);
+      issue(ahead, true, to);
+      issue(ahead, false, next());
+      next();
       if (ahead != -1) ahead = advance();
     }
-    issue(ahead, true, R - 1);
+    issue(ahead, true, to);
   }
 
-  int slot = 0;
-  uint32_t phase = 0;
-  bool dead = false;
   auto arrived = [&]() {
     const bool ok = f8_wait(&bar[slot], phase, a.timeout_ns, &abort_flag);
     dead = !__all_sync(0xffffffffu, ok);
@@ -848,8 +871,8 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     if (dead) break;
 
     // ---- the item's output, or this range's part of it
-    const bool whole = seg == at.lo && seg_end == at.hi;
-    if (seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
+    const bool whole = kWhole || (seg == at.lo && seg_end == at.hi);
+    if (!kWhole && seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
       a.parts[(int64_t)at.s * items + at.item] =
           make_int4((int)worker, (int)(shares.owner(at.hi - 1) - worker) + 1, first_item ? 0 : 1, 0);
     float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
@@ -890,6 +913,7 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
     at.seek(a, u);
     u = at.lo;
   }
+  }  // rounds
   if (dead) {
     // no copy may be in flight when the CTA exits
     if (lane == 0) {
