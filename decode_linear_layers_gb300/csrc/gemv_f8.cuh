@@ -241,15 +241,19 @@ struct F8Form {
   static constexpr int kGroupsOfWarps = kPrompt ? 2 : 1;                      // scaling warpgroups
   static constexpr int kThreads = kF8RoleThreads + 128 * kGroupsOfWarps;
   static constexpr int kCols = N / kGroupsOfWarps;                           // columns of a thread
-  static constexpr int kAcc = N == 256 ? 2 : 4;                              // accumulators in tensor memory
-  static constexpr int kTmemCols = kAcc * N < 32 ? 32 : kAcc * N;
-  static constexpr int kStage = (kF8Rows + N) * kF8Group;                    // bytes
-  // after the ring: the scales of kScales k-blocks, and (prompts) each scaling warp's
+  // k-blocks of a stage: its copies, products and scales are handed on together, which
+  // takes each role some hundred cycles a stage
+  static constexpr int kAtoms = N <= 16 ? 4 : N <= 64 ? 2 : 1;
+  static constexpr int kAcc = N == 256 ? 2 : 4;                              // stages' accumulators in tensor memory
+  static constexpr int kTmemCols = kAcc * kAtoms * N < 32 ? 32 : kAcc * kAtoms * N;
+  static constexpr int kRowsBytes = kF8Rows * kF8Group, kColsBytes = N * kF8Group;  // a k-block's two operands
+  static constexpr int kStage = kAtoms * (kRowsBytes + kColsBytes);
+  // after the ring: the scales of kScales stages, and (prompts) each scaling warp's
   // output staging
   static constexpr int kScales = 8;
-  static constexpr int kScaleFloats = (kPrompt ? kF8Rows : N) + 4;  // the vectors', then the weight blocks'
+  static constexpr int kScaleFloats = (kPrompt ? kF8Rows : N) + 4;  // of a k-block: the vectors', then the weight blocks'
   static constexpr int kWarpBytes = kPrompt ? 32 * 64 : 0;
-  static constexpr int kTail = kScales * kScaleFloats * 4 + 4 * kGroupsOfWarps * kWarpBytes;
+  static constexpr int kTail = kScales * kAtoms * kScaleFloats * 4 + 4 * kGroupsOfWarps * kWarpBytes;
   static constexpr int kStages = (226 * 1024 - kTail) / kStage < kF8MaxStages ? (226 * 1024 - kTail) / kStage : kF8MaxStages;
   static constexpr int kSmem = 1024 + kStages * kStage + kTail;
   static constexpr int64_t kPartial = (int64_t)kF8Rows * N;                  // floats of a partial sum
@@ -261,7 +265,7 @@ template <int N, bool kPrompt>
 __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     k_f8(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const F8Args a) {
   using F = F8Form<N, kPrompt>;
-  constexpr int S = F::kStages, NACC = F::kAcc, COLS = F::kCols;
+  constexpr int S = F::kStages, NACC = F::kAcc, COLS = F::kCols, KA = F::kAtoms;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC], facf[F::kScales], face[F::kScales];
   __shared__ uint32_t tmem_slot;
@@ -327,15 +331,20 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         int im, in;
         f8_tile(a, g.tile, im, in);
         const int32_t p0 = kPrompt ? in * kF8Rows : im * kF8Rows, q0 = kPrompt ? im * N : in * N;
-        for (int kb = g.k0; kb < g.k1; ++kb) {
+        for (int kb = g.k0; kb < g.k1; kb += KA) {
           ok = i < S || f8_wait(&empty[s], ph, a.timeout_ns, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           unsigned char *st = smem + (size_t)s * F::kStage;
           if (f8_elect()) {
-            tc_mbar_arrive_expect_tx(&full[s], F::kStage);
-            tc_tma_2d(st, &map_p, kb * kF8Group, p0, &full[s]);
-            tc_tma_2d(st + kF8Rows * kF8Group, &map_q, kb * kF8Group, q0, &full[s]);
+            const int n = g.k1 - kb < KA ? g.k1 - kb : KA;
+            tc_mbar_arrive_expect_tx(&full[s], (uint32_t)n * (F::kRowsBytes + F::kColsBytes));
+#pragma unroll
+            for (int j = 0; j < KA; ++j) {
+              if (j >= n) break;
+              tc_tma_2d(st + j * F::kRowsBytes, &map_p, (kb + j) * kF8Group, p0, &full[s]);
+              tc_tma_2d(st + KA * F::kRowsBytes + j * F::kColsBytes, &map_q, (kb + j) * kF8Group, q0, &full[s]);
+            }
           }
           ++i;
           if (++s == S) {
@@ -347,16 +356,16 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       if (lane == 0) sh_loaded = i - 1;
     } else if (warp == 1) {  // MMAs
       const uint32_t idesc = f8_idesc(N);
-      const uint64_t dp0 = tc_smem_desc(tc_smem_u32(smem)), dq0 = dp0 + (kF8Rows * kF8Group >> 4);
+      const uint64_t dp0 = tc_smem_desc(tc_smem_u32(smem)), dq0 = dp0 + (KA * F::kRowsBytes >> 4);
       int i = 0, last = -1, consumed = -1;
-      if (a.test_stall && blockIdx.x == 0) {  // test: the last k-block of the first CTA never completes
+      if (a.test_stall && blockIdx.x == 0) {  // test: the last stage of the first CTA never completes
         F8Walk w(a);
-        while (w.next(g)) last += g.k1 - g.k0;
+        while (w.next(g)) last += (g.k1 - g.k0 + KA - 1) / KA;
       }
       int s = 0, c = 0;
       uint32_t ph = 0, cph = 1;
       while (ok && walk.next(g)) {
-        for (int kb = g.k0; kb < g.k1; ++kb) {
+        for (int kb = g.k0; kb < g.k1; kb += KA) {
           // (the copies are ahead as a rule: their wait is over before the accumulator's)
           ok = f8_wait(&full[s], ph, a.timeout_ns, abort) && (i < NACC || f8_wait(&acce[c], cph, a.timeout_ns, abort));
           ok = __all_sync(0xffffffffu, ok);
@@ -368,8 +377,13 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           const uint64_t dp = dp0 + (uint64_t)(s * (F::kStage >> 4)), dq = dq0 + (uint64_t)(s * (F::kStage >> 4));
           if (f8_elect()) {
 #pragma unroll
-            for (int kk = 0; kk < kF8Group / 32; ++kk)
-              f8_mma(tmem + (uint32_t)(c * N), dp + 2 * kk, dq + 2 * kk, idesc, kk > 0);
+            for (int j = 0; j < KA; ++j) {
+              if (kb + j >= g.k1) break;
+#pragma unroll
+              for (int kk = 0; kk < kF8Group / 32; ++kk)
+                f8_mma(tmem + (uint32_t)((c * KA + j) * N), dp + j * (F::kRowsBytes >> 4) + 2 * kk,
+                       dq + j * (F::kColsBytes >> 4) + 2 * kk, idesc, kk > 0);
+            }
             tc_commit(&accf[c]);  // one commit: the scaling warps pass on that the stage is free
           }
           ++i;
@@ -405,15 +419,19 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           vx[v] = b < a.B;
           sx[v] = a.x_scale + (vx[v] ? b : 0) * G;
         }
-        for (int kb = g.k0; kb < g.k1; ++kb) {
+        for (int kb = g.k0; kb < g.k1; kb += KA) {
           ok = i < F::kScales || f8_wait(&face[t], ph, a.timeout_ns, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          float *w = scales + t * F::kScaleFloats;
+          float *w = scales + t * (KA * F::kScaleFloats);
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
-            if (kPrompt || lane + 32 * v < N) f8_copy4(w + lane + 32 * v, sx[v] + kb, vx[v]);
-          if (lane < 2) f8_copy4(w + F::kScaleFloats - 4 + lane, sa + kb, va);
+          for (int j = 0; j < KA; ++j, w += F::kScaleFloats) {
+            if (kb + j >= g.k1) break;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+              if (kPrompt || lane + 32 * v < N) f8_copy4(w + lane + 32 * v, sx[v] + kb + j, vx[v]);
+            if (lane < 2) f8_copy4(w + F::kScaleFloats - 4 + lane, sa + kb + j, va);
+          }
           f8_copy4_arrive(&facf[t]);
           ++i;
           if (++t == F::kScales) {
@@ -436,7 +454,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     const int wq = warp & 3, wg = (warp >> 2) - 1;     // tensor-memory lanes 32 wq .. + 31
     const int row = wq * 32 + lane;                    // of the tile
     const int col0 = wg * COLS;
-    unsigned char *mine = smem + (size_t)S * F::kStage + F::kScales * F::kScaleFloats * 4 + (size_t)(warp - 4) * F::kWarpBytes;
+    unsigned char *mine = smem + (size_t)S * F::kStage + F::kScales * F::kAtoms * F::kScaleFloats * 4 + (size_t)(warp - 4) * F::kWarpBytes;
     constexpr int CH = COLS < 32 || kPrompt ? 16 : 32, P = COLS / CH, U = P < 2 ? 1 : 2;
     int c = 0, t = 0, st = 0;
     uint32_t cph = 0, tph = 0;
@@ -449,43 +467,48 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      for (int kb = g.k0; kb < g.k1; ++kb) {
+      for (int kb = g.k0; kb < g.k1; kb += KA) {
         ok = f8_wait(&facf[t], tph, a.timeout_ns, abort) && f8_wait(&accf[c], cph, a.timeout_ns, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (warp == 4 && lane == 0) tc_mbar_arrive(&empty[st]);  // the product is done: its stage is free
         st = st + 1 == S ? 0 : st + 1;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * N + col0);
-        // two pieces of CH columns on their way at a time
-        uint32_t r[U][CH];
+        const int n = g.k1 - kb < KA ? g.k1 - kb : KA;
 #pragma unroll
-        for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
-        const float *fs = scales + t * F::kScaleFloats;
-        const float fa = fs[F::kScaleFloats - 4 + wg], f = kPrompt ? fs[row] * fa : 0.f;
+        for (int ka = 0; ka < KA; ++ka) {
+          if (ka >= n) break;
+          const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)((c * KA + ka) * N + col0);
+          // two pieces of CH columns on their way at a time
+          uint32_t r[U][CH];
 #pragma unroll
-        for (int h0 = 0; h0 < P; h0 += U) {
+          for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
+          const float *fs = scales + (t * KA + ka) * F::kScaleFloats;
+          const float fa = fs[F::kScaleFloats - 4 + wg], f = kPrompt ? fs[row] * fa : 0.f;
 #pragma unroll
-          for (int h = 0; h < U; ++h) f8_ld_wait<CH>(r[h]);
-          if (h0 + U >= P) {
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) tc_mbar_arrive(&acce[c]);
-          }
+          for (int h0 = 0; h0 < P; h0 += U) {
 #pragma unroll
-          for (int h = 0; h < U; ++h) {
-            float *sum = acc + (h0 + h) * CH;
-#pragma unroll
-            for (int j = 0; j < CH; j += 4) {
-              float4 q = make_float4(f, f, f, f);
-              if constexpr (!kPrompt) {
-                q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
-                q = make_float4(q.x * fa, q.y * fa, q.z * fa, q.w * fa);
-              }
-              f8_fma2(sum[j], sum[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
-              f8_fma2(sum[j + 2], sum[j + 3], q.z, q.w, r[h][j + 2], r[h][j + 3]);
+            for (int h = 0; h < U; ++h) f8_ld_wait<CH>(r[h]);
+            if (h0 + U >= P && ka + 1 == n) {
+              asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) tc_mbar_arrive(&acce[c]);
             }
-            if (h0 + U + h < P) f8_ld<CH>(at + (h0 + U + h) * CH, r[h]);
+#pragma unroll
+            for (int h = 0; h < U; ++h) {
+              float *sum = acc + (h0 + h) * CH;
+#pragma unroll
+              for (int j = 0; j < CH; j += 4) {
+                float4 q = make_float4(f, f, f, f);
+                if constexpr (!kPrompt) {
+                  q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
+                  q = make_float4(q.x * fa, q.y * fa, q.z * fa, q.w * fa);
+                }
+                f8_fma2(sum[j], sum[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
+                f8_fma2(sum[j + 2], sum[j + 3], q.z, q.w, r[h][j + 2], r[h][j + 3]);
+              }
+              if (h0 + U + h < P) f8_ld<CH>(at + (h0 + U + h) * CH, r[h]);
+            }
           }
         }
         __syncwarp();  // every lane has read the scales
