@@ -48,7 +48,7 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   a.tiles = (int64_t)a.tm * a.tn;
   const int64_t blocks = a.tiles * a.groups;
   int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
-  cudaError_t e = allow_smem(k_f8<N, kPrompt>, F::kSmem);
+  cudaError_t e = allow_smem_once<k_f8<N, kPrompt>>(F::kSmem);
   if (e != cudaSuccess) return fail((int)e);
   if (a.tiles * 2 <= sms && a.groups > 1) {  // few tiles: a cluster of up to eight for each
     int64_t n = sms / a.tiles < kTcMaxSlices ? sms / a.tiles : kTcMaxSlices;
@@ -196,7 +196,11 @@ gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, 
   if (B <= 16) return f8_launch<16, false>(a, A, x, K, sms, s);
   if (B <= 32) return f8_launch<32, false>(a, A, x, K, sms, s);
   if (B <= 64) return f8_launch<64, false>(a, A, x, K, sms, s);
-  if (B <= 128) return f8_launch<128, false>(a, A, x, K, sms, s);
+  // More vectors: they are the tile's rows, a thread's factor then one number per k-block
+  // (us, 128 vectors as rows / as columns: 14336x4096 16.7 / 20.9, 4096x14336 21.4 / 23.9).
+  // Tiles of 256 weight rows where those occupy half the SMs, of 128 else (us, 256 / 128:
+  // 4096x4096 B=256 20.6 / 17.4, B=1000 21.6 / 26.1, 1000x2048 B=500 17.3 / 11.9).
+  if (B <= 128 || (M + 255) / 256 * (((int64_t)B + 127) / 128) * 2 < sms) return f8_launch<128, true>(a, A, x, K, sms, s);
   return f8_launch<256, true>(a, A, x, K, sms, s);
 }
 

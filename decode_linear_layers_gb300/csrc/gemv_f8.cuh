@@ -233,18 +233,19 @@ __device__ __forceinline__ void f8_fma2(float &s0, float &s1, float f0, float f1
 // ------------------------------------------------------------------ the product
 // kPrompt = false: a tile is 128 weight rows x N vectors (one tile of vectors, B <= N);
 //   thread = weight row, column = vector.
-// kPrompt = true: a tile is 128 vectors x N = 256 weight rows; thread = vector, and the
-//   256 columns are two blocks of 128 weight rows, one per scaling warpgroup, so that a
-//   thread's factor sa sx is one number per k-block.
+// kPrompt = true: a tile is 128 vectors x N weight rows (128, or 256 in two blocks, one per
+//   scaling warpgroup); thread = vector, so that its factor sa sx is one number per k-block.
 template <int N, bool kPrompt>
 struct F8Form {
-  static constexpr int kGroupsOfWarps = kPrompt ? 2 : 1;                      // scaling warpgroups
+  static constexpr int kGroupsOfWarps = N >= 64 ? 2 : 1;                     // scaling warpgroups
+  static constexpr int kBlocks = kPrompt ? N / kF8Group : 1;                 // blocks of weight rows of a tile
+  static constexpr bool kSplitRegs = N == 256;                               // roles give registers to the scaling warps
   static constexpr int kThreads = kF8RoleThreads + 128 * kGroupsOfWarps;
   static constexpr int kCols = N / kGroupsOfWarps;                           // columns of a thread
   // k-blocks of a stage: its copies, products and scales are handed on together, which
   // takes each role some hundred cycles a stage
-  static constexpr int kAtoms = N <= 16 ? 4 : N <= 64 ? 2 : 1;
-  static constexpr int kAcc = N == 256 ? 2 : 4;                              // stages' accumulators in tensor memory
+  static constexpr int kAtoms = N <= 16 ? 4 : N <= 128 ? 2 : 1;
+  static constexpr int kAcc = N >= 128 ? 2 : 4;                              // stages' accumulators in tensor memory
   static constexpr int kTmemCols = kAcc * kAtoms * N < 32 ? 32 : kAcc * kAtoms * N;
   static constexpr int kRowsBytes = kF8Rows * kF8Group, kColsBytes = N * kF8Group;  // a k-block's two operands
   static constexpr int kStage = kAtoms * (kRowsBytes + kColsBytes);
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   };
 
   if (warp < 4) {
-    if constexpr (kPrompt) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (F::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     F8Walk walk(a);
     F8Seg g;
     bool ok = true;
@@ -409,8 +410,8 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         int im, in;
         f8_tile(a, g.tile, im, in);
         const int64_t b0 = kPrompt ? (int64_t)in * kF8Rows : 0;     // the first vector
-        const int64_t mb = (kPrompt ? (int64_t)im * 2 : im) + lane;  // lane 0 (and 1): block of weight rows
-        const bool va = lane < (kPrompt ? 2 : 1) && mb * kF8Group < a.M;
+        const int64_t mb = (int64_t)im * F::kBlocks + lane;          // lane 0 (and 1): block of weight rows
+        const bool va = lane < F::kBlocks && mb * kF8Group < a.M;
         const float *sa = a.a_scale + (va ? mb : 0) * G, *sx[NV];
         bool vx[NV];
 #pragma unroll
@@ -450,12 +451,12 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       tc_cluster_sync();
     }
   } else {
-    if constexpr (kPrompt) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (F::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int wq = warp & 3, wg = (warp >> 2) - 1;     // tensor-memory lanes 32 wq .. + 31
     const int row = wq * 32 + lane;                    // of the tile
     const int col0 = wg * COLS;
     unsigned char *mine = smem + (size_t)S * F::kStage + F::kScales * F::kAtoms * F::kScaleFloats * 4 + (size_t)(warp - 4) * F::kWarpBytes;
-    constexpr int CH = COLS < 32 || kPrompt ? 16 : 32, P = COLS / CH, U = P < 2 ? 1 : 2;
+    constexpr int CH = COLS < 32 || N == 256 ? 16 : 32, P = COLS / CH, U = P < 2 ? 1 : 2;
     int c = 0, t = 0, st = 0;
     uint32_t cph = 0, tph = 0;
     F8Walk walk(a);
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
           const float *fs = scales + (t * KA + ka) * F::kScaleFloats;
-          const float fa = fs[F::kScaleFloats - 4 + wg], f = kPrompt ? fs[row] * fa : 0.f;
+          const float fa = fs[F::kScaleFloats - 4 + (kPrompt ? col0 / kF8Group : 0)], f = kPrompt ? fs[row] * fa : 0.f;
 #pragma unroll
           for (int h0 = 0; h0 < P; h0 += U) {
 #pragma unroll
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
               for (int j = 0; j < CH; j += 4) {
                 float4 q = make_float4(f, f, f, f);
                 if constexpr (!kPrompt) {
-                  q = *reinterpret_cast<const float4 *>(fs + (h0 + h) * CH + j);
+                  q = *reinterpret_cast<const float4 *>(fs + col0 + (h0 + h) * CH + j);
                   q = make_float4(q.x * fa, q.y * fa, q.z * fa, q.w * fa);
                 }
                 f8_fma2(sum[j], sum[j + 1], q.x, q.y, r[h][j], r[h][j + 1]);
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
         } else {
 #pragma unroll
           for (int j = 0; j < COLS; ++j)
-            if (j < a.B) p[j * kF8Rows + row] = acc[j];
+            if (col0 + j < a.B) p[(col0 + j) * kF8Rows + row] = acc[j];
         }
         continue;
       }
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           const float bias = a.bias != nullptr ? f8_bias(a, m) : 0.f;
 #pragma unroll
           for (int j = 0; j < COLS; ++j)
-            if (j < a.B) f8_store(a, (int64_t)j * a.M + m, acc[j] + bias);
+            if (col0 + j < a.B) f8_store(a, (int64_t)(col0 + j) * a.M + m, acc[j] + bias);
         }
       } else {
         // the warp's 32 rows leave through its staging buffer, 64 bytes of each at a time

@@ -78,12 +78,10 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   if ((int64_t)a.heads * a.row_tiles > 65535) return GEMV_ERR_UNSUPPORTED;
   const int items = a.heads * a.row_tiles;
   const int pdl = launch_overlap();
-  auto main = [&](auto kern) {
-    const cudaError_t e = allow_smem(kern, F::kSmem);
-    return e != cudaSuccess ? e : launch_k(kern, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
-  };
   if (a.width <= kKvWhole) {
-    const cudaError_t e = main(k_kv8_attention<D, NT, true>);
+    cudaError_t e = allow_smem_once<k_kv8_attention<D, NT, true>>(F::kSmem);
+    if (e == cudaSuccess)
+      e = launch_k(k_kv8_attention<D, NT, true>, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
     if (e != cudaSuccess) return fail((int)e);
     count_launches(1);
     return GEMV_SUCCESS;
@@ -94,7 +92,9 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return fail((int)e);
   a.ws = static_cast<float *>(ws);
   a.parts = reinterpret_cast<int4 *>(static_cast<char *>(ws) + parts);
-  e = main(k_kv8_attention<D, NT, false>);
+  e = allow_smem_once<k_kv8_attention<D, NT, false>>(F::kSmem);
+  if (e == cudaSuccess)
+    e = launch_k(k_kv8_attention<D, NT, false>, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);
   if (e == cudaSuccess) {
     const int rows = a.T * a.group < NT * 8 ? a.T * a.group : NT * 8;
     auto join = [&](auto kern, int along) {

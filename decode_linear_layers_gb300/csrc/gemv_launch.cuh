@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
 #include <utility>
 
@@ -92,6 +93,20 @@ template <typename Kern>
 cudaError_t allow_smem(Kern kern, int bytes) {
   if (bytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// The same, asked once for each kernel and device: a call of its own costs host time.
+template <auto kKernel>
+cudaError_t allow_smem_once(int bytes) {
+  static std::atomic<uint64_t> allowed{0};  // a bit for each of the first 64 devices
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+  if ((allowed.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = allow_smem(kKernel, bytes);
+  if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <class Op, int NB>
