@@ -244,7 +244,8 @@ gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, fl
  * rounded once.  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
  * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any.  A scratch buffer of a few MB
  * comes from the library's stream-ordered pool where tiles are shared between SMs.
- * The kernel's waits are bounded (gemv_get_device_status). */
+ * The kernel's waits are bounded (gemv_get_device_status; y is undefined where one ran
+ * out). */
 gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
                       void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream);
 
@@ -315,7 +316,8 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
  * 11 bits.  The result does not depend on the run: partial results are merged in a
  * fixed order.  lens beyond the table count as the table's size.  A table entry outside
  * the pool counts as a block that no query sees, and gemv_get_device_status then
- * returns GEMV_ERR_INVALID_VALUE with bit 64.  The kernel's waits are bounded. */
+ * returns GEMV_ERR_INVALID_VALUE with bit 64.  The kernel's waits are bounded (out and lse
+ * are undefined where one ran out). */
 gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
                                  const int32_t *lens, void *out, float *lse, int S, int T, int q_heads, float scale,
                                  int64_t window, int64_t sinks, gemv_stream_t stream);

@@ -234,9 +234,10 @@ def test_quantized_product_end_to_end():
     check_product(product(A, sa, q, s, None, "f32"), *reference(A, sa, q, s, None), "f32")
 
 
-@pytest.mark.parametrize("B", [1, 200])
-def test_bounded_wait(B):
-    A, sa, x, sx = operands(300, 512, B, seed=8)
+# (clusters of few tiles, whole tiles, tiles that CTAs share; a tile's columns and rows)
+@pytest.mark.parametrize("M,K,B", [(300, 512, 1), (300, 512, 200), (20000, 256, 2), (12000, 4096, 3), (40000, 256, 200)])
+def test_bounded_wait(M, K, B):
+    A, sa, x, sx = operands(M, K, B, seed=8)
     torch.cuda.synchronize()
     g.test_stall(True, 50_000_000)
     product(A, sa, x, sx, None, "bf16")
