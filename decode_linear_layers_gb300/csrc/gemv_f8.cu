@@ -98,6 +98,24 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   return GEMV_SUCCESS;
 }
 
+gemv_status_t f8_launch_pair(F8Args a, const void *A, const void *x, int64_t K, int sms, cudaStream_t s) {
+  using F = F8Pair;
+  a.tm = (int)((a.M + F::kN - 1) / F::kN);
+  a.tn = (a.B + 255) / 256;
+  a.tiles = (int64_t)a.tm * a.tn;
+  const int64_t pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
+  cudaError_t e = allow_smem_once<k_f8_pair>(F::kSmem);
+  if (e != cudaSuccess) return fail((int)e);
+  CUtensorMap map_a, map_x;
+  if (!map_bytes(&map_a, A, a.M, K, 128, kF8Group, true) || !map_bytes(&map_x, x, a.B, K, 128, kF8Group, true))
+    return fail((int)cudaErrorInvalidValue);
+  e = launch_k_cluster_x(k_f8_pair, dim3((unsigned)(2 * pairs)), dim3(F::kThreads), (size_t)F::kSmem, s, launch_overlap(), 2,
+                         map_x, map_a, a);
+  if (e != cudaSuccess) return fail((int)e);
+  count_launches(1);
+  return GEMV_SUCCESS;
+}
+
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
 
@@ -201,6 +219,11 @@ gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, 
   // Tiles of 256 weight rows where those occupy half the SMs, of 128 else (us, 256 / 128:
   // 4096x4096 B=256 20.6 / 17.4, B=1000 21.6 / 26.1, 1000x2048 B=500 17.3 / 11.9).
   if (B <= 128 || (M + 255) / 256 * (((int64_t)B + 127) / 128) * 2 < sms) return f8_launch<128, true>(a, A, x, K, sms, s);
+  // From two rounds of 256 x 256 tiles on, pairs of SMs: they move less through shared memory
+  // and so draw less power (us, pairs / single: 4096x14336 B=8192 374 / 396 alone, 403 / 453
+  // where seconds of it run into the power limit; 128256x4096 B=256 139 / 145; 28672x4096
+  // B=4096 435 / 438; 4096x4096 B=2048, one round, 40.7 / 40.4).
+  if ((M + 255) / 256 * (((int64_t)B + 255) / 256) >= sms) return f8_launch_pair(a, A, x, K, sms, s);
   return f8_launch<256, true>(a, A, x, K, sms, s);
 }
 

@@ -230,6 +230,85 @@ __device__ __forceinline__ void f8_fma2(float &s0, float &s1, float f0, float f1
       : "f"(f0), "f"(f1), "r"(v0), "r"(v1));
 }
 
+// A warp's 32 vectors (from b0 on) of COLS weight rows each (from m0 on), a vector to a
+// lane: bias, rounding, and out through the warp's staging buffer, 64 bytes of each vector
+// at a time (16-byte pieces, their order rotated by the lane: free of bank conflicts), so
+// that four lanes store 64 consecutive bytes of y.
+template <int COLS>
+__device__ __forceinline__ void f8_rows_out(const F8Args &a, float (&acc)[COLS], unsigned char *mine, int lane, int64_t b0, int64_t m0) {
+  const bool f32 = a.y_dtype == GEMV_DTYPE_F32;
+  const int esz = f32 ? 4 : 2;
+  const bool vec = (a.M * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  if (a.bias != nullptr) {  // through the staging buffer, four columns a lane
+    float *sb = reinterpret_cast<float *>(mine);
+#pragma unroll
+    for (int j = 0; j < COLS; j += 32) sb[j + lane] = m0 + j + lane < a.M ? f8_bias(a, m0 + j + lane) : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < COLS; j += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(sb + j);
+      acc[j] += q.x;
+      acc[j + 1] += q.y;
+      acc[j + 2] += q.z;
+      acc[j + 3] += q.w;
+    }
+    __syncwarp();
+  }
+  // columns c0 .. of the tile's COLS, `per` to a piece, lie staged: store them
+  auto pass = [&](int64_t c0, int per) {
+    if (c0 >= a.M) return;
+    __syncwarp();
+    if (vec) {  // M is a whole number of pieces
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int rr = it * 8 + (lane >> 2), pc = lane & 3;
+        const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((pc ^ ((rr >> 1) & 3)) * 16));
+        const int64_t b = b0 + rr, m = c0 + pc * per;
+        if (b < a.B && m < a.M) *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz) = w;
+      }
+    } else if (f32) {  // rows that start anywhere: neighbouring lanes store neighbouring values
+#pragma unroll 4
+      for (int rr = lane >> 4; rr < 32; rr += 2) {
+        const int j = lane & 15;
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(mine + rr * 64 + (((j >> 2) ^ ((rr >> 1) & 3)) * 16) + (j & 3) * 4);
+        if (b0 + rr < a.B && c0 + j < a.M) reinterpret_cast<uint32_t *>(a.y)[(b0 + rr) * a.M + c0 + j] = w;
+      }
+    } else {
+#pragma unroll 4
+      for (int rr = 0; rr < 32; ++rr) {
+        const unsigned short w =
+            *reinterpret_cast<const unsigned short *>(mine + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) * 16) + (lane & 7) * 2);
+        if (b0 + rr < a.B && c0 + lane < a.M) reinterpret_cast<unsigned short *>(a.y)[(b0 + rr) * a.M + c0 + lane] = w;
+      }
+    }
+    __syncwarp();  // read before the next pass overwrites the buffer
+  };
+  unsigned char *const my_row = mine + lane * 64;
+  const int turn = (lane >> 1) & 3;
+  if (f32) {
+#pragma unroll
+    for (int h = 0; h < COLS; h += 16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4 *>(my_row + ((q ^ turn) * 16)) =
+            make_float4(acc[h + q * 4], acc[h + q * 4 + 1], acc[h + q * 4 + 2], acc[h + q * 4 + 3]);
+      pass(m0 + h, 4);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < COLS; h += 32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float *v = acc + h + q * 8;
+        *reinterpret_cast<uint4 *>(my_row + ((q ^ turn) * 16)) =
+            make_uint4(f8_pack16(v[0], v[1], a.y_dtype), f8_pack16(v[2], v[3], a.y_dtype),
+                       f8_pack16(v[4], v[5], a.y_dtype), f8_pack16(v[6], v[7], a.y_dtype));
+      }
+      pass(m0 + h, 8);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the product
 // kPrompt = false: a tile is 128 weight rows x N vectors (one tile of vectors, B <= N);
 //   thread = weight row, column = vector.
@@ -594,81 +673,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
             if (col0 + j < a.B) f8_store(a, (int64_t)(col0 + j) * a.M + m, acc[j] + bias);
         }
       } else {
-        // the warp's 32 rows leave through its staging buffer, 64 bytes of each at a time
-        // (16-byte pieces, their order rotated by the row: free of bank conflicts), so that
-        // four lanes store 64 consecutive bytes of y
-        const int64_t b0 = (int64_t)in * kF8Rows + wq * 32, m0 = (int64_t)im * N + col0;
-        const bool f32 = a.y_dtype == GEMV_DTYPE_F32;
-        const int esz = f32 ? 4 : 2;
-        const bool vec = (a.M * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-        if (a.bias != nullptr) {  // through the staging buffer, four columns a lane
-          float *sb = reinterpret_cast<float *>(mine);
-#pragma unroll
-          for (int j = 0; j < COLS; j += 32) sb[j + lane] = m0 + j + lane < a.M ? f8_bias(a, m0 + j + lane) : 0.f;
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < COLS; j += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(sb + j);
-            acc[j] += q.x;
-            acc[j + 1] += q.y;
-            acc[j + 2] += q.z;
-            acc[j + 3] += q.w;
-          }
-          __syncwarp();
-        }
-        // columns c0 .. of the tile's COLS, `per` to a piece, lie staged: store them
-        auto pass = [&](int64_t c0, int per) {
-          if (c0 >= a.M) return;
-          __syncwarp();
-          if (vec) {  // M is a whole number of pieces
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-              const int rr = it * 8 + (lane >> 2), pc = lane & 3;
-              const uint4 w = *reinterpret_cast<const uint4 *>(mine + rr * 64 + ((pc ^ ((rr >> 1) & 3)) * 16));
-              const int64_t b = b0 + rr, m = c0 + pc * per;
-              if (b < a.B && m < a.M) *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz) = w;
-            }
-          } else if (f32) {  // rows that start anywhere: neighbouring lanes store neighbouring values
-#pragma unroll 4
-            for (int rr = lane >> 4; rr < 32; rr += 2) {
-              const int j = lane & 15;
-              const uint32_t w = *reinterpret_cast<const uint32_t *>(mine + rr * 64 + (((j >> 2) ^ ((rr >> 1) & 3)) * 16) + (j & 3) * 4);
-              if (b0 + rr < a.B && c0 + j < a.M) reinterpret_cast<uint32_t *>(a.y)[(b0 + rr) * a.M + c0 + j] = w;
-            }
-          } else {
-#pragma unroll 4
-            for (int rr = 0; rr < 32; ++rr) {
-              const unsigned short w =
-                  *reinterpret_cast<const unsigned short *>(mine + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) * 16) + (lane & 7) * 2);
-              if (b0 + rr < a.B && c0 + lane < a.M) reinterpret_cast<unsigned short *>(a.y)[(b0 + rr) * a.M + c0 + lane] = w;
-            }
-          }
-          __syncwarp();  // read before the next pass overwrites the buffer
-        };
-        unsigned char *const my_row = mine + lane * 64;
-        const int turn = (lane >> 1) & 3;
-        if (f32) {
-#pragma unroll
-          for (int h = 0; h < COLS; h += 16) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<float4 *>(my_row + ((q ^ turn) * 16)) =
-                  make_float4(acc[h + q * 4], acc[h + q * 4 + 1], acc[h + q * 4 + 2], acc[h + q * 4 + 3]);
-            pass(m0 + h, 4);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < COLS; h += 32) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float *v = acc + h + q * 8;
-              *reinterpret_cast<uint4 *>(my_row + ((q ^ turn) * 16)) =
-                  make_uint4(f8_pack16(v[0], v[1], a.y_dtype), f8_pack16(v[2], v[3], a.y_dtype),
-                             f8_pack16(v[4], v[5], a.y_dtype), f8_pack16(v[6], v[7], a.y_dtype));
-            }
-            pass(m0 + h, 8);
-          }
-        }
+        f8_rows_out<COLS>(a, acc, mine, lane, (int64_t)in * kF8Rows + wq * 32, (int64_t)im * N + col0);
       }
     }
   }
@@ -683,6 +688,320 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)F::kTmemCols) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ pairs of SMs
+// Prompts with many tiles: a tile is 256 vectors x 256 weight rows, done by a cluster of two
+// CTAs whose tensor cores work as one (cta_group::2).  Each has the 128 vectors of its own
+// accumulator rows and half of the weight rows in shared memory, so that a k-block writes
+// and reads 32 KB in each SM instead of 48 (those 48 KB cost 768 cycles of shared-memory
+// bandwidth, the MMA itself 512).  CTA 0's MMA warp issues for both; a commit reaches both
+// CTAs' barriers, and both CTAs' scaling warps hand the accumulator back to CTA 0.
+// Whole tiles only, round-robin over the pairs.
+struct F8Pair {
+  static constexpr int kN = 256, kCols = 128, kThreads = 384, kAcc = 2;
+  static constexpr int kHalf = 128 * kF8Group;                  // bytes of 128 rows of a k-block
+  static constexpr int kStage = 2 * kHalf, kStages = 6;
+  static constexpr int kBatch = 4, kBatches = 3;                // k-blocks whose scales come together, and such sets
+  static constexpr int kScaleFloats = kF8Rows + 4;
+  static constexpr int kScaleBytes = kBatches * kBatch * kScaleFloats * 4;
+  static constexpr int kWarpBytes = 32 * 64;
+  static constexpr int kSmem = 1024 + kStages * kStage + kScaleBytes + 8 * kWarpBytes;
+};
+__device__ __forceinline__ uint32_t f8_remote(const void *p, uint32_t rank) {  // the same place in the cluster's CTA `rank`
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc_smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ bool f8_try_wait_cluster(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc_smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// map_x: the vectors, map_a: the weights, both in boxes of 128 rows.  grid: pairs of CTAs.
+static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
+    k_f8_pair(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a, const F8Args a) {
+  using F = F8Pair;
+  constexpr int S = F::kStages, NACC = F::kAcc, COLS = F::kCols;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[S], empty[S], accf[NACC], acce[NACC], facf[F::kBatches], face[F::kBatches];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int sh_loaded, sh_consumed, sh_committed;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)(blockIdx.x & 1);
+  unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
+  float *scales = reinterpret_cast<float *>(smem + S * F::kStage);
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc_mbar_init(&full[s], 1);   // CTA 0's, for both CTAs' copies
+      tc_mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NACC; ++b) {
+      tc_mbar_init(&accf[b], 1);
+      tc_mbar_init(&acce[b], 16);  // CTA 0's: the scaling warps of both
+    }
+    for (int b = 0; b < F::kBatches; ++b) {
+      tc_mbar_init(&facf[b], 32);
+      tc_mbar_init(&face[b], 8);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+    sh_loaded = sh_consumed = sh_committed = -1;
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  __syncthreads();
+  tc_cluster_sync();  // both CTAs' barriers and tensor memory are there
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort = &abort_flag;
+  const int G = a.groups, pairs = (int)gridDim.x / 2;
+  const int tiles = (int)a.tiles;
+  // (bounded as f8_wait is, for arrivals from the other CTA)
+  auto wait_cluster = [&](uint64_t *b, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+      if (f8_try_wait_cluster(b, parity)) return true;
+      if ((i & 255) == 0) {
+        if (*abort) return false;
+        const uint64_t t = tc_global_ns();
+        if (t0 == 0) t0 = t;
+        if ((int64_t)(t - t0) > a.timeout_ns) {
+          *abort = 1;
+          return false;
+        }
+      }
+    }
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    bool ok = true;
+    if (warp == 0) {  // copies of this CTA's halves; CTA 0's barrier counts both CTAs'
+      int i = 0, s = 0;
+      uint32_t ph = 1;
+      for (int tile = (int)blockIdx.x / 2; ok && tile < tiles; tile += pairs) {
+        int im, in;
+        f8_tile(a, tile, im, in);
+        const int32_t p0 = (2 * in + rank) * 128, q0 = (2 * im + rank) * 128;
+        for (int kb = 0; kb < G; ++kb) {
+          ok = i < S || f8_wait(&empty[s], ph, a.timeout_ns, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          unsigned char *st = smem + s * F::kStage;
+          if (f8_elect()) {
+            if (rank == 0) tc_mbar_arrive_expect_tx(&full[s], 2 * F::kStage);
+            const uint32_t bar = f8_remote(&full[s], 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                      tc_smem_u32(st + h * F::kHalf)),
+                  "l"(reinterpret_cast<uint64_t>(h == 0 ? &map_x : &map_a)), "r"(kb * kF8Group), "r"(h == 0 ? p0 : q0), "r"(bar)
+                  : "memory");
+          }
+          ++i;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (lane == 0) sh_loaded = i - 1;
+    } else if (warp == 1 && rank == 0) {  // MMAs of both CTAs
+      // M = 256 (both CTAs' rows), N = 256, e4m3
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(F::kN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+      const uint64_t dp0 = tc_smem_desc(tc_smem_u32(smem)), dq0 = dp0 + (F::kHalf >> 4);
+      int i = 0, consumed = -1, s = 0, c = 0;
+      uint32_t ph = 0, cph = 1;
+      for (int tile = (int)blockIdx.x / 2; ok && tile < tiles; tile += pairs) {
+        const bool stall = a.test_stall && blockIdx.x == 0 && tile + pairs >= tiles;  // test: the last k-block never completes
+        for (int kb = 0; kb < G; ++kb) {
+          ok = f8_wait(&full[s], ph, a.timeout_ns, abort) && (i < NACC || wait_cluster(&acce[c], cph));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          consumed = i;
+          if (stall && kb == G - 1) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t dp = dp0 + (uint64_t)(s * (F::kStage >> 4)), dq = dq0 + (uint64_t)(s * (F::kStage >> 4));
+          if (f8_elect()) {
+#pragma unroll
+            for (int kk = 0; kk < kF8Group / 32; ++kk)
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)(c * F::kN)),
+                  "l"(dp + 2 * kk), "l"(dq + 2 * kk), "r"(idesc), "r"(kk > 0 ? 1 : 0)
+                  : "memory");
+            asm volatile(
+                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                    tc_smem_u32(&accf[c])),
+                "h"((uint16_t)3)
+                : "memory");
+          }
+          ++i;
+          if (++s == S) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++c == NACC) {
+            c = 0;
+            cph ^= 1;
+          }
+        }
+      }
+      if (lane == 0) {
+        sh_consumed = consumed;
+        sh_committed = i - 1;
+      }
+    } else if (warp == 2) {  // scales, a batch of k-blocks at a time
+      int i = 0, t = 0;
+      uint32_t ph = 1;
+      for (int tile = (int)blockIdx.x / 2; ok && tile < tiles; tile += pairs) {
+        int im, in;
+        f8_tile(a, tile, im, in);
+        const int64_t b0 = (int64_t)(2 * in + rank) * 128, mb = (int64_t)im * 2 + lane;
+        const bool va = lane < 2 && mb * kF8Group < a.M;
+        const float *sa = a.a_scale + (va ? mb : 0) * G, *sx[4];
+        bool vx[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t b = b0 + lane + 32 * v;
+          vx[v] = b < a.B;
+          sx[v] = a.x_scale + (vx[v] ? b : 0) * G;
+        }
+        for (int kb0 = 0; kb0 < G; kb0 += F::kBatch) {
+          ok = i < F::kBatches || f8_wait(&face[t], ph, a.timeout_ns, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float *w = scales + t * (F::kBatch * F::kScaleFloats);
+#pragma unroll
+          for (int k = 0; k < F::kBatch; ++k, w += F::kScaleFloats) {
+            if (kb0 + k >= G) break;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) f8_copy4(w + lane + 32 * v, sx[v] + kb0 + k, vx[v]);
+            if (lane < 2) f8_copy4(w + kF8Rows + lane, sa + kb0 + k, va);
+          }
+          f8_copy4_arrive(&facf[t]);
+          ++i;
+          if (++t == F::kBatches) {
+            t = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      f8_copy4_drain();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int wq = warp & 3, wg = (warp >> 2) - 1;
+    const int row = wq * 32 + lane, col0 = wg * COLS;
+    unsigned char *mine = smem + S * F::kStage + F::kScaleBytes + (warp - 4) * F::kWarpBytes;
+    const uint32_t back[NACC] = {f8_remote(&acce[0], 0), f8_remote(&acce[1], 0)};
+    constexpr int CH = 16, P = COLS / CH, U = 2;
+    int c = 0, t = 0, st = 0;
+    uint32_t cph = 0, tph = 0;
+    bool ok = true;
+    for (int tile = (int)blockIdx.x / 2; ok && tile < tiles; tile += pairs) {
+      int im, in;
+      f8_tile(a, tile, im, in);
+      float acc[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      for (int kb = 0; kb < G; ++kb) {
+        const int k = kb % F::kBatch;
+        ok = (k != 0 || f8_wait(&facf[t], tph, a.timeout_ns, abort)) && f8_wait(&accf[c], cph, a.timeout_ns, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (warp == 4 && lane == 0) tc_mbar_arrive(&empty[st]);
+        st = st + 1 == S ? 0 : st + 1;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(c * F::kN + col0);
+        uint32_t r[U][CH];
+#pragma unroll
+        for (int h = 0; h < U; ++h) f8_ld<CH>(at + h * CH, r[h]);
+        const float *fs = scales + (t * F::kBatch + k) * F::kScaleFloats;
+        const float f = fs[row] * fs[kF8Rows + wg];
+#pragma unroll
+        for (int h0 = 0; h0 < P; h0 += U) {
+#pragma unroll
+          for (int h = 0; h < U; ++h) f8_ld_wait<CH>(r[h]);
+          if (h0 + U >= P) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(c == 0 ? back[0] : back[1]) : "memory");
+          }
+#pragma unroll
+          for (int h = 0; h < U; ++h) {
+            float *sum = acc + (h0 + h) * CH;
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) f8_fma2(sum[j], sum[j + 1], f, f, r[h][j], r[h][j + 1]);
+            if (h0 + U + h < P) f8_ld<CH>(at + (h0 + U + h) * CH, r[h]);
+          }
+        }
+        if (++c == NACC) {
+          c = 0;
+          cph ^= 1;
+        }
+        if (k == F::kBatch - 1 || kb == G - 1) {
+          __syncwarp();  // every lane has read the batch's scales
+          if (lane == 0) tc_mbar_arrive(&face[t]);
+          if (++t == F::kBatches) {
+            t = 0;
+            tph ^= 1;
+          }
+        }
+      }
+      if (!ok) break;
+      f8_rows_out<COLS>(a, acc, mine, lane, (int64_t)(2 * in + rank) * 128 + wq * 32, (int64_t)im * F::kN + col0);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  __syncthreads();
+  if (abort_flag != 0) {
+    // nothing may be in flight when the pair frees its tensor memory and exits: CTA 0 waits
+    // for the MMAs and for the copies of both that its barriers know of; the other CTA's
+    // last ones may be unknown to them: both wait a tenth of a millisecond more, a hundred
+    // times what a copy takes
+    if (tid == 0) {
+      if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
+      bool drained = true;
+      if (rank == 0) {
+        const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
+        drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
+        for (int t = consumed + 1; t <= loaded && drained; ++t)
+          drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
+      }
+      if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
+      const uint64_t t0 = tc_global_ns();
+      while (tc_global_ns() - t0 < 100000) {
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  tc_cluster_sync();  // the other CTA's MMAs, copies and arrivals are done with this one
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 

@@ -154,7 +154,9 @@ def test_product(name, B):
 
 # more tiles than SMs (whole tiles and shared ones), and one tile whose columns all share
 @pytest.mark.parametrize("M,K,B", [(20000, 384, 4), (40000, 256, 40), (128, 16384, 1), (7000, 272, 1000), (256, 8192, 130),
-                                   (39168, 128, 16)])
+                                   (39168, 128, 16),
+                                   # pairs of SMs: one tile of 256 vectors, several, ragged ends
+                                   (40000, 272, 200), (39937, 144, 300), (10250, 400, 1100), (4100, 16, 2600)])
 def test_product_many_tiles(M, K, B):
     A, sa, x, sx = operands(M, K, B, seed=M)
     y = product(A, sa, x, sx, None, "bf16")
