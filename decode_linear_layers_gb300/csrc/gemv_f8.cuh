@@ -267,18 +267,22 @@ __device__ __forceinline__ void f8_rows_out(const F8Args &a, float (&acc)[COLS],
         if (b < a.B && m < a.M) *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(a.y) + (b * a.M + m) * esz) = w;
       }
     } else if (f32) {  // rows that start anywhere: neighbouring lanes store neighbouring values
-#pragma unroll 4
-      for (int rr = lane >> 4; rr < 32; rr += 2) {
-        const int j = lane & 15;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(mine + rr * 64 + (((j >> 2) ^ ((rr >> 1) & 3)) * 16) + (j & 3) * 4);
-        if (b0 + rr < a.B && c0 + j < a.M) reinterpret_cast<uint32_t *>(a.y)[(b0 + rr) * a.M + c0 + j] = w;
+      const int jj = lane & 15, r0 = lane >> 4;
+      uint32_t *dst = reinterpret_cast<uint32_t *>(a.y) + (b0 + r0) * a.M + c0 + jj;
+      const int rows = c0 + jj < a.M ? (a.B - b0 < 32 ? (int)(a.B - b0) : 32) : 0;
+#pragma unroll 8
+      for (int rr = r0; rr < 32; rr += 2, dst += 2 * a.M) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(mine + rr * 64 + (((jj >> 2) ^ ((rr >> 1) & 3)) * 16) + (jj & 3) * 4);
+        if (rr < rows) *dst = w;
       }
     } else {
-#pragma unroll 4
-      for (int rr = 0; rr < 32; ++rr) {
+      unsigned short *dst = reinterpret_cast<unsigned short *>(a.y) + b0 * a.M + c0 + lane;
+      const int rows = c0 + lane < a.M ? (a.B - b0 < 32 ? (int)(a.B - b0) : 32) : 0;
+#pragma unroll 8
+      for (int rr = 0; rr < 32; ++rr, dst += a.M) {
         const unsigned short w =
             *reinterpret_cast<const unsigned short *>(mine + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) * 16) + (lane & 7) * 2);
-        if (b0 + rr < a.B && c0 + lane < a.M) reinterpret_cast<unsigned short *>(a.y)[(b0 + rr) * a.M + c0 + lane] = w;
+        if (rr < rows) *dst = w;
       }
     }
     __syncwarp();  // read before the next pass overwrites the buffer
