@@ -375,12 +375,14 @@ __device__ __forceinline__ uint32_t kv_pack_half(float lo, float hi) {
   return r;
 }
 
-template <int D>
+template <int D, int NT>
 struct KvForm {
-  // warps x slots x slot bytes of copies in flight or in use: 192 to 224 KB; an odd number
-  // of slots, so that each freed one takes the other half of a block
-  static constexpr int kWarps = D <= 128 ? 8 : D == 192 ? 6 : 4;
-  static constexpr int kSlots = D == 64 ? 7 : 3;
+  // warps x slots x slot bytes of copies in flight or in use: 144 to 216 KB; an odd number
+  // of slots, so that each freed one takes the other half of a block.  Twelve warps where
+  // 168 registers do (us, 12 / 8 warps, 64 channels, 30 sequences of up to 8000 tokens:
+  // one tile 32.5 / 33.3, two 36.1 / 39.2; three tiles would spill).
+  static constexpr int kWarps = D == 64 && NT <= 2 ? 12 : D <= 128 ? 8 : D == 192 ? 6 : 4;
+  static constexpr int kSlots = D == 64 && NT > 2 ? 5 : 3;
   static constexpr int kSlot = kKvBlock * D;  // the keys or the values of a block
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kSmem = 128 + kWarps * kSlots * kSlot;
@@ -421,8 +423,8 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 // At the end of an item (or of the range) the warp writes the output, or a partial
 // result that k_kv8_join adds up.
 template <int D, int NT, bool kWhole>
-__global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const KvArgs a) {
-  using F = KvForm<D>;
+__global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(const KvArgs a) {
+  using F = KvForm<D, NT>;
   constexpr int W = F::kWarps, R = F::kSlots, Q = D / 64, DT = D / 16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[W * R];
@@ -723,19 +725,27 @@ __global__ void __launch_bounds__(KvForm<D>::kThreads, 1) k_kv8_attention(const 
       for (int n = 0; n < NT; ++n) {
         const float f0 = qs[n][0] * ks, f1 = qs[n][1] * ks;
         float m0 = m[n][0], m1 = m[n][1];
-        // the tokens that the queries of rows 2 c, 2 c + 1 see, from this lane's first on
-        uint32_t wa = ~0u, wb = ~0u;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          s[n][t][0] *= f0;
+          s[n][t][1] *= f1;
+          s[n][t][2] *= f0;
+          s[n][t][3] *= f1;
+        }
         if (edge) {
+          // the tokens that the queries of rows 2 c, 2 c + 1 see, from this lane's first on
           const int r0 = row0 + n * 8 + 2 * c, first = 16 * (g >> 1) + (g & 1);
-          wa = (uint32_t)(mask(r0 / a.group) >> first);
-          wb = (uint32_t)(mask((r0 + 1) / a.group) >> first);
+          const uint32_t wa = (uint32_t)(mask(r0 / a.group) >> first), wb = (uint32_t)(mask((r0 + 1) / a.group) >> first);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (!(wa >> (4 * t) & 1)) s[n][t][0] = -INFINITY;
+            if (!(wb >> (4 * t) & 1)) s[n][t][1] = -INFINITY;
+            if (!(wa >> (4 * t + 2) & 1)) s[n][t][2] = -INFINITY;
+            if (!(wb >> (4 * t + 2) & 1)) s[n][t][3] = -INFINITY;
+          }
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          s[n][t][0] = wa >> (4 * t) & 1 ? s[n][t][0] * f0 : -INFINITY;
-          s[n][t][1] = wb >> (4 * t) & 1 ? s[n][t][1] * f1 : -INFINITY;
-          s[n][t][2] = wa >> (4 * t + 2) & 1 ? s[n][t][2] * f0 : -INFINITY;
-          s[n][t][3] = wb >> (4 * t + 2) & 1 ? s[n][t][3] * f1 : -INFINITY;
           m0 = fmaxf(m0, fmaxf(s[n][t][0], s[n][t][2]));
           m1 = fmaxf(m1, fmaxf(s[n][t][1], s[n][t][3]));
         }
