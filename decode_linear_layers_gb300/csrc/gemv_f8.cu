@@ -121,7 +121,8 @@ bool aligned(const void *p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes
 
 template <int DT>
 cudaError_t quantize(const void *x, uint8_t *q, float *scale, int64_t K, int64_t G, int64_t groups, int sms, cudaStream_t s) {
-  const bool vec = K % 8 == 0 && aligned(x, 16) && aligned(q, 8);
+  const bool eight = K % 8 == 0 && aligned(x, 16) && aligned(q, 8);
+  const bool two = K % 2 == 0 && aligned(x, DT == GEMV_DTYPE_F32 ? 8 : 4) && aligned(q, 2);
   constexpr int kTeams = kF8QThreads / kF8QTeam;
   // two groups of a team in flight once every SM's threads have one
   const bool many = groups > (int64_t)sms * (2048 / kF8QTeam) * 2;
@@ -130,8 +131,9 @@ cudaError_t quantize(const void *x, uint8_t *q, float *scale, int64_t K, int64_t
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
     return launch_k(kern, dim3((unsigned)grid), dim3(kF8QThreads), 0, s, launch_overlap(), x, q, scale, K, (int)G, groups);
   };
-  if (vec) return many ? go(k_f8_quantize<DT, true, 2>, 2) : go(k_f8_quantize<DT, true, 1>, 1);
-  return many ? go(k_f8_quantize<DT, false, 2>, 2) : go(k_f8_quantize<DT, false, 1>, 1);
+  if (eight) return many ? go(k_f8_quantize<DT, 8, 2>, 2) : go(k_f8_quantize<DT, 8, 1>, 1);
+  if (two) return many ? go(k_f8_quantize<DT, 2, 2>, 2) : go(k_f8_quantize<DT, 2, 1>, 1);
+  return many ? go(k_f8_quantize<DT, 1, 2>, 2) : go(k_f8_quantize<DT, 1, 1>, 1);
 }
 
 }  // namespace

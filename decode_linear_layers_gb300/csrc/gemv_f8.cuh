@@ -1097,9 +1097,10 @@ __device__ __forceinline__ void f8_load8(const void *p, int64_t i, float (&v)[8]
   }
 }
 
-// Eight lanes hold a group's 128 values, sixteen each (in two pieces of eight consecutive
-// ones where rows are whole 16-byte pieces, kVec; else every eighth), so the group is read
-// once and its largest value found by three shuffles.  The largest absolute value is taken
+// Eight lanes hold a group's 128 values, sixteen each, so the group is read once and its
+// largest value found by three shuffles.  kWide: how many consecutive ones a lane reads and
+// writes at a time: eight (rows of whole 16-byte pieces), two (rows of an even length) or
+// one (us, 3204 x 5080, 5082 and 5081 in bf16: 9.2, 13.7 and 24.1).  The largest absolute value is taken
 // first over all values, infinities among them, on two 16-bit values per instruction;
 // only where it is infinite are the finite ones looked at one by one.
 constexpr int kF8QThreads = 256, kF8QTeam = 8;
@@ -1124,6 +1125,15 @@ struct F8Raw {  // eight values as loaded
       w[e] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
     else
       w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p) + i) << (16 * (e & 1));
+  }
+  __device__ __forceinline__ void set2(int e, const void *p, int64_t i) {  // values e, e + 1 (e even, i even)
+    if constexpr (DT == GEMV_DTYPE_F32) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint32_t *>(p) + i));
+      w[e] = v.x;
+      w[e + 1] = v.y;
+    } else {
+      w[e / 2] = __ldg(reinterpret_cast<const uint32_t *>(reinterpret_cast<const unsigned short *>(p) + i));
+    }
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (DT == GEMV_DTYPE_F32) return __uint_as_float(w[e]);
@@ -1158,7 +1168,7 @@ struct F8Raw {  // eight values as loaded
     }
   }
 };
-template <int DT, bool kVec, int U>
+template <int DT, int kWide, int U>
 __global__ void __launch_bounds__(kF8QThreads)
     k_f8_quantize(const void *x, uint8_t *q, float *scale, int64_t K, int G, int64_t groups) {
   pdl_trigger();
@@ -1186,8 +1196,12 @@ __global__ void __launch_bounds__(kF8QThreads)
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if constexpr (kVec) {
+      if constexpr (kWide == 8) {
         if (h * 64 + lane * 8 < n[u]) v[u][h].load(x, base[u] + h * 64 + lane * 8);
+      } else if constexpr (kWide == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+          if (h * 64 + e * 8 + lane * 2 < n[u]) v[u][h].set2(e, x, base[u] + h * 64 + e * 8 + lane * 2);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -1213,12 +1227,18 @@ __global__ void __launch_bounds__(kF8QThreads)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const F8Raw<DT> &w = v[u][h];
-      if constexpr (kVec) {
+      if constexpr (kWide == 8) {
         uint32_t o[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           o[i] = f8_pack2(w.get(4 * i) * r, w.get(4 * i + 1) * r) | (f8_pack2(w.get(4 * i + 2) * r, w.get(4 * i + 3) * r) << 16);
         if (h * 64 + lane * 8 < n[u]) *reinterpret_cast<uint2 *>(q + base[u] + h * 64 + lane * 8) = make_uint2(o[0], o[1]);
+      } else if constexpr (kWide == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+          if (h * 64 + e * 8 + lane * 2 < n[u])
+            *reinterpret_cast<unsigned short *>(q + base[u] + h * 64 + e * 8 + lane * 2) =
+                (unsigned short)f8_pack2(w.get(e) * r, w.get(e + 1) * r);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
