@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
   constexpr int kActive = kStride * kPieces;              // threads with channels
   static_assert(kActive <= kKvAppendThreads && kKvBlock % kLoads == 0);
   __shared__ float part[kKvAppendThreads / 32];
-  __shared__ uint32_t tile[D * (kKvBlock / 4)];           // values: words of four tokens
+  __shared__ __align__(16) uint32_t tile[D * (kKvBlock / 4)];  // values: words of four tokens
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -205,33 +205,44 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
       }
       continue;
     }
-    // word `w` (four tokens) of channel c lies at tile[c][w ^ (c / 8 mod 16)]: the lanes of a
-    // warp, which write eight channels apart, meet different banks
+    // word `w` (four tokens) of channel c lies at tile[c][w ^ 4 (c / 8 mod 4)]: the lanes of
+    // a warp, which write eight channels apart, spread over the banks, and four words of
+    // a channel stay together
 #pragma unroll
     for (int i = 0; i < kLoads; i += 4) {
       const int w = token(i) / 4;
       if (tid < kActive) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          tile[(ch + j) * (kKvBlock / 4) + (w ^ ((ch >> 3) & 15))] =
+          tile[(ch + j) * (kKvBlock / 4) + (w ^ (((ch >> 3) & 3) * 4))] =
               f8_pack2(x[i].get(j) * r, x[i + 1].get(j) * r) | (f8_pack2(x[i + 2].get(j) * r, x[i + 3].get(j) * r) << 16);
       }
     }
     __syncthreads();
-    // the words with new tokens, and with held ones to move; bytes of no token stay
-    const int w_lo = move ? 0 : held / 4, w_n = (end + 3) / 4 - w_lo;
-    for (int i = tid; i < D * w_n; i += kKvAppendThreads) {
-      const int c = w_n == kKvBlock / 4 ? i / (kKvBlock / 4) : i / w_n, at_w = w_lo + i - c * w_n, tok = at_w * 4;
-      uint32_t *at = reinterpret_cast<uint32_t *>(dst) + c * (kKvBlock / 4) + at_w;
-      const int lo = held - tok, hi = end - tok;  // bytes [lo, hi) are new
-      uint32_t w = tile[c * (kKvBlock / 4) + (at_w ^ ((c >> 3) & 15))];
-      if (lo > 0 || hi < 4) {
-        const uint32_t was = *at;
-        const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
-        const uint32_t above = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1);                       // bytes of no token
-        w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
+    // sixteen tokens of a channel at a time: with new ones, and with held ones to move;
+    // bytes of no token stay
+    const int q_lo = move ? 0 : held / 16, q_n = (end + 15) / 16 - q_lo;
+    for (int i = tid; i < D * q_n; i += kKvAppendThreads) {
+      const int c = q_n == 4 ? i / 4 : q_n == 1 ? i : i / q_n, at_q = q_lo + i - c * q_n, tok0 = at_q * 16;
+      const uint32_t *from = tile + c * (kKvBlock / 4) + (at_q ^ ((c >> 3) & 3)) * 4;
+      uint32_t *at = reinterpret_cast<uint32_t *>(dst) + c * (kKvBlock / 4) + at_q * 4;
+      if (tok0 >= held && tok0 + 16 <= end) {
+        *reinterpret_cast<uint4 *>(at) = *reinterpret_cast<const uint4 *>(from);
+        continue;
       }
-      *at = w;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int lo = held - (tok0 + 4 * k), hi = end - (tok0 + 4 * k);  // bytes [lo, hi) of the word are new
+        if (hi <= 0 || (!move && lo >= 4)) continue;
+        uint32_t w = from[k];
+        if (lo > 0 || hi < 4) {
+          const uint32_t was = at[k];
+          const uint32_t below = lo >= 4 ? 0xffffffffu : lo > 0 ? (1u << (8 * lo)) - 1 : 0u;  // held bytes
+          const uint32_t above = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1);                       // bytes of no token
+          w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
+        }
+        at[k] = w;
+      }
     }
   }
 }
