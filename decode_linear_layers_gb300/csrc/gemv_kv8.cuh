@@ -71,7 +71,9 @@ __device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float r) {
 // its values): it reads a unit's new tokens once (eight values of a token per load), finds
 // their largest, and so the unit's scale; where that grows it moves the tokens the block
 // held to the new scale; and it writes the new ones.  No other CTA touches the unit, so
-// nothing is atomic.  Values pass through shared memory to lie token-innermost.
+// nothing is atomic.  Values pass through shared memory to lie token-innermost.  Bound by
+// latency (lengths, table, tokens, one after the other) and instructions: 64 sequences of
+// one new token 6 us, 5 prompts of 10 k tokens in all 17 us (67 MB: 9.8 at the copy rate).
 constexpr int kKvAppendThreads = 256;
 template <int D, int DT>
 __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
@@ -433,6 +435,11 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 // product is added to the running sums.
 // At the end of an item (or of the range) the warp writes the output, or a partial
 // result that k_kv8_join adds up.
+// Decode is bound by the cache's bytes: 64 sequences of up to 8192 tokens (537 MB) 94 us,
+// 5.7 TB/s with the join; one of 131072 tokens 53 us.  mma.sync at a sixth of its rate is
+// enough for that, and takes eight rows where tcgen05 would take 128.  More rows a block
+// (16 with 128 channels: 38 us where the bytes take 18) are bound by the latency of eight
+// warps' dependent instructions; their registers allow no more.
 template <int D, int NT, bool kWhole>
 __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(const KvArgs a) {
   using F = KvForm<D, NT>;
@@ -956,7 +963,8 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
 // order of the blocks; and the outputs of sequences without tokens: zeros.  A thread adds
 // up four channels of a row, eight parts on their way at a time; kGroups warps share the
 // parts of the same channels, where there are few items, each perhaps in a hundred parts.
-// grid (S, items, pieces of a tile's rows).
+// grid (S, items, pieces of a tile's rows).  Three dependent reads: 2 to 6 us after the
+// attention kernel.
 constexpr int kKvJoinThreads = 256;
 struct KvSum {  // a row's (part of a) softmax: largest logit, sum of weights, weighted values
   float m = -INFINITY, den = 0.f;
