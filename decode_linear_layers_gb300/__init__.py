@@ -12,7 +12,8 @@ The names and argument order are those of ``include/gemv.h``:
     gemv_kv8_attention(dtype, *cache, q, lens, out, lse, S, T, q_heads, scale,
                        window=0, sinks=0, stream=None)
 
-(``cache``: k, v, k_scale, v_scale, table, whose shapes give the sizes).
+(``cache``: k, v, k_scale, v_scale, table: tensors, whose shapes give the sizes; k, v and
+q are tensors, too, whose strides give the distance of their rows).
 
 Buffers may be torch CUDA tensors (checked for device, contiguity, element size
 and minimum length before the call) or raw device addresses (ints, unchecked).

@@ -70,8 +70,8 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   }
   a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
-  if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group, true) ||
-      !map_bytes(&map_x, x, a.B, K, kPrompt ? kF8Rows : N, kF8Group, true))
+  if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group) ||
+      !map_bytes(&map_x, x, a.B, K, kPrompt ? kF8Rows : N, kF8Group))
     return fail((int)cudaErrorInvalidValue);
   void *ws = nullptr;
   if (a.shared > 0) {
@@ -107,7 +107,7 @@ gemv_status_t f8_launch_pair(F8Args a, const void *A, const void *x, int64_t K, 
   cudaError_t e = allow_smem_once<k_f8_pair>(F::kSmem);
   if (e != cudaSuccess) return fail((int)e);
   CUtensorMap map_a, map_x;
-  if (!map_bytes(&map_a, A, a.M, K, 128, kF8Group, true) || !map_bytes(&map_x, x, a.B, K, 128, kF8Group, true))
+  if (!map_bytes(&map_a, A, a.M, K, 128, kF8Group) || !map_bytes(&map_x, x, a.B, K, 128, kF8Group))
     return fail((int)cudaErrorInvalidValue);
   e = launch_k_cluster_x(k_f8_pair, dim3((unsigned)(2 * pairs)), dim3(F::kThreads), (size_t)F::kSmem, s, launch_overlap(), 2,
                          map_x, map_a, a);

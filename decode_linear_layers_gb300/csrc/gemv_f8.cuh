@@ -21,7 +21,6 @@ constexpr int kF8Group = 128;    // columns per scale, and per k-block: one 128-
 constexpr int kF8Rows = 128;     // rows of a tile: the MMA's M
 constexpr int kF8RoleThreads = 128;  // warps 0 (copies), 1 (MMAs) and 2 (scales), one idle
 constexpr int kF8MaxStages = 12;
-constexpr int kF8TileM = 256;    // weight rows of a tile of the prompt form
 
 struct F8Args {
   const float *a_scale = nullptr, *x_scale = nullptr;
@@ -36,7 +35,7 @@ struct F8Args {
   int sharers = 0;       // CTAs that the shared tiles are split over
   int slices = 1;        // or: CTAs of the cluster that each tile is split over
   int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
-  int y_dtype = 0, stages = 0, test_stall = 0;
+  int y_dtype = 0, test_stall = 0;
 };
 
 // A bounded wait of one of several cooperating threads: false after timeout_ns, or once
@@ -1073,37 +1072,6 @@ __device__ __forceinline__ float f8_finite_abs(float v) {
   const float m = fabsf(v);
   return m < __int_as_float(0x7f800000) ? m : 0.f;
 }
-template <int DT>
-__device__ __forceinline__ float f8_load1(const void *p, int64_t i) {
-  if constexpr (DT == GEMV_DTYPE_F32) return __ldg(reinterpret_cast<const float *>(p) + i);
-  const unsigned short h = __ldg(reinterpret_cast<const unsigned short *>(p) + i);
-  if constexpr (DT == GEMV_DTYPE_F16) return __half2float(__ushort_as_half(h));
-  return __uint_as_float((uint32_t)h << 16);
-}
-template <int DT>
-__device__ __forceinline__ void f8_load8(const void *p, int64_t i, float (&v)[8]) {
-  if constexpr (DT == GEMV_DTYPE_F32) {
-    const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
-    const float4 a = __ldg(q), b = __ldg(q + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const unsigned short *>(p) + i));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (DT == GEMV_DTYPE_F16) {
-        const float2 f = f16x2_to_f2(w[e]);
-        v[2 * e] = f.x;
-        v[2 * e + 1] = f.y;
-      } else {
-        v[2 * e] = bf16_lo(w[e]);
-        v[2 * e + 1] = bf16_hi(w[e]);
-      }
-    }
-  }
-}
-
 // Eight lanes hold a group's 128 values, sixteen each, so the group is read once and its
 // largest value found by three shuffles.  kWide: how many consecutive ones a lane reads and
 // writes at a time: eight (rows of whole 16-byte pieces), two (rows of an even length) or

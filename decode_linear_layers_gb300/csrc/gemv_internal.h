@@ -24,9 +24,9 @@ gemv_status_t device_status_word(int **out);
 int64_t wait_limit(int *stall);
 // [p, p + n) and [q, q + m) share a byte.
 bool overlaps(const void *p, int64_t n, const void *q, int64_t m);
-// Tensor map of a row-major matrix of bytes, in boxes of box_rows x box_cols, zeros
-// outside; 128-byte swizzle or none.
-bool map_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows, int box_cols, bool swizzle);
+// Tensor map of a row-major matrix of bytes, in boxes of box_rows x box_cols (128-byte
+// swizzle), zeros outside.
+bool map_bytes(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int box_rows, int box_cols);
 // Stream-ordered memory from the library's own pool of the current device, which keeps
 // what it has mapped (the device's default pool gives it back at each synchronisation,
 // and mapping it again costs more than these kernels take).  Free with cudaFreeAsync.

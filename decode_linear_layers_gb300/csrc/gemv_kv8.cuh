@@ -471,476 +471,476 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
   bool dead = false;
   // by shares: one round; else (kWhole, short sequences) an item, whole, each round
   for (int64_t round = worker; !dead && (kWhole ? round < (int64_t)a.S * items : round == worker); round += workers) {
-  if constexpr (kWhole) {
-    const int s = (int)kv_div(round, items);
-    at.load(a, s, 0);
-    at.item = (int)(round - (int64_t)s * items);
-    u_lo = at.lo;
-    u_hi = at.hi;
-    if (u_lo >= u_hi) {  // no tokens
-      const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
-      for (int r = 0; r < NT * 8 && row0 + r < a.T * a.group; ++r) {
-        const int64_t at_row = kv_out_row(a, s, h, row0 + r);
-        for (int d = lane; d < D; d += 32) reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = 0;
-        if (lane == 0 && a.lse != nullptr) a.lse[at_row] = -INFINITY;
+    if constexpr (kWhole) {
+      const int s = (int)kv_div(round, items);
+      at.load(a, s, 0);
+      at.item = (int)(round - (int64_t)s * items);
+      u_lo = at.lo;
+      u_hi = at.hi;
+      if (u_lo >= u_hi) {  // no tokens
+        const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
+        for (int r = 0; r < NT * 8 && row0 + r < a.T * a.group; ++r) {
+          const int64_t at_row = kv_out_row(a, s, h, row0 + r);
+          for (int d = lane; d < D; d += 32) reinterpret_cast<unsigned short *>(a.out)[at_row * D + d] = 0;
+          if (lane == 0 && a.lse != nullptr) a.lse[at_row] = -INFINITY;
+        }
+        continue;
       }
-      continue;
-    }
-  } else {
-  shares.cut(kv_before(a, a.S, lane) * items, workers);
-  u_lo = shares.first(worker);
-  u_hi = shares.first(worker + 1);
-  if (u_lo >= u_hi) break;
+    } else {
+      shares.cut(kv_before(a, a.S, lane) * items, workers);
+      u_lo = shares.first(worker);
+      u_hi = shares.first(worker + 1);
+      if (u_lo >= u_hi) break;
 
-  // the item of place u_lo
-  int64_t base = 0;
-  for (int s0 = 0;; s0 += 32) {  // 32 sequences at a time
-    const int s = s0 + lane;
-    unsigned n = s < a.S ? (unsigned)kv_places(kv_seen(a, s)) : 0u;
+      // the item of place u_lo
+      int64_t base = 0;
+      for (int s0 = 0;; s0 += 32) {  // 32 sequences at a time
+        const int s = s0 + lane;
+        unsigned n = s < a.S ? (unsigned)kv_places(kv_seen(a, s)) : 0u;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned o = __shfl_up_sync(0xffffffffu, n, d);
-      if (lane >= d) n += o;
+        for (int d = 1; d < 32; d <<= 1) {
+          const unsigned o = __shfl_up_sync(0xffffffffu, n, d);
+          if (lane >= d) n += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + (int64_t)n * items > u_lo);
+        if (past != 0) {
+          const int f = __ffs(past) - 1;
+          const unsigned before = __shfl_sync(0xffffffffu, n, f > 0 ? f - 1 : 0);
+          at.load(a, s0 + f, base + (f > 0 ? (int64_t)before * items : 0));
+          at.skip(kv_div(u_lo - (at.lo - kKvItemCost), kv_places(at.seen)));
+          break;
+        }
+        base += (int64_t)__shfl_sync(0xffffffffu, n, 31) * items;
+      }
     }
-    const unsigned past = __ballot_sync(0xffffffffu, base + (int64_t)n * items > u_lo);
-    if (past != 0) {
-      const int f = __ffs(past) - 1;
-      const unsigned before = __shfl_sync(0xffffffffu, n, f > 0 ? f - 1 : 0);
-      at.load(a, s0 + f, base + (f > 0 ? (int64_t)before * items : 0));
-      at.skip(kv_div(u_lo - (at.lo - kKvItemCost), kv_places(at.seen)));
-      break;
-    }
-    base += (int64_t)__shfl_sync(0xffffffffu, n, 31) * items;
-  }
-  }
 
-  // An item's queries as stored: rows g of its tiles, 16 channels 16 c .. of each 64.  The
-  // first item's are on their way before the blocks are: behind those they would wait.
-  const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
-  constexpr bool kEarly = NT * DT <= 16;  // (more would not stay in registers)
-  uint32_t raw[NT][DT][2];
-  auto load_q = [&](const KvItem &it) {
-    const int h = it.item / a.row_tiles, row0 = (it.item - h * a.row_tiles) * NT * 8;
+    // An item's queries as stored: rows g of its tiles, 16 channels 16 c .. of each 64.  The
+    // first item's are on their way before the blocks are: behind those they would wait.
+    const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
+    constexpr bool kEarly = NT * DT <= 16;  // (more would not stay in registers)
+    uint32_t raw[NT][DT][2];
+    auto load_q = [&](const KvItem &it) {
+      const int h = it.item / a.row_tiles, row0 = (it.item - h * a.row_tiles) * NT * 8;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = row0 + n * 8 + g, t = row / a.group;
-      const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)it.s * a.T + t) * a.q_stride +
-                                 ((int64_t)h * a.group + row - t * a.group) * D + 16 * c;
+      for (int n = 0; n < NT; ++n) {
+        const int row = row0 + n * 8 + g, t = row / a.group;
+        const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)it.s * a.T + t) * a.q_stride +
+                                   ((int64_t)h * a.group + row - t * a.group) * D + 16 * c;
 #pragma unroll
-      for (int i = 0; i < DT; ++i) raw[n][i][0] = raw[n][i][1] = 0;
-      if (row < a.T * a.group) {
-        if (q_vec) {
+        for (int i = 0; i < DT; ++i) raw[n][i][0] = raw[n][i][1] = 0;
+        if (row < a.T * a.group) {
+          if (q_vec) {
 #pragma unroll
-          for (int i = 0; i < DT; i += 2) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + (i >> 2) * 64 + (i & 3) * 4));
-            raw[n][i][0] = v.x;
-            raw[n][i][1] = v.y;
-            raw[n][i + 1][0] = v.z;
-            raw[n][i + 1][1] = v.w;
+            for (int i = 0; i < DT; i += 2) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + (i >> 2) * 64 + (i & 3) * 4));
+              raw[n][i][0] = v.x;
+              raw[n][i][1] = v.y;
+              raw[n][i + 1][0] = v.z;
+              raw[n][i + 1][1] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+              const uint2 v = kv_load4(qp + (i >> 2) * 64 + (i & 3) * 4);
+              raw[n][i][0] = v.x;
+              raw[n][i][1] = v.y;
+            }
           }
+        }
+      }
+    };
+
+    // ---- copies: the pieces of this warp's blocks
+    KvItem is = at;                          // the item of place `iu`
+    int64_t iu = u_lo > at.lo ? u_lo : at.lo;
+    int batch = -1;                          // first of the item's blocks whose table entries the lanes hold
+    int32_t entries = 0;
+    auto look = [&](int j) {
+      batch = j;
+      const int i = j + lane;
+      entries = -1;
+      if (i < is.seen.count)
+        entries = __ldg(a.table + (int64_t)is.s * a.width + (i < is.seen.sink ? i : is.seen.from + i - is.seen.sink));
+    };
+    // the next block: its number in the pool x heads + head; -1: none is left, -2 - head:
+    // the table's entry is none of the pool
+    auto advance = [&]() -> int64_t {
+      if (iu >= u_hi) return -1;
+      const int j = (int)(iu - is.lo), h = is.item / a.row_tiles;
+      if (batch < 0 || j >= batch + 32) look(j);
+      const int32_t entry = __shfl_sync(0xffffffffu, entries, j - batch);
+      if (++iu == is.hi) {
+        if (iu + kKvItemCost < u_hi) {
+          is.seek(a, iu);
+          iu = is.lo;
+          batch = -1;
         } else {
-#pragma unroll
-          for (int i = 0; i < DT; ++i) {
-            const uint2 v = kv_load4(qp + (i >> 2) * 64 + (i & 3) * 4);
-            raw[n][i][0] = v.x;
-            raw[n][i][1] = v.y;
-          }
+          iu = u_hi;
         }
       }
-    }
-  };
-
-  // ---- copies: the pieces of this warp's blocks
-  KvItem is = at;                          // the item of place `iu`
-  int64_t iu = u_lo > at.lo ? u_lo : at.lo;
-  int batch = -1;                          // first of the item's blocks whose table entries the lanes hold
-  int32_t entries = 0;
-  auto look = [&](int j) {
-    batch = j;
-    const int i = j + lane;
-    entries = -1;
-    if (i < is.seen.count)
-      entries = __ldg(a.table + (int64_t)is.s * a.width + (i < is.seen.sink ? i : is.seen.from + i - is.seen.sink));
-  };
-  // the next block: its number in the pool x heads + head; -1: none is left, -2 - head:
-  // the table's entry is none of the pool
-  auto advance = [&]() -> int64_t {
-    if (iu >= u_hi) return -1;
-    const int j = (int)(iu - is.lo), h = is.item / a.row_tiles;
-    if (batch < 0 || j >= batch + 32) look(j);
-    const int32_t entry = __shfl_sync(0xffffffffu, entries, j - batch);
-    if (++iu == is.hi) {
-      if (iu + kKvItemCost < u_hi) {
-        is.seek(a, iu);
-        iu = is.lo;
-        batch = -1;
-      } else {
-        iu = u_hi;
+      return entry >= 0 && entry < a.blocks ? (int64_t)entry * a.heads + h : -2 - (int64_t)h;
+    };
+    auto issue = [&](int64_t block, bool keys, int to) {
+      if (block == -1) return;
+      if (lane == 0) {
+        const bool good = block >= 0;
+        const int64_t at_block = good ? block : -2 - block;  // (of an entry that is no block: any, unseen)
+        uint64_t *b = &bar[to];
+        if (keys) {
+          meta_bad[warp * R + to] = !good;
+          if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+          f8_copy4(&meta[warp * R + to][0], a.k_scale + at_block, true);
+          f8_copy4(&meta[warp * R + to][1], a.v_scale + at_block, true);
+          f8_copy4_arrive(b);
+        } else {
+          tc_mbar_arrive(b);
+        }
+        if (!a.test_stall || keys) {  // test: no values ever come
+          tc_mbar_arrive_expect_tx(b, F::kSlot);
+          kv_bulk(ring + (size_t)to * F::kSlot, (keys ? a.k : a.v) + at_block * F::kSlot, F::kSlot, b);
+        }
       }
+      ++issued;
+    };
+    if (iu < u_hi) {
+      look((int)(iu - is.lo));
+      if constexpr (kEarly) load_q(at);
     }
-    return entry >= 0 && entry < a.blocks ? (int64_t)entry * a.heads + h : -2 - (int64_t)h;
-  };
-  auto issue = [&](int64_t block, bool keys, int to) {
-    if (block == -1) return;
-    if (lane == 0) {
-      const bool good = block >= 0;
-      const int64_t at_block = good ? block : -2 - block;  // (of an entry that is no block: any, unseen)
-      uint64_t *b = &bar[to];
-      if (keys) {
-        meta_bad[warp * R + to] = !good;
-        if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-        f8_copy4(&meta[warp * R + to][0], a.k_scale + at_block, true);
-        f8_copy4(&meta[warp * R + to][1], a.v_scale + at_block, true);
-        f8_copy4_arrive(b);
-      } else {
-        tc_mbar_arrive(b);
-      }
-      if (!a.test_stall || keys) {  // test: no values ever come
-        tc_mbar_arrive_expect_tx(b, F::kSlot);
-        kv_bulk(ring + (size_t)to * F::kSlot, (keys ? a.k : a.v) + at_block * F::kSlot, F::kSlot, b);
-      }
-    }
-    ++issued;
-  };
-  if (iu < u_hi) {
-    look((int)(iu - is.lo));
-    if constexpr (kEarly) load_q(at);
-  }
-  // While block n's keys are used, the ring holds its values and the R - 2 pieces after
-  // them; the slot of the keys takes the values of block n + R / 2 (`ahead`), that of its
-  // values the keys of the block after that.
-  static_assert(R % 2 == 1);
-  int64_t ahead;
-  {
-    ahead = advance();
-    int to = slot;
-    auto next = [&]() { return to = to + 1 == R ? 0 : to + 1; };
-#pragma unroll 1
-    for (int i = 0; i + 1 < R; i += 2) {
-      issue(ahead, true, to);
-      issue(ahead, false, next());
-      next();
-      if (ahead != -1) ahead = advance();
-    }
-    issue(ahead, true, to);
-  }
-
-  auto arrived = [&]() {
-    const bool ok = f8_wait(&bar[slot], phase, a.timeout_ns, &abort_flag);
-    dead = !__all_sync(0xffffffffu, ok);
-    return !dead;
-  };
-  auto release = [&](bool keys) {
-    __syncwarp();  // every lane has read the slot
-    if (!keys && ahead != -1) ahead = advance();
-    issue(ahead, !keys, slot);
-    ++taken;
-    if (++slot == R) {
-      slot = 0;
-      phase ^= 1;
-    }
-  };
-
-  bool first_item = true;
-  int64_t u = u_lo > at.lo ? u_lo : at.lo;
-  while (u < u_hi) {
-    const int64_t seg = u, seg_end = at.hi < u_hi ? at.hi : u_hi;
-    const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
-    const int rows = a.T * a.group - row0;  // of this tile, at most NT * 8
-    const int len = at.seen.len;
-
-    // Q's registers: row g of each tile, in the order of the key pieces.  Each row is
-    // scaled by a power of two so that its largest value lies in [2^14, 2^15): fp16
-    // then holds what is within 2^-28 of it as the input does.
-    uint32_t qf[NT][DT][2];
-    float qs[NT][2];  // factor of the logits of rows 2 c, 2 c + 1: softmax scale x log2 e / that power
-    if (!kEarly || !first_item) load_q(at);
+    // While block n's keys are used, the ring holds its values and the R - 2 pieces after
+    // them; the slot of the keys takes the values of block n + R / 2 (`ahead`), that of its
+    // values the keys of the block after that.
+    static_assert(R % 2 == 1);
+    int64_t ahead;
     {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // (an infinity takes the largest exponent: the row's result is NaN, or 0, with it)
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) top = kv_max2(top, raw[n][i][e] & 0x7fff7fffu, a.dtype);
-        float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int e = (__float_as_int(mx) >> 23) & 0xff;  // exponent field, 127 for [1, 2)
-        e = e < 16 ? 16 : e;
-        const float up = __int_as_float((127 + 14 + 127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            qf[n][i][k] = kv_pack_half(kv_wide_lo(raw[n][i][k], a.dtype) * up, kv_wide_hi(raw[n][i][k], a.dtype) * up);
-        const float f = a.scale_log2 / up;
-        qs[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
-        qs[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-      }
-    }
-
-    float o[NT][DT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
-    }
-
-    for (; u < seg_end; ++u) {
-      const int j = (int)(u - at.lo);
-      const int64_t pos0 = (int64_t)(j < at.seen.sink ? j : at.seen.from + j - at.seen.sink) * kKvBlock;
-      if (!arrived()) break;
-      const float ks = meta[warp * R + slot][0];
-      const bool bad = meta_bad[warp * R + slot] != 0;  // no such block: nothing of it is seen
-      const float vs = bad ? 0.f : meta[warp * R + slot][1];
-      // does every query see every token of the block?
-      const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
-                        (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
-      // bit `tok`: query t sees that token of the block
-      auto mask = [&](int t) {
-        const int64_t i = (int64_t)len - a.T + t - pos0;  // the query's position, from the block's start
-        uint64_t w = kv_low_bits(i + 1);
-        if (a.window > 0) w &= ~kv_low_bits(i + 1 - a.window) | kv_low_bits(a.sinks - pos0);
-        return bad ? 0ull : w;
-      };
-
-      // ---- logits: tile j holds tokens 16 (r / 2) + 4 j + r % 2 (rows r = 0..7 of the
-      // tile) and those + 2 (rows 8..15)
-      float s[NT][4][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
-      const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(kp + (4 * t) * D + 64 * q);
-          const uint4 y = *reinterpret_cast<const uint4 *>(kp + (4 * t + 2) * D + 64 * q);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t f[4] = {kv_half2_lo(xw[i]), kv_half2_lo(yw[i]), kv_half2_hi(xw[i]), kv_half2_hi(yw[i])};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) kv_mma(s[n][t], f, qf[n][q * 4 + i][0], qf[n][q * 4 + i][1]);
-          }
-        }
-      release(true);
-
-      // ---- weights
-      uint32_t p[NT][4][2];
-      float keep[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float f0 = qs[n][0] * ks, f1 = qs[n][1] * ks;
-        float m0 = m[n][0], m1 = m[n][1];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          s[n][t][0] *= f0;
-          s[n][t][1] *= f1;
-          s[n][t][2] *= f0;
-          s[n][t][3] *= f1;
-        }
-        if (edge) {
-          // the tokens that the queries of rows 2 c, 2 c + 1 see, from this lane's first on
-          const int r0 = row0 + n * 8 + 2 * c, first = 16 * (g >> 1) + (g & 1);
-          const uint32_t wa = (uint32_t)(mask(r0 / a.group) >> first), wb = (uint32_t)(mask((r0 + 1) / a.group) >> first);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (!(wa >> (4 * t) & 1)) s[n][t][0] = -INFINITY;
-            if (!(wb >> (4 * t) & 1)) s[n][t][1] = -INFINITY;
-            if (!(wa >> (4 * t + 2) & 1)) s[n][t][2] = -INFINITY;
-            if (!(wb >> (4 * t + 2) & 1)) s[n][t][3] = -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          m0 = fmaxf(m0, fmaxf(s[n][t][0], s[n][t][2]));
-          m1 = fmaxf(m1, fmaxf(s[n][t][1], s[n][t][3]));
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-          m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-        }
-        // a row that has seen nothing yet: any finite reference leaves its weights 0
-        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-        keep[n][0] = kv_exp2(m[n][0] - z0);
-        keep[n][1] = kv_exp2(m[n][1] - z1);
-        m[n][0] = m0;
-        m[n][1] = m1;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float w0 = kv_exp2(s[n][t][0] - z0 + kKvLift), w1 = kv_exp2(s[n][t][1] - z1 + kKvLift);
-          const float w2 = kv_exp2(s[n][t][2] - z0 + kKvLift), w3 = kv_exp2(s[n][t][3] - z1 + kKvLift);
-          l0 += w0 + w2;
-          l1 += w1 + w3;
-          p[n][t][0] = kv_transpose(kv_pack_half(w0, w1));
-          p[n][t][1] = kv_transpose(kv_pack_half(w2, w3));
-        }
-        // (this lane's tokens; the lanes' sums meet at the end)
-        l[n][0] = l[n][0] * keep[n][0] + l0;
-        l[n][1] = l[n][1] * keep[n][1] + l1;
-      }
-
-      // ---- sums
-      // Values that no query of the tile sees may be anything, NaN among it: they count as
-      // 0.  So do, to a query, those that only others see: their weights are 0; unless
-      // they are NaN, then its product leaves them out.
-      uint32_t keep4[4] = {~0u, ~0u, ~0u, ~0u};  // the bytes that count, tile t of tokens
-      bool mixed = false;                        // some queries see what others do not
-      if (edge) {
-        const int t_lo = row0 / a.group, t_hi = (row0 + (rows < NT * 8 ? rows : NT * 8) - 1) / a.group;
-        uint64_t some = 0, all = ~0ull;
-        for (int q = t_lo; q <= t_hi; ++q) {
-          some |= mask(q);
-          all &= mask(q);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(some >> (16 * c + 4 * t)));
-        mixed = some != all;
-      }
-      if (!arrived()) break;
-      const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
-      // channels 16 k ..: V^T's registers, tile t of tokens
-      auto load_v = [&](int k, uint32_t (&f)[4][4]) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 16 * kKvBlock);
-        const uint4 y = *reinterpret_cast<const uint4 *>(vp + (k * 16 + 8) * kKvBlock);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t xm = xw[t] & keep4[t], ym = yw[t] & keep4[t];
-          f[t][0] = kv_half2_lo(xm);
-          f[t][1] = kv_half2_lo(ym);
-          f[t][2] = kv_half2_hi(xm);
-          f[t][3] = kv_half2_hi(ym);
-        }
-      };
-      bool nan = false;
-      if (mixed) {
+      ahead = advance();
+      int to = slot;
+      auto next = [&]() { return to = to + 1 == R ? 0 : to + 1; };
 #pragma unroll 1
-        for (int k = 0; k < 2 * DT; ++k) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 8 * kKvBlock);
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int t = 0; t < 4; ++t) nan |= __vcmpeq4(xw[t] & keep4[t] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-        }
-        nan = __any_sync(0xffffffffu, nan);
+      for (int i = 0; i + 1 < R; i += 2) {
+        issue(ahead, true, to);
+        issue(ahead, false, next());
+        next();
+        if (ahead != -1) ahead = advance();
       }
-      if (!nan) {
-#pragma unroll
-        for (int k = 0; k < DT; ++k) {
-          uint32_t f[4][4];
-          load_v(k, f);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            float(&acc)[4] = o[n][k];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
-            acc[0] = fmaf(vs, d[0], acc[0] * keep[n][0]);
-            acc[1] = fmaf(vs, d[1], acc[1] * keep[n][1]);
-            acc[2] = fmaf(vs, d[2], acc[2] * keep[n][0]);
-            acc[3] = fmaf(vs, d[3], acc[3] * keep[n][1]);
-          }
-        }
-      } else {
-        // for each query of a tile of rows the product with the values that it sees,
-        // for its rows only
-        const uint32_t any4[4] = {keep4[0], keep4[1], keep4[2], keep4[3]};
+      issue(ahead, true, to);
+    }
+
+    auto arrived = [&]() {
+      const bool ok = f8_wait(&bar[slot], phase, a.timeout_ns, &abort_flag);
+      dead = !__all_sync(0xffffffffu, ok);
+      return !dead;
+    };
+    auto release = [&](bool keys) {
+      __syncwarp();  // every lane has read the slot
+      if (!keys && ahead != -1) ahead = advance();
+      issue(ahead, !keys, slot);
+      ++taken;
+      if (++slot == R) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+
+    bool first_item = true;
+    int64_t u = u_lo > at.lo ? u_lo : at.lo;
+    while (u < u_hi) {
+      const int64_t seg = u, seg_end = at.hi < u_hi ? at.hi : u_hi;
+      const int h = at.item / a.row_tiles, row0 = (at.item - h * a.row_tiles) * NT * 8;
+      const int rows = a.T * a.group - row0;  // of this tile, at most NT * 8
+      const int len = at.seen.len;
+
+      // Q's registers: row g of each tile, in the order of the key pieces.  Each row is
+      // scaled by a power of two so that its largest value lies in [2^14, 2^15): fp16
+      // then holds what is within 2^-28 of it as the input does.
+      uint32_t qf[NT][DT][2];
+      float qs[NT][2];  // factor of the logits of rows 2 c, 2 c + 1: softmax scale x log2 e / that power
+      if (!kEarly || !first_item) load_q(at);
+      {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
-          const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+          // (an infinity takes the largest exponent: the row's result is NaN, or 0, with it)
+          uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < DT; ++k)
+          for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[n][e & 1];
+            for (int e = 0; e < 2; ++e) top = kv_max2(top, raw[n][i][e] & 0x7fff7fffu, a.dtype);
+          float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int e = (__float_as_int(mx) >> 23) & 0xff;  // exponent field, 127 for [1, 2)
+          e = e < 16 ? 16 : e;
+          const float up = __int_as_float((127 + 14 + 127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              qf[n][i][k] = kv_pack_half(kv_wide_lo(raw[n][i][k], a.dtype) * up, kv_wide_hi(raw[n][i][k], a.dtype) * up);
+          const float f = a.scale_log2 / up;
+          qs[n][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+          qs[n][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+        }
+      }
+
+      float o[NT][DT][4], m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+      }
+
+      for (; u < seg_end; ++u) {
+        const int j = (int)(u - at.lo);
+        const int64_t pos0 = (int64_t)(j < at.seen.sink ? j : at.seen.from + j - at.seen.sink) * kKvBlock;
+        if (!arrived()) break;
+        const float ks = meta[warp * R + slot][0];
+        const bool bad = meta_bad[warp * R + slot] != 0;  // no such block: nothing of it is seen
+        const float vs = bad ? 0.f : meta[warp * R + slot][1];
+        // does every query see every token of the block?
+        const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
+                          (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
+        // bit `tok`: query t sees that token of the block
+        auto mask = [&](int t) {
+          const int64_t i = (int64_t)len - a.T + t - pos0;  // the query's position, from the block's start
+          uint64_t w = kv_low_bits(i + 1);
+          if (a.window > 0) w &= ~kv_low_bits(i + 1 - a.window) | kv_low_bits(a.sinks - pos0);
+          return bad ? 0ull : w;
+        };
+
+        // ---- logits: tile j holds tokens 16 (r / 2) + 4 j + r % 2 (rows r = 0..7 of the
+        // tile) and those + 2 (rows 8..15)
+        float s[NT][4][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][t][e] = 0.f;
+        const unsigned char *kp = ring + (size_t)slot * F::kSlot + (16 * (g >> 1) + (g & 1)) * D + 16 * c;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kp + (4 * t) * D + 64 * q);
+            const uint4 y = *reinterpret_cast<const uint4 *>(kp + (4 * t + 2) * D + 64 * q);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t f[4] = {kv_half2_lo(xw[i]), kv_half2_lo(yw[i]), kv_half2_hi(xw[i]), kv_half2_hi(yw[i])};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) kv_mma(s[n][t], f, qf[n][q * 4 + i][0], qf[n][q * 4 + i][1]);
+            }
+          }
+        release(true);
+
+        // ---- weights
+        uint32_t p[NT][4][2];
+        float keep[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float f0 = qs[n][0] * ks, f1 = qs[n][1] * ks;
+          float m0 = m[n][0], m1 = m[n][1];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            s[n][t][0] *= f0;
+            s[n][t][1] *= f1;
+            s[n][t][2] *= f0;
+            s[n][t][3] *= f1;
+          }
+          if (edge) {
+            // the tokens that the queries of rows 2 c, 2 c + 1 see, from this lane's first on
+            const int r0 = row0 + n * 8 + 2 * c, first = 16 * (g >> 1) + (g & 1);
+            const uint32_t wa = (uint32_t)(mask(r0 / a.group) >> first), wb = (uint32_t)(mask((r0 + 1) / a.group) >> first);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              if (!(wa >> (4 * t) & 1)) s[n][t][0] = -INFINITY;
+              if (!(wb >> (4 * t) & 1)) s[n][t][1] = -INFINITY;
+              if (!(wa >> (4 * t + 2) & 1)) s[n][t][2] = -INFINITY;
+              if (!(wb >> (4 * t + 2) & 1)) s[n][t][3] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            m0 = fmaxf(m0, fmaxf(s[n][t][0], s[n][t][2]));
+            m1 = fmaxf(m1, fmaxf(s[n][t][1], s[n][t][3]));
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+          }
+          // a row that has seen nothing yet: any finite reference leaves its weights 0
+          const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+          keep[n][0] = kv_exp2(m[n][0] - z0);
+          keep[n][1] = kv_exp2(m[n][1] - z1);
+          m[n][0] = m0;
+          m[n][1] = m1;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float w0 = kv_exp2(s[n][t][0] - z0 + kKvLift), w1 = kv_exp2(s[n][t][1] - z1 + kKvLift);
+            const float w2 = kv_exp2(s[n][t][2] - z0 + kKvLift), w3 = kv_exp2(s[n][t][3] - z1 + kKvLift);
+            l0 += w0 + w2;
+            l1 += w1 + w3;
+            p[n][t][0] = kv_transpose(kv_pack_half(w0, w1));
+            p[n][t][1] = kv_transpose(kv_pack_half(w2, w3));
+          }
+          // (this lane's tokens; the lanes' sums meet at the end)
+          l[n][0] = l[n][0] * keep[n][0] + l0;
+          l[n][1] = l[n][1] * keep[n][1] + l1;
+        }
+
+        // ---- sums
+        // Values that no query of the tile sees may be anything, NaN among it: they count as
+        // 0.  So do, to a query, those that only others see: their weights are 0; unless
+        // they are NaN, then its product leaves them out.
+        uint32_t keep4[4] = {~0u, ~0u, ~0u, ~0u};  // the bytes that count, tile t of tokens
+        bool mixed = false;                        // some queries see what others do not
+        if (edge) {
+          const int t_lo = row0 / a.group, t_hi = (row0 + (rows < NT * 8 ? rows : NT * 8) - 1) / a.group;
+          uint64_t some = 0, all = ~0ull;
+          for (int q = t_lo; q <= t_hi; ++q) {
+            some |= mask(q);
+            all &= mask(q);
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(some >> (16 * c + 4 * t)));
+          mixed = some != all;
+        }
+        if (!arrived()) break;
+        const unsigned char *vp = ring + (size_t)slot * F::kSlot + g * kKvBlock + 16 * c;
+        // channels 16 k ..: V^T's registers, tile t of tokens
+        auto load_v = [&](int k, uint32_t (&f)[4][4]) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 16 * kKvBlock);
+          const uint4 y = *reinterpret_cast<const uint4 *>(vp + (k * 16 + 8) * kKvBlock);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t xm = xw[t] & keep4[t], ym = yw[t] & keep4[t];
+            f[t][0] = kv_half2_lo(xm);
+            f[t][1] = kv_half2_lo(ym);
+            f[t][2] = kv_half2_hi(xm);
+            f[t][3] = kv_half2_hi(ym);
+          }
+        };
+        bool nan = false;
+        if (mixed) {
 #pragma unroll 1
-          for (int t1 = r_lo / a.group; t1 <= r_hi / a.group; ++t1) {
-            const uint64_t w = mask(t1);
+          for (int k = 0; k < 2 * DT; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(vp + k * 8 * kKvBlock);
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(w >> (16 * c + 4 * t)));
+            for (int t = 0; t < 4; ++t) nan |= __vcmpeq4(xw[t] & keep4[t] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+          }
+          nan = __any_sync(0xffffffffu, nan);
+        }
+        if (!nan) {
 #pragma unroll
-            for (int k = 0; k < DT; ++k) {
-              uint32_t f[4][4];
-              load_v(k, f);
+          for (int k = 0; k < DT; ++k) {
+            uint32_t f[4][4];
+            load_v(k, f);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
               float d[4] = {0.f, 0.f, 0.f, 0.f};
               float(&acc)[4] = o[n][k];
 #pragma unroll
               for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
-              if (ta == t1) {
-                acc[0] = fmaf(vs, d[0], acc[0]);
-                acc[2] = fmaf(vs, d[2], acc[2]);
-              }
-              if (tb == t1) {
-                acc[1] = fmaf(vs, d[1], acc[1]);
-                acc[3] = fmaf(vs, d[3], acc[3]);
+              acc[0] = fmaf(vs, d[0], acc[0] * keep[n][0]);
+              acc[1] = fmaf(vs, d[1], acc[1] * keep[n][1]);
+              acc[2] = fmaf(vs, d[2], acc[2] * keep[n][0]);
+              acc[3] = fmaf(vs, d[3], acc[3] * keep[n][1]);
+            }
+          }
+        } else {
+          // for each query of a tile of rows the product with the values that it sees,
+          // for its rows only
+          const uint32_t any4[4] = {keep4[0], keep4[1], keep4[2], keep4[3]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int r_lo = row0 + n * 8, r_hi = r_lo + 7 < a.T * a.group - 1 ? r_lo + 7 : a.T * a.group - 1;
+            const int ta = (r_lo + 2 * c) / a.group, tb = (r_lo + 2 * c + 1) / a.group;
+#pragma unroll
+            for (int k = 0; k < DT; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[n][e & 1];
+#pragma unroll 1
+            for (int t1 = r_lo / a.group; t1 <= r_hi / a.group; ++t1) {
+              const uint64_t w = mask(t1);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) keep4[t] = kv_bytes((uint32_t)(w >> (16 * c + 4 * t)));
+#pragma unroll
+              for (int k = 0; k < DT; ++k) {
+                uint32_t f[4][4];
+                load_v(k, f);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                float(&acc)[4] = o[n][k];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) kv_mma(d, f[t], p[n][t][0], p[n][t][1]);
+                if (ta == t1) {
+                  acc[0] = fmaf(vs, d[0], acc[0]);
+                  acc[2] = fmaf(vs, d[2], acc[2]);
+                }
+                if (tb == t1) {
+                  acc[1] = fmaf(vs, d[1], acc[1]);
+                  acc[3] = fmaf(vs, d[3], acc[3]);
+                }
               }
             }
           }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) keep4[t] = any4[t];
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) keep4[t] = any4[t];
+        release(false);
       }
-      release(false);
-    }
 
-    if (dead) break;
+      if (dead) break;
 
-    // ---- the item's output, or this range's part of it
-    const bool whole = kWhole || (seg == at.lo && seg_end == at.hi);
-    if (!kWhole && seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
-      a.parts[(int64_t)at.s * items + at.item] =
-          make_int4((int)worker, (int)(shares.owner(at.hi - 1) - worker) + 1, first_item ? 0 : 1, 0);
-    float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
+      // ---- the item's output, or this range's part of it
+      const bool whole = kWhole || (seg == at.lo && seg_end == at.hi);
+      if (!kWhole && seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
+        a.parts[(int64_t)at.s * items + at.item] =
+            make_int4((int)worker, (int)(shares.owner(at.hi - 1) - worker) + 1, first_item ? 0 : 1, 0);
+      float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float den = l[n][e];
+        for (int e = 0; e < 2; ++e) {
+          float den = l[n][e];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
-        const int r = n * 8 + 2 * c + e;
-        if (r >= rows) continue;
-        if (whole) {
-          const int64_t at_row = kv_out_row(a, at.s, h, row0 + r);
-          unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + g;
-          const float inv = den == 0.f ? 0.f : 1.f / den;
+          for (int d = 4; d < 32; d <<= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
+          const int r = n * 8 + 2 * c + e;
+          if (r >= rows) continue;
+          if (whole) {
+            const int64_t at_row = kv_out_row(a, at.s, h, row0 + r);
+            unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + g;
+            const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-          for (int i = 0; i < DT; ++i) {
-            out[16 * i] = f8_round16(o[n][i][e] * inv, a.dtype);
-            out[16 * i + 8] = f8_round16(o[n][i][e + 2] * inv, a.dtype);
-          }
-          if (g == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(m[n][e], den);
-        } else {
+            for (int i = 0; i < DT; ++i) {
+              out[16 * i] = f8_round16(o[n][i][e] * inv, a.dtype);
+              out[16 * i + 8] = f8_round16(o[n][i][e + 2] * inv, a.dtype);
+            }
+            if (g == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(m[n][e], den);
+          } else {
 #pragma unroll
-          for (int i = 0; i < DT; ++i) {
-            part[r * D + 16 * i + g] = o[n][i][e];
-            part[r * D + 16 * i + 8 + g] = o[n][i][e + 2];
-          }
-          if (g == 0) {
-            part[NT * 8 * D + r] = m[n][e];
-            part[NT * 8 * (D + 1) + r] = den;
+            for (int i = 0; i < DT; ++i) {
+              part[r * D + 16 * i + g] = o[n][i][e];
+              part[r * D + 16 * i + 8 + g] = o[n][i][e + 2];
+            }
+            if (g == 0) {
+              part[NT * 8 * D + r] = m[n][e];
+              part[NT * 8 * (D + 1) + r] = den;
+            }
           }
         }
       }
+      first_item = false;
+      if (u >= u_hi) break;
+      at.seek(a, u);
+      u = at.lo;
     }
-    first_item = false;
-    if (u >= u_hi) break;
-    at.seek(a, u);
-    u = at.lo;
-  }
   }  // rounds
   if (dead) {
     // no copy may be in flight when the CTA exits

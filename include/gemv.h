@@ -242,10 +242,10 @@ gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, fl
  *   bias     M of y's type, may be NULL;  y  B x M of y_dtype (F32, F16 or BF16)
  * Each group's products are summed by the tensor cores, the groups in fp32; y is
  * rounded once.  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
- * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any.  A scratch buffer of a few MB
- * comes from the library's stream-ordered pool where tiles are shared between SMs.
- * The kernel's waits are bounded (gemv_get_device_status; y is undefined where one ran
- * out). */
+ * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any, up to 2^31 - 256, K up to 2^29, and
+ * (M / 128 + 1) (B / 128 + 1) up to 2^30.  A scratch buffer of a few MB comes from the
+ * library's stream-ordered pool where tiles are shared between SMs.  The kernel's waits
+ * are bounded (gemv_get_device_status; y is undefined where one ran out). */
 gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
                       void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream);
 
@@ -311,6 +311,9 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
  *   out      S x T x q_heads x dim of `dtype`, contiguous
  *   lse      S x T x q_heads fp32: log of the sum of exp(scale q . k_j), -infinity where
  *            nothing is seen; may be NULL
+ * GEMV_ERR_UNSUPPORTED for T > GEMV_KV8_MAX_TOKENS, and where the cache's heads times
+ * the tiles of 8 to 24 query rows (T x q_heads / heads of them) that each has come to
+ * more than 65535.
  * Sums, maxima and logits are fp32; the products' operands are fp16: q scaled by a
  * power of two per row, the 8-bit values exactly, and the softmax weights, rounded to
  * 11 bits.  The result does not depend on the run: partial results are merged in a
