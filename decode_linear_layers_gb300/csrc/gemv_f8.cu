@@ -46,35 +46,47 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
   a.tm = (int)((a.M + (kPrompt ? N : kF8Rows) - 1) / (kPrompt ? N : kF8Rows));
   a.tn = kPrompt ? (a.B + kF8Rows - 1) / kF8Rows : 1;
   a.tiles = (int64_t)a.tm * a.tn;
-  const int64_t blocks = a.tiles * a.groups;
-  int64_t W = blocks < sms ? blocks : sms;  // one CTA per SM
   cudaError_t e = allow_smem_once<k_f8<N, kPrompt>>(F::kSmem);
   if (e != cudaSuccess) return fail((int)e);
-  if (a.tiles * 2 <= sms && a.groups > 1) {  // few tiles: a cluster of up to eight for each
-    int64_t n = sms / a.tiles < kTcMaxSlices ? sms / a.tiles : kTcMaxSlices;
-    if (n > a.groups) n = a.groups;
-    while (n > 1 && f8_clusters<N, kPrompt>((int)n) < a.tiles) --n;
-    a.slices = (int)n;
-    if (n > 1) W = a.tiles * n;
-  }
-  // Tiles that fill no whole round of the CTAs: a round of their own costs as many
-  // k-blocks as a tile has; shared among all CTAs they cost their share of it, and the
-  // join, about as long as kJoin k-blocks (us, shared / a round: 14336x3584 B=4 16.3 /
-  // 14.5, 10000x3584 B=100 20.1 / 22.1, 24000x3584 B=100 33.4 / 41.1; prompts, whose
-  // parts are 128 KB each, 11593x3584 B=1430 98.7 / 85.2, 11592x7168 130 / 115).
+  // The tiles that fill no whole round of the CTAs.  Each form's cost, in k-blocks of a CTA:
+  //   - a round of their own, as many as a tile has;
+  //   - shared among all CTAs, their share of it and the join, kJoin (us, shared / a round:
+  //     14336x3584 B=4 16.3 / 14.5, 10000x3584 B=100 20.1 / 22.1, 24000x3584 B=100 33.4 /
+  //     41.1; prompts, whose parts are 128 KB each, 11593x3584 B=1430 98.7 / 85.2,
+  //     11592x7168 130 / 115); not for few tiles, where its second launch shows;
+  //   - a cluster for each, their slice and its sum.  That weighs more against a round that
+  //     leaves SMs free, whose k-blocks are quick, than against the join (us, clusters / a
+  //     round: 4096x1024 B=1 5.2 / 4.5, 4096x2048 B=64 7.0 / 7.7, 28672x1024 B=16 8.3 / 7.1,
+  //     14336x4096 B=300 31.4 / 42.5, 7168x2048 B=1024 25.0 / 22.3; clusters / shared:
+  //     28672x4096 B=16 22.7 / 25.1, 20480x4096 B=1 18.2 / 20.6, 10000x8192 B=500 46.5 / 57.4).
   constexpr int64_t kJoin = kPrompt ? 28 : 12;
-  if (a.slices == 1) {
-    const int64_t rest = a.tiles % sms;
-    a.shared = (sms - rest) * a.groups > kJoin * sms ? rest : 0;
-    if (a.shared == 0) W = a.tiles < sms ? a.tiles : sms;
+  const int64_t rest = a.tiles % sms;
+  int64_t W = a.tiles < sms ? a.tiles : sms;  // one CTA per SM
+  int64_t least = (a.tiles + sms - 1) / sms * a.groups, sum = kPrompt ? 14 : 12;
+  if (a.tiles * 2 > sms && a.tiles * a.groups / sms + kJoin < least) {
+    least = a.tiles * a.groups / sms + kJoin;
+    a.shared = rest;
+    W = sms;
+    sum = kPrompt ? 6 : 2;
+  }
+  for (int64_t n = 2; n <= kTcMaxSlices && n <= a.groups; ++n) {
+    const int64_t c = f8_clusters<N, kPrompt>((int)n), q = a.tiles / (c * n), r = a.tiles - q * c * n;
+    const int64_t cost = q * a.groups + (a.groups + n - 1) / n + sum;
+    if (r > 0 && r <= c && cost < least) {
+      least = cost;
+      a.slices = (int)n;
+      a.shared = r;
+      W = (q > 0 ? c : r) * n;
+    }
   }
   a.sharers = (int)(a.shared * a.groups < W ? a.shared * a.groups : W);
   CUtensorMap map_a, map_x;
   if (!map_bytes(&map_a, A, a.M, K, kPrompt ? N : kF8Rows, kF8Group) ||
       !map_bytes(&map_x, x, a.B, K, kPrompt ? kF8Rows : N, kF8Group))
     return fail((int)cudaErrorInvalidValue);
+  const bool join = a.slices == 1 && a.shared > 0;
   void *ws = nullptr;
-  if (a.shared > 0) {
+  if (join) {
     e = workspace(&ws, (size_t)(W * 2 * F::kPartial * 4), s);
     if (e != cudaSuccess) return fail((int)e);
     a.ws = static_cast<float *>(ws);
@@ -84,7 +96,7 @@ gemv_status_t f8_launch(F8Args a, const void *A, const void *x, int64_t K, int s
     e = launch_k_cluster_x(k_f8<N, kPrompt>, dim3((unsigned)W), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a.slices,
                            kPrompt ? map_x : map_a, kPrompt ? map_a : map_x, a);
   int n = 1;
-  if (e == cudaSuccess && a.shared > 0) {
+  if (e == cudaSuccess && join) {
     e = launch_k(k_f8_join<N, kPrompt>, dim3((unsigned)a.shared, (unsigned)(F::kPartial / kF8JoinPiece)),
                  dim3(kF8JoinThreads), 0, s, pdl, a);
     n = 2;

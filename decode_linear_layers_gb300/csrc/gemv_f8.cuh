@@ -30,10 +30,10 @@ struct F8Args {
   int *status = nullptr;
   int64_t timeout_ns = 0, M = 0;
   int64_t tiles = 0;     // row tiles x column tiles
-  int64_t shared = 0;    // tiles 0 .. shared - 1 are split over all CTAs, the rest go whole
+  int64_t shared = 0;    // tiles 0 .. shared - 1 are split, the rest go whole
   int B = 0, groups = 0; // groups = k-blocks
   int sharers = 0;       // CTAs that the shared tiles are split over
-  int slices = 1;        // or: CTAs of the cluster that each tile is split over
+  int slices = 1;        // or: CTAs of the cluster that each of them is split over
   int tm = 0, tn = 0;    // tiles along the weight rows and along the vectors
   int y_dtype = 0, test_stall = 0;
 };
@@ -79,38 +79,43 @@ __device__ __forceinline__ void f8_store(const F8Args &a, int64_t i, float v) {
 // each of the first R: so a few tiles keep every SM busy.  A range is no longer than a
 // tile's k-blocks, so it meets two tiles at most.  The other tiles, a multiple of the
 // CTAs, go round whole.  Each role of a CTA walks the same segments.
-// With fewer tiles than half the SMs (slices > 1) each tile is one cluster's instead, its
-// k-blocks cut among the cluster's CTAs, which add their sums in distributed shared
-// memory: one launch and no scratch buffer.
+// Or (slices > 1) the CTAs form clusters, and each of the shared tiles is one cluster's, its
+// k-blocks cut among the cluster's CTAs, which add their sums in distributed shared memory:
+// one launch and no scratch buffer.  The whole tiles go first then, for the sums need the
+// rings idle.
+constexpr int kF8Whole = -1, kF8Sliced = -2;
 struct F8Seg {
   int tile, k0, k1;
-  int slot;  // which of the CTA's two partial sums it fills; -1: the whole tile
+  int slot;  // which of the CTA's two partial sums it fills; or kF8Whole, kF8Sliced
 };
 struct F8Walk {  // (the host limits tiles, and the k-blocks of a CTA, to 32 bits)
   uint32_t lo, hi;
   int next_tile, tiles, groups, part;
+  bool sliced;  // [lo, hi) is a slice of the cluster's tile
   __device__ F8Walk(const F8Args &a) {
     groups = a.groups;
     part = 0;
-    if (a.slices > 1) {
-      const uint32_t tile = blockIdx.x / a.slices, r = blockIdx.x - tile * a.slices;
-      lo = tile * groups + r * groups / a.slices;
-      hi = tile * groups + (r + 1) * groups / a.slices;
-      next_tile = tiles = 0;
-      return;
-    }
-    const int64_t R = a.shared * a.groups, w = blockIdx.x;
-    lo = w < a.sharers ? (uint32_t)(w * R / a.sharers) : 0u;
-    hi = w < a.sharers ? (uint32_t)((w + 1) * R / a.sharers) : 0u;
+    const int64_t w = blockIdx.x;
     next_tile = (int)(a.shared + w);
     tiles = (int)a.tiles;
+    sliced = false;
+    if (a.slices > 1) {
+      const uint32_t tile = blockIdx.x / a.slices, r = blockIdx.x - tile * a.slices;
+      sliced = tile < a.shared;
+      lo = tile * groups + r * groups / a.slices;
+      hi = sliced ? tile * groups + (r + 1) * groups / a.slices : lo;
+      return;
+    }
+    const int64_t R = a.shared * a.groups;
+    lo = w < a.sharers ? (uint32_t)(w * R / a.sharers) : 0u;
+    hi = w < a.sharers ? (uint32_t)((w + 1) * R / a.sharers) : 0u;
   }
   __device__ bool next(F8Seg &s) {
-    if (lo < hi) {
+    if (lo < hi && !(sliced && next_tile < tiles)) {
       s.tile = (int)(lo / groups);
       s.k0 = (int)(lo - (uint32_t)s.tile * groups);
       s.k1 = hi - lo < (uint32_t)(groups - s.k0) ? s.k0 + (int)(hi - lo) : groups;
-      s.slot = s.k0 == 0 && s.k1 == groups ? -1 : part;
+      s.slot = sliced ? kF8Sliced : s.k0 == 0 && s.k1 == groups ? kF8Whole : part;
       ++part;
       lo += s.k1 - s.k0;
       return true;
@@ -119,7 +124,7 @@ struct F8Walk {  // (the host limits tiles, and the k-blocks of a CTA, to 32 bit
     s.tile = next_tile;
     s.k0 = 0;
     s.k1 = groups;
-    s.slot = -1;
+    s.slot = kF8Whole;
     next_tile += gridDim.x;
     return true;
   }
@@ -220,6 +225,58 @@ __device__ __forceinline__ uint32_t f8_pack16(float a, float b, int dt) {
   else
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+// Four consecutive values of y's row b, from column m (a multiple of 4) on, with the bias.
+// (The type is asked once: a branch for each value chains their latencies.)
+__device__ __forceinline__ void f8_store_along(const F8Args &a, int64_t b, int64_t m, float4 q) {
+  float v[4] = {q.x, q.y, q.z, q.w};
+  const int n = a.M - m < 4 ? (int)(a.M - m) : 4;
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += j < n ? f8_bias(a, m + j) : 0.f;
+  }
+  const bool f32 = a.y_dtype == GEMV_DTYPE_F32, vec = a.M % 4 == 0;
+  const int64_t i = b * a.M + m;
+  if (f32) {
+    float *p = reinterpret_cast<float *>(a.y) + i;
+    if (vec && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0) {
+      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) p[j] = v[j];
+    }
+  } else {
+    const uint32_t lo = f8_pack16(v[0], v[1], a.y_dtype), hi = f8_pack16(v[2], v[3], a.y_dtype);
+    unsigned short *p = reinterpret_cast<unsigned short *>(a.y) + i;
+    if (vec && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0) {
+      *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    } else {
+      p[0] = (unsigned short)lo;
+      if (n > 1) p[1] = (unsigned short)(lo >> 16);
+      if (n > 2) p[2] = (unsigned short)hi;
+      if (n > 3) p[3] = (unsigned short)(hi >> 16);
+    }
+  }
+}
+// C values of y's column m, from row b on; bias: the column's.
+template <int C>
+__device__ __forceinline__ void f8_store_down(const F8Args &a, int b, int64_t m, const float *v, float bias) {
+  const int64_t i = (int64_t)b * a.M + m;
+  if (a.y_dtype == GEMV_DTYPE_F32) {
+    float *p = reinterpret_cast<float *>(a.y) + i;
+#pragma unroll
+    for (int j = 0; j < C; ++j, p += a.M)
+      if (b + j < a.B) *p = v[j] + bias;
+  } else {
+    unsigned short *p = reinterpret_cast<unsigned short *>(a.y) + i;
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int j = 0; j < C / 2; ++j) w[j] = f8_pack16(v[2 * j] + bias, v[2 * j + 1] + bias, a.y_dtype);
+#pragma unroll
+    for (int j = 0; j < C; ++j, p += a.M)
+      if (b + j < a.B) *p = (unsigned short)(w[j / 2] >> (16 * (j & 1)));
+  }
 }
 // (s0, s1) += (f0, f1) * (v0, v1), one packed instruction.
 __device__ __forceinline__ void f8_fma2(float &s0, float &s1, float f0, float f1, uint32_t v0, uint32_t v1) {
@@ -393,6 +450,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   const uint32_t tmem = tmem_slot;
   volatile int *abort = &abort_flag;
   const int G = a.groups;
+  const bool sliced = a.slices > 1 && blockIdx.x < a.shared * a.slices;  // the cluster ends with a tile of its own
   float *scales = reinterpret_cast<float *>(smem + (size_t)S * F::kStage);
   // after an abort nothing may be in flight when the CTA frees its tensor memory and exits:
   // the last committed MMAs (their commit covers all earlier ones) and every copy issued
@@ -529,7 +587,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       }
       f8_copy4_drain();  // nothing in flight when the CTA exits
     }
-    if (a.slices > 1) {  // (the scaling warps' meetings, below)
+    if (sliced) {  // (the scaling warps' meetings, below)
       __syncwarp();
       __syncthreads();
       if (tid == 0 && abort_flag != 0) drain();
@@ -548,13 +606,13 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     F8Walk walk(a);
     F8Seg g;
     bool ok = true;
-    while (ok && walk.next(g)) {
+    while ((ok || sliced) && walk.next(g)) {
       int im, in;
       f8_tile(a, g.tile, im, in);
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      for (int kb = g.k0; kb < g.k1; kb += KA) {
+      for (int kb = g.k0; kb < g.k1 && ok; kb += KA) {
         ok = f8_wait(&facf[t], tph, a.timeout_ns, abort) && f8_wait(&accf[c], cph, a.timeout_ns, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -609,53 +667,63 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
           tph ^= 1;
         }
       }
-      if (a.slices > 1) {
+      if (g.slot == kF8Sliced) {  // (reached after an abort, too: the cluster's CTAs meet here)
         // Every CTA of the cluster holds the sums of its slice.  CTA q adds up rows
-        // ceil(128 q / slices) .. of the tile: all send it theirs, into its idle ring
-        // ([slice][row][column], rows padded against bank conflicts), and it adds the
-        // slices in the order of the k-blocks.
+        // ceil(128 q / slices) .. of the tile: all send it theirs, into its idle ring, and
+        // it adds the slices in the order of the k-blocks.  [slice][group of four
+        // columns][row]: a warp's rows lie side by side, so that they leave in whole lines
+        // (16-byte pieces of 32 lines at a time cost two CTAs 128 x 128 sums 0.7 us more);
+        // an odd number of rows against bank conflicts.
         __syncwarp();
         __syncthreads();
         const int n = a.slices, rank = (int)blockIdx.x % n, most = (kF8Rows + n - 1) / n;
         const bool aborted = abort_flag != 0;
-        constexpr int kPitch = N + 4;
+        const int pitch = most | 1;
         float *parts = reinterpret_cast<float *>(smem);
         auto first_row = [&](int q) { return (kF8Rows * q + n - 1) / n; };
-        // groups of four columns that y has
+        // columns that y has
         const int cols = kPrompt ? (a.M - (int64_t)im * N < N ? (int)(a.M - (int64_t)im * N) : N) : (a.B < N ? a.B : N);
-        const int quads = (cols + 3) / 4;
         tc_cluster_sync();  // every ring is idle
         const int to = row * n / kF8Rows;
         if (tid - kF8RoleThreads < n) tc_st_dsmem_int(&abort_of[rank], (uint32_t)(tid - kF8RoleThreads), aborted ? 1 : 0);
         if (!aborted) {
-          const float *at = parts + ((size_t)rank * most + row - first_row(to)) * kPitch + col0;
+          const float *at = parts + 4 * ((rank * (N / 4) + col0 / 4) * pitch + row - first_row(to));
 #pragma unroll
-          for (int j = 0; j < COLS; j += 4)
-            if (col0 + j < cols) tc_st_dsmem4(at + j, (uint32_t)to, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+          for (int j = 0; j < COLS; j += 4, at += 4 * pitch)
+            if (col0 + j < cols) tc_st_dsmem4(at, (uint32_t)to, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
         tc_cluster_sync();  // every slice's sums of the owned rows (and every abort flag) are here
         bool any = false;
         for (int q = 0; q < n; ++q) any |= abort_of[q] != 0;
         const int r0 = first_row(rank), rows = first_row(rank + 1) - r0;
-        for (int i = tid - kF8RoleThreads; i < rows * quads && !any; i += 128 * F::kGroupsOfWarps) {
-          // neighbouring threads along y's rows: the tile's columns (prompts) or its rows
-          const int r = kPrompt ? i / quads : i % rows, cc = 4 * (kPrompt ? i % quads : i / rows);
-          float4 v = *reinterpret_cast<const float4 *>(parts + (size_t)r * kPitch + cc);
+        // neighbouring threads along y's rows: the tile's columns, four each (prompts), or its
+        // rows, up to 64, 32 or 16 of them
+        constexpr int kQuads = N / 4;
+        const int lg = n <= 3 ? 6 : n <= 7 ? 5 : 4;
+        const int items = kPrompt ? rows * kQuads : (cols + 3) / 4 << lg;
+#pragma unroll 1
+        for (int i = tid - kF8RoleThreads; i < items && !any; i += 128 * F::kGroupsOfWarps) {
+          const int r = kPrompt ? i / kQuads : i & ((1 << lg) - 1), quad = kPrompt ? i % kQuads : i >> lg;
+          if (kPrompt ? 4 * quad >= cols : r >= rows) continue;
+          const float *at = parts + 4 * (quad * pitch + r);
+          float4 v = *reinterpret_cast<const float4 *>(at);
+#pragma unroll 1
           for (int q = 1; q < n; ++q) {
-            const float4 u = *reinterpret_cast<const float4 *>(parts + ((size_t)q * most + r) * kPitch + cc);
+            const float4 u = *reinterpret_cast<const float4 *>(at + q * N * pitch);
             v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
           }
-          const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t b = kPrompt ? (int64_t)in * kF8Rows + r0 + r : cc + j;
-            const int64_t m = kPrompt ? (int64_t)im * N + cc + j : (int64_t)im * kF8Rows + r0 + r;
-            if (b < a.B && m < a.M) f8_store(a, b * a.M + m, e[j] + (a.bias != nullptr ? f8_bias(a, m) : 0.f));
+          if constexpr (kPrompt) {
+            const int64_t b = (int64_t)in * kF8Rows + r0 + r;
+            if (b < a.B) f8_store_along(a, b, (int64_t)im * N + 4 * quad, v);
+          } else {
+            const int64_t m = (int64_t)im * kF8Rows + r0 + r;
+            const float e[4] = {v.x, v.y, v.z, v.w};
+            if (m < a.M) f8_store_down<4>(a, 4 * quad, m, e, a.bias != nullptr ? f8_bias(a, m) : 0.f);
           }
         }
         break;
       }
-      if (!ok) break;
+      if (!ok) continue;
       if (g.slot >= 0) {
         // a part of the tile's k-blocks: k_f8_join adds the parts.  Prompts [row][column]
         // (four columns at a time), else [column][row]: both as the join writes y
@@ -674,10 +742,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
       if constexpr (!kPrompt) {
         const int64_t m = (int64_t)im * kF8Rows + row;
         if (m < a.M) {
-          const float bias = a.bias != nullptr ? f8_bias(a, m) : 0.f;
-#pragma unroll
-          for (int j = 0; j < COLS; ++j)
-            if (col0 + j < a.B) f8_store(a, (int64_t)(col0 + j) * a.M + m, acc[j] + bias);
+          f8_store_down<COLS>(a, col0, m, acc, a.bias != nullptr ? f8_bias(a, m) : 0.f);
         }
       } else {
         f8_rows_out<COLS>(a, acc, mine, lane, (int64_t)in * kF8Rows + wq * 32, (int64_t)im * N + col0);
@@ -687,7 +752,7 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();  // the role threads rejoin their warps: the CTA barrier counts whole warps
   __syncthreads();
-  if (abort_flag != 0 && a.slices == 1) {
+  if (abort_flag != 0 && !sliced) {
     if (tid == 0) drain();
     __syncwarp();
     __syncthreads();
@@ -1044,10 +1109,7 @@ __global__ void __launch_bounds__(kF8JoinThreads) k_f8_join(const F8Args a) {
     const float4 v = *reinterpret_cast<const float4 *>(q + i * kStep);
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (m + j < a.M) f8_store(a, b * a.M + m + j, v[j] + (a.bias != nullptr ? f8_bias(a, m + j) : 0.f));
+  f8_store_along(a, b, m, s);
 }
 
 // No columns: the empty sum.

@@ -163,6 +163,34 @@ def test_product_many_tiles(M, K, B):
     check_product(y, *reference(A, sa, x, sx, None), "bf16")
 
 
+# clusters for all tiles, and for those left over after rounds of whole ones
+@pytest.mark.parametrize("M,K,B,name", [(301, 4112, 1, "bf16"), (300, 4096, 17, "f16"), (131, 8192, 40, "f32"), (700, 6160, 65, "bf16"),
+                                        (1001, 8192, 129, "f32"), (3000, 8192, 200, "f16"), (516, 14336, 128, "f32"),
+                                        (20353, 4096, 2, "bf16"), (24001, 3600, 40, "f32"), (21000, 7168, 30, "f16"),
+                                        (42000, 2064, 1, "f32"), (24000, 3600, 100, "bf16"), (14301, 4096, 300, "f16"),
+                                        (10004, 8192, 257, "f32"), (4097, 14336, 700, "bf16")])
+def test_product_clusters(M, K, B, name):
+    A, sa, x, sx = operands(M, K, B, seed=13)
+    bias = torch.randn(M, generator=gen(14), device="cuda").to(TYPES[name])
+    y = product(A, sa, x, sx, bias, name)
+    check_product(y, *reference(A, sa, x, sx, bias), name)
+    assert torch.equal(y, product(A, sa, x, sx, bias, name))
+    assert g.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("M,K,B", [(301, 4112, 1), (700, 6160, 65), (20353, 4096, 2), (14301, 4096, 300)])
+def test_bounded_wait_in_clusters(M, K, B):
+    A, sa, x, sx = operands(M, K, B, seed=15)
+    torch.cuda.synchronize()
+    g.test_stall(True, 50_000_000)
+    product(A, sa, x, sx, None, "bf16")
+    status, bits = g.device_status()
+    assert status == g.ERR_DEVICE_TIMEOUT and bits & 16
+    g.test_stall(False)
+    check_product(product(A, sa, x, sx, None, "bf16"), *reference(A, sa, x, sx, None), "bf16")
+    assert g.device_status() == (0, 0)
+
+
 @pytest.mark.parametrize("B", [3, 200])
 def test_product_scales_apart(B):
     # neighbouring groups whose scales differ by many orders: each group's own counts
