@@ -217,6 +217,9 @@ __device__ __forceinline__ void f8_copy4_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc_smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void f8_copy4_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void f8_prefetch_map(const CUtensorMap *m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
 // Two values of a 16-bit output type, `a` in the low half.
 __device__ __forceinline__ uint32_t f8_pack16(float a, float b, int dt) {
   uint32_t r;
@@ -375,8 +378,8 @@ __device__ __forceinline__ void f8_rows_out(const F8Args &a, float (&acc)[COLS],
 // kPrompt = true: a tile is 128 vectors x N weight rows (128, or 256 in two blocks, one per
 //   scaling warpgroup); thread = vector, so that its factor sa sx is one number per k-block.
 // What bounds it, on a GB300: up to some hundred vectors the weights' bytes (28672x4096 with
-// 16 vectors 26 us, 4.5 TB/s; 128256x4096 with 64 98 us, 5.5 TB/s) and, for small matrices,
-// the start of the ring and the sum of the slices (6144x4096 with one vector 8.1 us);
+// 16 vectors 23.3 us, 5.1 TB/s; 128256x4096 with 64 98 us, 5.5 TB/s) and, for small matrices,
+// the start of the ring and the sum of the slices (6144x4096 with one vector 7.9 us);
 // beyond, the hand-over of the accumulators between the MMA warp and the scaling warps.
 template <int N, bool kPrompt>
 struct F8Form {
@@ -416,16 +419,9 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
   __shared__ int abort_flag, abort_of[kTcMaxSlices];
   __shared__ int sh_loaded, sh_consumed, sh_committed;  // for the drain after an abort
   pdl_trigger();
-  pdl_wait();  // every read (TMA included) after the kernel before has finished
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
 
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)),
-                 "r"((uint32_t)F::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       tc_mbar_init(&full[s], 1);
@@ -443,11 +439,28 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
     abort_flag = 0;
     sh_loaded = sh_consumed = sh_committed = -1;
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  if (tid == 32) {
+    f8_prefetch_map(&map_p);
+    f8_prefetch_map(&map_q);
+  }
   __syncwarp();
   __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = tmem_slot;
+  pdl_wait();  // every read (TMA included) after the kernel before has finished
+  // Tensor memory only now: before, the kernel before could be waiting for it.  Who does not
+  // need it, the copies above all, goes ahead.
+  uint32_t tmem = 0;
+  if (warp == 1 || warp >= 4) {
+    if (warp == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)),
+                   "r"((uint32_t)F::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(32 + 128 * F::kGroupsOfWarps) : "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem = tmem_slot;
+  }
   volatile int *abort = &abort_flag;
   const int G = a.groups;
   const bool sliced = a.slices > 1 && blockIdx.x < a.shared * a.slices;  // the cluster ends with a tile of its own
