@@ -101,11 +101,23 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
       return launch_k(kern, dim3((unsigned)a.S, (unsigned)items, (unsigned)((rows * D / 4 + along - 1) / along)),
                       dim3(kKvJoinThreads), 0, s, pdl, a);
     };
-    // eight warps for the parts of the same channels while that makes few CTAs (us, eight / one:
-    // 256 CTAs, 8 sequences of 2000 tokens 10.7 / 12.3; 1152 CTAs, the window case 31.9 / 30.1)
-    const int64_t threads = (int64_t)a.S * items * rows * (D / 4);
-    e = threads * 8 / kKvJoinThreads <= (int64_t)sms * 4 ? join(k_kv8_join<D, NT, 8>, kKvJoinThreads / 8)
-                                                         : join(k_kv8_join<D, NT, 1>, kKvJoinThreads);
+    // Threads for the parts of the same channels: as many as two CTAs for each SM allow (us,
+    // 16 sequences of 1000 tokens, eight / four, 512 / 256 CTAs: 12.2 / 10.9; 32 of 2000,
+    // four / one, 512 / 128 CTAs: 21.4 / 20.0; 12 of a window of 4096, 24 rows, four / one,
+    // 288 / 72 CTAs: 20.2 / 22.8; 8 of 2000, eight / one 10.5 / 12.2), and 32 where an item can be
+    // in so many parts that eight would take two turns at them (32 / eight: one key head, 16
+    // queries of 192 channels, 30000 tokens 18.5 / 22.9; 8 key heads, 8000 tokens 9.9 /
+    // 10.9, 1000 tokens, 16 parts, 9.6 / 9.3).
+    const int64_t threads = (int64_t)a.S * items * rows * (D / 4), most = (int64_t)sms * 2 * kKvJoinThreads / threads;
+    const int64_t spread = (int64_t)sms * F::kWarps / ((int64_t)a.S * items), in_parts = a.width < spread ? a.width : spread;
+    if (most >= 32 && in_parts > 64)
+      e = join(k_kv8_join<D, NT, 32>, kKvJoinThreads / 32);
+    else if (most >= 8)
+      e = join(k_kv8_join<D, NT, 8>, kKvJoinThreads / 8);
+    else if (most >= 4)
+      e = join(k_kv8_join<D, NT, 4>, kKvJoinThreads / 4);
+    else
+      e = join(k_kv8_join<D, NT, 1>, kKvJoinThreads);
   }
   const cudaError_t e2 = cudaFreeAsync(ws, s);
   if (e == cudaSuccess) e = e2;

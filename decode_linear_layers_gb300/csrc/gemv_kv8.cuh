@@ -436,7 +436,7 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 // At the end of an item (or of the range) the warp writes the output, or a partial
 // result that k_kv8_join adds up.
 // Decode is bound by the cache's bytes: 64 sequences of up to 8192 tokens (537 MB) 94 us,
-// 5.7 TB/s with the join; one of 131072 tokens 53 us.  mma.sync at a sixth of its rate is
+// 5.7 TB/s with the join; one of 131072 tokens 51.5 us.  mma.sync at a sixth of its rate is
 // enough for that, and takes eight rows where tcgen05 would take 128.  More rows a block
 // (16 with 128 channels: 38 us where the bytes take 18) are bound by the latency of eight
 // warps' dependent instructions; their registers allow no more.
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
 
 // Items that several warps of k_kv8_attention share: their partial results, merged in the
 // order of the blocks; and the outputs of sequences without tokens: zeros.  A thread adds
-// up four channels of a row, eight parts on their way at a time; kGroups warps share the
+// up four channels of a row, eight parts on their way at a time; kGroups threads share the
 // parts of the same channels, where there are few items, each perhaps in a hundred parts.
 // grid (S, items, pieces of a tile's rows).  Three dependent reads: 2 to 6 us after the
 // attention kernel.
@@ -1020,9 +1020,19 @@ __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a) {
   if constexpr (kGroups > 1) {
     sums[grp][along] = sum;
     __syncthreads();
+    constexpr int kLast = kGroups < 8 ? kGroups : 8;
+    auto add = [&](int k) { sum.add(sums[k][along].m, sums[k][along].den, sums[k][along].v); };
+    if constexpr (kGroups > kLast) {  // to eight sums first
+      if (grp < kLast) {
+#pragma unroll
+        for (int k = kLast; k < kGroups; k += kLast) add(grp + k);
+        sums[grp][along] = sum;
+      }
+      __syncthreads();
+    }
     if (grp > 0) return;
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) sum.add(sums[k][along].m, sums[k][along].den, sums[k][along].v);
+    for (int k = 1; k < kLast; ++k) add(k);
   }
   if (r >= rows) return;
   const int64_t at_row = kv_out_row(a, s, h, row0 + r);

@@ -407,6 +407,19 @@ def test_attention_work_shares(lens):
     check_attention(c, queries(c, 1, 2, 51))
 
 
+# items in parts by the hundred and by the few: every width of the kernel that joins them
+@pytest.mark.parametrize("lens,heads,dim,T,group,window,sinks", [
+    ([30000], 1, 192, 1, 16, 0, 0), ([9001], 4, 128, 1, 4, 0, 0), ([7000], 2, 256, 1, 3, 0, 0), ([12000, 0, 5], 1, 64, 5, 5, 0, 0),
+    ([2000] * 5 + [1, 0, 777], 4, 128, 1, 4, 0, 0), ([1000] * 16, 8, 128, 1, 4, 0, 0), ([3000] * 12, 4, 64, 4, 6, 1030, 4),
+    ([900] * 40, 8, 64, 1, 8, 0, 0)])
+def test_attention_joins(lens, heads, dim, T, group, window, sinks):
+    c = Cache(lens, heads, dim, seed=60)
+    c.k &= 0x77
+    c.v &= 0x77
+    check_attention(c, queries(c, T, group, 61), window, sinks)
+    assert g.device_status() == (0, 0)
+
+
 def test_attention_far_blocks():
     """A pool beyond 2^32 bytes, its last blocks in use."""
     blocks, heads, dim = 70000, 8, 128
