@@ -312,7 +312,7 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
  *   lse      S x T x q_heads fp32: log of the sum of exp(scale q . k_j), -infinity where
  *            nothing is seen; may be NULL
  * GEMV_ERR_UNSUPPORTED for T > GEMV_KV8_MAX_TOKENS, and where the cache's heads times
- * the tiles of 8 to 24 query rows (T x q_heads / heads of them) that each has come to
+ * the tiles of 8 to 32 query rows (T x q_heads / heads of them) that each has come to
  * more than 65535.
  * Sums, maxima and logits are fp32; the products' operands are fp16: q scaled by a
  * power of two per row, the 8-bit values exactly, and the softmax weights, rounded to
