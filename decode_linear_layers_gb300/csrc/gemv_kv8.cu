@@ -86,7 +86,8 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
     count_launches(1);
     return GEMV_SUCCESS;
   }
-  const int64_t parts = (int64_t)sms * F::kWarps * 2 * kv_part<D, NT>() * 4;  // one CTA per SM
+  a.workers = sms * F::kWarps;  // one CTA per SM
+  const int64_t parts = (int64_t)a.workers * 2 * kv_part<D, NT>() * 4;
   void *ws = nullptr;
   cudaError_t e = workspace(&ws, (size_t)(parts + (int64_t)a.S * items * 16), s);
   if (e != cudaSuccess) return fail((int)e);

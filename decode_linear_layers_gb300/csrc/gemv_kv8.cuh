@@ -34,6 +34,7 @@ struct KvArgs {
   float *lse = nullptr;
   float *ws = nullptr;    // partial results: two for each warp
   int4 *parts = nullptr;  // of each item: the first warp with a part, parts, which of that warp's
+  int workers = 0;        // warps of the attention kernel: ws has two partial results of each
   int64_t q_stride = 0;
   int64_t timeout_ns = 0;
   int group = 0, window = 0, sinks = 0, row_tiles = 0, test_stall = 0;
@@ -1001,6 +1002,9 @@ __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a) {
   const int count = kv_seen(a, s).count;
   pdl_wait();  // by every CTA: the next kernel counts on it
   const int4 of = count > 0 ? __ldcg(&a.parts[(int64_t)s * items + item]) : make_int4(0, 0, 0, 0);
+  // A warp whose wait ran out leaves its items' entries as the scratch memory had them: any
+  // bits.  The call's outputs are undefined then; what is read stays within the partial results.
+  if (of.x < 0 || of.y < 0 || (int64_t)of.x + of.y > a.workers || (of.z & ~1) != 0) return;
   if (of.y == 1) return;  // one warp had the whole item and wrote it
   const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
   const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;

@@ -489,3 +489,24 @@ def test_bounded_wait():
     g.test_stall(False)
     check_attention(c, q, scale=0.1)
     assert g.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("lens,heads,dim,T,group", [([3000, 40, 0, 700], 2, 128, 1, 4), ([900] * 300, 1, 64, 4, 6), ([20000], 1, 192, 1, 16)])
+def test_bounded_wait_of_shared_items(lens, heads, dim, T, group):
+    """Items in parts, and warps with several items, whose waits run out: the kernel that joins
+    the parts finds what the scratch memory held before (here another call's sums)."""
+    c = Cache(lens, heads, dim, seed=66)
+    c.k &= 0x77
+    c.v &= 0x77
+    q = queries(c, T, group, 67)
+    A = torch.full((12000, 4096), 0x38, dtype=torch.uint8, device="cuda").view(E4M3)   # shared tiles: fp32 sums in the pool
+    x, ones = torch.full((3, 4096), 0x38, dtype=torch.uint8, device="cuda").view(E4M3), torch.ones(94, 32, device="cuda")
+    g.gemv_f8(A, ones, x, ones[:3], None, torch.empty(3, 12000, dtype=torch.bfloat16, device="cuda"), 12000, 4096, 3)
+    torch.cuda.synchronize()
+    g.test_stall(True, 20_000_000)
+    attend(c, q, 0.1)
+    status, bits = g.device_status()
+    assert status == g.ERR_DEVICE_TIMEOUT and bits & 16
+    g.test_stall(False)
+    check_attention(c, q, scale=0.1)
+    assert g.device_status() == (0, 0)
