@@ -407,8 +407,10 @@ template <int D, int NT>
 __host__ __device__ constexpr int64_t kv_part() { return (int64_t)NT * 8 * (D + 4); }
 
 // The weights leave exp2 times 2^14, so that fp16 holds those down to 2^-28 of the
-// largest in full; the factor cancels against the sum of weights, which has it too.
-constexpr float kKvLift = 14.f;
+// largest in full.  The sums of weights keep that factor, the values' scales take it
+// back: weighted values then overflow fp32 only where their sum, relative to the largest
+// weight, does.
+constexpr float kKvLift = 14.f, kKvLifted = 16384.f;
 __device__ __forceinline__ float kv_lse(float m, float den) {
   return den == 0.f ? -INFINITY : (m - kKvLift + log2f(den)) * 0.693147180559945f;
 }
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
         if (!arrived()) break;
         const float ks = meta[warp * R + slot][0];
         const bool bad = meta_bad[warp * R + slot] != 0;  // no such block: nothing of it is seen
-        const float vs = bad ? 0.f : meta[warp * R + slot][1];
+        const float vs = bad ? 0.f : meta[warp * R + slot][1] * (1.f / kKvLifted);
         // does every query see every token of the block?
         const bool edge = bad || pos0 + kKvBlock - 1 > (int64_t)len - a.T ||
                           (a.window > 0 && len - 1 - pos0 >= a.window && pos0 + kKvBlock > a.sinks);
@@ -927,7 +929,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
           if (whole) {
             const int64_t at_row = kv_out_row(a, at.s, h, row0 + r);
             unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + g;
-            const float inv = den == 0.f ? 0.f : 1.f / den;
+            const float inv = den == 0.f ? 0.f : kKvLifted / den;
 #pragma unroll
             for (int i = 0; i < DT; ++i) {
               out[16 * i] = f8_round16(o[n][i][e] * inv, a.dtype);
@@ -1051,7 +1053,7 @@ __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a) {
   if (r >= rows) return;
   const int64_t at_row = kv_out_row(a, s, h, row0 + r);
   unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
-  const float inv = sum.den == 0.f ? 0.f : 1.f / sum.den, v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
+  const float inv = sum.den == 0.f ? 0.f : kKvLifted / sum.den, v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
   if (d == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(sum.m, sum.den);

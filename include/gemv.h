@@ -316,8 +316,9 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
  * more than 65535.
  * Sums, maxima and logits are fp32; the products' operands are fp16: q scaled by a
  * power of two per row, the 8-bit values exactly, and the softmax weights, rounded to
- * 11 bits.  The result does not depend on the run: partial results are merged in a
- * fixed order.  lens beyond the table count as the table's size.  A table entry outside
+ * 11 bits.  The values' sum, weighted relative to the largest weight, has to stay in
+ * fp32's range (any value does alone, n equally weighted ones up to 3.4e38 / n).  The
+ * result does not depend on the run: partial results are merged in a fixed order.  lens beyond the table count as the table's size.  A table entry outside
  * the pool counts as a block that no query sees, and gemv_get_device_status then
  * returns GEMV_ERR_INVALID_VALUE with bit 64.  The kernel's waits are bounded (out and lse
  * are undefined where one ran out). */

@@ -383,6 +383,29 @@ def test_attention_scales_apart():
     check_attention(c, queries(c, 2, 4, 45))
 
 
+@pytest.mark.parametrize("lens,dim,T,group", [([1, 200], 128, 1, 4), ([1000, 64], 64, 1, 8), ([900, 70], 192, 3, 4), ([300], 256, 1, 2)])
+def test_attention_large_and_small_values(lens, dim, T, group):
+    """Values up to 7.8e34, a thousand of them: the largest sum of weighted values there can be is
+    7.8e37.  And a power of two in the values' scales is one in the output, bit for bit (nothing
+    here gets subnormal)."""
+    c = Cache(lens, 2, dim, seed=70)
+    c.k &= 0x77
+    c.v &= 0xF7   # (both signs, at most 240, no NaN)
+    q = queries(c, T, group, 71)
+    vs = torch.exp2(torch.randint(-9, -5, c.vs.shape, generator=gen(72), device="cuda").float())
+    c.vs = vs
+    want, want_lse = check_attention(c, q, scale=0.05)
+    for e in (114, -60):
+        c.vs = vs * 2.0 ** e
+        out, lse = check_attention(c, q, scale=0.05)
+        assert torch.equal(out.float(), want.float() * 2.0 ** e) and torch.equal(lse, want_lse)
+    # one visible value near the end of bf16's range
+    c.lens[:] = 1
+    c.vs = torch.full_like(vs, 2.0 ** 119)
+    c.v[:] = 0x7E
+    assert bool((attend(c, q[:, :1].contiguous(), 0.05)[0].float() == 448 * 2.0 ** 119).all())
+
+
 def test_attention_strided_queries():
     c = Cache([100, 77, 300], 2, 64, seed=46).fill(47)
     wide = torch.randn(3, 2, 8 * 64 + 256, generator=gen(48), device="cuda").to(torch.bfloat16)
