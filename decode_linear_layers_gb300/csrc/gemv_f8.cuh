@@ -6,10 +6,13 @@
 //
 // A and x hold e4m3 values; g runs over the groups of 128 columns.  The tensor cores
 // (tcgen05 kind::f8f6f4) compute P_g, a tile of 128 x N values for each k-block of 128
-// columns, into one of a few accumulators in tensor memory.  The scales are any fp32
-// numbers, so P_g cannot stay there: the scaling warps read it (tcgen05.ld), and
-// add sa sx P_g to the tile's fp32 sums in their registers, while the next k-blocks'
-// products fill the other accumulators.
+// columns, into one of a few accumulators in tensor memory.  The scales are fp32 numbers,
+// not powers of two alone, so P_g cannot stay there: the scaling warps read it
+// (tcgen05.ld), and add (sa sx) P_g to the tile's fp32 sums in their registers, while the
+// next k-blocks' products fill the other accumulators.  sa sx is formed first and has to
+// be 0 or a normal number: a test of it for each k-block, with P_g taking one scale after
+// the other where it is not, costs 2 to 5 % (us, tested / not: 6144x4096 B=1 8.2 / 7.8,
+// 28672x4096 B=16 23.4 / 22.9, 4096x14336 B=8192 388 / 381), for sums of 1e-31 or 1e38.
 #pragma once
 
 #include "../../include/gemv.h"

@@ -241,7 +241,9 @@ gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, fl
  *            gemv_f8_quantize writes them)
  *   bias     M of y's type, may be NULL;  y  B x M of y_dtype (F32, F16 or BF16)
  * Each group's products are summed by the tensor cores, the groups in fp32; y is
- * rounded once.  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
+ * rounded once.  The scales are fp32 numbers whose products a_scale x_scale, formed
+ * first, are 0 or in fp32's normal range: beyond it the group counts as infinite or NaN,
+ * below it bits are lost (a group of zeros stays 0).  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
  * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any, up to 2^31 - 256, K up to 2^29, and
  * (M / 128 + 1) (B / 128 + 1) up to 2^30.  A scratch buffer of a few MB comes from the
  * library's stream-ordered pool where tiles are shared between SMs.  The kernel's waits

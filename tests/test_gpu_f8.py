@@ -199,6 +199,28 @@ def test_product_scales_apart(B):
     check_product(y, *reference(A, sa, x, sx, None), "f32")
 
 
+# (every form: up to 16, 32, 64 vectors, 128 and 256 weight rows a tile, pairs of SMs)
+@pytest.mark.parametrize("M,K,B", [(300, 656, 1), (300, 656, 20), (300, 656, 50), (300, 656, 100), (12000, 272, 300), (40000, 272, 200)])
+def test_product_scales_at_the_ends(M, K, B):
+    """sa sx at the ends of what it may be, fp32's normal range (and 0), each scale far from 1."""
+    # above: e4m3's subnormals, so that a group's sum is at most 128 x (7 x 2^-9)^2 < 2^-5
+    r = gen(16)
+    A, x = ((torch.randint(-7, 8, (n, K), generator=r, device="cuda") * 2.0 ** -9).to(E4M3) for n in (M, B))
+    _, sa, _, sx = operands(M, K, B, seed=17, scales=(1.0, 2.0 ** 0.5))
+    sa, sx = sa * 2.0 ** 66, sx * 2.0 ** 60.9   # 2^126.9 to 2^127.9
+    x[B // 2], sx[B // 2] = 0, 2.0 ** 61
+    y = product(A, sa, x, sx, None, "f32")
+    check_product(y, *reference(A, sa, x, sx, None), "f32")
+    assert bool((y[B // 2] == 0).all())
+    # below; and a scale of 0
+    A, sa, x, sx = operands(M, K, B, seed=18, scales=(1.0, 4.0))
+    sa, sx = sa * 2.0 ** -86, sx * 2.0 ** -40   # 2^-126 to 2^-122
+    sa[0, 0], sx[B // 2, 1] = 0, 0
+    y = product(A, sa, x, sx, None, "f32")
+    check_product(y, *reference(A, sa, x, sx, None), "f32")
+    assert g.device_status() == (0, 0)
+
+
 @pytest.mark.parametrize("B", [2, 150])
 def test_product_nan_stays_in_its_row(B):
     A, sa, x, sx = operands(300, 256, B, seed=6)
