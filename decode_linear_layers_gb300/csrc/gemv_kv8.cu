@@ -14,13 +14,15 @@ namespace {
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
 bool aligned(const void *p, int bytes) { return ((uintptr_t)p % (uintptr_t)bytes) == 0; }
 
+constexpr int kKvMaxWidth = 1 << 24;  // blocks of a sequence: positions stay below 2^30
+
 // The cache's own checks: sizes, pointers, alignment (a block is copied in 16-byte
 // pieces).  On success *bytes is the size of the keys (and of the values).
 gemv_status_t check_cache(const gemv_kv8_cache_t *c, int64_t *bytes) {
   if (c == nullptr || c->blocks < 0 || c->heads < 0 || c->dim < 0 || c->width < 0) return GEMV_ERR_INVALID_VALUE;
   if (c->dim != 64 && c->dim != 128 && c->dim != 192 && c->dim != 256) return GEMV_ERR_UNSUPPORTED;
   // grid dimensions and block numbers
-  if (c->heads > 65535 || c->blocks > 0x7fffffff || c->width > (1 << 24)) return GEMV_ERR_INVALID_VALUE;
+  if (c->heads > 65535 || c->blocks > 0x7fffffff || c->width > kKvMaxWidth) return GEMV_ERR_INVALID_VALUE;
   if (!mul_ok(c->blocks * (int64_t)c->heads, kKvBlock * c->dim, bytes)) return GEMV_ERR_INVALID_VALUE;
   return GEMV_SUCCESS;
 }
@@ -220,8 +222,8 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
   a.T = T;
   a.group = q_heads / cache->heads;
   a.dtype = (int)dtype;
-  // no position is as large: beyond it a window is no window
-  const int64_t most = 0x3fffffff;
+  // (positions are below it, by the limit on the table's width)
+  const int64_t most = (int64_t)kKvMaxWidth * kKvBlock;
   a.window = (int)(window < most ? window : most);
   a.sinks = (int)(sinks < most ? sinks : most);
   a.scale_log2 = scale * 1.44269504088896f;

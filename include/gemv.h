@@ -265,7 +265,7 @@ gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, 
  *   v        blocks x heads x dim x GEMV_KV8_BLOCK e4m3 (token index innermost)
  *   k_scale, v_scale   blocks x heads fp32, powers of two: a cached key is k * k_scale
  *   table    sequences x width: the pool's block for each GEMV_KV8_BLOCK tokens of a
- *            sequence; entries that a call does not need are not read
+ *            sequence (width up to 2^24); entries that a call does not need are not read
  *   dim      channels of a head: 64, 128, 192 or 256 (GEMV_ERR_UNSUPPORTED otherwise)
  * k and v are 16-byte aligned. */
 typedef struct gemv_kv8_cache {

@@ -462,6 +462,27 @@ def test_attention_far_blocks():
     assert bool(((got - want).abs() <= 2.0 ** -4 * want.abs() + c.vs[blocks - 1, 3] * 2.0 ** -10).all())
 
 
+@pytest.mark.parametrize("window,first_seen", [(0, True), (2 ** 30 - 1, False), (2 ** 30, True), (2 ** 40, True)])
+def test_attention_longest_table(window, first_seen):
+    """2^30 tokens, in a pool of 4096 blocks that the table goes over again and again: the first
+    token decides the result of a query that sees it (its weight is e^64 times another's)."""
+    c = Cache([1], 1, 64, seed=80, width=2 ** 24)
+    blocks = 4096
+    c.k = torch.zeros(blocks, 1, BLOCK, 64, dtype=torch.uint8, device="cuda")
+    c.v = torch.ones(blocks, 1, 64, BLOCK, device="cuda").to(E4M3).view(torch.uint8)
+    c.ks, c.vs = torch.ones(blocks, 1, device="cuda"), torch.ones(blocks, 1, device="cuda")
+    c.table[0] = torch.arange(2 ** 24, dtype=torch.int32, device="cuda") % (blocks - 1) + 1
+    c.table[0, 0] = 0
+    one, three = (int(torch.tensor(f).to(E4M3).view(torch.uint8)) for f in (1.0, 3.0))
+    c.k[0, 0, 0], c.v[0, 0, :, 0] = one, three
+    c.lens[:] = 2 ** 30
+    out, lse = attend(c, torch.ones(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda"), 1.0, window=window)
+    assert bool((out == (3.0 if first_seen else 1.0)).all())
+    # (equal weights: fp32 holds their sums to 2^-24 for each of the blocks that a warp adds, 14 k)
+    want = 64.0 if first_seen else math.log(2 ** 30 - 1)
+    assert abs(float(lse[0, 0, 0]) - want) <= 14000 * 2.0 ** -24 + 1e-5
+
+
 def test_attention_where_the_cache_has_no_block():
     c = Cache([300, 100], 1, 64, seed=55).fill(56)
     c.table[0, 2] = -5
