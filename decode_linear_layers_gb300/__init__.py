@@ -170,10 +170,11 @@ def device_status(stream=None) -> tuple:
     return st, int(bits.value)
 
 
-def test_stall(stall: bool, timeout_ns: int = 0) -> None:
+def test_stall(stall: int, timeout_ns: int = 0) -> None:
     """TEST ONLY: make later tensor-core launches skip their first CTA's last MMA,
-    so that CTA's wait runs out after timeout_ns (<= 0: 2 s)."""
-    _check(lib().gemv_test_stall(int(bool(stall)), int(timeout_ns)))
+    so that CTA's wait runs out after timeout_ns (<= 0: 2 s).  2, 3: where gemv_f8 runs on
+    pairs of SMs, the last copies of the first pair's first or second CTA instead."""
+    _check(lib().gemv_test_stall(int(stall), int(timeout_ns)))
 
 
 def force_kernel(kernel, param: int = 0) -> None:

@@ -438,7 +438,7 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits) {
 }
 
 gemv_status_t gemv_test_stall(int stall, int64_t timeout_ns) {
-  g_test_stall = stall != 0;
+  g_test_stall = stall;
   g_test_timeout_ns = stall != 0 ? timeout_ns : 0;
   return GEMV_SUCCESS;
 }

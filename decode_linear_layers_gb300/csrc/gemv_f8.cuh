@@ -814,6 +814,10 @@ __device__ __forceinline__ bool f8_try_wait_cluster(uint64_t *b, uint32_t parity
       : "memory");
   return ok != 0;
 }
+// `bytes` of a barrier's phase that no copy will bring.
+__device__ __forceinline__ void f8_complete_tx(uint64_t *b, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(tc_smem_u32(b)), "r"(bytes) : "memory");
+}
 
 // map_x: the vectors, map_a: the weights, both in boxes of 128 rows.  grid: pairs of CTAs.
 static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
@@ -825,6 +829,7 @@ static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int sh_loaded, sh_consumed, sh_committed;
+  __shared__ int other[3];  // the other CTA's abort flag, k-blocks copied, k-blocks committed
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -889,9 +894,11 @@ static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
         int im, in;
         f8_tile(a, tile, im, in);
         const int32_t p0 = (2 * in + rank) * 128, q0 = (2 * im + rank) * 128;
+        // test: this CTA of the first pair never copies its last two k-blocks
+        const bool stall = a.test_stall == 2 + rank && blockIdx.x < 2 && tile + pairs >= tiles;
         for (int kb = 0; kb < G; ++kb) {
           ok = i < S || f8_wait(&empty[s], ph, a.timeout_ns, abort);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, ok) && !(stall && kb + 2 >= G);
           if (!ok) break;
           unsigned char *st = smem + s * F::kStage;
           if (f8_elect()) {
@@ -920,7 +927,7 @@ static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
       int i = 0, consumed = -1, s = 0, c = 0;
       uint32_t ph = 0, cph = 1;
       for (int tile = (int)blockIdx.x / 2; ok && tile < tiles; tile += pairs) {
-        const bool stall = a.test_stall && blockIdx.x == 0 && tile + pairs >= tiles;  // test: the last k-block never completes
+        const bool stall = a.test_stall == 1 && blockIdx.x == 0 && tile + pairs >= tiles;  // test: the last k-block never completes
         for (int kb = 0; kb < G; ++kb) {
           ok = f8_wait(&full[s], ph, a.timeout_ns, abort) && (i < NACC || wait_cluster(&acce[c], cph));
           ok = __all_sync(0xffffffffu, ok);
@@ -1066,29 +1073,38 @@ static __global__ void __launch_bounds__(F8Pair::kThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
   __syncthreads();
-  if (abort_flag != 0) {
-    // nothing may be in flight when the pair frees its tensor memory and exits: CTA 0 waits
-    // for the MMAs and for the copies of both that its barriers know of; the other CTA's
-    // last ones may be unknown to them: both wait a tenth of a millisecond more, a hundred
-    // times what a copy takes
+  if (tid == 0) {
+    tc_st_dsmem_int(&other[0], (uint32_t)(rank ^ 1), abort_flag);
+    tc_st_dsmem_int(&other[1], (uint32_t)(rank ^ 1), sh_loaded);
+    tc_st_dsmem_int(&other[2], (uint32_t)(rank ^ 1), sh_committed);
+  }
+  tc_cluster_sync();  // the other CTA's MMAs, copies and arrivals are done with this one; or:
+  if (abort_flag != 0 || other[0] != 0) {
+    // Nothing may be in flight when the pair frees its tensor memory and exits.  Both wait for
+    // the last commit, which reaches both.  CTA 0's barriers count both CTAs' copies: for
+    // k-blocks that it has not begun and the other has, it expects the other's half alone;
+    // for those that only it has begun, it accounts for the other's half itself.  (None is
+    // a ring's length past the last product, so each stage's phase is that of its k-block.)
     if (tid == 0) {
       if (a.status != nullptr) atomicOr(a.status, kTcStatusMma);
-      bool drained = true;
+      const int committed = rank == 0 ? sh_committed : other[2];
+      bool drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
       if (rank == 0) {
-        const int committed = sh_committed, consumed = sh_consumed, loaded = sh_loaded;
-        drained = committed < 0 || tc_mbar_wait(&accf[committed % NACC], (uint32_t)((committed / NACC) & 1), a.timeout_ns);
-        for (int t = consumed + 1; t <= loaded && drained; ++t)
+        const int mine = sh_loaded, theirs = other[1], last = mine > theirs ? mine : theirs;
+        for (int t = sh_consumed + 1; t <= last && drained; ++t) {
+          if (t > mine)
+            tc_mbar_arrive_expect_tx(&full[t % S], F::kStage);
+          else if (t > theirs)
+            f8_complete_tx(&full[t % S], F::kStage);
           drained = tc_mbar_wait(&full[t % S], (uint32_t)((t / S) & 1), a.timeout_ns);
+        }
       }
       if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
-      const uint64_t t0 = tc_global_ns();
-      while (tc_global_ns() - t0 < 100000) {
-      }
     }
     __syncwarp();
     __syncthreads();
+    tc_cluster_sync();
   }
-  tc_cluster_sync();  // the other CTA's MMAs, copies and arrivals are done with this one
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");

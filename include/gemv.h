@@ -465,7 +465,8 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits);
  * CTA's last k-tile), and every gemv_kv8_attention launch the last copy of each
  * warp, so that the wait for it runs out after `timeout_ns` (<= 0: the
  * default of 2 s) and gemv_get_device_status reports GEMV_ERR_DEVICE_TIMEOUT.
- * stall = 0 restores normal launches. */
+ * With 2 or 3, where gemv_f8 runs on pairs of SMs, the first or the second CTA of the first
+ * pair skips its last copies instead.  stall = 0 restores normal launches. */
 gemv_status_t gemv_test_stall(int stall, int64_t timeout_ns);
 
 #ifdef __cplusplus

@@ -301,6 +301,22 @@ def test_bounded_wait(M, K, B):
     assert g.device_status() == (0, 0)
 
 
+@pytest.mark.parametrize("M,K,B", [(40000, 1040, 200), (39937, 256, 300), (40000, 128, 200)])
+@pytest.mark.parametrize("cta", [0, 1])
+def test_bounded_wait_in_pairs(M, K, B, cta):
+    """One CTA of a pair has begun copies that the other has not: all that are in flight are
+    waited for (no bit 32) before the pair leaves."""
+    A, sa, x, sx = operands(M, K, B, seed=8)
+    torch.cuda.synchronize()
+    g.test_stall(2 + cta, 50_000_000)
+    product(A, sa, x, sx, None, "bf16")
+    assert g.device_status() == (g.ERR_DEVICE_TIMEOUT, 16)
+    g.test_stall(False)
+    y = product(A, sa, x, sx, None, "bf16")
+    check_product(y, *reference(A, sa, x, sx, None), "bf16")
+    assert g.device_status() == (0, 0)
+
+
 def test_refusals_on_real_buffers():
     A, sa, x, sx = operands(64, 64, 2, seed=9)
     y = torch.empty(2, 64, dtype=torch.bfloat16, device="cuda")
