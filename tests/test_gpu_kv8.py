@@ -364,6 +364,43 @@ def test_attention_unseen_values_are_anything(T):
     assert torch.equal(out[~want], ref[~want])
 
 
+@pytest.mark.parametrize("dim,T,group,window,sinks", [
+    (64, 4, 6, 0, 0), (64, 4, 6, 70, 3), (64, 8, 4, 0, 0), (64, 64, 1, 30, 0), (64, 3, 4, 65, 1),   # two to four row tiles, several items
+    (128, 4, 4, 0, 0), (128, 8, 4, 100, 2), (192, 3, 5, 64, 0), (256, 5, 2, 0, 0)])
+@pytest.mark.parametrize("longest", [180, 700])   # one launch, and items in parts
+def test_attention_values_that_some_queries_see(dim, T, group, window, sinks, longest):
+    """NaN in tokens that the later queries see and the earlier do not, or (with a window) the
+    other way round: each query's result has it or is untouched, whatever row tile it is in."""
+    lens = [longest, longest - 63, T]
+    c = Cache(lens, 2, dim, seed=81).fill(82)
+    c.k &= 0x77
+    c.v &= 0xF7
+    q = queries(c, T, group, 83)
+    ref, ref_lse = check_attention(c, q, window, sinks, 0.1)
+    want = torch.zeros_like(ref, dtype=torch.bool)
+    for s, n in enumerate(lens):
+        # a drafted token; and one that leaves the first queries' windows
+        for j, ch in ((n - T + T // 2, 5), (n - T + T // 2 - window, dim - 1)):
+            if not 0 <= j < n or (ch != 5 and not window):
+                continue
+            c.v[int(c.table[s, j // BLOCK]), 1, ch, j % BLOCK] = 0xFF
+            for t in range(T):
+                if bool((visible(n, T, t, window, sinks) == j).any()):
+                    want[s, t, group:, ch] = True
+    assert bool(want.any()) and not bool(want[:, :, group:, 5].all())
+    out, lse = attend(c, q, 0.1, window, sinks)
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(out[~want], ref[~want]) and torch.equal(lse, ref_lse)
+    # a key: the whole result of the queries that see it
+    j = longest - T + T // 2
+    c.k[int(c.table[0, j // BLOCK]), 0, j % BLOCK, 3] = 0x7F
+    out, lse = attend(c, q, 0.1, window, sinks)
+    for t in range(T):
+        if bool((visible(longest, T, t, window, sinks) == j).any()):
+            want[0, t, :group] = True
+    assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], ref[~want])
+
+
 def test_attention_large_and_small_logits():
     c = Cache([500, 90], 2, 64, seed=39).fill(40)
     for factor in (1e-6, 30.0, 3e3):
