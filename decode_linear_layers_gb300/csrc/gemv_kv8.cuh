@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
           if (whole) {
             const int64_t at_row = kv_out_row(a, at.s, h, row0 + r);
             unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + g;
-            const float inv = den == 0.f ? 0.f : kKvLifted / den;
+            const float inv = den == 0.f ? 0.f : kKvLifted * (1.f / den);
 #pragma unroll
             for (int i = 0; i < DT; ++i) {
               out[16 * i] = f8_round16(o[n][i][e] * inv, a.dtype);
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(kKvJoinThreads) k_kv8_join(const KvArgs a) {
   if (r >= rows) return;
   const int64_t at_row = kv_out_row(a, s, h, row0 + r);
   unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + d;
-  const float inv = sum.den == 0.f ? 0.f : kKvLifted / sum.den, v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
+  const float inv = sum.den == 0.f ? 0.f : kKvLifted * (1.f / sum.den), v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
   if (d == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(sum.m, sum.den);
