@@ -234,9 +234,11 @@ gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, 
   // 4096x4096 B=256 20.6 / 17.4, B=1000 21.6 / 26.1, 1000x2048 B=500 17.3 / 11.9).
   if (B <= 128 || (M + 255) / 256 * (((int64_t)B + 127) / 128) * 2 < sms) return f8_launch<128, true>(a, A, x, K, sms, s);
   // From two rounds of 256 x 256 tiles on, pairs of SMs: they move less through shared memory
-  // and so draw less power (us, pairs / single: 4096x14336 B=8192 374 / 396 alone, 403 / 453
-  // where seconds of it run into the power limit; 128256x4096 B=256 139 / 145; 28672x4096
-  // B=4096 435 / 438; 4096x4096 B=2048, one round, 40.7 / 40.4).
+  // and so draw less power (us, pairs / single, thirty calls in a row: 4096x14336 B=8192 391 /
+  // 425, B=4864 228 / 240, B=3584 160 / 171; 128256x4096 B=256 132 / 141; 28672x4096 B=4096
+  // 429 / 430; 4096x4096 B=2048, one round, 40.7 / 40.4).  They know whole rounds only, and
+  // lose where the last one is nearly empty: 4096x14336 B=2432 and 2560, 160 tiles for 152
+  // pairs' places, 155 / 109 and 156 / 135; B=2816 157 / 143.
   if ((M + 255) / 256 * (((int64_t)B + 255) / 256) >= sms) return f8_launch_pair(a, A, x, K, sms, s);
   return f8_launch<256, true>(a, A, x, K, sms, s);
 }

@@ -381,8 +381,8 @@ __device__ __forceinline__ void f8_rows_out(const F8Args &a, float (&acc)[COLS],
 // kPrompt = true: a tile is 128 vectors x N weight rows (128, or 256 in two blocks, one per
 //   scaling warpgroup); thread = vector, so that its factor sa sx is one number per k-block.
 // What bounds it, on a GB300: up to some hundred vectors the weights' bytes (28672x4096 with
-// 16 vectors 23.3 us, 5.1 TB/s; 128256x4096 with 64 98 us, 5.5 TB/s) and, for small matrices,
-// the start of the ring and the sum of the slices (6144x4096 with one vector 7.9 us);
+// 16 vectors 23.4 us, 5.1 TB/s; 128256x4096 with 64 90.6 us, 6.0 TB/s) and, for small matrices,
+// the start of the ring and the sum of the slices (6144x4096 with one vector 7.8 us);
 // beyond, the hand-over of the accumulators between the MMA warp and the scaling warps.
 template <int N, bool kPrompt>
 struct F8Form {
@@ -786,8 +786,9 @@ __global__ void __launch_bounds__(F8Form<N, kPrompt>::kThreads, 1)
 // and reads 32 KB in each SM instead of 48 (those 48 KB cost 768 cycles of shared-memory
 // bandwidth, the MMA itself 512).  CTA 0's MMA warp issues for both; a commit reaches both
 // CTAs' barriers, and both CTAs' scaling warps hand the accumulator back to CTA 0.
-// Whole tiles only, round-robin over the pairs.  4096x14336 with 8192 vectors: 374 us, 2570
-// TFLOP/s (396 with single SMs); a k-block takes 900 cycles, of which the MMA warp waits
+// Whole tiles only, round-robin over the pairs.  4096x14336 with 8192 vectors, thirty calls in
+// a row: 390 us, 2470 TFLOP/s (425 with single SMs); in longer runs, at the power limit, 405;
+// after a pause 375; a k-block takes 900 cycles, of which the MMA warp waits
 // 500 for the accumulator (two of 256 columns fill the tensor memory).
 struct F8Pair {
   static constexpr int kN = 256, kCols = 128, kThreads = 384, kAcc = 2;

@@ -88,8 +88,8 @@ class Layer:
         return (qkv[:, :a].view(n, self.q_heads, d), qkv[:, a:b].view(n, self.heads, d), qkv[:, b:].view(n, self.heads, d))
 
     def prompt(self, x, counts):
-        """The prompts' keys and values into the cache (their attention is not needed to
-        decode from them)."""
+        """The prompts' keys and values into the cache.  (This one layer can decode from them
+        without their attention; a layer above it would need that for its own keys.)"""
         qkv = torch.empty(x.shape[0], self.qkv.shape[1], dtype=torch.bfloat16, device="cuda")
         self.linear(x, self.w_qkv, qkv)
         _, k, v = self.split(qkv)

@@ -33,11 +33,14 @@
  * Ownership and memory: every pointer is caller-owned DEVICE memory on the
  * current CUDA device.  A, x, bias and row_scale are only read; y is only written
  * and must not overlap any input (checked on the host).  The library keeps no
- * pointer after the call returns.  Only the CUDA-core split-K paths (few long rows,
- * or x[0..B) too large to stage whole) use scratch memory: they take it from the
- * stream-ordered pool (cudaMallocAsync / cudaFreeAsync on the caller's stream), so
- * nothing is allocated or freed synchronously.  The tensor-core kernel sums its K
- * slices in the shared memory of one thread-block cluster and needs none.
+ * pointer after the call returns.  Scratch memory is used by the CUDA-core split-K paths
+ * (few long rows, or x[0..B) too large to stage whole), which take it from the device's
+ * stream-ordered pool, and by gemv_f8 (where tiles are shared between SMs) and
+ * gemv_kv8_attention (tables of more than four blocks), which take it from a pool of the
+ * library's own: one for each device, which keeps the memory that it has mapped.  Both
+ * are stream-ordered (cudaMallocAsync / cudaFreeAsync on the caller's stream), so
+ * nothing is allocated or freed synchronously.  The fp16/bf16 tensor-core kernel sums
+ * its K slices in the shared memory of one thread-block cluster and needs none.
  *
  * Execution: asynchronous on `stream` (NULL = the legacy default stream).  The
  * call validates its arguments, picks a kernel from (dtype, M, K, B, alignment)
@@ -245,8 +248,9 @@ gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, fl
  * first, are 0 or in fp32's normal range: beyond it the group counts as infinite or NaN,
  * below it bits are lost (a group of zeros stays 0).  K must be a multiple of GEMV_F8_ALIGN and A and x aligned to it
  * (GEMV_ERR_INVALID_VALUE otherwise); M and B are any, up to 2^31 - 256, K up to 2^29, and
- * (M / 128 + 1) (B / 128 + 1) up to 2^30.  A scratch buffer of a few MB comes from the
- * library's stream-ordered pool where tiles are shared between SMs.  The kernel's waits
+ * (M / 128 + 1) (B / 128 + 1) up to 2^30.  A scratch buffer (3 to 40 MB with 152 SMs:
+ * two partial sums of a tile for each) comes from the library's stream-ordered pool
+ * where tiles are shared between SMs.  The kernel's waits
  * are bounded (gemv_get_device_status; y is undefined where one ran out). */
 gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
                       void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream);
@@ -323,7 +327,9 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
  * result does not depend on the run: partial results are merged in a fixed order.  lens beyond the table count as the table's size.  A table entry outside
  * the pool counts as a block that no query sees, and gemv_get_device_status then
  * returns GEMV_ERR_INVALID_VALUE with bit 64.  The kernel's waits are bounded (out and lse
- * are undefined where one ran out). */
+ * are undefined where one ran out).  Tables of more than four blocks take a scratch buffer
+ * from the library's stream-ordered pool: 8 to 23 MB with 152 SMs (two partial results for
+ * each warp), and 16 bytes for each sequence, head and tile of query rows. */
 gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
                                  const int32_t *lens, void *out, float *lse, int S, int T, int q_heads, float scale,
                                  int64_t window, int64_t sinks, gemv_stream_t stream);
@@ -462,8 +468,8 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits);
 
 /* TEST ONLY — not thread-safe.  With `stall` != 0 every later GEMV_KERNEL_TC or gemv_f8
  * launch skips the last MMA of its first CTA (in the persistent form: the MMAs of that
- * CTA's last k-tile), and every gemv_kv8_attention launch the last copy of each
- * warp, so that the wait for it runs out after `timeout_ns` (<= 0: the
+ * CTA's last k-tile), and every gemv_kv8_attention launch all copies of values,
+ * so that the wait for it runs out after `timeout_ns` (<= 0: the
  * default of 2 s) and gemv_get_device_status reports GEMV_ERR_DEVICE_TIMEOUT.
  * With 2 or 3, where gemv_f8 runs on pairs of SMs, the first or the second CTA of the first
  * pair skips its last copies instead.  stall = 0 restores normal launches. */
