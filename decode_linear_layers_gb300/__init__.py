@@ -8,7 +8,10 @@ The names and argument order are those of ``include/gemv.h``:
     gemv_w8  (A, row_scale, x, bias, y, M, K, B, stream=None)
     gemv_f8  (A, a_scale, x, x_scale, bias, y, M, K, B, y_dtype="bf16", stream=None)
     gemv_f8_quantize(dtype, x, q, scale, K, B, stream=None)
+    gemv_qk_norm_rope(dtype, q, k, q_out, k_out, q_weight, k_weight, inv_freq, lens, starts, S, N,
+                      q_heads, k_heads, dim, rot, layout="half", eps=1e-6, factor=1.0, stream=None)
     gemv_kv8_append(dtype, *cache, k, v, lens, starts, S, N, stream=None)
+    gemv_kv8_read  (dtype, *cache, k, v, lens, starts, S, N, stream=None)
     gemv_kv8_attention(dtype, *cache, q, lens, out, lse, S, T, q_heads, scale,
                        window=0, sinks=0, stream=None)
 
@@ -34,7 +37,8 @@ __all__ = [
     "gemv_f32", "gemv_f16", "gemv_bf16", "gemv_w8", "gemv_w4", "gemv_bf16_splitk_noalloc", "gemv_ex",
     "gemv_swiglu", "gemv_host", "set_launch_overlap", "ACT_NONE", "ACT_SILU", "GemvError", "Plan", "plan_for",
     "status_string", "launch_count", "last_cuda_error", "force_kernel", "last_plan",
-    "gemv_f8", "gemv_f8_quantize", "gemv_kv8_append", "gemv_kv8_attention", "F8_GROUP", "KV8_BLOCK",
+    "gemv_f8", "gemv_f8_quantize", "gemv_kv8_append", "gemv_kv8_read", "gemv_kv8_attention", "gemv_qk_norm_rope",
+    "rope_frequencies", "F8_GROUP", "KV8_BLOCK",
     "KERNELS", "DTYPE_CODES", "lib", "build", "LIB_PATH", "device_status", "test_stall",
 ]
 
@@ -113,6 +117,13 @@ def lib() -> ctypes.CDLL:
         L.gemv_f8.restype = ci
         L.gemv_kv8_append.argtypes = [ci, vp, vp, i64, vp, i64, vp, vp, ci, i64, vp]
         L.gemv_kv8_append.restype = ci
+        L.gemv_kv8_read.argtypes = [ci, vp, vp, i64, vp, i64, vp, vp, ci, i64, vp]
+        L.gemv_kv8_read.restype = ci
+        cf, cd = ctypes.c_float, ctypes.c_double
+        L.gemv_qk_norm_rope.argtypes = ([ci] + [vp, i64, vp, i64, vp, ci] * 2 + [ci, cf, vp, ci, ci, cf, vp, vp, ci, i64, vp])
+        L.gemv_qk_norm_rope.restype = ci
+        L.gemv_rope_frequencies.argtypes = [ctypes.POINTER(cf), ci, cd, ci, cd, cd, cd, cd, ctypes.POINTER(cf)]
+        L.gemv_rope_frequencies.restype = ci
         L.gemv_kv8_attention.argtypes = [ci, vp, vp, i64, vp, vp, vp, ci, ci, ci, ctypes.c_float, i64, i64, vp]
         L.gemv_kv8_attention.restype = ci
         L.gemv_set_launch_overlap.argtypes = [ci]
@@ -413,6 +424,46 @@ def gemv_f8(A, a_scale, x, x_scale, bias, y, M, K, B, y_dtype="bf16", stream=Non
     _check(_fn("gemv_f8")(*args, DTYPE_CODES[y_dtype], M, K, B, _stream(stream)))
 
 
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
+
+
+def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0, high=32.0) -> tuple:
+    """(rot / 2 floats for gemv_qk_norm_rope's inv_freq, its `factor`), worked out on the
+    host: base^(-2 i / rot), for a context `factor` times as long as `original` tokens by
+    "linear", "base", "turns" (low, high: turns of a pair in the original context) or
+    "index" scaling."""
+    freq, att = (ctypes.c_float * max(1, rot // 2))(), ctypes.c_float(1.0)
+    _check(lib().gemv_rope_frequencies(freq, int(rot), float(base), ROPE_SCALINGS[scaling], float(factor), float(original),
+                                       float(low), float(high), ctypes.byref(att)))
+    return list(freq)[:rot // 2], float(att.value)
+
+
+def gemv_qk_norm_rope(dtype, q, k, q_out, k_out, q_weight, k_weight, inv_freq, lens, starts, S, N, q_heads, k_heads, dim,
+                      rot, layout="half", eps=1e-6, factor=1.0, stream=None) -> None:
+    """Norm (over each head's dim channels, with q_weight and k_weight; None: none) and
+    rotation by the position of N rows of queries (q_heads x dim of `dtype`) and keys
+    (k_heads x dim): pair i of the first `rot` channels, (i, i + rot / 2) ("half") or
+    (2 i, 2 i + 1) ("interleaved"), by position x inv_freq[i] (fp32), cos and sin times
+    `factor`.  lens and starts (int32) say where the rows stand, as gemv_kv8_append takes
+    them.  q, k, q_out and k_out may be columns of wider tensors; an output of None means in
+    place; k may be None with k_heads == 0, and q with q_heads == 0."""
+    S, N, q_heads, k_heads, dim, rot = int(S), int(N), int(q_heads), int(k_heads), int(dim), int(rot)
+    size, n = _ESIZE[dtype][1], max(N, 0)
+    sides = []
+    for x, y, w, heads, what in ((q, q_out, q_weight, q_heads, "q"), (k, k_out, k_weight, k_heads, "k")):
+        row = max(0, heads * dim)
+        if row == 0 and x is None:
+            sides += [None, 0, None, 0, None, heads]
+            continue
+        xa, xs = _rows(x, size, n, row, what)
+        ya, ys = (xa, xs) if y is None else _rows(y, size, n, row, what + "_out")
+        sides += [xa, xs, ya, ys, _addr(w, size, max(dim, 0), what + "_weight"), heads]
+    _check(_fn("gemv_qk_norm_rope")(DTYPE_CODES[dtype], *sides, dim, float(eps), _addr(inv_freq, 4, max(0, rot // 2), "inv_freq"),
+                                    rot, ROPE_LAYOUTS[layout], float(factor), _addr(lens, 4, max(S, 0), "lens"),
+                                    _addr(starts, 4, S + 1, "starts"), S, N, _stream(stream)))
+
+
 def _kv8_cache(k, v, k_scale, v_scale, table, S):
     """The cache as the library takes it (packed), heads and dim; sizes from the
     tensors' shapes."""
@@ -472,6 +523,19 @@ def gemv_kv8_append(dtype, k_cache, v_cache, k_scale, v_scale, table, k, v, lens
     va, vs = _rows(v, size, max(N, 0), row, "v")
     _check(_fn("gemv_kv8_append")(DTYPE_CODES[dtype], cache, ka, ks, va, vs, _addr(lens, 4, max(S, 0), "lens"),
                                   _addr(starts, 4, S + 1, "starts"), S, N, _stream(stream)))
+
+
+def gemv_kv8_read(dtype, k_cache, v_cache, k_scale, v_scale, table, k, v, lens, starts, S, N, stream=None) -> None:
+    """Cached tokens as N rows of k and v (each heads x dim of `dtype`, columns of a wider
+    tensor as well; None: not read): the rows starts[s] .. starts[s + 1] (int32, S + 1
+    values; None: N / S each) are the last ones of the lens[s] tokens of sequence s."""
+    S, N = int(S), int(N)
+    cache, heads, dim = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, row = _ESIZE[dtype][1], heads * dim
+    ka, ks = (None, 0) if k is None else _rows(k, size, max(N, 0), row, "k")
+    va, vs = (None, 0) if v is None else _rows(v, size, max(N, 0), row, "v")
+    _check(_fn("gemv_kv8_read")(DTYPE_CODES[dtype], cache, ka, ks, va, vs, _addr(lens, 4, max(S, 0), "lens"),
+                                _addr(starts, 4, S + 1, "starts"), S, N, _stream(stream)))
 
 
 def gemv_kv8_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, q, lens, out, lse, S, T, q_heads, scale,

@@ -1,4 +1,4 @@
-// gemv_kv8_append and gemv_kv8_attention: argument checks, the choice of the form,
+// gemv_kv8_append, gemv_kv8_read and gemv_kv8_attention: argument checks, the choice of the form,
 // launches.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -37,6 +37,15 @@ bool span(int64_t rows, int64_t row, int64_t stride, int size, int64_t *out) {
   return mul_ok(rows - 1, stride, &n) && !__builtin_add_overflow(n, row, &n) && mul_ok(n, size, out);
 }
 
+// Two sets of rows of `row` elements are different columns of the same matrix.
+bool columns(const void *p, int64_t p_stride, const void *q, int64_t q_stride, int64_t row, int size) {
+  if (p == nullptr || q == nullptr || p_stride != q_stride) return false;
+  const int64_t stride = p_stride * size, bytes = row * size;
+  int64_t d = (int64_t)((uintptr_t)q - (uintptr_t)p) % stride;
+  if (d < 0) d += stride;
+  return d >= bytes && stride - d >= bytes;
+}
+
 KvArgs cache_args(const gemv_kv8_cache_t *c) {
   KvArgs a;
   a.k = c->k;
@@ -50,10 +59,14 @@ KvArgs cache_args(const gemv_kv8_cache_t *c) {
   return a;
 }
 
+// Blocks that the rows can reach, at most: CTAs along x.
+int64_t reached(const KvArgs &a) {
+  return a.starts == nullptr ? (int64_t)a.S * ((a.T + kKvBlock - 2) / kKvBlock + 1) : a.N / kKvBlock + 2 * (int64_t)a.S;
+}
+
 template <int D>
 cudaError_t append(KvArgs a, int sms, cudaStream_t s) {
-  // CTAs along x: the blocks that the new tokens can reach, at most
-  const int64_t x = a.starts == nullptr ? (int64_t)a.S * ((a.T + kKvBlock - 2) / kKvBlock + 1) : a.N / kKvBlock + 2 * (int64_t)a.S;
+  const int64_t x = reached(a);
   if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // one unit for each CTA while the SMs hold all of them (four CTAs each), else two, so that
   // finding the block is paid once for both (us with one / two / four, 5 ragged prompts of
@@ -64,6 +77,15 @@ cudaError_t append(KvArgs a, int sms, cudaStream_t s) {
                                                                          : k_kv8_append<D, GEMV_DTYPE_BF16>;
   return launch_k(kern, dim3((unsigned)x, (unsigned)((units + a.per_cta - 1) / a.per_cta)), dim3(kKvAppendThreads), 0, s,
                   launch_overlap(), a);
+}
+
+template <int D>
+cudaError_t read_back(const KvArgs &a, cudaStream_t s) {
+  const int64_t x = reached(a), parts = (int64_t)a.sides * a.heads * (D / 64), y = (parts + kKvReadThreads / 32 - 1) / (kKvReadThreads / 32);
+  if (x > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  auto kern = a.dtype == GEMV_DTYPE_F32 ? k_kv8_read<D, GEMV_DTYPE_F32> : a.dtype == GEMV_DTYPE_F16 ? k_kv8_read<D, GEMV_DTYPE_F16>
+                                                                         : k_kv8_read<D, GEMV_DTYPE_BF16>;
+  return launch_k(kern, dim3((unsigned)x, (unsigned)(y < 65535 ? y : 65535)), dim3(kKvReadThreads), 0, s, launch_overlap(), a);
 }
 
 // Tables of at most so many blocks per sequence: every item is one warp's, whole, in one
@@ -178,6 +200,52 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
   if ((st = device_sms(&sms)) != GEMV_SUCCESS) return st;
   const cudaError_t e = cache->dim == 64 ? append<64>(a, sms, s) : cache->dim == 128 ? append<128>(a, sms, s)
                         : cache->dim == 192 ? append<192>(a, sms, s) : append<256>(a, sms, s);
+  if (e != cudaSuccess) return fail((int)e);
+  count_launches(1);
+  return GEMV_SUCCESS;
+}
+
+gemv_status_t gemv_kv8_read(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, void *k, int64_t k_stride, void *v,
+                            int64_t v_stride, const int32_t *lens, const int32_t *starts, int S, int64_t N,
+                            gemv_stream_t stream) {
+  if (dtype < GEMV_DTYPE_F32 || dtype > GEMV_DTYPE_BF16 || S < 0 || N < 0) return GEMV_ERR_INVALID_VALUE;
+  int64_t kv_bytes;
+  gemv_status_t st = check_cache(cache, &kv_bytes);
+  if (st != GEMV_SUCCESS) return st;
+  if (S == 0 || N == 0 || cache->heads == 0 || (k == nullptr && v == nullptr)) return GEMV_SUCCESS;
+  if (N > 0x7fffffff || (starts == nullptr && N % S != 0)) return GEMV_ERR_INVALID_VALUE;
+  const int size = dtype == GEMV_DTYPE_F32 ? 4 : 2;
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  int64_t kb = 0, vb = 0;
+  if (k != nullptr && (k_stride < row || !aligned(k, size) || !span(N, row, k_stride, size, &kb))) return GEMV_ERR_INVALID_VALUE;
+  if (v != nullptr && (v_stride < row || !aligned(v, size) || !span(N, row, v_stride, size, &vb))) return GEMV_ERR_INVALID_VALUE;
+  if (!cache_pointers(cache) || lens == nullptr || !aligned(lens, 4) || !aligned(starts, 4)) return GEMV_ERR_INVALID_VALUE;
+  // nothing that is written may overlap anything else
+  const int64_t sb = cache->blocks * cache->heads * 4;
+  const struct { const void *p; int64_t n; } part[] = {
+      {k, kb}, {v, vb}, {cache->k, kv_bytes}, {cache->v, kv_bytes}, {cache->k_scale, sb}, {cache->v_scale, sb},
+      {cache->table, (int64_t)S * cache->width * 4}, {lens, (int64_t)S * 4}, {starts, ((int64_t)S + 1) * 4}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < 9; ++j) {
+      if (i == 0 && j == 1 && columns(k, k_stride, v, v_stride, row, size)) continue;
+      if (overlaps(part[i].p, part[i].n, part[j].p, part[j].n)) return GEMV_ERR_INVALID_VALUE;
+    }
+  KvArgs a = cache_args(cache);
+  if ((st = device_status_word(&a.status)) != GEMV_SUCCESS) return st;
+  a.out_k = k;
+  a.out_v = v;
+  a.sides = (k != nullptr) + (v != nullptr);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.lens = lens;
+  a.starts = starts;
+  a.S = S;
+  a.N = N;
+  a.T = (int)(N / S);
+  a.dtype = (int)dtype;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->dim == 64 ? read_back<64>(a, s) : cache->dim == 128 ? read_back<128>(a, s)
+                        : cache->dim == 192 ? read_back<192>(a, s) : read_back<256>(a, s);
   if (e != cudaSuccess) return fail((int)e);
   count_launches(1);
   return GEMV_SUCCESS;

@@ -1,5 +1,6 @@
 // Kernels of the 8-bit cache of keys and values: the append of new tokens
-// (gemv_kv8_append) and the attention over it (gemv_kv8_attention).
+// (gemv_kv8_append), cached tokens read back (gemv_kv8_read) and the attention over it
+// (gemv_kv8_attention).
 //
 // A block holds kKvBlock = 64 tokens of one head: the keys as 64 rows of D e4m3 values,
 // the values as D rows of 64 (token index innermost, so that the second product finds
@@ -28,6 +29,9 @@ struct KvArgs {
   const int32_t *starts = nullptr;
   int64_t N = 0;
   int dtype = 0, per_cta = 1;
+  // read
+  void *out_k = nullptr, *out_v = nullptr;
+  int sides = 0;  // keys, values: how many of them
   // attention
   const void *q = nullptr;
   void *out = nullptr;
@@ -67,27 +71,17 @@ __device__ __forceinline__ uint32_t kv_rescale4(uint32_t w, float r) {
   return f8_pack2(a.x * r, a.y * r) | (f8_pack2(b.x * r, b.y * r) << 16);
 }
 
-// ------------------------------------------------------------------ append
-// A CTA has a block that new tokens reach, and of it one or more units (a head's keys, or
-// its values): it reads a unit's new tokens once (eight values of a token per load), finds
-// their largest, and so the unit's scale; where that grows it moves the tokens the block
-// held to the new scale; and it writes the new ones.  No other CTA touches the unit, so
-// nothing is atomic.  Values pass through shared memory to lie token-innermost.  Bound by
-// latency (lengths, table, tokens, one after the other) and instructions: 64 sequences of
-// one new token 6 us, 5 prompts of 10 k tokens in all 17 us (67 MB: 9.8 at the copy rate).
-constexpr int kKvAppendThreads = 256;
-template <int D, int DT>
-__global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
-  constexpr int kPieces = D / 8;                          // of a token
-  constexpr int kLoads = (kKvBlock * kPieces / kKvAppendThreads + 3) / 4 * 4;
-  constexpr int kStride = kKvBlock / kLoads;              // threads along the tokens
-  constexpr int kActive = kStride * kPieces;              // threads with channels
-  static_assert(kActive <= kKvAppendThreads && kKvBlock % kLoads == 0);
-  __shared__ float part[kKvAppendThreads / 32];
-  __shared__ __align__(16) uint32_t tile[D * (kKvBlock / 4)];  // values: words of four tokens
-  pdl_trigger();
-  pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31;
+// ------------------------------------------------------------------ rows and blocks
+// The rows of gemv_kv8_append and gemv_kv8_read: n of each sequence, its last n positions.
+// A CTA (blockIdx.x) has one block that they reach.
+struct KvReach {
+  int64_t first, before, len, p0;  // the sequence's first row, its tokens before that, all, the block's first token
+  int32_t block;                   // of the pool
+};
+// One warp, converged; false where there is nothing to do.  `tell` (one thread of the CTA):
+// reports a block that is missing, and (`once`: one CTA of those with the same blockIdx.x)
+// a sequence with fewer tokens than rows.
+__device__ __forceinline__ bool kv_reach(const KvArgs &a, int lane, bool tell, bool once, KvReach &r) {
   // the sequence, and which of its blocks
   int s;
   int64_t first, n, nth;  // its first new token, how many, and the block's number among those they reach
@@ -116,20 +110,50 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
     n = (e > a.N ? a.N : e) - first;
     nth = (int64_t)blockIdx.x - (b / kKvBlock + 2 * (int64_t)s);
   }
-  const int64_t len = __ldg(a.lens + s), before = len - n;
-  if (n <= 0 || nth < 0) return;
-  if (before < 0) {  // fewer tokens than the new ones: nothing says where they go
-    if (tid == 0 && nth == 0 && blockIdx.y == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-    return;
+  r.first = first;
+  r.len = __ldg(a.lens + s);
+  r.before = r.len - n;
+  if (n <= 0 || nth < 0) return false;
+  if (r.before < 0) {  // fewer tokens than the new ones: nothing says where they go
+    if (tell && nth == 0 && once && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+    return false;
   }
-  const int64_t blk = before / kKvBlock + nth;
-  const int64_t p0 = blk * kKvBlock;
-  if (p0 >= len) return;
-  const int32_t pb = blk < a.width ? __ldg(a.table + (int64_t)s * a.width + blk) : -1;
-  if (pb < 0 || pb >= a.blocks) {
-    if (tid == 0 && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-    return;
+  const int64_t blk = r.before / kKvBlock + nth;
+  r.p0 = blk * kKvBlock;
+  if (r.p0 >= r.len) return false;
+  r.block = blk < a.width ? __ldg(a.table + (int64_t)s * a.width + blk) : -1;
+  if (r.block < 0 || r.block >= a.blocks) {
+    if (tell && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+    return false;
   }
+  return true;
+}
+
+// ------------------------------------------------------------------ append
+// A CTA has a block that new tokens reach, and of it one or more units (a head's keys, or
+// its values): it reads a unit's new tokens once (eight values of a token per load), finds
+// their largest, and so the unit's scale; where that grows it moves the tokens the block
+// held to the new scale; and it writes the new ones.  No other CTA touches the unit, so
+// nothing is atomic.  Values pass through shared memory to lie token-innermost.  Bound by
+// latency (lengths, table, tokens, one after the other) and instructions: 64 sequences of
+// one new token 6 us, 5 prompts of 10 k tokens in all 17 us (67 MB: 9.8 at the copy rate).
+constexpr int kKvAppendThreads = 256;
+template <int D, int DT>
+__global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a) {
+  constexpr int kPieces = D / 8;                          // of a token
+  constexpr int kLoads = (kKvBlock * kPieces / kKvAppendThreads + 3) / 4 * 4;
+  constexpr int kStride = kKvBlock / kLoads;              // threads along the tokens
+  constexpr int kActive = kStride * kPieces;              // threads with channels
+  static_assert(kActive <= kKvAppendThreads && kKvBlock % kLoads == 0);
+  __shared__ float part[kKvAppendThreads / 32];
+  __shared__ __align__(16) uint32_t tile[D * (kKvBlock / 4)];  // values: words of four tokens
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
+  KvReach b;
+  if (!kv_reach(a, lane, tid == 0, blockIdx.y == 0, b)) return;
+  const int64_t p0 = b.p0, len = b.len, before = b.before, first = b.first;
+  const int32_t pb = b.block;
   const int held = before > p0 ? (int)(before - p0) : 0;             // tokens the block has
   const int end = len - p0 < kKvBlock ? (int)(len - p0) : kKvBlock;  // and will have
   const int64_t t0 = first + (p0 + held - before);                   // the first of its new tokens
@@ -245,6 +269,109 @@ __global__ void __launch_bounds__(kKvAppendThreads) k_kv8_append(const KvArgs a)
           w = (w & ~(below | above)) | ((move ? kv_rescale4(was, ratio) : was) & below) | (was & above);
         }
         at[k] = w;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read
+// The mirror of the append: cached tokens back as rows.  A warp has 64 x 64 values of a
+// block and head at a time, keys or values, and no other does; there is nothing to share.
+//   keys    a lane reads eight channels of a token (eight bytes), sixteen times
+//   values  a lane reads sixteen tokens of eight channels (eight words of 16 bytes; four
+//           lanes read a channel's 64 tokens) and turns 4 x 4 bytes at a time, so that it
+//           has eight channels of a token to store, and eight neighbours 128 bytes (16 bits)
+// Either way 64 or 128 bytes a lane are on their way at once.  Bound by the bytes.
+constexpr int kKvReadThreads = 128;
+
+__device__ __forceinline__ uint32_t kv_prmt(uint32_t a, uint32_t b, uint32_t how) { return __byte_perm(a, b, how); }
+// Eight e4m3 values (channels, as two words) times the scale, as a row's elements.
+template <int DT>
+__device__ __forceinline__ void kv_row8(void *out, int64_t i, uint32_t lo, uint32_t hi, float scale, bool vec) {
+  const float2 a = f16x2_to_f2(kv_half2_lo(lo)), b = f16x2_to_f2(kv_half2_hi(lo));
+  const float2 c = f16x2_to_f2(kv_half2_lo(hi)), d = f16x2_to_f2(kv_half2_hi(hi));
+  const float v[8] = {a.x * scale, a.y * scale, b.x * scale, b.y * scale, c.x * scale, c.y * scale, d.x * scale, d.y * scale};
+  if constexpr (DT == GEMV_DTYPE_F32) {
+    float *p = reinterpret_cast<float *>(out) + i;
+    if (vec) {
+      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = v[j];
+    }
+  } else {
+    unsigned short *p = reinterpret_cast<unsigned short *>(out) + i;
+    const uint4 w = make_uint4(f8_pack16(v[0], v[1], DT), f8_pack16(v[2], v[3], DT), f8_pack16(v[4], v[5], DT), f8_pack16(v[6], v[7], DT));
+    if (vec) {
+      *reinterpret_cast<uint4 *>(p) = w;
+    } else {
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = (unsigned short)(h[j / 2] >> (16 * (j & 1)));
+    }
+  }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kKvReadThreads) k_kv8_read(const KvArgs a) {
+  constexpr int kParts = D / 64;  // 64 x 64 values: of a head's keys, and of its values
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
+  KvReach b;
+  if (!kv_reach(a, lane, tid == 0, blockIdx.y == 0, b)) return;
+  const int lo = b.before > b.p0 ? (int)(b.before - b.p0) : 0;                // the block's tokens that are asked for
+  const int hi = b.len - b.p0 < kKvBlock ? (int)(b.len - b.p0) : kKvBlock;
+  const int64_t row0 = b.first + b.p0 - b.before;                            // row of the block's token 0
+  constexpr int kSize = DT == GEMV_DTYPE_F32 ? 4 : 2;
+  const int of_side = a.heads * kParts;
+  for (int part = blockIdx.y * (kKvReadThreads / 32) + (tid >> 5); part < a.sides * of_side; part += gridDim.y * (kKvReadThreads / 32)) {
+    // keys first, then values, of those that are asked for
+    const int side = part / of_side, at = part - side * of_side, h = at / kParts, q = at - h * kParts;
+    const bool values = side == 1 || a.out_k == nullptr;
+    void *const out = values ? a.out_v : a.out_k;
+    const int64_t stride = values ? a.v_stride : a.k_stride;
+    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && (stride * kSize) % 16 == 0;
+    const int64_t unit = (int64_t)b.block * a.heads + h;
+    const float scale = __ldg((values ? a.v_scale : a.k_scale) + unit);
+    const uint8_t *src = (values ? a.v : a.k) + unit * (kKvBlock * D) + q * (kKvBlock * 64);
+    if (!values) {
+      // bytes 4096 q .. of the block's keys, 16 pieces of 8 for each lane
+      const uint2 *p = reinterpret_cast<const uint2 *>(src) + lane;
+      uint2 x[16];
+  #pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __ldg(p + i * 32);
+  #pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int byte = q * (kKvBlock * 64) + (i * 32 + lane) * 8, tok = byte / D, ch = byte - tok * D;
+        if (tok >= lo && tok < hi) kv_row8<DT>(out, (row0 + tok) * stride + (int64_t)h * D + ch, x[i].x, x[i].y, scale, vec);
+      }
+      continue;
+    }
+    const int ch = (lane >> 2) * 8, t0 = (lane & 3) * 16;  // channels 64 q + ch .., tokens t0 ..
+    uint4 x[8];
+  #pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __ldg(reinterpret_cast<const uint4 *>(src + (ch + j) * kKvBlock + t0));
+  #pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t r[8];
+  #pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = w == 0 ? x[j].x : w == 1 ? x[j].y : w == 2 ? x[j].z : x[j].w;
+  #pragma unroll
+      for (int g = 0; g < 2; ++g) {  // four channels of four tokens to four tokens of four channels
+        const uint32_t e0 = kv_prmt(r[4 * g], r[4 * g + 1], 0x5140), e1 = kv_prmt(r[4 * g + 2], r[4 * g + 3], 0x5140);
+        const uint32_t f0 = kv_prmt(r[4 * g], r[4 * g + 1], 0x7362), f1 = kv_prmt(r[4 * g + 2], r[4 * g + 3], 0x7362);
+        r[4 * g] = kv_prmt(e0, e1, 0x5410);
+        r[4 * g + 1] = kv_prmt(e0, e1, 0x7632);
+        r[4 * g + 2] = kv_prmt(f0, f1, 0x5410);
+        r[4 * g + 3] = kv_prmt(f0, f1, 0x7632);
+      }
+  #pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int tok = t0 + 4 * w + t;
+        if (tok >= lo && tok < hi)
+          kv_row8<DT>(out, (row0 + tok) * stride + (int64_t)h * D + q * 64 + ch, r[t], r[4 + t], scale, vec);
       }
     }
   }

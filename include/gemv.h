@@ -255,6 +255,60 @@ gemv_status_t gemv_f8_quantize(gemv_dtype_t dtype, const void *x, uint8_t *q, fl
 gemv_status_t gemv_f8(const uint8_t *A, const float *a_scale, const uint8_t *x, const float *x_scale, const void *bias,
                       void *y, gemv_dtype_t y_dtype, int64_t M, int64_t K, int B, gemv_stream_t stream);
 
+/* --------------------------------------- queries and keys before the attention */
+
+/* Which channels of a head form pair i of rot / 2: (i, i + rot / 2), or (2 i, 2 i + 1). */
+typedef enum gemv_rope_layout {
+  GEMV_ROPE_HALF = 0,
+  GEMV_ROPE_INTERLEAVED = 1
+} gemv_rope_layout_t;
+
+/* Norm of each head of the queries and keys and its rotation by the token's position, in
+ * one pass.  With x a head of a row at position p, of `dim` channels:
+ *     n_c = x_c w_c / sqrt(mean_c(x_c^2) + eps)     (n_c = x_c where the weight is NULL)
+ *     y_a = factor (n_a cos t - n_b sin t),  y_b = factor (n_b cos t + n_a sin t),
+ *           t = p inv_freq[i], for pair i = (a, b) of the first `rot` channels
+ *     y_c = n_c for the channels from `rot` on
+ * N rows of q_heads (k_heads) x dim elements of `dtype` (F32, F16, BF16), q_stride
+ * (k_stride) elements apart: both may be columns of one projection's output.  The rows'
+ * positions are those to which gemv_kv8_append writes them: with starts, row i of
+ * starts[s] .. starts[s + 1] - 1 (S + 1 values, rising from 0 to N) is at position
+ * lens[s] - starts[s + 1] + i; with starts == NULL every sequence has N / S rows.
+ *   q_out, k_out  rows as q and k; either may be its input, with the same stride (in place),
+ *            and overlaps nothing else (columns of one matrix do not overlap)
+ *   q_weight, k_weight  dim of `dtype`, or NULL: no norm
+ *   inv_freq rot / 2 fp32, finite, below 2^24: radians per position
+ *            (gemv_rope_frequencies has the usual ones); any with rot == 0
+ *   rot      even, 0 .. dim;  dim up to 512 (GEMV_ERR_UNSUPPORTED above);  eps >= 0
+ * With k_heads == 0 (q_heads == 0) there are no keys (queries).  Rows that no sequence has,
+ * and those of a sequence with fewer tokens than rows, are left as they were.
+ * Sums and products are fp32, rounded once at the end; angles are good to 2^-23 radians at
+ * any position.  The mean of squares has to be in fp32's range. */
+gemv_status_t gemv_qk_norm_rope(gemv_dtype_t dtype, const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                                const void *q_weight, int q_heads, const void *k, int64_t k_stride, void *k_out,
+                                int64_t k_out_stride, const void *k_weight, int k_heads, int dim, float eps,
+                                const float *inv_freq, int rot, gemv_rope_layout_t layout, float factor, const int32_t *lens,
+                                const int32_t *starts, int S, int64_t N, gemv_stream_t stream);
+
+/* How the frequencies f_i = base^(-2 i / rot) are changed for contexts `factor` times as
+ * long as the `original` one that a model was trained on. */
+typedef enum gemv_rope_scaling {
+  GEMV_ROPE_SCALE_NONE = 0,
+  GEMV_ROPE_SCALE_LINEAR = 1, /* f_i / factor: positions pressed together */
+  GEMV_ROPE_SCALE_BASE = 2,   /* base times factor^(rot / (rot - 2)): the last pair / factor, the first as it is */
+  GEMV_ROPE_SCALE_TURNS = 3,  /* by the turns r = original f_i / (2 pi) of a pair: f_i with r >= high,
+                                 f_i / factor with r <= low, linear in r between them */
+  GEMV_ROPE_SCALE_INDEX = 4   /* linear in i between the pairs, rounded outwards, that would turn high
+                                 and low times; attention is 0.1 ln(factor) + 1 */
+} gemv_rope_scaling_t;
+
+/* Host only: fills inv_freq (host memory, rot / 2 values) for gemv_qk_norm_rope, and
+ * *attention (may be NULL) with what the scaling multiplies cos and sin by (`factor` of
+ * gemv_qk_norm_rope; 1 except for GEMV_ROPE_SCALE_INDEX with factor > 1).  factor > 0 is used by
+ * the scalings 1 to 4, original > 0 and 0 < low < high (turns) by 3 and 4.  base > 1. */
+gemv_status_t gemv_rope_frequencies(float *inv_freq, int rot, double base, gemv_rope_scaling_t scaling, double factor,
+                                    double original, double low, double high, float *attention);
+
 /* ------------------------------------------- 8-bit cache of keys and values */
 
 /* Tokens of a block of the cache; each block has one scale per head, for its keys and
@@ -301,6 +355,20 @@ typedef struct gemv_kv8_cache {
 gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *k, int64_t k_stride,
                               const void *v, int64_t v_stride, const int32_t *lens, const int32_t *starts, int S,
                               int64_t N, gemv_stream_t stream);
+
+/* Cached tokens back as rows, the mirror of gemv_kv8_append: with the same lens, starts, S
+ * and N, row i of k and v becomes the key and value that the cache holds at the position
+ * to which gemv_kv8_append would write row i, k * k_scale rounded once to `dtype` (F32, F16,
+ * BF16; NaN stays NaN).  So a sequence's rows are the last starts[s + 1] - starts[s] of its
+ * lens[s] tokens; a range that ends earlier is read with that end as lens[s].  k or v may be
+ * NULL: it is not read.  Both may be columns of one matrix; they overlap nothing else.
+ * Rows that no sequence has are left as they were.  So are those of a sequence with fewer
+ * tokens than rows and of a position that has no block of the pool, and
+ * gemv_get_device_status then returns GEMV_ERR_INVALID_VALUE with bit 64.  Blocks without
+ * such positions, and their table entries, are not read. */
+gemv_status_t gemv_kv8_read(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, void *k, int64_t k_stride, void *v,
+                            int64_t v_stride, const int32_t *lens, const int32_t *starts, int S, int64_t N,
+                            gemv_stream_t stream);
 
 /* Attention of the newest T tokens (T <= GEMV_KV8_MAX_TOKENS: one in plain decoding, a
  * few drafted ones checked at once) of S sequences over the cache, which holds them
