@@ -14,6 +14,8 @@ The names and argument order are those of ``include/gemv.h``:
     gemv_kv8_read  (dtype, *cache, k, v, lens, starts, S, N, stream=None)
     gemv_kv8_attention(dtype, *cache, q, lens, out, lse, S, T, q_heads, scale,
                        window=0, sinks=0, stream=None)
+    gemv_kv8_prefix_attention(dtype, *cache, q, lens, firsts, prefix, out, lse, S, T, q_heads,
+                              scale, stream=None)
 
 (``cache``: k, v, k_scale, v_scale, table: tensors, whose shapes give the sizes; k, v and
 q are tensors, too, whose strides give the distance of their rows).
@@ -37,7 +39,8 @@ __all__ = [
     "gemv_f32", "gemv_f16", "gemv_bf16", "gemv_w8", "gemv_w4", "gemv_bf16_splitk_noalloc", "gemv_ex",
     "gemv_swiglu", "gemv_host", "set_launch_overlap", "ACT_NONE", "ACT_SILU", "GemvError", "Plan", "plan_for",
     "status_string", "launch_count", "last_cuda_error", "force_kernel", "last_plan",
-    "gemv_f8", "gemv_f8_quantize", "gemv_kv8_append", "gemv_kv8_read", "gemv_kv8_attention", "gemv_qk_norm_rope",
+    "gemv_f8", "gemv_f8_quantize", "gemv_kv8_append", "gemv_kv8_read", "gemv_kv8_attention", "gemv_kv8_prefix_attention",
+    "gemv_qk_norm_rope",
     "rope_frequencies", "F8_GROUP", "KV8_BLOCK",
     "KERNELS", "DTYPE_CODES", "lib", "build", "LIB_PATH", "device_status", "test_stall",
 ]
@@ -126,6 +129,8 @@ def lib() -> ctypes.CDLL:
         L.gemv_rope_frequencies.restype = ci
         L.gemv_kv8_attention.argtypes = [ci, vp, vp, i64, vp, vp, vp, ci, ci, ci, ctypes.c_float, i64, i64, vp]
         L.gemv_kv8_attention.restype = ci
+        L.gemv_kv8_prefix_attention.argtypes = [ci, vp, vp, i64, vp, vp, vp, ci, vp, vp, ci, ci, ci, cf, vp]
+        L.gemv_kv8_prefix_attention.restype = ci
         L.gemv_set_launch_overlap.argtypes = [ci]
         L.gemv_set_launch_overlap.restype = ci
         L.gemv_status_string.argtypes = [ci]
@@ -552,3 +557,22 @@ def gemv_kv8_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, q, lens
                                      _addr(out, size, rows * row, "out"),
                                      _addr(lse, 4, rows * max(q_heads, 0), "lse"), S, T, q_heads, float(scale),
                                      int(window), int(sinks), _stream(stream)))
+
+
+def gemv_kv8_prefix_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, q, lens, firsts, prefix, out, lse, S, T,
+                              q_heads, scale, stream=None) -> None:
+    """gemv_kv8_attention (no window) for groups of sequences whose tables begin with the
+    same blocks, read once for all of a group's queries: group g has the sequences
+    firsts[g] .. firsts[g + 1] (int32, groups + 1 values; None: one group of all), which have
+    their first prefix[g] tokens (int32; one value for each group) in common.  lens counts
+    all tokens of a sequence, the prefix among them."""
+    S, T, q_heads = int(S), int(T), int(q_heads)
+    cache, _, dim = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
+    size, rows, row = _ESIZE[dtype][1], max(0, S * T), max(0, q_heads * dim)
+    groups = prefix.numel()
+    qa, qs = _rows(q, size, rows, row, "q")
+    _check(_fn("gemv_kv8_prefix_attention")(DTYPE_CODES[dtype], cache, qa, qs, _addr(lens, 4, max(S, 0), "lens"),
+                                            _addr(firsts, 4, groups + 1, "firsts"), _addr(prefix, 4, groups, "prefix"), groups,
+                                            _addr(out, size, rows * row, "out"),
+                                            _addr(lse, 4, rows * max(q_heads, 0), "lse"), S, T, q_heads, float(scale),
+                                            _stream(stream)))

@@ -25,9 +25,9 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE]
 SOURCES = ["gemv_api.cu", "gemv_plan.cpp", "gemv_f32.cu", "gemv_f16.cu", "gemv_bf16.cu", "gemv_w8.cu", "gemv_w4.cu",
-           "gemv_noalloc.cu", "gemv_f8.cu", "gemv_kv8.cu", "gemv_rope.cu"]
+           "gemv_noalloc.cu", "gemv_f8.cu", "gemv_kv8.cu", "gemv_rope.cu", "gemv_prefix.cu"]
 HEADERS = ["gemv_kernels.cuh", "gemv_launch.cuh", "gemv_plan.h", "gemv_tc.cuh", "gemv_internal.h", "gemv_f8.cuh",
-           "gemv_kv8.cuh"]
+           "gemv_kv8.cuh", "gemv_kv8_host.h", "gemv_prefix.cuh"]
 
 
 def nvcc() -> str:

@@ -43,6 +43,11 @@ struct KvArgs {
   int64_t timeout_ns = 0;
   int group = 0, window = 0, sinks = 0, row_tiles = 0, test_stall = 0;
   float scale_log2 = 0.f;  // softmax scale x log2 e
+  // attention of groups that share a prefix
+  const int32_t *firsts = nullptr, *prefix = nullptr;  // first sequence of each group (and S); its tokens in common
+  int groups = 0;
+  float *px_ws = nullptr;    // partial results of the shared blocks
+  int4 *px_parts = nullptr;  // of each item of theirs: the first CTA with a part, parts
 };
 
 // ------------------------------------------------------------------ values
@@ -383,11 +388,55 @@ __global__ void __launch_bounds__(kKvReadThreads) k_kv8_read(const KvArgs a) {
 struct KvSeen {
   int len, sink, from, count;
 };
+// A group of sequences: [first, end), and the blocks that they have in common.
+struct KvGroup {
+  int first, end, blocks;
+};
+__device__ __forceinline__ KvGroup kv_group(const KvArgs &a, int g) {
+  KvGroup k = {0, a.S, 0};
+  if (a.firsts != nullptr) {
+    k.first = __ldg(a.firsts + g);
+    k.end = __ldg(a.firsts + g + 1);
+    k.first = k.first < 0 ? 0 : k.first > a.S ? a.S : k.first;
+    k.end = k.end < k.first ? k.first : k.end > a.S ? a.S : k.end;
+  }
+  const int n = __ldg(a.prefix + g) / kKvBlock;
+  k.blocks = n < 0 || k.first == k.end ? 0 : n < a.width ? n : a.width;
+  return k;
+}
+// The group that sequence s is in, or -1.
+__device__ __forceinline__ int kv_group_of(const KvArgs &a, int s) {
+  if (a.firsts == nullptr) return 0;
+  int lo = 0, hi = a.groups;  // the last one that starts at s or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (__ldg(a.firsts + mid) <= s)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return s >= __ldg(a.firsts + lo) && s < __ldg(a.firsts + lo + 1) ? lo : -1;
+}
+// Blocks of sequence s that are attended to for its whole group at once: those in common,
+// if every query of it sees all of them, else none.
+__device__ __forceinline__ int kv_shared(const KvArgs &a, int s, int len) {
+  const int g = kv_group_of(a, s);
+  if (g < 0) return 0;
+  const int n = kv_group(a, g).blocks;
+  return len - a.T >= n * kKvBlock ? n : 0;
+}
+template <bool kOwn = false>
 __device__ __forceinline__ KvSeen kv_seen(const KvArgs &a, int s) {
   KvSeen v;
   v.len = __ldg(a.lens + s);
   v.len = v.len < 0 ? 0 : v.len;
   if ((int64_t)v.len > (int64_t)a.width * kKvBlock) v.len = a.width * kKvBlock;
+  if constexpr (kOwn) {
+    v.from = kv_shared(a, s, v.len);
+    v.sink = 0;
+    v.count = (v.len + kKvBlock - 1) / kKvBlock - v.from;
+    return v;
+  }
   const int64_t lo = a.window > 0 ? (int64_t)v.len - a.T - a.window + 1 : 0;
   v.from = lo > 0 ? (int)(lo / kKvBlock) : 0;
   const int need = a.window > 0 ? (a.sinks + kKvBlock - 1) / kKvBlock : 0;
@@ -406,10 +455,11 @@ constexpr int kKvItemCost = 1;
 __device__ __forceinline__ int kv_places(const KvSeen &v) { return v.count > 0 ? v.count + kKvItemCost : 0; }
 // Places of one item of each of the sequences [0, s).  (A sequence has at most 2^24
 // blocks: those of 32 fit 32 bits.)
+template <bool kOwn>
 __device__ __forceinline__ int64_t kv_before(const KvArgs &a, int s, int lane) {
   int64_t n = 0;
   for (int i = 0; i < s; i += 32)
-    n += __reduce_add_sync(0xffffffffu, i + lane < s ? (unsigned)kv_places(kv_seen(a, i + lane)) : 0u);
+    n += __reduce_add_sync(0xffffffffu, i + lane < s ? (unsigned)kv_places(kv_seen<kOwn>(a, i + lane)) : 0u);
   return n;
 }
 __device__ __forceinline__ int64_t kv_div(int64_t a, int64_t b) {
@@ -430,6 +480,7 @@ struct KvShares {
 };
 
 // An item, and the places [lo, hi) of its blocks.
+template <bool kOwn>
 struct KvItem {
   int64_t lo, hi;
   int s, item;
@@ -437,7 +488,7 @@ struct KvItem {
   __device__ void load(const KvArgs &a, int s_, int64_t at) {
     s = s_;
     item = 0;
-    seen = kv_seen(a, s);
+    seen = kv_seen<kOwn>(a, s);
     lo = at + (seen.count > 0 ? kKvItemCost : 0);
     hi = lo + seen.count;
   }
@@ -479,7 +530,7 @@ __device__ __forceinline__ uint64_t kv_low_bits(int64_t n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 // Four 16-bit values from anywhere (a call: such rows are rare, and their loads many).
-__device__ __noinline__ uint2 kv_load4(const unsigned short *p) {
+static __device__ __noinline__ uint2 kv_load4(const unsigned short *p) {
   const uint32_t a = __ldg(p), b = __ldg(p + 1), c = __ldg(p + 2), d = __ldg(p + 3);
   return make_uint2(a | (b << 16), c | (d << 16));
 }
@@ -570,8 +621,12 @@ __device__ __forceinline__ int64_t kv_out_row(const KvArgs &a, int s, int h, int
 // enough for that, and takes eight rows where tcgen05 would take 128.  More rows a block
 // (16 with 128 channels: 38 us where the bytes take 18) are bound by the latency of eight
 // warps' dependent instructions; their registers allow no more.
-template <int D, int NT, bool kWhole>
+// kOwn: only the blocks that a sequence does not share with its group (gemv_kv8_prefix_attention);
+// every result is a part then, in the place of its warp's number plus its item's, both of which
+// only rise along the work list.
+template <int D, int NT, bool kWhole, bool kOwn = false>
 __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(const KvArgs a) {
+  static_assert(!(kWhole && kOwn));
   using F = KvForm<D, NT>;
   constexpr int W = F::kWarps, R = F::kSlots, Q = D / 64, DT = D / 16;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -594,7 +649,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
   const int items = a.heads * a.row_tiles;
   const int64_t worker = (int64_t)warp * gridDim.x + blockIdx.x, workers = (int64_t)gridDim.x * W;  // (few blocks: one for each SM)
   KvShares shares;
-  KvItem at;
+  KvItem<kOwn> at;
   int64_t u_lo, u_hi;
   int slot = 0, issued = 0, taken = 0;  // the ring: slot in use, pieces begun, pieces used
   uint32_t phase = 0;
@@ -617,7 +672,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
         continue;
       }
     } else {
-      shares.cut(kv_before(a, a.S, lane) * items, workers);
+      shares.cut(kv_before<kOwn>(a, a.S, lane) * items, workers);
       u_lo = shares.first(worker);
       u_hi = shares.first(worker + 1);
       if (u_lo >= u_hi) break;
@@ -626,7 +681,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
       int64_t base = 0;
       for (int s0 = 0;; s0 += 32) {  // 32 sequences at a time
         const int s = s0 + lane;
-        unsigned n = s < a.S ? (unsigned)kv_places(kv_seen(a, s)) : 0u;
+        unsigned n = s < a.S ? (unsigned)kv_places(kv_seen<kOwn>(a, s)) : 0u;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const unsigned o = __shfl_up_sync(0xffffffffu, n, d);
@@ -649,7 +704,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
     const bool q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
     constexpr bool kEarly = NT * DT <= 16;  // (more would not stay in registers)
     uint32_t raw[NT][DT][2];
-    auto load_q = [&](const KvItem &it) {
+    auto load_q = [&](const KvItem<kOwn> &it) {
       const int h = it.item / a.row_tiles, row0 = (it.item - h * a.row_tiles) * NT * 8;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -681,7 +736,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
     };
 
     // ---- copies: the pieces of this warp's blocks
-    KvItem is = at;                          // the item of place `iu`
+    KvItem<kOwn> is = at;                          // the item of place `iu`
     int64_t iu = u_lo > at.lo ? u_lo : at.lo;
     int batch = -1;                          // first of the item's blocks whose table entries the lanes hold
     int32_t entries = 0;
@@ -1039,11 +1094,12 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
       if (dead) break;
 
       // ---- the item's output, or this range's part of it
-      const bool whole = kWhole || (seg == at.lo && seg_end == at.hi);
+      const bool whole = !kOwn && (kWhole || (seg == at.lo && seg_end == at.hi));
       if (!kWhole && seg == at.lo && lane == 0)  // the item's first blocks: where its parts are
         a.parts[(int64_t)at.s * items + at.item] =
             make_int4((int)worker, (int)(shares.owner(at.hi - 1) - worker) + 1, first_item ? 0 : 1, 0);
-      float *part = a.ws + (worker * 2 + (first_item ? 0 : 1)) * kv_part<D, NT>();
+      const int64_t place = kOwn ? worker + (int64_t)at.s * items + at.item : worker * 2 + (first_item ? 0 : 1);
+      float *part = a.ws + place * kv_part<D, NT>();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll

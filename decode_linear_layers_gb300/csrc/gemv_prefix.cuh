@@ -1,0 +1,701 @@
+// Kernels of the attention of sequences that share a prefix (gemv_kv8_prefix_attention):
+// the shared blocks against the queries of all sequences of a group, on the tensor cores,
+// and the join with the parts of each sequence's own blocks (k_kv8_attention<.., kOwn>).
+//
+// A group's queries of one of the cache's heads are the rows of a matrix, row
+// (s T + t) group + i for query head i of that head's group.  For a block of 64 tokens
+//     S = Q K^T          128 rows x 64 tokens, tcgen05 kind::f16
+//     P = 2^(S f - ..)   fp32, rounded to fp16
+//     O += P V           128 rows x D channels, in tensor memory over all blocks
+// The cached values become fp16 (exact) in shared memory once for all rows of the CTA; Q, S,
+// P and O stay in tensor memory, so that shared memory only feeds K and V.
+#pragma once
+
+#include "gemv_kv8.cuh"
+
+namespace gemv {
+
+template <int D>
+struct PxForm {
+  // Two sets of S and O where tensor memory holds them: an item has up to 256 rows, a tile of
+  // 128 for each set; an item of up to 128 rows gives both sets its rows, and the blocks to
+  // them by turns.  One set (192 and 256 channels) has two buffers for S.
+  static constexpr int kSets = D <= 128 ? 2 : 1;
+  static constexpr int kRows = 128 * kSets;
+  static constexpr int kSoft = 4 * kSets, kConv = 4;             // warps
+  static constexpr int kWarps = kSoft + kConv + 2, kThreads = kWarps * 32;
+  static constexpr int kRaw = kKvBlock * D, kStage = 2 * kRaw;   // bytes of keys or values: as cached, as fp16
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // of keys, and of values
+  static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 12 : D == 192 ? 8 : 5;
+  static constexpr int kSmem = 1024 + 2 * kStages * kStage + kSlots * kRaw;
+  // tensor memory columns: O of each set, two of S, Q of each set
+  static constexpr int kS = kSets * D, kQ = kS + 128;
+  static_assert(kQ + kSets * D / 2 <= 512);
+  // one CTA an SM (each takes all of the tensor memory)
+  static_assert(kSmem > 114 * 1024 && kSmem <= 226 * 1024);
+  // floats of a partial result's set: O as [D / 4][128 rows][4], largest logits, sums
+  static constexpr int64_t kPart = 128 * (D + 2);
+};
+// Blocks whose scales are kept.  While the softmax is at block j, the converters are at
+// j + kStages + 1 at most, and the copies kSlots / 2 + 1 further on.
+constexpr int kPxMeta = 16;
+constexpr int kPxCost1 = 2, kPxCost2 = 3;  // places of a block: of an item of up to 128 rows, of more
+constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
+// The weights leave with a factor of 2^11 and may outgrow their reference by 2^4 before O is
+// scaled anew: fp16 holds them up to 2^15, and in full down to 2^-25 of the reference.
+constexpr float kPxLift = 11.f, kPxSlack = 4.f;
+
+// A group's part of the work list: its tiles of kRows rows, of each the heads, of each the
+// shared blocks.
+struct PxGroup {
+  int first, blocks, rows, tiles;
+  int full, last;  // places of a block in a whole tile, in the last one
+  int64_t places;
+};
+template <int D>
+__device__ __forceinline__ PxGroup px_group(const KvArgs &a, int g) {
+  PxGroup p;
+  const KvGroup k = kv_group(a, g);
+  p.first = k.first;
+  p.blocks = k.blocks;
+  p.rows = (k.end - k.first) * a.T * a.group;
+  constexpr int R = PxForm<D>::kRows;
+  p.tiles = (p.rows + R - 1) / R;
+  const int rest = p.rows - (p.tiles - 1) * R;
+  p.full = R > 128 ? kPxCost2 : kPxCost1;
+  p.last = rest > 128 ? kPxCost2 : kPxCost1;
+  p.places = p.tiles == 0 ? 0 : (int64_t)a.heads * p.blocks * ((int64_t)(p.tiles - 1) * p.full + p.last);
+  return p;
+}
+// Number of a group's first tile, rising with the groups, none twice (a group has at most
+// one more than the rows before its end, by the tile, take it further on).
+template <int D>
+__device__ __forceinline__ int px_tile0(const KvArgs &a, int g, int first) {
+  return (int)((int64_t)first * a.T * a.group / PxForm<D>::kRows) + g;
+}
+
+struct PxSeg {
+  int g, tile, h;   // group, tile of its rows, head
+  int b0, b1;       // its blocks
+  int rows;         // of the tile
+  int first;        // the group's first sequence
+  int item;         // (tile's number) x heads + head
+  bool whole_start; // b0 is the item's first block
+  int64_t last;     // place of the item's last block
+};
+// The CTA's share of the work list: places [lo, hi), of all groups' `total`.  Blocks whose
+// first place is in there are its own.
+template <int D>
+struct PxWalk {
+  KvShares shares;
+  int64_t at, hi, base;  // next place, end, place of the group's first
+  int g;
+  PxGroup p;
+  __device__ void begin(const KvArgs &a, int lane) {  // one warp, converged
+    int64_t total = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 32) {
+      int64_t n = g0 + lane < a.groups ? px_group<D>(a, g0 + lane).places : 0;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+      total += n;
+    }
+    int64_t W = total / (kPxLeast * kPxCost2);
+    W = W < 1 ? 1 : W < gridDim.x ? W : gridDim.x;
+    shares.cut(total, W);
+    at = blockIdx.x < W ? shares.first(blockIdx.x) : total;
+    hi = blockIdx.x < W ? shares.first(blockIdx.x + 1) : total;
+    g = 0;
+    base = 0;
+    if (at >= hi) return;
+    p = px_group<D>(a, 0);
+    while (at >= base + p.places) {
+      base += p.places;
+      p = px_group<D>(a, ++g);
+    }
+  }
+  __device__ bool next(const KvArgs &a, PxSeg &s) {
+    while (at < hi) {
+      if (at >= base + p.places) {
+        base += p.places;
+        p = px_group<D>(a, ++g);
+        continue;
+      }
+      int64_t r = at - base;
+      const int64_t tile = (int64_t)a.heads * p.blocks * p.full;
+      s.tile = (int)kv_div(r, tile);
+      if (s.tile > p.tiles - 1) s.tile = p.tiles - 1;
+      const int cost = s.tile == p.tiles - 1 ? p.last : p.full;
+      const int64_t item = (int64_t)p.blocks * cost;
+      r -= s.tile * tile;
+      s.h = (int)kv_div(r, item);
+      r -= s.h * item;
+      const int64_t item0 = at - r, left = hi - item0;
+      s.g = g;
+      s.first = p.first;
+      s.rows = s.tile == p.tiles - 1 ? p.rows - s.tile * PxForm<D>::kRows : PxForm<D>::kRows;
+      s.item = (px_tile0<D>(a, g, p.first) + s.tile) * a.heads + s.h;
+      s.b0 = (int)((r + cost - 1) / cost);
+      s.b1 = left >= item ? p.blocks : (int)((left + cost - 1) / cost);
+      s.whole_start = s.b0 == 0;
+      s.last = item0 + (int64_t)(p.blocks - 1) * cost;
+      at = item0 + item < hi ? item0 + item : hi;
+      if (s.b0 < s.b1) return true;
+    }
+    return false;
+  }
+};
+
+// ------------------------------------------------------------------ instructions
+// D (tensor memory, fp32) (+)= A (tensor memory, fp16, two columns of k to a word) B
+__device__ __forceinline__ void px_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 words of this thread's tensor-memory lane; stored after px_st_wait.
+__device__ __forceinline__ void px_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void px_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void px_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void px_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// (x, y) = (x, y) f + c;  (x, y) *= f;  (x, y) += (u, v)
+__device__ __forceinline__ void px_fma2(float &x, float &y, float f, float c) {
+  asm("{\n\t.reg .b64 a, f, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+      "fma.rn.f32x2 a, a, f, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(f), "f"(c));
+}
+__device__ __forceinline__ void px_mul2(float &x, float &y, float f) {
+  asm("{\n\t.reg .b64 a, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmul.rn.f32x2 a, a, f;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(f));
+}
+__device__ __forceinline__ void px_add2(float &x, float &y, float u, float v) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
+
+// ------------------------------------------------------------------ the shared blocks
+// One CTA per SM over its share of the work list.  Warps, each walking the same segments:
+//   copies       a block's keys, then its values, by the bulk copy engine into a ring of raw
+//                slots, its scales beside them
+//   converters   raw e4m3 to fp16, in the 128-byte swizzle that the MMA reads: keys as 64 rows of
+//                tokens, values as D rows of channels, both along the product's k
+//   MMAs         steps in order: S of step 0, S of step 1, then for each step i its P V and S of step
+//                i + 2, which has the same S columns; one commit for both (a commit costs the
+//                issuing warp some 200 cycles).  Step i uses set i % 2 and block i / 2 (more than 128
+//                rows: both sets meet every block), or block i
+//   softmax      four warps a set, a row to a thread: Q to tensor memory at an item's start, S to P
+//                for each step, O out at its end
+// O is scaled anew only where a row's largest weight (times its block's values' scale, which
+// goes into P) outgrows the reference by 2^4: as a rule in the first blocks only.  Weights and
+// their sums refer to the running maximum of the logits alone: a block of tiny values still counts
+// in full in the sum.
+template <int D>
+__global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvArgs a) {
+  using F = PxForm<D>;
+  constexpr int R = F::kSlots, NS = F::kStages;
+  static_assert(NS + R / 2 + 2 < kPxMeta);
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t rawf[R], rawe[R], kf[NS], ke[NS], vf[NS], ve[NS], qf[F::kSets], sf[2], pf[2], fin;
+  __shared__ float meta[kPxMeta][2];  // of a block: the keys' and the values' scale
+  __shared__ int meta_bad[kPxMeta];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  pdl_wait();
+  pdl_trigger();  // after the wait: the next kernels read the batch's lengths before theirs
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char *kst = smem, *vst = smem + NS * F::kStage, *raw = vst + NS * F::kStage;
+  constexpr int kLoad = F::kSoft + F::kConv, kMma = kLoad + 1;
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      tc_mbar_init(&rawf[i], 2);  // the piece, and with keys the block's scales
+      tc_mbar_init(&rawe[i], F::kConv);
+    }
+    for (int i = 0; i < NS; ++i) {
+      tc_mbar_init(&kf[i], F::kConv);
+      tc_mbar_init(&vf[i], F::kConv);
+      tc_mbar_init(&ke[i], F::kSets);
+      tc_mbar_init(&ve[i], F::kSets);
+    }
+    for (int i = 0; i < F::kSets; ++i) tc_mbar_init(&qf[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      tc_mbar_init(&sf[i], 1);
+      tc_mbar_init(&pf[i], 4);
+    }
+    tc_mbar_init(&fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    abort_flag = 0;
+  }
+  px_fence_before();
+  __syncwarp();
+  __syncthreads();
+  px_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort = &abort_flag;
+  auto wait = [&](uint64_t *b, int n, int of) {  // phase n of a ring of `of`
+    return __all_sync(0xffffffffu, f8_wait(b, (uint32_t)(n / of) & 1u, a.timeout_ns, abort)) != 0;
+  };
+
+  PxWalk<D> walk;
+  PxSeg s;
+  walk.begin(a, lane);
+  bool ok = true;
+  int c0 = 0;     // blocks of the segments before
+  int piece = 0;  // of the ring of raw slots
+  if (warp == kLoad) {  // ---- copies
+    while (ok && walk.next(a, s)) {
+      int32_t entries = 0;
+      for (int b = s.b0; ok && b < s.b1; ++b) {
+        const int i = (b - s.b0) & 31;
+        if (i == 0) entries = b + lane < s.b1 ? __ldg(a.table + (int64_t)s.first * a.width + b + lane) : -1;
+        const int32_t entry = __shfl_sync(0xffffffffu, entries, i);
+        const bool good = entry >= 0 && entry < a.blocks;
+        const int64_t unit = (good ? (int64_t)entry : 0) * a.heads + s.h;  // (of an entry that is no block: any, unseen)
+        const int n = (c0 + b - s.b0) % kPxMeta;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const int to = piece % R;
+          ok = piece < R || wait(&rawe[to], piece - R, R);
+          if (!ok) break;
+          if (f8_elect()) {
+            if (side == 0) {
+              meta_bad[n] = !good;
+              if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+              f8_copy4(&meta[n][0], a.k_scale + unit, true);
+              f8_copy4(&meta[n][1], a.v_scale + unit, true);
+              f8_copy4_arrive(&rawf[to]);
+            } else {
+              tc_mbar_arrive(&rawf[to]);
+            }
+            if (!a.test_stall || side == 0) {  // test: no values ever come
+              tc_mbar_arrive_expect_tx(&rawf[to], F::kRaw);
+              kv_bulk(raw + (size_t)to * F::kRaw, (side == 0 ? a.k : a.v) + unit * F::kRaw, F::kRaw, &rawf[to]);
+            }
+          }
+          __syncwarp();
+          ++piece;
+        }
+      }
+      c0 += s.b1 - s.b0;
+    }
+    f8_copy4_drain();
+  } else if (warp == kMma) {  // ---- products
+    const uint32_t is = tc_idesc(false, kKvBlock), io = tc_idesc(false, D);
+    const uint64_t dk = tc_smem_desc(tc_smem_u32(kst)), dv = tc_smem_desc(tc_smem_u32(vst));
+    uint32_t qbits = 0, pbits = 0;  // phases of qf and pf
+    while (ok && walk.next(a, s)) {
+      const bool both = F::kSets > 1 && s.rows > 128;
+      const int n = (s.b1 - s.b0) * (both ? 2 : 1);
+      auto block = [&](int i) { return c0 + (both ? i >> 1 : i); };
+      auto scores = [&](int i) {  // S of step i, once its keys are there
+        ok = ok && wait(&kf[block(i) % NS], block(i), NS);
+        if (!ok) return;
+        px_fence_after();
+        const int x = i & 1;
+        const uint32_t q = tmem + F::kQ + (F::kSets > 1 ? x * (D / 2) : 0), d = tmem + F::kS + x * 64;
+        const uint64_t at = dk + (uint64_t)(block(i) % NS * (F::kStage >> 4));
+        if (f8_elect()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) px_mma(d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is, k > 0);
+        }
+        __syncwarp();
+      };
+      for (int x = 0; x < F::kSets && x < n; ++x) {
+        ok = ok && wait(&qf[x], (qbits >> x) & 1, 1);
+        qbits ^= 1u << x;
+      }
+      for (int i = 0; i < 2 && i < n && ok; ++i) {
+        scores(i);
+        if (ok && f8_elect()) tc_commit(&sf[i]);
+        __syncwarp();
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int x = i & 1, st = block(i) % NS;
+        ok = wait(&vf[st], block(i), NS) && wait(&pf[x], (pbits >> x) & 1, 1);
+        if (!ok) break;
+        pbits ^= 1u << x;
+        px_fence_after();
+        const uint32_t d = tmem + (F::kSets > 1 ? x * D : 0), w = tmem + F::kS + x * 64;
+        const uint64_t at = dv + (uint64_t)(st * (F::kStage >> 4));
+        if (f8_elect()) {
+#pragma unroll
+          for (int k = 0; k < kKvBlock / 16; ++k) px_mma(d, w + k * 8, at + k * 2, io, k > 0 || i >= F::kSets);
+        }
+        __syncwarp();
+        if (i + 2 < n) scores(i + 2);
+        if (ok && f8_elect()) tc_commit(&sf[x]);
+        __syncwarp();
+      }
+      c0 += s.b1 - s.b0;
+    }
+  } else if (warp >= F::kSoft) {  // ---- e4m3 to fp16
+    const int ct = tid - F::kSoft * 32;
+    auto widen = [&](const uint4 &x, unsigned char *row, int chunk, int turn, bool swap) {
+      const uint4 lo = make_uint4(kv_half2_lo(x.x), kv_half2_hi(x.x), kv_half2_lo(x.y), kv_half2_hi(x.y));
+      const uint4 hi = make_uint4(kv_half2_lo(x.z), kv_half2_hi(x.z), kv_half2_lo(x.w), kv_half2_hi(x.w));
+      // (which half goes first: neighbouring threads' stores spread over the banks)
+      *reinterpret_cast<uint4 *>(row + (((chunk + (swap ? 1 : 0)) ^ turn) * 16)) = swap ? hi : lo;
+      *reinterpret_cast<uint4 *>(row + (((chunk + (swap ? 0 : 1)) ^ turn) * 16)) = swap ? lo : hi;
+    };
+    auto hand_on = [&](uint64_t *full) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        tc_mbar_arrive(full);
+        tc_mbar_arrive(&rawe[piece % R]);
+      }
+      ++piece;
+    };
+    constexpr int kPer = kKvBlock * D / 16 / (F::kConv * 32);  // 16-byte pieces of a thread
+    while (ok && walk.next(a, s)) {
+      for (int b = s.b0; b < s.b1; ++b, ++c0) {
+        const int st = c0 % NS;
+        ok = wait(&rawf[piece % R], piece, R) && (c0 < NS || wait(&ke[st], c0 - NS, NS));
+        if (!ok) break;
+        const bool bad = meta_bad[c0 % kPxMeta] != 0;
+        uint4 x[kPer];
+        const uint4 *from = reinterpret_cast<const uint4 *>(raw + (size_t)(piece % R) * F::kRaw) + ct;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = from[i * F::kConv * 32];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int p = i * F::kConv * 32 + ct, tok = p / (D / 16), cp = p - tok * (D / 16);
+          widen(x[i], kst + st * F::kStage + (cp >> 2) * (kKvBlock * 128) + tok * 128, (cp & 3) * 2, tok & 7, (cp >> 2) & 1);
+        }
+        hand_on(&kf[st]);
+        ok = wait(&rawf[piece % R], piece, R) && (c0 < NS || wait(&ve[st], c0 - NS, NS));
+        if (!ok) break;
+        from = reinterpret_cast<const uint4 *>(raw + (size_t)(piece % R) * F::kRaw) + ct;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = bad ? make_uint4(0, 0, 0, 0) : from[i * F::kConv * 32];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int p = i * F::kConv * 32 + ct, d = p >> 2;
+          widen(x[i], vst + st * F::kStage + d * 128, (p & 3) * 2, d & 7, false);
+        }
+        hand_on(&vf[st]);
+      }
+    }
+  } else {  // ---- softmax
+    const int x = warp >> 2, in_tile = (warp & 3) * 32 + lane;  // set, row of its tile: tensor-memory lane
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = mine + x * D, tq = mine + F::kQ + x * (D / 2);
+    const bool signals = (warp & 3) == 0 && lane == 0;
+    uint32_t sbits = 0;  // phases of sf
+    while (ok && walk.next(a, s)) {
+      const bool both = F::kSets > 1 && s.rows > 128;
+      const int nb = s.b1 - s.b0, n = nb * (both ? 2 : 1);
+      auto block = [&](int i) { return c0 + (both ? i >> 1 : i); };
+      const int row0 = (both ? x * 128 : 0) + (warp & 3) * 32;
+      const bool alive = row0 + lane < s.rows, any = row0 < s.rows;  // the row's, the warp's
+      float *part = a.px_ws + ((int64_t)blockIdx.x + s.item) * (F::kSets * F::kPart) + x * F::kPart;
+      if (s.whole_start && tid == 0)  // the item's first blocks: where its parts are
+        a.px_parts[s.item] = make_int4((int)blockIdx.x, (int)(walk.shares.owner(s.last) - blockIdx.x) + 1, 0, 0);
+      if (F::kSets > 1 && x >= n) {  // a single block, the other set's
+        part[128 * D + in_tile] = -INFINITY;
+        part[128 * (D + 1) + in_tile] = 0.f;
+        c0 += nb;
+        continue;
+      }
+      // Q: each row scaled by a power of two so that its largest value lies in [2^14, 2^15), as fp16;
+      // the softmax's factor is what is left, its sign goes with Q
+      float f = 0.f;
+      if (any) {
+        const int row = s.tile * F::kRows + row0 + lane, of = a.T * a.group;
+        const int sq = s.first + row / of, rt = row % of, t = rt / a.group;
+        const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)sq * a.T + t) * a.q_stride +
+                                   ((int64_t)s.h * a.group + rt - t * a.group) * D;
+        const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
+        auto fetch = [&](int c) {  // channels c .. c + 7
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (alive) {
+            if (vec) {
+              v = __ldg(reinterpret_cast<const uint4 *>(qp + c));
+            } else {
+              const uint2 lo = kv_load4(qp + c), hi = kv_load4(qp + c + 4);
+              v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+          }
+          return v;
+        };
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 8) {
+          const uint4 v = fetch(c);
+          top = kv_max2(kv_max2(top, v.x & 0x7fff7fffu, a.dtype), v.y & 0x7fff7fffu, a.dtype);
+          top = kv_max2(kv_max2(top, v.z & 0x7fff7fffu, a.dtype), v.w & 0x7fff7fffu, a.dtype);
+        }
+        const float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
+        int e = (__float_as_int(mx) >> 23) & 0xff;  // (an infinity takes the largest exponent)
+        e = e < 16 ? 16 : e;
+        float up = __int_as_float((127 + 14 + 127 - e) << 23);
+        f = fabsf(a.scale_log2) / up;
+        if (a.scale_log2 < 0.f) up = -up;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 v = fetch(c + 8 * j);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[4 * j + k] = kv_pack_half(kv_wide_lo(u[k], a.dtype) * up, kv_wide_hi(u[k], a.dtype) * up);
+          }
+          px_st32(tq + c / 2, w);
+        }
+        px_st_wait();
+      }
+      px_fence_before();
+      __syncwarp();
+      if (lane == 0) tc_mbar_arrive(&qf[x]);
+
+      float m = -INFINITY, l = 0.f, ref = -INFINITY;  // largest logit, sum of weights, O's reference
+      auto release = [&](uint64_t *ring, int i) {     // step i is done with its stage
+        uint64_t *b = &ring[block(i) % NS];
+        tc_mbar_arrive(b);
+        if (F::kSets > 1 && !both) tc_mbar_arrive(b);  // (no other set waits for it)
+      };
+#pragma unroll 1
+      for (int i = F::kSets > 1 ? x : 0; i < n; i += F::kSets) {
+        const int buf = i & 1, st = block(i) % NS, slot = block(i) % kPxMeta;
+        // (the keys came before S did: no wait, but the scales are this warp's to read then)
+        ok = wait(&sf[buf], (sbits >> buf) & 1, 1) && wait(&kf[st], block(i), NS);
+        if (!ok) break;
+        sbits ^= 1u << buf;
+        px_fence_after();
+        const float ks = meta[slot][0], vs = meta[slot][1];
+        const bool bad = meta_bad[slot] != 0;
+        __syncwarp();
+        if (signals) {
+          release(ke, i);
+          if (i >= 2) release(ve, i - 2);
+        }
+        if (any) {
+          const uint32_t ts = mine + F::kS + buf * 64;
+          uint32_t p[32];
+          if (!bad) {
+            uint32_t r[2][32];
+            f8_ld<32>(ts, r[0]);
+            f8_ld<32>(ts + 32, r[1]);
+            f8_ld_wait<32>(r[0]);
+            f8_ld_wait<32>(r[1]);
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              mx = fmaxf(mx, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[0][j + 1])));
+              my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
+            }
+            const float ff = f * ks, bm = fmaxf(mx, my) * ff, lv = log2f(vs), cand = bm + lv;
+            if (bm > m) {
+              l *= kv_exp2(m - bm);
+              m = bm;
+            }
+            if (i < F::kSets) {
+              ref = cand;
+            } else {
+              const bool grow = cand > ref + kPxSlack;
+              if (__any_sync(0xffffffffu, grow)) {
+                // (the other buffer's product before this one has to be done, too)
+                if (F::kSets == 1) ok = wait(&sf[buf ^ 1], (sbits >> (buf ^ 1)) & 1, 1);
+                if (!ok) break;
+                px_fence_after();
+                const float by = grow ? kv_exp2(ref - cand) : 1.f;
+                if (grow) ref = cand;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  f8_ld<32>(to + c, o);
+                  f8_ld_wait<32>(o);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+                  px_st32(to + c, o);
+                }
+                px_st_wait();
+              }
+            }
+            const float z = m == -INFINITY ? 0.f : m;
+            const float g = kv_exp2(fminf(z + lv - (ref == -INFINITY ? 0.f : ref) + kPxLift, 127.f));
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+              px_fma2(u, v, ff, -z);
+              u = kv_exp2(u);
+              v = kv_exp2(v);
+              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
+              px_mul2(u, v, g);
+              p[j] = kv_pack_half(u, v);
+            }
+            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) p[j] = 0;
+          }
+          px_st32(ts, p);
+          px_st_wait();
+        }
+        px_fence_before();
+        __syncwarp();
+        if (lane == 0) tc_mbar_arrive(&pf[buf]);
+      }
+      if (!ok) break;
+      const int end = F::kSets > 1 ? n - 1 - ((n - 1 - x) & 1) : n - 1;  // this set's last step
+      ok = wait(&sf[end & 1], (sbits >> (end & 1)) & 1, 1);
+      if (!ok) break;
+      sbits ^= F::kSets == 1 && n > 1 ? 3u : 1u << (end & 1);
+      px_fence_after();
+      if (signals) {
+        if (F::kSets == 1 && n > 1) release(ve, end - 1);
+        release(ve, end);
+      }
+      if (any) {
+        const float by = kv_exp2(ref - kPxLift - m);  // O in units of the largest weight
+        float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          f8_ld<32>(to + c, o);
+          f8_ld_wait<32>(o);
+          if (alive) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              out[(c + j) / 4 * 128] = make_float4(__uint_as_float(o[j]) * by, __uint_as_float(o[j + 1]) * by,
+                                                   __uint_as_float(o[j + 2]) * by, __uint_as_float(o[j + 3]) * by);
+          }
+        }
+        if (alive) {
+          part[128 * D + in_tile] = m;
+          part[128 * (D + 1) + in_tile] = l * kKvLifted;
+        }
+      }
+      c0 += nb;
+    }
+  }
+  px_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (abort_flag != 0) {
+    // after an abort nothing may be in flight when the CTA frees its tensor memory and exits
+    if (warp == kMma) {
+      if (f8_elect()) tc_commit(&fin);
+      __syncwarp();
+      const bool drained = tc_mbar_wait(&fin, 0, a.timeout_ns);
+      if (lane == 0 && a.status != nullptr) atomicOr(a.status, drained ? kTcStatusMma : kTcStatusMma | kTcStatusDrain);
+    }
+    if (warp == kLoad) {
+      bool drained = true;
+      for (int i = piece > R ? piece - R : 0; i < piece; ++i)
+        if (!tc_mbar_wait(&rawf[i % R], (uint32_t)(i / R) & 1u, a.timeout_ns)) drained = false;
+      if (!drained && lane == 0 && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  if (warp == kMma) {
+    px_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ join
+// A sequence's rows of a head: the parts of its own blocks and of its group's shared ones,
+// in that order; zeros where there are none.  A thread adds up four channels of a row, kGroups
+// threads share the parts of the same channels.  grid (S, items, pieces of a tile's rows)
+template <int D, int NT, int kGroups>
+__global__ void __launch_bounds__(kKvJoinThreads, 3) k_kv8_prefix_join(const KvArgs a, int ctas) {
+  constexpr int kAlong = kKvJoinThreads / kGroups;
+  using F = PxForm<D>;
+  __shared__ KvSum sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kAlong : 1];
+  pdl_trigger();
+  pdl_wait();
+  const int s = blockIdx.x, item = blockIdx.y, items = a.heads * a.row_tiles;
+  const KvSeen seen = kv_seen<true>(a, s);
+  const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
+  const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
+  const int64_t own_item = (int64_t)s * items + item;
+  // (a kernel whose wait ran out leaves its entries as the scratch memory had them: what is
+  // read stays within the partial results)
+  int4 of = seen.count > 0 ? __ldcg(&a.parts[own_item]) : make_int4(0, 0, 0, 0);
+  if (of.x < 0 || of.y < 0 || (int64_t)of.x + of.y > a.workers) of.y = 0;
+  const float *const own = a.ws + ((int64_t)of.x + own_item) * kv_part<D, NT>();
+  const int along = threadIdx.x % kAlong, grp = threadIdx.x / kAlong;
+  const int idx = blockIdx.z * kAlong + along, quad = idx / rows, r = idx - quad * rows;
+  const bool on = quad < D / 4;
+  // the row's place among those of its group
+  const float *px = nullptr;
+  int n_px = 0, sets = 1, rr = 0;
+  if (seen.from > 0 && on) {
+    const int g = kv_group_of(a, s);
+    const KvGroup k = kv_group(a, g);
+    const int of_seq = a.T * a.group, row = (s - k.first) * of_seq + row0 + r, tile = row / F::kRows;
+    const bool both = F::kSets > 1 && (k.end - k.first) * of_seq - tile * F::kRows > 128;
+    const int px_item = (px_tile0<D>(a, g, k.first) + tile) * a.heads + h, in_tile = row - tile * F::kRows;
+    const int4 w = __ldcg(&a.px_parts[px_item]);
+    if (w.x >= 0 && w.y >= 0 && w.x + w.y <= ctas) {
+      sets = F::kSets > 1 && !both ? 2 : 1;
+      n_px = w.y * sets;
+      rr = in_tile % 128;
+      px = a.px_ws + ((int64_t)w.x + px_item) * (F::kSets * F::kPart) + (both ? in_tile / 128 * F::kPart : 0);
+    }
+  }
+  // two sets of a CTA's part lie one behind the other, with one set it is the next CTA's
+  const int64_t step = sets == 2 ? F::kPart : F::kSets * F::kPart;
+  KvSum sum;
+  if (on) {
+    const int total = of.y + n_px;
+    for (int i0 = grp; i0 < total; i0 += 8 * kGroups) {
+      float m[8], den[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kGroups;
+        if (i < total) {
+          const bool mine = i < of.y;
+          const float *q = mine ? own + (int64_t)i * kv_part<D, NT>() : px + (i - of.y) * step;
+          m[k] = __ldcg(q + (mine ? NT * 8 * D + r : 128 * D + rr));
+          den[k] = __ldcg(q + (mine ? NT * 8 * (D + 1) + r : 128 * (D + 1) + rr));
+          v[k] = __ldcg(reinterpret_cast<const float4 *>(q + (mine ? r * D + quad * 4 : (quad * 128 + rr) * 4)));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        // (a set that had no block has no sums, either)
+        if (i0 + k * kGroups < total && !(m[k] == -INFINITY && den[k] == 0.f)) sum.add(m[k], den[k], v[k]);
+    }
+  }
+  if constexpr (kGroups > 1) {
+    sums[grp][along] = sum;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) sum.add(sums[k][along].m, sums[k][along].den, sums[k][along].v);
+  }
+  if (!on) return;
+  const int64_t at_row = kv_out_row(a, s, h, row0 + r);
+  const float inv = sum.den == 0.f ? 0.f : kKvLifted * (1.f / sum.den);
+  unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + quad * 4;
+  const float v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
+  if (quad == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(sum.m, sum.den);
+}
+
+}  // namespace gemv

@@ -402,6 +402,30 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
                                  const int32_t *lens, void *out, float *lse, int S, int T, int q_heads, float scale,
                                  int64_t window, int64_t sinks, gemv_stream_t stream);
 
+/* Attention as gemv_kv8_attention has it (no window) for a batch whose sequences share
+ * prefixes: the tables of a group's sequences begin with the same blocks, which are read
+ * once and meet the queries of the whole group on the tensor cores.
+ *   groups   number of groups, up to S: group g has the sequences firsts[g] .. firsts[g + 1] - 1
+ *            (groups + 1 values, rising; those in no group share nothing); firsts == NULL:
+ *            one group has them all
+ *   prefix   groups values: tokens that the group's sequences have in common.  The whole
+ *            blocks of GEMV_KV8_BLOCK among them are taken from the table of the group's first
+ *            sequence, once for the group; what is left of them, from each sequence's own
+ * lens[s] counts all tokens of sequence s, the prefix among them: out and lse are those of
+ * gemv_kv8_attention with the same arguments (up to rounding), and gemv_kv8_append writes
+ * the new tokens as ever.  A sequence some of whose queries do not see all of the shared blocks
+ * (lens[s] - T below them; an idle place of the batch with lens[s] == 0) is attended to by
+ * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, and
+ * GEMV_ERR_UNSUPPORTED for S x T x q_heads / heads above 2^30.  The shared values' sums, over
+ * a share of the blocks each, are in units of the row's largest weight x value scale; the weights
+ * are rounded to 11 bits as there, those below 2^-25 of that largest to fewer.  A scratch buffer
+ * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and
+ * 4 (dim + 2) bytes twice for each row of out.  Tables of up to four blocks, and groups == 0: the
+ * call is passed on to gemv_kv8_attention. */
+gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
+                                        const int32_t *lens, const int32_t *firsts, const int32_t *prefix, int groups, void *out,
+                                        float *lse, int S, int T, int q_heads, float scale, gemv_stream_t stream);
+
 /* Launch overlap for the calling thread's later calls (initially GEMV_OVERLAP_LAUNCH).
  * Programmatic dependent launch: a GEMV's kernels may be scheduled while the kernel
  * before them on the stream is finishing, so that back-to-back GEMVs (a decode layer,
@@ -524,7 +548,7 @@ gemv_status_t gemv_test_force_kernel(int kernel, int param);
 gemv_status_t gemv_test_last_plan(gemv_plan_t *plan);
 
 /* Device-side status of the kernels with bounded waits (GEMV_KERNEL_TC, gemv_f8,
- * gemv_kv8_attention) and of the 8-bit cache's own checks.
+ * gemv_kv8_attention, gemv_kv8_prefix_attention) and of the 8-bit cache's own checks.
  * Synchronises `stream`, then returns GEMV_ERR_DEVICE_TIMEOUT if a wait of a kernel
  * launched on the current device since the previous call ran out (the kernel then
  * left its outputs unwritten, freed its tensor memory and returned with nothing in
@@ -536,7 +560,7 @@ gemv_status_t gemv_get_device_status(gemv_stream_t stream, int *bits);
 
 /* TEST ONLY — not thread-safe.  With `stall` != 0 every later GEMV_KERNEL_TC or gemv_f8
  * launch skips the last MMA of its first CTA (in the persistent form: the MMAs of that
- * CTA's last k-tile), and every gemv_kv8_attention launch all copies of values,
+ * CTA's last k-tile), and every gemv_kv8_attention and gemv_kv8_prefix_attention launch all copies of values,
  * so that the wait for it runs out after `timeout_ns` (<= 0: the
  * default of 2 s) and gemv_get_device_status reports GEMV_ERR_DEVICE_TIMEOUT.
  * With 2 or 3, where gemv_f8 runs on pairs of SMs, the first or the second CTA of the first

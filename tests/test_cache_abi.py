@@ -129,3 +129,33 @@ def test_frequencies_refusals():
         with pytest.raises(g.GemvError) as e:
             g.rope_frequencies(**bad)
         assert e.value.status == INVALID
+
+
+def prefixed(c=None, dt=2, q=at(5), q_stride=1024, lens=at(6), firsts=at(9), prefix=at(10), groups=2, out=at(7), lse=at(8), S=3, T=1,
+             heads=8):
+    c = cache(width=40) if c is None else c
+    return g.lib().gemv_kv8_prefix_attention(dt, c, q, q_stride, lens, firsts, prefix, groups, out, lse, S, T, heads, 0.1, None)
+
+
+def test_prefix_attention_refusals():
+    for dim in (0, 32, 96, 512):
+        assert prefixed(cache(dim=dim)) == UNSUPPORTED
+    for k in ("blocks", "width", "heads", "dim"):
+        assert prefixed(cache(**{k: -1})) == INVALID
+    for k in ("k", "v", "ks", "vs", "table"):
+        assert prefixed(cache(**{k: None})) == INVALID
+    assert prefixed(cache(v=at(1) + 8)) == INVALID and prefixed(cache(vs=at(3) + 2)) == INVALID
+    assert prefixed(dt=0) == INVALID and prefixed(dt=3) == INVALID
+    assert prefixed(T=-1) == INVALID and prefixed(T=65) == UNSUPPORTED and prefixed(T=0) == 0
+    assert prefixed(S=-1) == INVALID and prefixed(S=0) == 0
+    assert prefixed(heads=7) == INVALID and prefixed(heads=-8) == INVALID and prefixed(heads=0) == 0
+    assert prefixed(q_stride=1023) == INVALID
+    for k in ("q", "out", "lens", "prefix"):
+        assert prefixed(**{k: None}) == INVALID
+    assert prefixed(groups=-1) == INVALID and prefixed(groups=4) == INVALID and prefixed(firsts=None, groups=2) == INVALID
+    assert prefixed(q=at(5) + 1) == INVALID and prefixed(out=at(7) + 1) == INVALID and prefixed(lse=at(8) + 2) == INVALID
+    assert prefixed(firsts=at(9) + 2) == INVALID and prefixed(prefix=at(10) + 1) == INVALID and prefixed(lens=at(6) + 2) == INVALID
+    for i in (0, 1, 2, 3, 4, 5, 6, 9, 10):
+        assert prefixed(out=at(i)) == INVALID and prefixed(lse=at(i)) == INVALID
+    assert prefixed(lse=at(7)) == INVALID
+    assert prefixed(S=1 << 22, T=64, heads=65534, q_stride=65534 * 128) == UNSUPPORTED   # rows of a group
