@@ -11,26 +11,32 @@
 // P and O stay in tensor memory, so that shared memory only feeds K and V.
 #pragma once
 
+#include <type_traits>
+
 #include "gemv_kv8.cuh"
 
 namespace gemv {
 
 template <int D>
 struct PxForm {
-  // Two sets of S and O where tensor memory holds them: an item has up to 256 rows, a tile of
+  // Two sets of S, P and O where tensor memory holds them: an item has up to 256 rows, a tile of
   // 128 for each set; an item of up to 128 rows gives both sets its rows, and the blocks to
-  // them by turns.  One set (192 and 256 channels) has two buffers for S.
+  // them by turns.  192 and 256 channels: one set, items of up to 128 rows.
   static constexpr int kSets = D <= 128 ? 2 : 1;
   static constexpr int kRows = 128 * kSets;
-  static constexpr int kSoft = 4 * kSets, kConv = 4;             // warps
-  static constexpr int kWarps = kSoft + kConv + 2, kThreads = kWarps * 32;
+  static constexpr int kSoft = 4 * kSets, kConv = 4;                      // warps
+  static constexpr int kWarps = kSoft + kConv + 2, kThreads = kWarps * 32;  // copies, products
   static constexpr int kRaw = kKvBlock * D, kStage = 2 * kRaw;   // bytes of keys or values: as cached, as fp16
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // of keys, and of values
-  static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 12 : D == 192 ? 8 : 5;
-  static constexpr int kSmem = 1024 + 2 * kStages * kStage + kSlots * kRaw;
-  // tensor memory columns: O of each set, two of S, Q of each set
-  static constexpr int kS = kSets * D, kQ = kS + 128;
-  static_assert(kQ + kSets * D / 2 <= 512);
+  static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 10 : D == 192 ? 8 : 5;
+  // tensor memory columns: O of each set, S and P of each, Q
+  static constexpr int kS = kSets * D, kQ = kS + kSets * 96;
+  // with 128 channels the second set's Q finds no room there: it stays in shared memory (48 cycles
+  // an MMA, not 32)
+  static constexpr bool kQShared = D == 128;
+  static_assert(kQ + (kQShared ? 1 : kSets) * D / 2 <= 512);
+  static constexpr int kQBytes = kQShared ? 128 * D * 2 : 0;
+  static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kStage + kSlots * kRaw;
   // one CTA an SM (each takes all of the tensor memory)
   static_assert(kSmem > 114 * 1024 && kSmem <= 226 * 1024);
   // floats of a partial result's set: O as [D / 4][128 rows][4], largest logits, sums
@@ -75,13 +81,12 @@ __device__ __forceinline__ int px_tile0(const KvArgs &a, int g, int first) {
 }
 
 struct PxSeg {
-  int g, tile, h;   // group, tile of its rows, head
-  int b0, b1;       // its blocks
+  int tile, h;      // tile of its group's rows, head
+  int b0, b1;       // its blocks; none: the share's end
   int rows;         // of the tile
   int first;        // the group's first sequence
   int item;         // (tile's number) x heads + head
-  bool whole_start; // b0 is the item's first block
-  int64_t last;     // place of the item's last block
+  int parts;        // with the item's first blocks: CTAs that have some of it; else 0
 };
 // The CTA's share of the work list: places [lo, hi), of all groups' `total`.  Blocks whose
 // first place is in there are its own.
@@ -130,28 +135,47 @@ struct PxWalk {
       s.h = (int)kv_div(r, item);
       r -= s.h * item;
       const int64_t item0 = at - r, left = hi - item0;
-      s.g = g;
       s.first = p.first;
       s.rows = s.tile == p.tiles - 1 ? p.rows - s.tile * PxForm<D>::kRows : PxForm<D>::kRows;
       s.item = (px_tile0<D>(a, g, p.first) + s.tile) * a.heads + s.h;
       s.b0 = (int)((r + cost - 1) / cost);
       s.b1 = left >= item ? p.blocks : (int)((left + cost - 1) / cost);
-      s.whole_start = s.b0 == 0;
-      s.last = item0 + (int64_t)(p.blocks - 1) * cost;
+      s.parts = s.b0 == 0 ? (int)(shares.owner(item0 + (int64_t)(p.blocks - 1) * cost) - blockIdx.x) + 1 : 0;
       at = item0 + item < hi ? item0 + item : hi;
       if (s.b0 < s.b1) return true;
     }
+    s = {0, 0, 0, 0, 0, 0, 0, 0};
     return false;
   }
 };
+constexpr int kPxSegs = 4;  // segments that the copies' warp is ahead
 
 // ------------------------------------------------------------------ instructions
-// D (tensor memory, fp32) (+)= A (tensor memory, fp16, two columns of k to a word) B
-__device__ __forceinline__ void px_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D (tensor memory, fp32) (+)= A (tensor memory, fp16, two columns of k to a word) B, by
+// the elected lane.  The instruction is predicated, not branched around: addresses worked out
+// inside a branch of one lane leave the uniform registers (75 cycles to issue each, not 32).
+__device__ __forceinline__ void px_mma(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+// The same with A in shared memory.
+__device__ __forceinline__ void px_mma_shared(uint32_t elected, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void px_commit(uint32_t elected, uint64_t *b) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc_smem_u32(b)),
+      "r"(elected)
       : "memory");
 }
 // 32 words of this thread's tensor-memory lane; stored after px_st_wait.
@@ -165,9 +189,21 @@ __device__ __forceinline__ void px_st32(uint32_t addr, const uint32_t (&r)[32]) 
       "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void px_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void px_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void px_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void px_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ float px_log2(float v) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 // (x, y) = (x, y) f + c;  (x, y) *= f;  (x, y) += (u, v)
 __device__ __forceinline__ void px_fma2(float &x, float &y, float f, float c) {
   asm("{\n\t.reg .b64 a, f, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
@@ -187,15 +223,14 @@ __device__ __forceinline__ void px_add2(float &x, float &y, float u, float v) {
 }
 
 // ------------------------------------------------------------------ the shared blocks
-// One CTA per SM over its share of the work list.  Warps, each walking the same segments:
-//   copies       a block's keys, then its values, by the bulk copy engine into a ring of raw
+// One CTA per SM over its share of the work list.  Warps:
+//   copies       finds the share's segments and tells the others; a block's keys, then its values, by the bulk copy engine into a ring of raw
 //                slots, its scales beside them
 //   converters   raw e4m3 to fp16, in the 128-byte swizzle that the MMA reads: keys as 64 rows of
 //                tokens, values as D rows of channels, both along the product's k
-//   MMAs         steps in order: S of step 0, S of step 1, then for each step i its P V and S of step
-//                i + 2, which has the same S columns; one commit for both (a commit costs the
-//                issuing warp some 200 cycles).  Step i uses set i % 2 and block i / 2 (more than 128
-//                rows: both sets meet every block), or block i
+//   MMAs         step i uses set i % 2 and block i / 2 (more than 128 rows: both sets meet every
+//                block), or block i.  S of a set's next step is begun as soon as its softmax has
+//                read the last one, before P V of that: P has columns of its own
 //   softmax      four warps a set, a row to a thread: Q to tensor memory at an item's start, S to P
 //                for each step, O out at its end
 // O is scaled anew only where a row's largest weight (times its block's values' scale, which
@@ -208,7 +243,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   constexpr int R = F::kSlots, NS = F::kStages;
   static_assert(NS + R / 2 + 2 < kPxMeta);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t rawf[R], rawe[R], kf[NS], ke[NS], vf[NS], ve[NS], qf[F::kSets], sf[2], pf[2], fin;
+  __shared__ __align__(8) uint64_t rawf[R], rawe[R], kf[NS], ke[NS], vf[NS], ve[NS], qf[F::kSets], sf[F::kSets], sr[F::kSets], pf[F::kSets], of[F::kSets], gf[kPxSegs], ge[kPxSegs], fin;
+  __shared__ PxSeg segs[kPxSegs];
   __shared__ float meta[kPxMeta][2];  // of a block: the keys' and the values' scale
   __shared__ int meta_bad[kPxMeta];
   __shared__ uint32_t tmem_slot;
@@ -217,7 +253,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   pdl_trigger();  // after the wait: the next kernels read the batch's lengths before theirs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char *kst = smem, *vst = smem + NS * F::kStage, *raw = vst + NS * F::kStage;
+  unsigned char *qst = smem, *kst = smem + F::kQBytes, *vst = kst + NS * F::kStage, *raw = vst + NS * F::kStage;
   constexpr int kLoad = F::kSoft + F::kConv, kMma = kLoad + 1;
   if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)), "r"(512u) : "memory");
@@ -234,10 +270,16 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       tc_mbar_init(&ke[i], F::kSets);
       tc_mbar_init(&ve[i], F::kSets);
     }
-    for (int i = 0; i < F::kSets; ++i) tc_mbar_init(&qf[i], 4);
-    for (int i = 0; i < 2; ++i) {
-      tc_mbar_init(&sf[i], 1);
-      tc_mbar_init(&pf[i], 4);
+    for (int i = 0; i < F::kSets; ++i) {
+      tc_mbar_init(&qf[i], 4);  // Q is there
+      tc_mbar_init(&sf[i], 1);  // S is
+      tc_mbar_init(&sr[i], 4);  // S has been read
+      tc_mbar_init(&pf[i], 4);  // P is there
+      tc_mbar_init(&of[i], 1);  // P V is done
+    }
+    for (int i = 0; i < kPxSegs; ++i) {
+      tc_mbar_init(&gf[i], 1);
+      tc_mbar_init(&ge[i], F::kSoft + F::kConv + 1);
     }
     tc_mbar_init(&fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -253,14 +295,35 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     return __all_sync(0xffffffffu, f8_wait(b, (uint32_t)(n / of) & 1u, a.timeout_ns, abort)) != 0;
   };
 
-  PxWalk<D> walk;
-  PxSeg s;
-  walk.begin(a, lane);
   bool ok = true;
   int c0 = 0;     // blocks of the segments before
   int piece = 0;  // of the ring of raw slots
+  int seg = 0;
+  PxSeg s;
+  auto take = [&]() {  // the next segment; false at the end
+    const int at = seg % kPxSegs;
+    ok = ok && wait(&gf[at], seg, kPxSegs);
+    if (!ok) return false;
+    s = segs[at];
+    __syncwarp();
+    if (lane == 0) tc_mbar_arrive(&ge[at]);
+    ++seg;
+    return s.b0 < s.b1;
+  };
   if (warp == kLoad) {  // ---- copies
-    while (ok && walk.next(a, s)) {
+    PxWalk<D> walk;
+    walk.begin(a, lane);
+    for (bool more = true; more;) {
+      more = walk.next(a, s);
+      const int at = seg % kPxSegs;
+      ok = seg < kPxSegs || wait(&ge[at], seg - kPxSegs, kPxSegs);
+      if (!ok) break;
+      if (lane == 0) {
+        segs[at] = s;
+        tc_mbar_arrive(&gf[at]);
+      }
+      __syncwarp();
+      ++seg;
       int32_t entries = 0;
       for (int b = s.b0; ok && b < s.b1; ++b) {
         const int i = (b - s.b0) & 31;
@@ -293,59 +356,86 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           ++piece;
         }
       }
+      if (!ok) break;
       c0 += s.b1 - s.b0;
     }
     f8_copy4_drain();
   } else if (warp == kMma) {  // ---- products
-    const uint32_t is = tc_idesc(false, kKvBlock), io = tc_idesc(false, D);
+    // (Addresses and counts that the compiler knows to be alike in all lanes stay in uniform
+    // registers, which the MMA takes: __reduce_max_sync and the votes give such.)
+    constexpr uint32_t kAll = 0xffffffffu;
+    const uint32_t is = tc_idesc(false, kKvBlock), io = tc_idesc(false, D), tm = __reduce_max_sync(kAll, tmem);
     const uint64_t dk = tc_smem_desc(tc_smem_u32(kst)), dv = tc_smem_desc(tc_smem_u32(vst));
-    uint32_t qbits = 0, pbits = 0;  // phases of qf and pf
-    while (ok && walk.next(a, s)) {
-      const bool both = F::kSets > 1 && s.rows > 128;
-      const int n = (s.b1 - s.b0) * (both ? 2 : 1);
-      auto block = [&](int i) { return c0 + (both ? i >> 1 : i); };
-      auto scores = [&](int i) {  // S of step i, once its keys are there
-        ok = ok && wait(&kf[block(i) % NS], block(i), NS);
+    const uint32_t elected = f8_elect();
+    const uint64_t dq = tc_smem_desc(tc_smem_u32(qst));
+    uint32_t ik = 0, iv = 0, kph = 0, vph = 0, qph[2] = {0, 0}, ph[2] = {0, 0};  // stages in use, phases
+    auto ready = [&](uint64_t *b, uint32_t parity) { ok = ok && __all_sync(kAll, f8_wait(b, parity, a.timeout_ns, abort)) != 0; };
+    while (__any_sync(kAll, take())) {
+      const bool both = __any_sync(kAll, F::kSets > 1 && s.rows > 128);
+      const int n = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)) * (both ? 2 : 1);
+      auto scores = [&](auto set) {  // S of the set's next step
+        constexpr int x = decltype(set)::value;
+        ready(&kf[ik], kph);
         if (!ok) return;
         px_fence_after();
-        const int x = i & 1;
-        const uint32_t q = tmem + F::kQ + (F::kSets > 1 ? x * (D / 2) : 0), d = tmem + F::kS + x * 64;
-        const uint64_t at = dk + (uint64_t)(block(i) % NS * (F::kStage >> 4));
-        if (f8_elect()) {
+        const uint32_t d = tm + F::kS + x * 96;
+        const uint64_t at = dk + (uint64_t)(ik * (F::kStage >> 4));
+        if (x == 1 && F::kQShared && both) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) px_mma(d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is, k > 0);
+          for (int k = 0; k < D / 16; ++k)
+            px_mma_shared(elected, d, dq + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is,
+                          k > 0);
+        } else {
+          const uint32_t q = tm + F::kQ + (x == 1 && both ? D / 2 : 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            px_mma(elected, d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is, k > 0);
         }
-        __syncwarp();
+        px_commit(elected, &sf[x]);
+        if ((!both || x == 1) && ++ik == NS) {
+          ik = 0;
+          kph ^= 1;
+        }
       };
-      for (int x = 0; x < F::kSets && x < n; ++x) {
-        ok = ok && wait(&qf[x], (qbits >> x) & 1, 1);
-        qbits ^= 1u << x;
-      }
-      for (int i = 0; i < 2 && i < n && ok; ++i) {
-        scores(i);
-        if (ok && f8_elect()) tc_commit(&sf[i]);
-        __syncwarp();
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const int x = i & 1, st = block(i) % NS;
-        ok = wait(&vf[st], block(i), NS) && wait(&pf[x], (pbits >> x) & 1, 1);
-        if (!ok) break;
-        pbits ^= 1u << x;
+      auto sums = [&](auto set, bool add) {  // P V of the set's step
+        constexpr int x = decltype(set)::value;
+        ready(&vf[iv], vph);
+        ready(&pf[x], ph[x]);
+        if (!ok) return;
+        ph[x] ^= 1;
         px_fence_after();
-        const uint32_t d = tmem + (F::kSets > 1 ? x * D : 0), w = tmem + F::kS + x * 64;
-        const uint64_t at = dv + (uint64_t)(st * (F::kStage >> 4));
-        if (f8_elect()) {
+        const uint32_t d = tm + x * D, w = tm + F::kS + x * 96 + 64;
+        const uint64_t at = dv + (uint64_t)(iv * (F::kStage >> 4));
 #pragma unroll
-          for (int k = 0; k < kKvBlock / 16; ++k) px_mma(d, w + k * 8, at + k * 2, io, k > 0 || i >= F::kSets);
+        for (int k = 0; k < kKvBlock / 16; ++k) px_mma(elected, d, w + k * 8, at + k * 2, io, k > 0 || add);
+        px_commit(elected, &of[x]);
+        if ((!both || x == 1) && ++iv == NS) {
+          iv = 0;
+          vph ^= 1;
         }
-        __syncwarp();
-        if (i + 2 < n) scores(i + 2);
-        if (ok && f8_elect()) tc_commit(&sf[x]);
-        __syncwarp();
+      };
+      const std::integral_constant<int, 0> set0;
+      const std::integral_constant<int, F::kSets - 1> set1;
+      ready(&qf[0], qph[0]);
+      qph[0] ^= 1;
+      if (both) {
+        ready(&qf[F::kSets - 1], qph[1]);
+        qph[1] ^= 1;
       }
-      c0 += s.b1 - s.b0;
+      if (ok) scores(set0);
+      if (F::kSets > 1 && ok && n > 1) scores(set1);
+      for (int i = 0; i < n && ok; i += F::kSets) {
+        ready(&sr[0], ph[0]);
+        if (ok && i + F::kSets < n) scores(set0);
+        if (F::kSets > 1 && i + 1 < n) {
+          ready(&sr[F::kSets - 1], ph[F::kSets - 1]);
+          if (ok && i + 3 < n) scores(set1);
+        }
+        if (ok) sums(set0, i > 0);
+        if (F::kSets > 1 && ok && i + 1 < n) sums(set1, i > 0);
+      }
     }
-  } else if (warp >= F::kSoft) {  // ---- e4m3 to fp16
+  } else if (warp >= F::kSoft && warp < kLoad) {  // ---- e4m3 to fp16
     const int ct = tid - F::kSoft * 32;
     auto widen = [&](const uint4 &x, unsigned char *row, int chunk, int turn, bool swap) {
       const uint4 lo = make_uint4(kv_half2_lo(x.x), kv_half2_hi(x.x), kv_half2_lo(x.y), kv_half2_hi(x.y));
@@ -364,7 +454,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       ++piece;
     };
     constexpr int kPer = kKvBlock * D / 16 / (F::kConv * 32);  // 16-byte pieces of a thread
-    while (ok && walk.next(a, s)) {
+    while (take()) {
       for (int b = s.b0; b < s.b1; ++b, ++c0) {
         const int st = c0 % NS;
         ok = wait(&rawf[piece % R], piece, R) && (c0 < NS || wait(&ke[st], c0 - NS, NS));
@@ -393,21 +483,20 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         hand_on(&vf[st]);
       }
     }
-  } else {  // ---- softmax
-    const int x = warp >> 2, in_tile = (warp & 3) * 32 + lane;  // set, row of its tile: tensor-memory lane
-    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t to = mine + x * D, tq = mine + F::kQ + x * (D / 2);
-    const bool signals = (warp & 3) == 0 && lane == 0;
-    uint32_t sbits = 0;  // phases of sf
-    while (ok && walk.next(a, s)) {
+  } else if (warp < F::kSoft) {  // ---- softmax
+    const int x = warp >> 2, quarter = warp & 3;
+    const int in_tile = quarter * 32 + lane;  // row of its tile: tensor-memory lane
+    const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ts = mine + F::kS + x * 96, to = mine + x * D;
+    const bool signals = quarter == 0 && lane == 0;
+    uint32_t ph = 0;  // phase of sf; of of, once a step on
+    while (take()) {
       const bool both = F::kSets > 1 && s.rows > 128;
       const int nb = s.b1 - s.b0, n = nb * (both ? 2 : 1);
-      auto block = [&](int i) { return c0 + (both ? i >> 1 : i); };
-      const int row0 = (both ? x * 128 : 0) + (warp & 3) * 32;
+      const int row0 = (both ? x * 128 : 0) + quarter * 32;
       const bool alive = row0 + lane < s.rows, any = row0 < s.rows;  // the row's, the warp's
       float *part = a.px_ws + ((int64_t)blockIdx.x + s.item) * (F::kSets * F::kPart) + x * F::kPart;
-      if (s.whole_start && tid == 0)  // the item's first blocks: where its parts are
-        a.px_parts[s.item] = make_int4((int)blockIdx.x, (int)(walk.shares.owner(s.last) - blockIdx.x) + 1, 0, 0);
+      if (s.parts > 0 && tid == 0) a.px_parts[s.item] = make_int4((int)blockIdx.x, s.parts, 0, 0);
       if (F::kSets > 1 && x >= n) {  // a single block, the other set's
         part[128 * D + in_tile] = -INFINITY;
         part[128 * (D + 1) + in_tile] = 0.f;
@@ -418,29 +507,40 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       // the softmax's factor is what is left, its sign goes with Q
       float f = 0.f;
       if (any) {
-        const int row = s.tile * F::kRows + row0 + lane, of = a.T * a.group;
-        const int sq = s.first + row / of, rt = row % of, t = rt / a.group;
+        const int row = s.tile * F::kRows + row0 + lane, of_seq = a.T * a.group;
+        const int sq = s.first + row / of_seq, rt = row % of_seq, t = rt / a.group;
         const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)sq * a.T + t) * a.q_stride +
                                    ((int64_t)s.h * a.group + rt - t * a.group) * D;
         const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
-        auto fetch = [&](int c) {  // channels c .. c + 7
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (alive) {
-            if (vec) {
-              v = __ldg(reinterpret_cast<const uint4 *>(qp + c));
-            } else {
-              const uint2 lo = kv_load4(qp + c), hi = kv_load4(qp + c + 4);
-              v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        constexpr int kHeld = D == 64 ? D : D / 2;  // channels that the registers hold at a time
+        uint32_t u[kHeld / 2];
+        auto fetch = [&](int c) {
+          if (alive && vec) {
+#pragma unroll
+            for (int j = 0; j < kHeld / 2; j += 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + c + 2 * j));
+              u[j] = v.x;
+              u[j + 1] = v.y;
+              u[j + 2] = v.z;
+              u[j + 3] = v.w;
+            }
+          } else if (alive) {
+#pragma unroll
+            for (int j = 0; j < kHeld / 2; j += 2) {
+              const uint2 v = kv_load4(qp + c + 2 * j);
+              u[j] = v.x;
+              u[j + 1] = v.y;
             }
           }
-          return v;
         };
+#pragma unroll
+        for (int j = 0; j < kHeld / 2; ++j) u[j] = 0;
         uint32_t top = 0;
-#pragma unroll 4
-        for (int c = 0; c < D; c += 8) {
-          const uint4 v = fetch(c);
-          top = kv_max2(kv_max2(top, v.x & 0x7fff7fffu, a.dtype), v.y & 0x7fff7fffu, a.dtype);
-          top = kv_max2(kv_max2(top, v.z & 0x7fff7fffu, a.dtype), v.w & 0x7fff7fffu, a.dtype);
+#pragma unroll 1
+        for (int c = D - kHeld; c >= 0; c -= kHeld) {
+          fetch(c);
+#pragma unroll
+          for (int j = 0; j < kHeld / 2; ++j) top = kv_max2(top, u[j] & 0x7fff7fffu, a.dtype);
         }
         const float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
         int e = (__float_as_int(mx) >> 23) & 0xff;  // (an infinity takes the largest exponent)
@@ -448,126 +548,135 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         float up = __int_as_float((127 + 14 + 127 - e) << 23);
         f = fabsf(a.scale_log2) / up;
         if (a.scale_log2 < 0.f) up = -up;
+        if (both || x == 0) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t w[32];
+          for (int c = 0; c < D; c += kHeld) {
+            if (c > 0) fetch(c);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 v = fetch(c + 8 * j);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < kHeld / 2; ++j) u[j] = kv_pack_half(kv_wide_lo(u[j], a.dtype) * up, kv_wide_hi(u[j], a.dtype) * up);
+            if (F::kQShared && x == 1) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[4 * j + k] = kv_pack_half(kv_wide_lo(u[k], a.dtype) * up, kv_wide_hi(u[k], a.dtype) * up);
+              for (int j = 0; j < kHeld / 2; j += 4) {
+                const int chunk = (c / 8 + j / 4) & 7, atom = (c + 2 * j) / 64;
+                *reinterpret_cast<uint4 *>(qst + atom * (128 * 128) + in_tile * 128 + ((chunk ^ (in_tile & 7)) * 16)) =
+                    make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < kHeld / 2; j += 16) px_st16(mine + F::kQ + x * (D / 2) + c / 2 + j, u + j);
+            }
           }
-          px_st32(tq + c / 2, w);
+          px_st_wait();
+          if (F::kQShared && x == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        px_st_wait();
       }
       px_fence_before();
       __syncwarp();
-      if (lane == 0) tc_mbar_arrive(&qf[x]);
+      if (lane == 0 && (both || x == 0)) tc_mbar_arrive(&qf[x]);
 
       float m = -INFINITY, l = 0.f, ref = -INFINITY;  // largest logit, sum of weights, O's reference
-      auto release = [&](uint64_t *ring, int i) {     // step i is done with its stage
-        uint64_t *b = &ring[block(i) % NS];
+      auto release = [&](uint64_t *ring, int blk) {   // this set is done with a block's stage
+        uint64_t *b = &ring[blk % NS];
         tc_mbar_arrive(b);
         if (F::kSets > 1 && !both) tc_mbar_arrive(b);  // (no other set waits for it)
       };
+      const int by = F::kSets > 1 && !both ? 2 : 1;  // from one of its blocks to the next
 #pragma unroll 1
-      for (int i = F::kSets > 1 ? x : 0; i < n; i += F::kSets) {
-        const int buf = i & 1, st = block(i) % NS, slot = block(i) % kPxMeta;
-        // (the keys came before S did: no wait, but the scales are this warp's to read then)
-        ok = wait(&sf[buf], (sbits >> buf) & 1, 1) && wait(&kf[st], block(i), NS);
+      for (int blk = c0 + (by == 2 ? x : 0); blk < c0 + nb; blk += by) {
+        const bool first = blk < c0 + by;
+        const int slot = blk % kPxMeta;
+        // (once the keys are converted the block's scales are there, too)
+        ok = wait(&kf[blk % NS], blk, NS);
         if (!ok) break;
-        sbits ^= 1u << buf;
-        px_fence_after();
-        const float ks = meta[slot][0], vs = meta[slot][1];
+        const float ff = f * meta[slot][0], lv = px_log2(meta[slot][1]);
         const bool bad = meta_bad[slot] != 0;
+        ok = wait(&sf[x], ph, 1);
+        if (!ok) break;
+        px_fence_after();
+        uint32_t r[2][32];
+        if (any) {
+          f8_ld<32>(ts, r[0]);
+          f8_ld<32>(ts + 32, r[1]);
+          f8_ld_wait<32>(r[0]);
+          f8_ld_wait<32>(r[1]);
+        }
+        px_fence_before();
         __syncwarp();
-        if (signals) {
-          release(ke, i);
-          if (i >= 2) release(ve, i - 2);
+        if (lane == 0) tc_mbar_arrive(&sr[x]);
+        if (signals) release(ke, blk);
+        float g = 0.f, z = 0.f;
+        bool grow = false;
+        float shrink = 1.f;
+        if (any && !bad) {
+          float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            mx = fmaxf(mx, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[0][j + 1])));
+            my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
+          }
+          const float bm = fmaxf(mx, my) * ff, cand = bm + lv;
+          if (bm > m) {
+            l *= kv_exp2(m - bm);
+            m = bm;
+          }
+          grow = first || cand > ref + kPxSlack;
+          if (grow) {
+            shrink = kv_exp2(ref - cand);
+            ref = cand;
+          }
+          z = m == -INFINITY ? 0.f : m;
+          g = kv_exp2(fminf(z + lv - (ref == -INFINITY ? 0.f : ref) + kPxLift, 127.f));
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+            px_fma2(u, v, ff, -z);
+            u = kv_exp2(u);
+            v = kv_exp2(v);
+            px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
+            px_mul2(u, v, g);
+            r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
+          }
+          l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[0][j] = 0;
+        }
+        // the product before this one: done with P, with its values, with O
+        if (!first) {
+          ok = wait(&of[x], ph ^ 1, 1);
+          if (!ok) break;
+          px_fence_after();
+          if (signals) release(ve, blk - by);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float to_new = grow ? shrink : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              f8_ld<16>(to + c, o);
+              f8_ld_wait<16>(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * to_new);
+              px_st16(to + c, o);
+            }
+          }
         }
         if (any) {
-          const uint32_t ts = mine + F::kS + buf * 64;
-          uint32_t p[32];
-          if (!bad) {
-            uint32_t r[2][32];
-            f8_ld<32>(ts, r[0]);
-            f8_ld<32>(ts + 32, r[1]);
-            f8_ld_wait<32>(r[0]);
-            f8_ld_wait<32>(r[1]);
-            float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              mx = fmaxf(mx, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[0][j + 1])));
-              my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
-            }
-            const float ff = f * ks, bm = fmaxf(mx, my) * ff, lv = log2f(vs), cand = bm + lv;
-            if (bm > m) {
-              l *= kv_exp2(m - bm);
-              m = bm;
-            }
-            if (i < F::kSets) {
-              ref = cand;
-            } else {
-              const bool grow = cand > ref + kPxSlack;
-              if (__any_sync(0xffffffffu, grow)) {
-                // (the other buffer's product before this one has to be done, too)
-                if (F::kSets == 1) ok = wait(&sf[buf ^ 1], (sbits >> (buf ^ 1)) & 1, 1);
-                if (!ok) break;
-                px_fence_after();
-                const float by = grow ? kv_exp2(ref - cand) : 1.f;
-                if (grow) ref = cand;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t o[32];
-                  f8_ld<32>(to + c, o);
-                  f8_ld_wait<32>(o);
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-                  px_st32(to + c, o);
-                }
-                px_st_wait();
-              }
-            }
-            const float z = m == -INFINITY ? 0.f : m;
-            const float g = kv_exp2(fminf(z + lv - (ref == -INFINITY ? 0.f : ref) + kPxLift, 127.f));
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-              px_fma2(u, v, ff, -z);
-              u = kv_exp2(u);
-              v = kv_exp2(v);
-              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
-              px_mul2(u, v, g);
-              p[j] = kv_pack_half(u, v);
-            }
-            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] = 0;
-          }
-          px_st32(ts, p);
+          px_st32(ts + 64, r[0]);
           px_st_wait();
         }
         px_fence_before();
         __syncwarp();
-        if (lane == 0) tc_mbar_arrive(&pf[buf]);
+        if (lane == 0) tc_mbar_arrive(&pf[x]);
+        ph ^= 1;
       }
       if (!ok) break;
-      const int end = F::kSets > 1 ? n - 1 - ((n - 1 - x) & 1) : n - 1;  // this set's last step
-      ok = wait(&sf[end & 1], (sbits >> (end & 1)) & 1, 1);
+      ok = wait(&of[x], ph ^ 1, 1);
       if (!ok) break;
-      sbits ^= F::kSets == 1 && n > 1 ? 3u : 1u << (end & 1);
       px_fence_after();
-      if (signals) {
-        if (F::kSets == 1 && n > 1) release(ve, end - 1);
-        release(ve, end);
-      }
+      if (signals) release(ve, by == 2 ? c0 + nb - 1 - ((nb - 1 - x) & 1) : c0 + nb - 1);  // its last block
       if (any) {
-        const float by = kv_exp2(ref - kPxLift - m);  // O in units of the largest weight
+        const float units = kv_exp2(ref - kPxLift - m);  // O in units of the largest weight
         float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -577,8 +686,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           if (alive) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              out[(c + j) / 4 * 128] = make_float4(__uint_as_float(o[j]) * by, __uint_as_float(o[j + 1]) * by,
-                                                   __uint_as_float(o[j + 2]) * by, __uint_as_float(o[j + 3]) * by);
+              out[(c + j) / 4 * 128] = make_float4(__uint_as_float(o[j]) * units, __uint_as_float(o[j + 1]) * units,
+                                                   __uint_as_float(o[j + 2]) * units, __uint_as_float(o[j + 3]) * units);
           }
         }
         if (alive) {
