@@ -40,8 +40,11 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   a.px_ws = reinterpret_cast<float *>(p + own);
   a.parts = reinterpret_cast<int4 *>(p + own + px);
   a.px_parts = a.parts + own_items;
-  e = allow_smem_once<k_kv8_prefix<D>>(P::kSmem);
-  if (e == cudaSuccess) e = launch_k(k_kv8_prefix<D>, dim3((unsigned)sms), dim3(P::kThreads), (size_t)P::kSmem, s, pdl, a);
+  const bool half = a.dtype == GEMV_DTYPE_F16;
+  e = half ? allow_smem_once<k_kv8_prefix<D, GEMV_DTYPE_F16>>(P::kSmem) : allow_smem_once<k_kv8_prefix<D, GEMV_DTYPE_BF16>>(P::kSmem);
+  if (e == cudaSuccess)
+    e = launch_k(half ? k_kv8_prefix<D, GEMV_DTYPE_F16> : k_kv8_prefix<D, GEMV_DTYPE_BF16>, dim3((unsigned)sms), dim3(P::kThreads),
+                 (size_t)P::kSmem, s, pdl, a);
   if (e == cudaSuccess) e = allow_smem_once<k_kv8_attention<D, NT, false, true>>(F::kSmem);
   if (e == cudaSuccess)
     e = launch_k(k_kv8_attention<D, NT, false, true>, dim3((unsigned)sms), dim3(F::kThreads), (size_t)F::kSmem, s, pdl, a);

@@ -25,7 +25,7 @@ struct PxForm {
   static constexpr int kSets = D <= 128 ? 2 : 1;
   static constexpr int kRows = 128 * kSets;
   static constexpr int kSoft = 4 * kSets, kConv = 4;                      // warps
-  static constexpr int kWarps = kSoft + kConv + 2, kThreads = kWarps * 32;  // copies, products
+  static constexpr int kWarps = kSoft + kConv + 3, kThreads = kWarps * 32;  // copies, the two products
   static constexpr int kRaw = kKvBlock * D, kStage = 2 * kRaw;   // bytes of keys or values: as cached, as fp16
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // of keys, and of values
   static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 10 : D == 192 ? 8 : 5;
@@ -44,12 +44,13 @@ struct PxForm {
 };
 // Blocks whose scales are kept.  While the softmax is at block j, the converters are at
 // j + kStages + 1 at most, and the copies kSlots / 2 + 1 further on.
-constexpr int kPxMeta = 16;
+constexpr int kPxMeta = 32;
 constexpr int kPxCost1 = 2, kPxCost2 = 3;  // places of a block: of an item of up to 128 rows, of more
 constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
-// The weights leave with a factor of 2^11 and may outgrow their reference by 2^4 before O is
-// scaled anew: fp16 holds them up to 2^15, and in full down to 2^-25 of the reference.
-constexpr float kPxLift = 11.f, kPxSlack = 4.f;
+// The weights leave with a factor of 2^8 and may outgrow their reference by 2^7 before O is
+// scaled anew (a warp takes some 1000 cycles for that): fp16 holds them up to 2^15, and in
+// full down to 2^-22 of the reference.
+constexpr float kPxLift = 8.f, kPxSlack = 7.f;
 
 // A group's part of the work list: its tiles of kRows rows, of each the heads, of each the
 // shared blocks.
@@ -222,22 +223,32 @@ __device__ __forceinline__ void px_add2(float &x, float &y, float u, float v) {
       : "f"(u), "f"(v));
 }
 
+// Eight 16-bit values from anywhere (a call: such rows are rare).
+static __device__ __noinline__ uint4 px_load8(const unsigned short *p) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = __ldg(p + 2 * j) | ((uint32_t)__ldg(p + 2 * j + 1) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // ------------------------------------------------------------------ the shared blocks
 // One CTA per SM over its share of the work list.  Warps:
 //   copies       finds the share's segments and tells the others; a block's keys, then its values, by the bulk copy engine into a ring of raw
 //                slots, its scales beside them
 //   converters   raw e4m3 to fp16, in the 128-byte swizzle that the MMA reads: keys as 64 rows of
 //                tokens, values as D rows of channels, both along the product's k
-//   MMAs         step i uses set i % 2 and block i / 2 (more than 128 rows: both sets meet every
-//                block), or block i.  S of a set's next step is begun as soon as its softmax has
-//                read the last one, before P V of that: P has columns of its own
+//   scores, sums the two products, a warp each: the queue between it and the tensor cores is
+//                short, and they idle while a single warp waits for its next barrier.  Step i
+//                uses set i % 2 and block i / 2 (more than 128 rows: both sets meet every block), or
+//                block i.  S of a set's next step is begun as soon as its softmax has read the last
+//                one: P has columns of its own
 //   softmax      four warps a set, a row to a thread: Q to tensor memory at an item's start, S to P
 //                for each step, O out at its end
 // O is scaled anew only where a row's largest weight (times its block's values' scale, which
-// goes into P) outgrows the reference by 2^4: as a rule in the first blocks only.  Weights and
+// goes into P) outgrows the reference by 2^7: as a rule in the first blocks only.  Weights and
 // their sums refer to the running maximum of the logits alone: a block of tiny values still counts
 // in full in the sum.
-template <int D>
+template <int D, int DT>
 __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvArgs a) {
   using F = PxForm<D>;
   constexpr int R = F::kSlots, NS = F::kStages;
@@ -254,8 +265,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char *qst = smem, *kst = smem + F::kQBytes, *vst = kst + NS * F::kStage, *raw = vst + NS * F::kStage;
-  constexpr int kLoad = F::kSoft + F::kConv, kMma = kLoad + 1;
-  if (warp == kMma) {
+  constexpr int kLoad = F::kSoft + F::kConv, kScores = kLoad + 1, kSums = kLoad + 2;
+  if (warp == kSums) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem_u32(&tmem_slot)), "r"(512u) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -279,9 +290,9 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     }
     for (int i = 0; i < kPxSegs; ++i) {
       tc_mbar_init(&gf[i], 1);
-      tc_mbar_init(&ge[i], F::kSoft + F::kConv + 1);
+      tc_mbar_init(&ge[i], F::kSoft + F::kConv + 2);
     }
-    tc_mbar_init(&fin, 1);
+    tc_mbar_init(&fin, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     abort_flag = 0;
   }
@@ -360,79 +371,100 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       c0 += s.b1 - s.b0;
     }
     f8_copy4_drain();
-  } else if (warp == kMma) {  // ---- products
+  } else if (warp == kScores || warp == kSums) {  // ---- products
     // (Addresses and counts that the compiler knows to be alike in all lanes stay in uniform
     // registers, which the MMA takes: __reduce_max_sync and the votes give such.)
     constexpr uint32_t kAll = 0xffffffffu;
-    const uint32_t is = tc_idesc(false, kKvBlock), io = tc_idesc(false, D), tm = __reduce_max_sync(kAll, tmem);
-    const uint64_t dk = tc_smem_desc(tc_smem_u32(kst)), dv = tc_smem_desc(tc_smem_u32(vst));
-    const uint32_t elected = f8_elect();
-    const uint64_t dq = tc_smem_desc(tc_smem_u32(qst));
-    uint32_t ik = 0, iv = 0, kph = 0, vph = 0, qph[2] = {0, 0}, ph[2] = {0, 0};  // stages in use, phases
+    const uint32_t tm = __reduce_max_sync(kAll, tmem), elected = f8_elect();
+    const std::integral_constant<int, 0> set0;
+    const std::integral_constant<int, F::kSets - 1> set1;
+    uint32_t ix = 0, iph = 0, ph[2] = {0, 0}, qph[2] = {0, 0};  // stage in use, phases
     auto ready = [&](uint64_t *b, uint32_t parity) { ok = ok && __all_sync(kAll, f8_wait(b, parity, a.timeout_ns, abort)) != 0; };
-    while (__any_sync(kAll, take())) {
-      const bool both = __any_sync(kAll, F::kSets > 1 && s.rows > 128);
-      const int n = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)) * (both ? 2 : 1);
-      auto scores = [&](auto set) {  // S of the set's next step
-        constexpr int x = decltype(set)::value;
-        ready(&kf[ik], kph);
-        if (!ok) return;
-        px_fence_after();
-        const uint32_t d = tm + F::kS + x * 96;
-        const uint64_t at = dk + (uint64_t)(ik * (F::kStage >> 4));
-        if (x == 1 && F::kQShared && both) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            px_mma_shared(elected, d, dq + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is,
-                          k > 0);
-        } else {
-          const uint32_t q = tm + F::kQ + (x == 1 && both ? D / 2 : 0);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            px_mma(elected, d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, is, k > 0);
-        }
-        px_commit(elected, &sf[x]);
-        if ((!both || x == 1) && ++ik == NS) {
-          ik = 0;
-          kph ^= 1;
-        }
-      };
-      auto sums = [&](auto set, bool add) {  // P V of the set's step
-        constexpr int x = decltype(set)::value;
-        ready(&vf[iv], vph);
-        ready(&pf[x], ph[x]);
-        if (!ok) return;
-        ph[x] ^= 1;
-        px_fence_after();
-        const uint32_t d = tm + x * D, w = tm + F::kS + x * 96 + 64;
-        const uint64_t at = dv + (uint64_t)(iv * (F::kStage >> 4));
-#pragma unroll
-        for (int k = 0; k < kKvBlock / 16; ++k) px_mma(elected, d, w + k * 8, at + k * 2, io, k > 0 || add);
-        px_commit(elected, &of[x]);
-        if ((!both || x == 1) && ++iv == NS) {
-          iv = 0;
-          vph ^= 1;
-        }
-      };
-      const std::integral_constant<int, 0> set0;
-      const std::integral_constant<int, F::kSets - 1> set1;
-      ready(&qf[0], qph[0]);
-      qph[0] ^= 1;
-      if (both) {
-        ready(&qf[F::kSets - 1], qph[1]);
-        qph[1] ^= 1;
+    auto pass = [&]() {  // to the next stage
+      if (++ix == NS) {
+        ix = 0;
+        iph ^= 1;
       }
-      if (ok) scores(set0);
-      if (F::kSets > 1 && ok && n > 1) scores(set1);
-      for (int i = 0; i < n && ok; i += F::kSets) {
-        ready(&sr[0], ph[0]);
-        if (ok && i + F::kSets < n) scores(set0);
-        if (F::kSets > 1 && i + 1 < n) {
-          ready(&sr[F::kSets - 1], ph[F::kSets - 1]);
-          if (ok && i + 3 < n) scores(set1);
+    };
+    if (warp == kScores) {
+      const uint32_t id = tc_idesc(false, kKvBlock);
+      const uint64_t dk = tc_smem_desc(tc_smem_u32(kst)), dq = tc_smem_desc(tc_smem_u32(qst));
+      while (__any_sync(kAll, take())) {
+        const bool both = __any_sync(kAll, F::kSets > 1 && s.rows > 128);
+        const int nb = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)), n = both ? 2 * nb : nb;
+        auto step = [&](auto set, bool first) {  // S of the set's next step, once it has read the last
+          constexpr int x = decltype(set)::value;
+          if (!(both && x == 1)) ready(&kf[ix], iph);
+          if (!first) {
+            ready(&sr[x], ph[x]);
+            ph[x] ^= 1;
+          }
+          if (!ok) return;
+          px_fence_after();
+          const uint32_t d = tm + F::kS + x * 96;
+          const uint64_t at = dk + (uint64_t)(ix * (F::kStage >> 4));
+          if (x == 1 && F::kQShared && both) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              px_mma_shared(elected, d, dq + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2,
+                            id, k > 0);
+          } else {
+            const uint32_t q = tm + F::kQ + (x == 1 && both ? D / 2 : 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              px_mma(elected, d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, id, k > 0);
+          }
+          px_commit(elected, &sf[x]);
+          px_commit(elected, &ke[ix]);
+          if (F::kSets > 1 && !both) px_commit(elected, &ke[ix]);  // (no other set needs the stage)
+          if (!both || x == 1) pass();
+        };
+        ready(&qf[0], qph[0]);
+        qph[0] ^= 1;
+        if (both) {
+          ready(&qf[F::kSets - 1], qph[1]);
+          qph[1] ^= 1;
         }
-        if (ok) sums(set0, i > 0);
-        if (F::kSets > 1 && ok && i + 1 < n) sums(set1, i > 0);
+        for (int i = 0; i < n && ok; i += F::kSets) {
+          step(set0, i == 0);
+          if (F::kSets > 1 && ok && i + 1 < n) step(set1, i == 0);
+        }
+        // each set's last S is read, too: the phases of the next segment begin behind it
+        if (n > 0) {
+          ready(&sr[0], ph[0]);
+          ph[0] ^= 1;
+        }
+        if (F::kSets > 1 && n > 1) {
+          ready(&sr[F::kSets - 1], ph[F::kSets - 1]);
+          ph[F::kSets - 1] ^= 1;
+        }
+      }
+    } else {
+      const uint32_t id = tc_idesc(false, D);
+      const uint64_t dv = tc_smem_desc(tc_smem_u32(vst));
+      while (__any_sync(kAll, take())) {
+        const bool both = __any_sync(kAll, F::kSets > 1 && s.rows > 128);
+        const int nb = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)), n = both ? 2 * nb : nb;
+        auto step = [&](auto set, bool add) {  // P V of the set's step
+          constexpr int x = decltype(set)::value;
+          if (!(both && x == 1)) ready(&vf[ix], iph);
+          ready(&pf[x], ph[x]);
+          if (!ok) return;
+          ph[x] ^= 1;
+          px_fence_after();
+          const uint32_t d = tm + x * D, w = tm + F::kS + x * 96 + 64;
+          const uint64_t at = dv + (uint64_t)(ix * (F::kStage >> 4));
+#pragma unroll
+          for (int k = 0; k < kKvBlock / 16; ++k) px_mma(elected, d, w + k * 8, at + k * 2, id, k > 0 || add);
+          px_commit(elected, &of[x]);
+          px_commit(elected, &ve[ix]);
+          if (F::kSets > 1 && !both) px_commit(elected, &ve[ix]);
+          if (!both || x == 1) pass();
+        };
+        for (int i = 0; i < n && ok; i += F::kSets) {
+          step(set0, i > 0);
+          if (F::kSets > 1 && ok && i + 1 < n) step(set1, i > 0);
+        }
       }
     }
   } else if (warp >= F::kSoft && warp < kLoad) {  // ---- e4m3 to fp16
@@ -488,8 +520,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     const int in_tile = quarter * 32 + lane;  // row of its tile: tensor-memory lane
     const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t ts = mine + F::kS + x * 96, to = mine + x * D;
-    const bool signals = quarter == 0 && lane == 0;
-    uint32_t ph = 0;  // phase of sf; of of, once a step on
+    uint32_t ph = 0;   // phase of sf; of of, once a step on
+    uint32_t ph1 = 0;  // (first set) phase of the second's sf
     while (take()) {
       const bool both = F::kSets > 1 && s.rows > 128;
       const int nb = s.b1 - s.b0, n = nb * (both ? 2 : 1);
@@ -512,37 +544,18 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)sq * a.T + t) * a.q_stride +
                                    ((int64_t)s.h * a.group + rt - t * a.group) * D;
         const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
-        constexpr int kHeld = D == 64 ? D : D / 2;  // channels that the registers hold at a time
-        uint32_t u[kHeld / 2];
-        auto fetch = [&](int c) {
-          if (alive && vec) {
-#pragma unroll
-            for (int j = 0; j < kHeld / 2; j += 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qp + c + 2 * j));
-              u[j] = v.x;
-              u[j + 1] = v.y;
-              u[j + 2] = v.z;
-              u[j + 3] = v.w;
-            }
-          } else if (alive) {
-#pragma unroll
-            for (int j = 0; j < kHeld / 2; j += 2) {
-              const uint2 v = kv_load4(qp + c + 2 * j);
-              u[j] = v.x;
-              u[j + 1] = v.y;
-            }
-          }
+        auto fetch = [&](int c) {  // channels c .. c + 7
+          if (!alive) return make_uint4(0, 0, 0, 0);
+          return vec ? __ldg(reinterpret_cast<const uint4 *>(qp + c)) : px_load8(qp + c);
         };
-#pragma unroll
-        for (int j = 0; j < kHeld / 2; ++j) u[j] = 0;
         uint32_t top = 0;
-#pragma unroll 1
-        for (int c = D - kHeld; c >= 0; c -= kHeld) {
-          fetch(c);
-#pragma unroll
-          for (int j = 0; j < kHeld / 2; ++j) top = kv_max2(top, u[j] & 0x7fff7fffu, a.dtype);
+#pragma unroll 8
+        for (int c = 0; c < D; c += 8) {
+          const uint4 v = fetch(c);
+          top = kv_max2(kv_max2(top, v.x & 0x7fff7fffu, DT), v.y & 0x7fff7fffu, DT);
+          top = kv_max2(kv_max2(top, v.z & 0x7fff7fffu, DT), v.w & 0x7fff7fffu, DT);
         }
-        const float mx = fmaxf(kv_wide_lo(top, a.dtype), kv_wide_hi(top, a.dtype));
+        const float mx = fmaxf(kv_wide_lo(top, DT), kv_wide_hi(top, DT));
         int e = (__float_as_int(mx) >> 23) & 0xff;  // (an infinity takes the largest exponent)
         e = e < 16 ? 16 : e;
         float up = __int_as_float((127 + 14 + 127 - e) << 23);
@@ -550,20 +563,25 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         if (a.scale_log2 < 0.f) up = -up;
         if (both || x == 0) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += kHeld) {
-            if (c > 0) fetch(c);
+          for (int c = 0; c < D; c += 32) {  // (short code: it runs once, and its lines have to come first)
+            uint32_t u[16];
 #pragma unroll
-            for (int j = 0; j < kHeld / 2; ++j) u[j] = kv_pack_half(kv_wide_lo(u[j], a.dtype) * up, kv_wide_hi(u[j], a.dtype) * up);
+            for (int j = 0; j < 4; ++j) {
+              const uint4 v = fetch(c + 8 * j);
+              u[4 * j] = v.x;
+              u[4 * j + 1] = v.y;
+              u[4 * j + 2] = v.z;
+              u[4 * j + 3] = v.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = kv_pack_half(kv_wide_lo(u[j], DT) * up, kv_wide_hi(u[j], DT) * up);
             if (F::kQShared && x == 1) {
 #pragma unroll
-              for (int j = 0; j < kHeld / 2; j += 4) {
-                const int chunk = (c / 8 + j / 4) & 7, atom = (c + 2 * j) / 64;
-                *reinterpret_cast<uint4 *>(qst + atom * (128 * 128) + in_tile * 128 + ((chunk ^ (in_tile & 7)) * 16)) =
-                    make_uint4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-              }
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(qst + c / 64 * (128 * 128) + in_tile * 128 + ((((c / 8 + j) & 7) ^ (in_tile & 7)) * 16)) =
+                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
             } else {
-#pragma unroll
-              for (int j = 0; j < kHeld / 2; j += 16) px_st16(mine + F::kQ + x * (D / 2) + c / 2 + j, u + j);
+              px_st16(mine + F::kQ + x * (D / 2) + c / 2, u);
             }
           }
           px_st_wait();
@@ -575,21 +593,11 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       if (lane == 0 && (both || x == 0)) tc_mbar_arrive(&qf[x]);
 
       float m = -INFINITY, l = 0.f, ref = -INFINITY;  // largest logit, sum of weights, O's reference
-      auto release = [&](uint64_t *ring, int blk) {   // this set is done with a block's stage
-        uint64_t *b = &ring[blk % NS];
-        tc_mbar_arrive(b);
-        if (F::kSets > 1 && !both) tc_mbar_arrive(b);  // (no other set waits for it)
-      };
       const int by = F::kSets > 1 && !both ? 2 : 1;  // from one of its blocks to the next
 #pragma unroll 1
       for (int blk = c0 + (by == 2 ? x : 0); blk < c0 + nb; blk += by) {
         const bool first = blk < c0 + by;
         const int slot = blk % kPxMeta;
-        // (once the keys are converted the block's scales are there, too)
-        ok = wait(&kf[blk % NS], blk, NS);
-        if (!ok) break;
-        const float ff = f * meta[slot][0], lv = px_log2(meta[slot][1]);
-        const bool bad = meta_bad[slot] != 0;
         ok = wait(&sf[x], ph, 1);
         if (!ok) break;
         px_fence_after();
@@ -597,14 +605,17 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         if (any) {
           f8_ld<32>(ts, r[0]);
           f8_ld<32>(ts + 32, r[1]);
+        }
+        // (S is there, so its keys were converted, so the block's scales had come)
+        const float ff = f * meta[slot][0], lv = px_log2(meta[slot][1]);
+        const bool bad = meta_bad[slot] != 0;
+        if (any) {
           f8_ld_wait<32>(r[0]);
           f8_ld_wait<32>(r[1]);
         }
         px_fence_before();
         __syncwarp();
         if (lane == 0) tc_mbar_arrive(&sr[x]);
-        if (signals) release(ke, blk);
-        float g = 0.f, z = 0.f;
         bool grow = false;
         float shrink = 1.f;
         if (any && !bad) {
@@ -615,29 +626,42 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
             my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
           }
           const float bm = fmaxf(mx, my) * ff, cand = bm + lv;
-          if (bm > m) {
-            l *= kv_exp2(m - bm);
-            m = bm;
-          }
+          const float top = fmaxf(m, bm);  // (of a NaN and a number, the number)
+          l *= kv_exp2(m - (top == -INFINITY ? 0.f : top));
+          m = top;
           grow = first || cand > ref + kPxSlack;
           if (grow) {
             shrink = kv_exp2(ref - cand);
             ref = cand;
           }
-          z = m == -INFINITY ? 0.f : m;
-          g = kv_exp2(fminf(z + lv - (ref == -INFINITY ? 0.f : ref) + kPxLift, 127.f));
+          // P = 2^(logit + up): the weight 2^(logit - m) times 2^(m + up)
+          const float z = m == -INFINITY ? 0.f : m, up = lv - (ref == -INFINITY ? 0.f : ref) + kPxLift;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          if (!__any_sync(0xffffffffu, z + up < -80.f)) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-            px_fma2(u, v, ff, -z);
-            u = kv_exp2(u);
-            v = kv_exp2(v);
-            px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
-            px_mul2(u, v, g);
-            r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
+            for (int j = 0; j < 32; ++j) {
+              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+              px_fma2(u, v, ff, up);
+              u = kv_exp2(u);
+              v = kv_exp2(v);
+              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
+              r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
+            }
+            l = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), kv_exp2(-(z + up)), l);
+          } else {  // values so small that the weights would be lost in P: their sum apart
+            const float g = kv_exp2(z + up);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+              px_fma2(u, v, ff, -z);
+              u = kv_exp2(u);
+              v = kv_exp2(v);
+              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
+              px_mul2(u, v, g);
+              r[0][j] = kv_pack_half(u, v);
+            }
+            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
           }
-          l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[0][j] = 0;
@@ -647,7 +671,6 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           ok = wait(&of[x], ph ^ 1, 1);
           if (!ok) break;
           px_fence_after();
-          if (signals) release(ve, blk - by);
           if (__any_sync(0xffffffffu, grow)) {
             const float to_new = grow ? shrink : 1.f;
 #pragma unroll 1
@@ -674,7 +697,15 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       ok = wait(&of[x], ph ^ 1, 1);
       if (!ok) break;
       px_fence_after();
-      if (signals) release(ve, by == 2 ? c0 + nb - 1 - ((nb - 1 - x) & 1) : c0 + nb - 1);  // its last block
+      if (F::kSets > 1 && x == 0) {
+        // one Q for both sets: the other's last scores have to be done before the next Q comes
+        const int other = both ? nb : nb / 2;
+        ph1 ^= other & 1;
+        if (!both && other > 0) {
+          ok = wait(&sf[F::kSets - 1], ph1 ^ 1, 1);
+          if (!ok) break;
+        }
+      }
       if (any) {
         const float units = kv_exp2(ref - kPxLift - m);  // O in units of the largest weight
         float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
@@ -703,7 +734,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   __syncthreads();
   if (abort_flag != 0) {
     // after an abort nothing may be in flight when the CTA frees its tensor memory and exits
-    if (warp == kMma) {
+    if (warp == kScores || warp == kSums) {
       if (f8_elect()) tc_commit(&fin);
       __syncwarp();
       const bool drained = tc_mbar_wait(&fin, 0, a.timeout_ns);
@@ -718,7 +749,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     __syncwarp();
     __syncthreads();
   }
-  if (warp == kMma) {
+  if (warp == kSums) {
     px_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }

@@ -418,7 +418,7 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, and
  * GEMV_ERR_UNSUPPORTED for S x T x q_heads / heads above 2^30.  The shared values' sums, over
  * a share of the blocks each, are in units of the row's largest weight x value scale; the weights
- * are rounded to 11 bits as there, those below 2^-25 of that largest to fewer.  A scratch buffer
+ * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer
  * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and
  * 4 (dim + 2) bytes twice for each row of out.  Tables of up to four blocks, and groups == 0: the
  * call is passed on to gemv_kv8_attention. */
