@@ -51,17 +51,14 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   if (e == cudaSuccess) {
     const int rows = a.T * a.group < NT * 8 ? a.T * a.group : NT * 8;
     auto join = [&](auto kern, int along) {
-      return launch_k(kern, dim3((unsigned)a.S, (unsigned)items, (unsigned)((rows * D / 4 + along - 1) / along)),
-                      dim3(kKvJoinThreads), 0, s, pdl, a, sms);
+      return launch_k(kern, dim3((unsigned)a.S, (unsigned)items, (unsigned)((rows * (D / 16) + along - 1) / along)),
+                      dim3(kPxJoinThreads), 0, s, pdl, a, sms);
     };
-    // threads for the parts of the same channels: as many as two CTAs for each SM allow
-    const int64_t threads = own_items * rows * (D / 4), most = (int64_t)sms * 2 * kKvJoinThreads / threads;
-    if (most >= 8)
-      e = join(k_kv8_prefix_join<D, NT, 8>, kKvJoinThreads / 8);
-    else if (most >= 4)
-      e = join(k_kv8_prefix_join<D, NT, 4>, kKvJoinThreads / 4);
+    // threads for the parts of the same channels: four where an item of the shared blocks is in many
+    if (px_items * 4 <= sms)
+      e = join(k_kv8_prefix_join<D, NT, 4>, kPxJoinThreads / 4);
     else
-      e = join(k_kv8_prefix_join<D, NT, 1>, kKvJoinThreads);
+      e = join(k_kv8_prefix_join<D, NT, 1>, kPxJoinThreads);
   }
   const cudaError_t e2 = cudaFreeAsync(ws, s);
   if (e == cudaSuccess) e = e2;
@@ -90,8 +87,10 @@ gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache
   if (cache->heads == 0 || q_heads % cache->heads != 0 || q_heads > 65535) return GEMV_ERR_INVALID_VALUE;
   if (groups > S || (firsts == nullptr && groups > 1) || (groups > 0 && prefix == nullptr)) return GEMV_ERR_INVALID_VALUE;
   const int64_t row = (int64_t)q_heads * cache->dim, tokens = (int64_t)S * T;
-  const bool pass_on = groups == 0 || cache->width <= kPxWhole;
-  if (!pass_on && tokens * (q_heads / cache->heads) > (1 << 30)) return GEMV_ERR_UNSUPPORTED;  // rows of a group
+  // places of the work list and rows of a group are counted in 31 bits
+  const int64_t most = (tokens * (q_heads / cache->heads) / 128 + groups) * cache->heads * kPxCost2;
+  const bool pass_on = groups == 0 || cache->width <= kPxWhole || most > 0x7fffffff / cache->width ||
+                       tokens * (q_heads / cache->heads) > (1 << 30);
   if (q_stride < row) return GEMV_ERR_INVALID_VALUE;
   int64_t qb, ob;
   if (!span(tokens, row, q_stride, 2, &qb) || !mul_ok(tokens, row * 2, &ob)) return GEMV_ERR_INVALID_VALUE;

@@ -53,12 +53,15 @@ constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
 constexpr float kPxLift = 8.f, kPxSlack = 7.f;
 
 // A group's part of the work list: its tiles of kRows rows, of each the heads, of each the
-// shared blocks.
+// shared blocks.  (The host limits all groups' places to 31 bits: the first thing that a CTA
+// does is to find its share, and a 64-bit division there costs a microsecond, most of it for
+// the code to come.)
 struct PxGroup {
   int first, blocks, rows, tiles;
-  int full, last;  // places of a block in a whole tile, in the last one
-  int64_t places;
+  unsigned last, places;  // places of a block in the last tile; of the group
 };
+template <int D>
+__host__ __device__ constexpr unsigned px_full() { return PxForm<D>::kRows > 128 ? kPxCost2 : kPxCost1; }  // in a whole tile
 template <int D>
 __device__ __forceinline__ PxGroup px_group(const KvArgs &a, int g) {
   PxGroup p;
@@ -68,17 +71,15 @@ __device__ __forceinline__ PxGroup px_group(const KvArgs &a, int g) {
   p.rows = (k.end - k.first) * a.T * a.group;
   constexpr int R = PxForm<D>::kRows;
   p.tiles = (p.rows + R - 1) / R;
-  const int rest = p.rows - (p.tiles - 1) * R;
-  p.full = R > 128 ? kPxCost2 : kPxCost1;
-  p.last = rest > 128 ? kPxCost2 : kPxCost1;
-  p.places = p.tiles == 0 ? 0 : (int64_t)a.heads * p.blocks * ((int64_t)(p.tiles - 1) * p.full + p.last);
+  p.last = p.rows - (p.tiles - 1) * R > 128 ? kPxCost2 : kPxCost1;
+  p.places = p.tiles == 0 ? 0u : (unsigned)a.heads * p.blocks * ((unsigned)(p.tiles - 1) * px_full<D>() + p.last);
   return p;
 }
 // Number of a group's first tile, rising with the groups, none twice (a group has at most
 // one more than the rows before its end, by the tile, take it further on).
 template <int D>
 __device__ __forceinline__ int px_tile0(const KvArgs &a, int g, int first) {
-  return (int)((int64_t)first * a.T * a.group / PxForm<D>::kRows) + g;
+  return first * a.T * a.group / PxForm<D>::kRows + g;
 }
 
 struct PxSeg {
@@ -89,60 +90,57 @@ struct PxSeg {
   int item;         // (tile's number) x heads + head
   int parts;        // with the item's first blocks: CTAs that have some of it; else 0
 };
-// The CTA's share of the work list: places [lo, hi), of all groups' `total`.  Blocks whose
+// The CTA's share of the work list: places [at, hi), of all groups' `total`.  Blocks whose
 // first place is in there are its own.
 template <int D>
 struct PxWalk {
-  KvShares shares;
-  int64_t at, hi, base;  // next place, end, place of the group's first
+  unsigned each, more;    // places of a CTA, the first `more` have one more
+  unsigned at, hi, base;  // next place, end, place of the group's first
   int g;
   PxGroup p;
+  __device__ unsigned owner(unsigned u) const {
+    const unsigned longer = more * (each + 1);
+    return u < longer ? u / (each + 1) : more + (u - longer) / each;
+  }
   __device__ void begin(const KvArgs &a, int lane) {  // one warp, converged
-    int64_t total = 0;
-    for (int g0 = 0; g0 < a.groups; g0 += 32) {
-      int64_t n = g0 + lane < a.groups ? px_group<D>(a, g0 + lane).places : 0;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-      total += n;
-    }
-    int64_t W = total / (kPxLeast * kPxCost2);
+    p = px_group<D>(a, 0);
+    unsigned total = p.places;
+    for (int g0 = 1; g0 < a.groups; g0 += 32)
+      total += __reduce_add_sync(0xffffffffu, g0 + lane < a.groups ? px_group<D>(a, g0 + lane).places : 0u);
+    unsigned W = total / (kPxLeast * kPxCost2);
     W = W < 1 ? 1 : W < gridDim.x ? W : gridDim.x;
-    shares.cut(total, W);
-    at = blockIdx.x < W ? shares.first(blockIdx.x) : total;
-    hi = blockIdx.x < W ? shares.first(blockIdx.x + 1) : total;
+    each = total / W;
+    more = total - each * W;
+    auto first = [&](unsigned w) { return w >= W ? total : w * each + (w < more ? w : more); };
+    at = first(blockIdx.x);
+    hi = first(blockIdx.x + 1);
     g = 0;
     base = 0;
-    if (at >= hi) return;
-    p = px_group<D>(a, 0);
-    while (at >= base + p.places) {
-      base += p.places;
-      p = px_group<D>(a, ++g);
-    }
   }
   __device__ bool next(const KvArgs &a, PxSeg &s) {
     while (at < hi) {
-      if (at >= base + p.places) {
+      if (at - base >= p.places) {
         base += p.places;
         p = px_group<D>(a, ++g);
         continue;
       }
-      int64_t r = at - base;
-      const int64_t tile = (int64_t)a.heads * p.blocks * p.full;
-      s.tile = (int)kv_div(r, tile);
-      if (s.tile > p.tiles - 1) s.tile = p.tiles - 1;
-      const int cost = s.tile == p.tiles - 1 ? p.last : p.full;
-      const int64_t item = (int64_t)p.blocks * cost;
+      unsigned r = at - base;
+      const unsigned per_block = (unsigned)a.heads * p.blocks, tile = per_block * px_full<D>();
+      const int last = p.tiles - 1;
+      s.tile = last == 0 ? 0 : (int)(r / tile);
+      if (s.tile > last) s.tile = last;
       r -= s.tile * tile;
-      s.h = (int)kv_div(r, item);
+      const unsigned cost = s.tile == last ? p.last : px_full<D>(), item = p.blocks * cost;
+      s.h = (int)(r / item);
       r -= s.h * item;
-      const int64_t item0 = at - r, left = hi - item0;
+      const unsigned item0 = at - r, left = hi - item0;
       s.first = p.first;
-      s.rows = s.tile == p.tiles - 1 ? p.rows - s.tile * PxForm<D>::kRows : PxForm<D>::kRows;
+      s.rows = s.tile == last ? p.rows - last * PxForm<D>::kRows : PxForm<D>::kRows;
       s.item = (px_tile0<D>(a, g, p.first) + s.tile) * a.heads + s.h;
       s.b0 = (int)((r + cost - 1) / cost);
       s.b1 = left >= item ? p.blocks : (int)((left + cost - 1) / cost);
-      s.parts = s.b0 == 0 ? (int)(shares.owner(item0 + (int64_t)(p.blocks - 1) * cost) - blockIdx.x) + 1 : 0;
-      at = item0 + item < hi ? item0 + item : hi;
+      s.parts = s.b0 == 0 ? (int)(owner(item0 + (p.blocks - 1) * cost) - blockIdx.x) + 1 : 0;
+      at = left >= item ? item0 + item : hi;
       if (s.b0 < s.b1) return true;
     }
     s = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -549,8 +547,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           return vec ? __ldg(reinterpret_cast<const uint4 *>(qp + c)) : px_load8(qp + c);
         };
         uint32_t top = 0;
-#pragma unroll 8
-        for (int c = 0; c < D; c += 8) {
+#pragma unroll 16
+        for (int c = 0; c < D; c += 8) {  // (on their way together: the blocks' copies fill the queue to memory)
           const uint4 v = fetch(c);
           top = kv_max2(kv_max2(top, v.x & 0x7fff7fffu, DT), v.y & 0x7fff7fffu, DT);
           top = kv_max2(kv_max2(top, v.z & 0x7fff7fffu, DT), v.w & 0x7fff7fffu, DT);
@@ -757,85 +755,126 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
 
 // ------------------------------------------------------------------ join
 // A sequence's rows of a head: the parts of its own blocks and of its group's shared ones,
-// in that order; zeros where there are none.  A thread adds up four channels of a row, kGroups
-// threads share the parts of the same channels.  grid (S, items, pieces of a tile's rows)
+// in that order; zeros where there are none.  A thread adds up sixteen channels of a row (four
+// times four), kGroups threads share the parts of the same channels.  grid (S, items, pieces
+// of a tile's rows).  Bound by its chain of dependent reads (lengths, where the parts are,
+// parts): small CTAs, so that all are there at once, and several reads of a thread on their way.
+constexpr int kPxJoinThreads = 128;
 template <int D, int NT, int kGroups>
-__global__ void __launch_bounds__(kKvJoinThreads, 3) k_kv8_prefix_join(const KvArgs a, int ctas) {
-  constexpr int kAlong = kKvJoinThreads / kGroups;
+__global__ void __launch_bounds__(kPxJoinThreads) k_kv8_prefix_join(const KvArgs a, int ctas) {
+  constexpr int kAlong = kPxJoinThreads / kGroups, kStep = D / 16;  // threads along the channels and rows; quads between a thread's
   using F = PxForm<D>;
-  __shared__ KvSum sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kAlong : 1];
+  __shared__ float4 sums[kGroups > 1 ? kGroups - 1 : 1][4][kGroups > 1 ? kAlong : 1];
+  __shared__ float2 stats[kGroups > 1 ? kGroups - 1 : 1][kGroups > 1 ? kAlong : 1];
   pdl_trigger();
-  pdl_wait();
   const int s = blockIdx.x, item = blockIdx.y, items = a.heads * a.row_tiles;
+  // (lens, prefix and firsts are older than the kernel before, which let this one start after
+  // its own wait)
   const KvSeen seen = kv_seen<true>(a, s);
   const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * NT * 8;
   const int rows = a.T * a.group - row0 < NT * 8 ? a.T * a.group - row0 : NT * 8;
   const int64_t own_item = (int64_t)s * items + item;
-  // (a kernel whose wait ran out leaves its entries as the scratch memory had them: what is
-  // read stays within the partial results)
-  int4 of = seen.count > 0 ? __ldcg(&a.parts[own_item]) : make_int4(0, 0, 0, 0);
-  if (of.x < 0 || of.y < 0 || (int64_t)of.x + of.y > a.workers) of.y = 0;
-  const float *const own = a.ws + ((int64_t)of.x + own_item) * kv_part<D, NT>();
   const int along = threadIdx.x % kAlong, grp = threadIdx.x / kAlong;
   const int idx = blockIdx.z * kAlong + along, quad = idx / rows, r = idx - quad * rows;
-  const bool on = quad < D / 4;
+  const bool on = quad < kStep;
   // the row's place among those of its group
-  const float *px = nullptr;
-  int n_px = 0, sets = 1, rr = 0;
+  int px_item = 0, px_set = 0, rr = 0, sets = 0;
   if (seen.from > 0 && on) {
     const int g = kv_group_of(a, s);
     const KvGroup k = kv_group(a, g);
     const int of_seq = a.T * a.group, row = (s - k.first) * of_seq + row0 + r, tile = row / F::kRows;
     const bool both = F::kSets > 1 && (k.end - k.first) * of_seq - tile * F::kRows > 128;
-    const int px_item = (px_tile0<D>(a, g, k.first) + tile) * a.heads + h, in_tile = row - tile * F::kRows;
-    const int4 w = __ldcg(&a.px_parts[px_item]);
-    if (w.x >= 0 && w.y >= 0 && w.x + w.y <= ctas) {
-      sets = F::kSets > 1 && !both ? 2 : 1;
-      n_px = w.y * sets;
-      rr = in_tile % 128;
-      px = a.px_ws + ((int64_t)w.x + px_item) * (F::kSets * F::kPart) + (both ? in_tile / 128 * F::kPart : 0);
-    }
+    const int in_tile = row - tile * F::kRows;
+    px_item = (px_tile0<D>(a, g, k.first) + tile) * a.heads + h;
+    sets = F::kSets > 1 && !both ? 2 : 1;
+    px_set = both ? in_tile / 128 : 0;
+    rr = in_tile % 128;
   }
+  pdl_wait();  // by every CTA: the next kernel counts on it
+  // (a kernel whose wait ran out leaves its entries as the scratch memory had them: what is
+  // read stays within the partial results)
+  int4 of = make_int4(0, 0, 0, 0), w = of;
+  if (seen.count > 0) of = __ldcg(&a.parts[own_item]);
+  if (sets > 0) w = __ldcg(&a.px_parts[px_item]);
+  if (of.x < 0 || of.y < 0 || (int64_t)of.x + of.y > a.workers) of.y = 0;
+  if (w.x < 0 || w.y < 0 || (int64_t)w.x + w.y > ctas) w.y = 0;
+  const float *const own = a.ws + ((int64_t)of.x + own_item) * kv_part<D, NT>();
+  const float *const px = a.px_ws + ((int64_t)w.x + px_item) * (F::kSets * F::kPart) + px_set * F::kPart;
   // two sets of a CTA's part lie one behind the other, with one set it is the next CTA's
   const int64_t step = sets == 2 ? F::kPart : F::kSets * F::kPart;
-  KvSum sum;
-  if (on) {
-    const int total = of.y + n_px;
-    for (int i0 = grp; i0 < total; i0 += 8 * kGroups) {
-      float m[8], den[8];
-      float4 v[8];
+  float m = -INFINITY, den = 0.f;
+  float4 v[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+  for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float fm, float fden, const float4 (&f)[4]) {
+    if (fm == -INFINITY && fden == 0.f) return;  // (a set that had no block has no sums, either)
+    const float big = fmaxf(m, fm), z = big == -INFINITY ? 0.f : big, x = kv_exp2(m - z), y = kv_exp2(fm - z);
+    m = big;
+    den = den * x + fden * y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j].x = v[j].x * x + f[j].x * y;
+      v[j].y = v[j].y * x + f[j].y * y;
+      v[j].z = v[j].z * x + f[j].z * y;
+      v[j].w = v[j].w * x + f[j].w * y;
+    }
+  };
+  if (on) {
+    const int total = of.y + w.y * sets;
+    for (int i0 = grp; i0 < total; i0 += 2 * kGroups) {
+      float fm[2], fden[2];
+      float4 f[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         const int i = i0 + k * kGroups;
         if (i < total) {
           const bool mine = i < of.y;
           const float *q = mine ? own + (int64_t)i * kv_part<D, NT>() : px + (i - of.y) * step;
-          m[k] = __ldcg(q + (mine ? NT * 8 * D + r : 128 * D + rr));
-          den[k] = __ldcg(q + (mine ? NT * 8 * (D + 1) + r : 128 * (D + 1) + rr));
-          v[k] = __ldcg(reinterpret_cast<const float4 *>(q + (mine ? r * D + quad * 4 : (quad * 128 + rr) * 4)));
+          fm[k] = __ldcg(q + (mine ? NT * 8 * D + r : 128 * D + rr));
+          fden[k] = __ldcg(q + (mine ? NT * 8 * (D + 1) + r : 128 * (D + 1) + rr));
+          q += mine ? r * D + quad * 4 : (quad * 128 + rr) * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[k][j] = __ldcg(reinterpret_cast<const float4 *>(q + j * kStep * (mine ? 4 : 128 * 4)));
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        // (a set that had no block has no sums, either)
-        if (i0 + k * kGroups < total && !(m[k] == -INFINITY && den[k] == 0.f)) sum.add(m[k], den[k], v[k]);
+      for (int k = 0; k < 2; ++k)
+        if (i0 + k * kGroups < total) add(fm[k], fden[k], f[k]);
     }
   }
   if constexpr (kGroups > 1) {
-    sums[grp][along] = sum;
+    if (grp > 0) {
+      stats[grp - 1][along] = make_float2(m, den);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sums[grp - 1][j][along] = v[j];
+    }
     __syncthreads();
     if (grp > 0) return;
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) sum.add(sums[k][along].m, sums[k][along].den, sums[k][along].v);
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float4 f[4] = {sums[k][0][along], sums[k][1][along], sums[k][2][along], sums[k][3][along]};
+      add(stats[k][along].x, stats[k][along].y, f);
+    }
   }
   if (!on) return;
   const int64_t at_row = kv_out_row(a, s, h, row0 + r);
-  const float inv = sum.den == 0.f ? 0.f : kKvLifted * (1.f / sum.den);
+  const float inv = den == 0.f ? 0.f : kKvLifted * (1.f / den);
   unsigned short *out = reinterpret_cast<unsigned short *>(a.out) + at_row * D + quad * 4;
-  const float v[4] = {sum.v.x, sum.v.y, sum.v.z, sum.v.w};
+  const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) out[j] = f8_round16(v[j] * inv, a.dtype);
-  if (quad == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(sum.m, sum.den);
+  for (int j = 0; j < 4; ++j) {
+    const uint2 o = make_uint2(f8_pack16(v[j].x * inv, v[j].y * inv, a.dtype), f8_pack16(v[j].z * inv, v[j].w * inv, a.dtype));
+    unsigned short *p = out + j * kStep * 4;
+    if (vec) {
+      *reinterpret_cast<uint2 *>(p) = o;
+    } else {
+      p[0] = (unsigned short)o.x;
+      p[1] = (unsigned short)(o.x >> 16);
+      p[2] = (unsigned short)o.y;
+      p[3] = (unsigned short)(o.y >> 16);
+    }
+  }
+  if (quad == 0 && a.lse != nullptr) a.lse[at_row] = kv_lse(m, den);
 }
 
 }  // namespace gemv

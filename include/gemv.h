@@ -415,13 +415,13 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  * gemv_kv8_attention with the same arguments (up to rounding), and gemv_kv8_append writes
  * the new tokens as ever.  A sequence some of whose queries do not see all of the shared blocks
  * (lens[s] - T below them; an idle place of the batch with lens[s] == 0) is attended to by
- * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, and
- * GEMV_ERR_UNSUPPORTED for S x T x q_heads / heads above 2^30.  The shared values' sums, over
+ * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, to which the
+ * call is passed on where sharing does not pay (groups == 0, tables of up to four blocks, batches
+ * that it reads in less time) or where its work list would pass 2^31.  The shared values' sums, over
  * a share of the blocks each, are in units of the row's largest weight x value scale; the weights
  * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer
  * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and
- * 4 (dim + 2) bytes twice for each row of out.  Tables of up to four blocks, and groups == 0: the
- * call is passed on to gemv_kv8_attention. */
+ * 4 (dim + 2) bytes twice for each row of out. */
 gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
                                         const int32_t *lens, const int32_t *firsts, const int32_t *prefix, int groups, void *out,
                                         float *lse, int S, int T, int q_heads, float scale, gemv_stream_t stream);

@@ -158,4 +158,3 @@ def test_prefix_attention_refusals():
     for i in (0, 1, 2, 3, 4, 5, 6, 9, 10):
         assert prefixed(out=at(i)) == INVALID and prefixed(lse=at(i)) == INVALID
     assert prefixed(lse=at(7)) == INVALID
-    assert prefixed(S=1 << 22, T=64, heads=65534, q_stride=65534 * 128) == UNSUPPORTED   # rows of a group
