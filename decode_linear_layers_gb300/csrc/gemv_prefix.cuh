@@ -26,9 +26,9 @@ struct PxForm {
   static constexpr int kRows = 128 * kSets;
   static constexpr int kSoft = 4 * kSets, kConv = 4;                      // warps
   static constexpr int kWarps = kSoft + kConv + 3, kThreads = kWarps * 32;  // copies, the two products
-  static constexpr int kRaw = kKvBlock * D, kStage = 2 * kRaw;   // bytes of keys or values: as cached, as fp16
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // of keys, and of values
-  static constexpr int kSlots = D == 64 ? 16 : D == 128 ? 10 : D == 192 ? 8 : 5;
+  static constexpr int kRaw = kKvBlock * D, kStage = 2 * kRaw;   // bytes of a block's keys or values: as cached, as fp16
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;  // blocks as fp16
+  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 5 : D == 192 ? 4 : 2;  // blocks as cached
   // tensor memory columns: O of each set, S and P of each, Q
   static constexpr int kS = kSets * D, kQ = kS + kSets * 96;
   // with 128 channels the second set's Q finds no room there: it stays in shared memory (48 cycles
@@ -36,14 +36,14 @@ struct PxForm {
   static constexpr bool kQShared = D == 128;
   static_assert(kQ + (kQShared ? 1 : kSets) * D / 2 <= 512);
   static constexpr int kQBytes = kQShared ? 128 * D * 2 : 0;
-  static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kStage + kSlots * kRaw;
+  static constexpr int kSmem = 1024 + kQBytes + 2 * (kStages * kStage + kSlots * kRaw);
   // one CTA an SM (each takes all of the tensor memory)
   static_assert(kSmem > 114 * 1024 && kSmem <= 226 * 1024);
   // floats of a partial result's set: O as [D / 4][128 rows][4], largest logits, sums
   static constexpr int64_t kPart = 128 * (D + 2);
 };
 // Blocks whose scales are kept.  While the softmax is at block j, the converters are at
-// j + kStages + 1 at most, and the copies kSlots / 2 + 1 further on.
+// j + kStages + 1 at most, and the copies kSlots + 1 further on.
 constexpr int kPxMeta = 32;
 constexpr int kPxCost1 = 2, kPxCost2 = 3;  // places of a block: of an item of up to 128 rows, of more
 constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
@@ -250,9 +250,9 @@ template <int D, int DT>
 __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvArgs a) {
   using F = PxForm<D>;
   constexpr int R = F::kSlots, NS = F::kStages;
-  static_assert(NS + R / 2 + 2 < kPxMeta);
+  static_assert(NS + R + 3 < kPxMeta);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t rawf[R], rawe[R], kf[NS], ke[NS], vf[NS], ve[NS], qf[F::kSets], sf[F::kSets], sr[F::kSets], pf[F::kSets], of[F::kSets], gf[kPxSegs], ge[kPxSegs], fin;
+  __shared__ __align__(8) uint64_t rawf[R], rawe[R], wf[NS], we[NS], ql, qf[F::kSets], sf[F::kSets], sr[F::kSets], pf[F::kSets], of[F::kSets], gf[kPxSegs], ge[kPxSegs], fin;
   __shared__ PxSeg segs[kPxSegs];
   __shared__ float meta[kPxMeta][2];  // of a block: the keys' and the values' scale
   __shared__ int meta_bad[kPxMeta];
@@ -270,15 +270,14 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   }
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
-      tc_mbar_init(&rawf[i], 2);  // the piece, and with keys the block's scales
+      tc_mbar_init(&rawf[i], 2);  // keys and values, and the scales
       tc_mbar_init(&rawe[i], F::kConv);
     }
     for (int i = 0; i < NS; ++i) {
-      tc_mbar_init(&kf[i], F::kConv);
-      tc_mbar_init(&vf[i], F::kConv);
-      tc_mbar_init(&ke[i], F::kSets);
-      tc_mbar_init(&ve[i], F::kSets);
+      tc_mbar_init(&wf[i], F::kConv);
+      tc_mbar_init(&we[i], 2 * F::kSets);  // both products of each set
     }
+    tc_mbar_init(&ql, F::kSoft);
     for (int i = 0; i < F::kSets; ++i) {
       tc_mbar_init(&qf[i], 4);  // Q is there
       tc_mbar_init(&sf[i], 1);  // S is
@@ -305,8 +304,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   };
 
   bool ok = true;
-  int c0 = 0;     // blocks of the segments before
-  int piece = 0;  // of the ring of raw slots
+  int c0 = 0;  // blocks of the segments before; of the copies and the converters, so far
   int seg = 0;
   PxSeg s;
   auto take = [&]() {  // the next segment; false at the end
@@ -334,39 +332,31 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       __syncwarp();
       ++seg;
       int32_t entries = 0;
-      for (int b = s.b0; ok && b < s.b1; ++b) {
-        const int i = (b - s.b0) & 31;
+      for (int b = s.b0; ok && b < s.b1; ++b, ++c0) {
+        const int i = (b - s.b0) & 31, to = c0 % R, n = c0 % kPxMeta;
         if (i == 0) entries = b + lane < s.b1 ? __ldg(a.table + (int64_t)s.first * a.width + b + lane) : -1;
         const int32_t entry = __shfl_sync(0xffffffffu, entries, i);
         const bool good = entry >= 0 && entry < a.blocks;
         const int64_t unit = (good ? (int64_t)entry : 0) * a.heads + s.h;  // (of an entry that is no block: any, unseen)
-        const int n = (c0 + b - s.b0) % kPxMeta;
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          const int to = piece % R;
-          ok = piece < R || wait(&rawe[to], piece - R, R);
-          if (!ok) break;
-          if (f8_elect()) {
-            if (side == 0) {
-              meta_bad[n] = !good;
-              if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
-              f8_copy4(&meta[n][0], a.k_scale + unit, true);
-              f8_copy4(&meta[n][1], a.v_scale + unit, true);
-              f8_copy4_arrive(&rawf[to]);
-            } else {
-              tc_mbar_arrive(&rawf[to]);
-            }
-            if (!a.test_stall || side == 0) {  // test: no values ever come
-              tc_mbar_arrive_expect_tx(&rawf[to], F::kRaw);
-              kv_bulk(raw + (size_t)to * F::kRaw, (side == 0 ? a.k : a.v) + unit * F::kRaw, F::kRaw, &rawf[to]);
-            }
-          }
-          __syncwarp();
-          ++piece;
+        // the first queries' reads go before most of the first blocks': behind them all they take
+        // three times as long
+        if (c0 == 2) ok = wait(&ql, 0, 1);
+        ok = ok && (c0 < R || wait(&rawe[to], c0 - R, R));
+        if (!ok) break;
+        if (f8_elect()) {
+          meta_bad[n] = !good;
+          if (!good && a.status != nullptr) atomicOr(a.status, kKvStatusTable);
+          f8_copy4(&meta[n][0], a.k_scale + unit, true);
+          f8_copy4(&meta[n][1], a.v_scale + unit, true);
+          f8_copy4_arrive(&rawf[to]);
+          tc_mbar_arrive_expect_tx(&rawf[to], 2 * F::kRaw);
+          unsigned char *at = raw + (size_t)to * (2 * F::kRaw);
+          kv_bulk(at, a.k + unit * F::kRaw, F::kRaw, &rawf[to]);
+          if (!a.test_stall) kv_bulk(at + F::kRaw, a.v + unit * F::kRaw, F::kRaw, &rawf[to]);  // test: no values ever come
         }
+        __syncwarp();
       }
       if (!ok) break;
-      c0 += s.b1 - s.b0;
     }
     f8_copy4_drain();
   } else if (warp == kScores || warp == kSums) {  // ---- products
@@ -392,7 +382,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         const int nb = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)), n = both ? 2 * nb : nb;
         auto step = [&](auto set, bool first) {  // S of the set's next step, once it has read the last
           constexpr int x = decltype(set)::value;
-          if (!(both && x == 1)) ready(&kf[ix], iph);
+          if (!(both && x == 1)) ready(&wf[ix], iph);
           if (!first) {
             ready(&sr[x], ph[x]);
             ph[x] ^= 1;
@@ -413,8 +403,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
               px_mma(elected, d, q + k * 8, at + (k >> 2) * (kKvBlock * 128 >> 4) + (k & 3) * 2, id, k > 0);
           }
           px_commit(elected, &sf[x]);
-          px_commit(elected, &ke[ix]);
-          if (F::kSets > 1 && !both) px_commit(elected, &ke[ix]);  // (no other set needs the stage)
+          px_commit(elected, &we[ix]);
+          if (F::kSets > 1 && !both) px_commit(elected, &we[ix]);  // (no other set needs the stage)
           if (!both || x == 1) pass();
         };
         ready(&qf[0], qph[0]);
@@ -445,7 +435,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         const int nb = (int)__reduce_max_sync(kAll, (unsigned)(s.b1 - s.b0)), n = both ? 2 * nb : nb;
         auto step = [&](auto set, bool add) {  // P V of the set's step
           constexpr int x = decltype(set)::value;
-          if (!(both && x == 1)) ready(&vf[ix], iph);
+          if (!(both && x == 1)) ready(&wf[ix], iph);
           ready(&pf[x], ph[x]);
           if (!ok) return;
           ph[x] ^= 1;
@@ -455,8 +445,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
 #pragma unroll
           for (int k = 0; k < kKvBlock / 16; ++k) px_mma(elected, d, w + k * 8, at + k * 2, id, k > 0 || add);
           px_commit(elected, &of[x]);
-          px_commit(elected, &ve[ix]);
-          if (F::kSets > 1 && !both) px_commit(elected, &ve[ix]);
+          px_commit(elected, &we[ix]);
+          if (F::kSets > 1 && !both) px_commit(elected, &we[ix]);
           if (!both || x == 1) pass();
         };
         for (int i = 0; i < n && ok; i += F::kSets) {
@@ -474,43 +464,39 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       *reinterpret_cast<uint4 *>(row + (((chunk + (swap ? 1 : 0)) ^ turn) * 16)) = swap ? hi : lo;
       *reinterpret_cast<uint4 *>(row + (((chunk + (swap ? 0 : 1)) ^ turn) * 16)) = swap ? lo : hi;
     };
-    auto hand_on = [&](uint64_t *full) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        tc_mbar_arrive(full);
-        tc_mbar_arrive(&rawe[piece % R]);
-      }
-      ++piece;
-    };
-    constexpr int kPer = kKvBlock * D / 16 / (F::kConv * 32);  // 16-byte pieces of a thread
+    constexpr int kPer = kKvBlock * D / 16 / (F::kConv * 32);  // 16-byte pieces of a thread, of keys and of values
+    constexpr int kBoth = D <= 128 ? 2 * kPer : kPer;          // of which the registers hold so many at a time
     while (take()) {
       for (int b = s.b0; b < s.b1; ++b, ++c0) {
-        const int st = c0 % NS;
-        ok = wait(&rawf[piece % R], piece, R) && (c0 < NS || wait(&ke[st], c0 - NS, NS));
+        const int st = c0 % NS, at = c0 % R;
+        ok = wait(&rawf[at], c0, R) && (c0 < NS || wait(&we[st], c0 - NS, NS));
         if (!ok) break;
         const bool bad = meta_bad[c0 % kPxMeta] != 0;
-        uint4 x[kPer];
-        const uint4 *from = reinterpret_cast<const uint4 *>(raw + (size_t)(piece % R) * F::kRaw) + ct;
+        const uint4 *from = reinterpret_cast<const uint4 *>(raw + (size_t)at * (2 * F::kRaw)) + ct;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = from[i * F::kConv * 32];
+        for (int i0 = 0; i0 < 2 * kPer; i0 += kBoth) {
+          uint4 x[kBoth];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int p = i * F::kConv * 32 + ct, tok = p / (D / 16), cp = p - tok * (D / 16);
-          widen(x[i], kst + st * F::kStage + (cp >> 2) * (kKvBlock * 128) + tok * 128, (cp & 3) * 2, tok & 7, (cp >> 2) & 1);
+          for (int i = 0; i < kBoth; ++i) x[i] = from[(i0 + i) * F::kConv * 32];  // (the values follow the keys)
+#pragma unroll
+          for (int i = 0; i < kBoth; ++i) {
+            const int p = (i0 + i) % kPer * F::kConv * 32 + ct;
+            if (i0 + i < kPer) {
+              const int tok = p / (D / 16), cp = p - tok * (D / 16);
+              widen(x[i], kst + st * F::kStage + (cp >> 2) * (kKvBlock * 128) + tok * 128, (cp & 3) * 2, tok & 7, (cp >> 2) & 1);
+            } else {
+              const int d = p >> 2;
+              if (bad) x[i] = make_uint4(0, 0, 0, 0);
+              widen(x[i], vst + st * F::kStage + d * 128, (p & 3) * 2, d & 7, false);
+            }
+          }
         }
-        hand_on(&kf[st]);
-        ok = wait(&rawf[piece % R], piece, R) && (c0 < NS || wait(&ve[st], c0 - NS, NS));
-        if (!ok) break;
-        from = reinterpret_cast<const uint4 *>(raw + (size_t)(piece % R) * F::kRaw) + ct;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = bad ? make_uint4(0, 0, 0, 0) : from[i * F::kConv * 32];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int p = i * F::kConv * 32 + ct, d = p >> 2;
-          widen(x[i], vst + st * F::kStage + d * 128, (p & 3) * 2, d & 7, false);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          tc_mbar_arrive(&wf[st]);
+          tc_mbar_arrive(&rawe[at]);
         }
-        hand_on(&vf[st]);
       }
     }
   } else if (warp < F::kSoft) {  // ---- softmax
@@ -528,6 +514,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       float *part = a.px_ws + ((int64_t)blockIdx.x + s.item) * (F::kSets * F::kPart) + x * F::kPart;
       if (s.parts > 0 && tid == 0) a.px_parts[s.item] = make_int4((int)blockIdx.x, s.parts, 0, 0);
       if (F::kSets > 1 && x >= n) {  // a single block, the other set's
+        if (c0 == 0 && lane == 0) tc_mbar_arrive(&ql);
         part[128 * D + in_tile] = -INFINITY;
         part[128 * (D + 1) + in_tile] = 0.f;
         c0 += nb;
@@ -542,49 +529,83 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         const unsigned short *qp = reinterpret_cast<const unsigned short *>(a.q) + ((int64_t)sq * a.T + t) * a.q_stride +
                                    ((int64_t)s.h * a.group + rt - t * a.group) * D;
         const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_stride % 8 == 0;
-        auto fetch = [&](int c) {  // channels c .. c + 7
-          if (!alive) return make_uint4(0, 0, 0, 0);
-          return vec ? __ldg(reinterpret_cast<const uint4 *>(qp + c)) : px_load8(qp + c);
-        };
         uint32_t top = 0;
-#pragma unroll 16
-        for (int c = 0; c < D; c += 8) {  // (on their way together: the blocks' copies fill the queue to memory)
-          const uint4 v = fetch(c);
+        auto larger = [&](const uint4 &v) {
           top = kv_max2(kv_max2(top, v.x & 0x7fff7fffu, DT), v.y & 0x7fff7fffu, DT);
           top = kv_max2(kv_max2(top, v.z & 0x7fff7fffu, DT), v.w & 0x7fff7fffu, DT);
-        }
-        const float mx = fmaxf(kv_wide_lo(top, DT), kv_wide_hi(top, DT));
-        int e = (__float_as_int(mx) >> 23) & 0xff;  // (an infinity takes the largest exponent)
-        e = e < 16 ? 16 : e;
-        float up = __int_as_float((127 + 14 + 127 - e) << 23);
-        f = fabsf(a.scale_log2) / up;
-        if (a.scale_log2 < 0.f) up = -up;
-        if (both || x == 0) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {  // (short code: it runs once, and its lines have to come first)
-            uint32_t u[16];
+        };
+        float up = 0.f;
+        auto factors = [&]() {
+          const float mx = fmaxf(kv_wide_lo(top, DT), kv_wide_hi(top, DT));
+          int e = (__float_as_int(mx) >> 23) & 0xff;  // (an infinity takes the largest exponent)
+          e = e < 16 ? 16 : e;
+          up = __int_as_float((127 + 14 + 127 - e) << 23);
+          f = fabsf(a.scale_log2) / up;
+          if (a.scale_log2 < 0.f) up = -up;
+        };
+        auto put = [&](int c, const uint4 (&v)[4]) {  // channels c .. c + 31
+          uint32_t u[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 v = fetch(c + 8 * j);
-              u[4 * j] = v.x;
-              u[4 * j + 1] = v.y;
-              u[4 * j + 2] = v.z;
-              u[4 * j + 3] = v.w;
-            }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) u[j] = kv_pack_half(kv_wide_lo(u[j], DT) * up, kv_wide_hi(u[j], DT) * up);
-            if (F::kQShared && x == 1) {
+            for (int i = 0; i < 4; ++i) u[4 * j + i] = kv_pack_half(kv_wide_lo(w[i], DT) * up, kv_wide_hi(w[i], DT) * up);
+          }
+          if (F::kQShared && x == 1) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4 *>(qst + c / 64 * (128 * 128) + in_tile * 128 + ((((c / 8 + j) & 7) ^ (in_tile & 7)) * 16)) =
-                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-            } else {
-              px_st16(mine + F::kQ + x * (D / 2) + c / 2, u);
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4 *>(qst + c / 64 * (128 * 128) + in_tile * 128 + ((((c / 8 + j) & 7) ^ (in_tile & 7)) * 16)) =
+                  make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+          } else {
+            px_st16(mine + F::kQ + x * (D / 2) + c / 2, u);
+          }
+        };
+        constexpr int kHeld = D <= 128 ? D : 0;  // channels of a row that the registers hold
+        uint4 v[kHeld > 0 ? kHeld / 8 : 4];
+        if (kHeld > 0 && vec) {
+#pragma unroll
+          for (int j = 0; j < kHeld / 8; ++j)
+            v[j] = alive ? __ldg(reinterpret_cast<const uint4 *>(qp) + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < kHeld / 8; ++j) larger(v[j]);
+          if (c0 == 0) {
+            __syncwarp();
+            if (lane == 0) tc_mbar_arrive(&ql);
+          }
+          factors();
+          if (both || x == 0) {
+#pragma unroll
+            for (int j = 0; j < kHeld / 8; j += 4) {
+              const uint4 w[4] = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+              put(8 * j, w);
             }
           }
+        } else {  // wide heads, rows that start anywhere: read twice
+          auto fetch = [&](int c) {
+            if (!alive) return make_uint4(0, 0, 0, 0);
+            return vec ? __ldg(reinterpret_cast<const uint4 *>(qp + c)) : px_load8(qp + c);
+          };
+#pragma unroll 8
+          for (int c = 0; c < D; c += 8) larger(fetch(c));
+          if (c0 == 0) {
+            __syncwarp();
+            if (lane == 0) tc_mbar_arrive(&ql);
+          }
+          factors();
+          if (both || x == 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              const uint4 w[4] = {fetch(c), fetch(c + 8), fetch(c + 16), fetch(c + 24)};
+              put(c, w);
+            }
+          }
+        }
+        if (both || x == 0) {
           px_st_wait();
           if (F::kQShared && x == 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+      } else if (c0 == 0 && lane == 0) {
+        tc_mbar_arrive(&ql);
       }
       px_fence_before();
       __syncwarp();
@@ -740,7 +761,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     }
     if (warp == kLoad) {
       bool drained = true;
-      for (int i = piece > R ? piece - R : 0; i < piece; ++i)
+      for (int i = c0 > R ? c0 - R : 0; i < c0; ++i)
         if (!tc_mbar_wait(&rawf[i % R], (uint32_t)(i / R) & 1u, a.timeout_ns)) drained = false;
       if (!drained && lane == 0 && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
     }
