@@ -423,7 +423,7 @@ __device__ __forceinline__ int kv_shared(const KvArgs &a, int s, int len) {
   const int g = kv_group_of(a, s);
   if (g < 0) return 0;
   const int n = kv_group(a, g).blocks;
-  return len - a.T >= n * kKvBlock ? n : 0;
+  return (int64_t)len - a.T >= (int64_t)n * kKvBlock ? n : 0;
 }
 template <bool kOwn = false>
 __device__ __forceinline__ KvSeen kv_seen(const KvArgs &a, int s) {

@@ -11,8 +11,18 @@
 namespace gemv {
 namespace {
 
-// Tables of at most so many blocks: gemv_kv8_attention, one launch.
-constexpr int kPxWhole = 4;
+// Where sharing pays: three launches and the time to fill the tensor cores against reading
+// every sequence's tokens apart, which takes some 9 us and 0.1 us for each MB of them and
+// eight query rows that meet them (the tables' width is what the host knows of the lengths).
+// us, apart / shared, 8 heads of 128 channels, 4 query heads each: 32 sequences behind 2048
+// tokens (142 MB) 24 / 37, 64 behind 2048 (285) 40 / 33, 8 behind 8192 (136) 23 / 39, 8 behind
+// 32768 (538) 65 / 54; 16 queries each (eight times eight rows), 2 behind 2048 (9 x 8) 20 / 39, 8
+// behind 2048 (36 x 8) 36 / 37, 32 behind 512 (42 x 8) 57 / 44; 256 channels: 8 behind 8192
+// (272) 46 / 43, 32 behind 2048 (285) 50 / 48.
+bool px_pays(int64_t S, int64_t width, int64_t heads, int64_t dim, int64_t rows) {
+  const double mb = (double)S * (double)width * kKvBlock * (double)heads * (double)dim * 2e-6;
+  return mb * (double)((rows + 7) / 8) > (dim <= 128 ? 230.0 : 300.0);
+}
 
 template <int D, int NT>
 gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
@@ -87,10 +97,11 @@ gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache
   if (cache->heads == 0 || q_heads % cache->heads != 0 || q_heads > 65535) return GEMV_ERR_INVALID_VALUE;
   if (groups > S || (firsts == nullptr && groups > 1) || (groups > 0 && prefix == nullptr)) return GEMV_ERR_INVALID_VALUE;
   const int64_t row = (int64_t)q_heads * cache->dim, tokens = (int64_t)S * T;
-  // places of the work list and rows of a group are counted in 31 bits
-  const int64_t most = (tokens * (q_heads / cache->heads) / 128 + groups) * cache->heads * kPxCost2;
-  const bool pass_on = groups == 0 || cache->width <= kPxWhole || most > 0x7fffffff / cache->width ||
-                       tokens * (q_heads / cache->heads) > (1 << 30);
+  // (places of the work list and rows of a group are counted in 31 bits)
+  const int64_t rows = (int64_t)T * (q_heads / cache->heads);
+  const int64_t most = (S * rows / 128 + groups) * cache->heads * kPxCost2;
+  const bool pass_on = groups == 0 || !px_pays(S, cache->width, cache->heads, cache->dim, rows) ||
+                       most > 0x7fffffff / cache->width || S * rows > (1 << 30);
   if (q_stride < row) return GEMV_ERR_INVALID_VALUE;
   int64_t qb, ob;
   if (!span(tokens, row, q_stride, 2, &qb) || !mul_ok(tokens, row * 2, &ob)) return GEMV_ERR_INVALID_VALUE;
@@ -127,7 +138,6 @@ gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache
   a.scale_log2 = scale * 1.44269504088896f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // rows of queries of one sequence that meet a block of its own at once, as in gemv_kv8_attention
-  const int rows = T * a.group;
   switch (cache->dim) {
     case 64:
       return rows <= 8 ? attend<64, 1>(a, sms, s) : rows <= 16 ? attend<64, 2>(a, sms, s)

@@ -58,16 +58,35 @@ constexpr float kPxLift = 8.f, kPxSlack = 7.f;
 // the code to come.)
 struct PxGroup {
   int first, blocks, rows, tiles;
+  int leader;              // the first sequence that shares the blocks: they are taken from its table
   unsigned last, places;  // places of a block in the last tile; of the group
 };
 template <int D>
 __host__ __device__ constexpr unsigned px_full() { return PxForm<D>::kRows > 128 ? kPxCost2 : kPxCost1; }  // in a whole tile
-template <int D>
-__device__ __forceinline__ PxGroup px_group(const KvArgs &a, int g) {
+// kWarp: by a converged warp for one group, else by each lane for a group of its own.
+template <int D, bool kWarp>
+__device__ __forceinline__ PxGroup px_group(const KvArgs &a, int g, int lane) {
   PxGroup p;
   const KvGroup k = kv_group(a, g);
   p.first = k.first;
   p.blocks = k.blocks;
+  p.leader = k.end;
+  const int need = k.blocks * kKvBlock + a.T;  // (a length beyond the table counts as the table's size)
+  if (k.blocks > 0 && (int64_t)need <= (int64_t)a.width * kKvBlock) {
+    if constexpr (kWarp) {
+      for (int s = k.first; s < k.end; s += 32) {
+        const unsigned sees = __ballot_sync(0xffffffffu, s + lane < k.end && __ldg(a.lens + s + lane) >= need);
+        if (sees != 0) {
+          p.leader = s + __ffs(sees) - 1;
+          break;
+        }
+      }
+    } else {
+      for (int s = k.first; s < k.end && p.leader == k.end; ++s)
+        if (__ldg(a.lens + s) >= need) p.leader = s;
+    }
+  }
+  if (p.leader == k.end) p.blocks = 0;  // no one shares them
   p.rows = (k.end - k.first) * a.T * a.group;
   constexpr int R = PxForm<D>::kRows;
   p.tiles = (p.rows + R - 1) / R;
@@ -87,6 +106,7 @@ struct PxSeg {
   int b0, b1;       // its blocks; none: the share's end
   int rows;         // of the tile
   int first;        // the group's first sequence
+  int table;        // the sequence whose table has the blocks
   int item;         // (tile's number) x heads + head
   int parts;        // with the item's first blocks: CTAs that have some of it; else 0
 };
@@ -103,10 +123,10 @@ struct PxWalk {
     return u < longer ? u / (each + 1) : more + (u - longer) / each;
   }
   __device__ void begin(const KvArgs &a, int lane) {  // one warp, converged
-    p = px_group<D>(a, 0);
+    p = px_group<D, true>(a, 0, lane);
     unsigned total = p.places;
     for (int g0 = 1; g0 < a.groups; g0 += 32)
-      total += __reduce_add_sync(0xffffffffu, g0 + lane < a.groups ? px_group<D>(a, g0 + lane).places : 0u);
+      total += __reduce_add_sync(0xffffffffu, g0 + lane < a.groups ? px_group<D, false>(a, g0 + lane, lane).places : 0u);
     unsigned W = total / (kPxLeast * kPxCost2);
     W = W < 1 ? 1 : W < gridDim.x ? W : gridDim.x;
     each = total / W;
@@ -117,11 +137,11 @@ struct PxWalk {
     g = 0;
     base = 0;
   }
-  __device__ bool next(const KvArgs &a, PxSeg &s) {
+  __device__ bool next(const KvArgs &a, int lane, PxSeg &s) {
     while (at < hi) {
       if (at - base >= p.places) {
         base += p.places;
-        p = px_group<D>(a, ++g);
+        p = px_group<D, true>(a, ++g, lane);
         continue;
       }
       unsigned r = at - base;
@@ -135,6 +155,7 @@ struct PxWalk {
       r -= s.h * item;
       const unsigned item0 = at - r, left = hi - item0;
       s.first = p.first;
+      s.table = p.leader;
       s.rows = s.tile == last ? p.rows - last * PxForm<D>::kRows : PxForm<D>::kRows;
       s.item = (px_tile0<D>(a, g, p.first) + s.tile) * a.heads + s.h;
       s.b0 = (int)((r + cost - 1) / cost);
@@ -143,7 +164,7 @@ struct PxWalk {
       at = left >= item ? item0 + item : hi;
       if (s.b0 < s.b1) return true;
     }
-    s = {0, 0, 0, 0, 0, 0, 0, 0};
+    s = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     return false;
   }
 };
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
     PxWalk<D> walk;
     walk.begin(a, lane);
     for (bool more = true; more;) {
-      more = walk.next(a, s);
+      more = walk.next(a, lane, s);
       const int at = seg % kPxSegs;
       ok = seg < kPxSegs || wait(&ge[at], seg - kPxSegs, kPxSegs);
       if (!ok) break;
@@ -334,7 +355,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       int32_t entries = 0;
       for (int b = s.b0; ok && b < s.b1; ++b, ++c0) {
         const int i = (b - s.b0) & 31, to = c0 % R, n = c0 % kPxMeta;
-        if (i == 0) entries = b + lane < s.b1 ? __ldg(a.table + (int64_t)s.first * a.width + b + lane) : -1;
+        if (i == 0) entries = b + lane < s.b1 ? __ldg(a.table + (int64_t)s.table * a.width + b + lane) : -1;
         const int32_t entry = __shfl_sync(0xffffffffu, entries, i);
         const bool good = entry >= 0 && entry < a.blocks;
         const int64_t unit = (good ? (int64_t)entry : 0) * a.heads + s.h;  // (of an entry that is no block: any, unseen)

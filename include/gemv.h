@@ -409,15 +409,15 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  *            (groups + 1 values, rising; those in no group share nothing); firsts == NULL:
  *            one group has them all
  *   prefix   groups values: tokens that the group's sequences have in common.  The whole
- *            blocks of GEMV_KV8_BLOCK among them are taken from the table of the group's first
- *            sequence, once for the group; what is left of them, from each sequence's own
+ *            blocks of GEMV_KV8_BLOCK among them are taken from the table of one of the group's
+ *            sequences, once for the group; what is left of them, from each sequence's own
  * lens[s] counts all tokens of sequence s, the prefix among them: out and lse are those of
  * gemv_kv8_attention with the same arguments (up to rounding), and gemv_kv8_append writes
  * the new tokens as ever.  A sequence some of whose queries do not see all of the shared blocks
  * (lens[s] - T below them; an idle place of the batch with lens[s] == 0) is attended to by
  * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, to which the
- * call is passed on where sharing does not pay (groups == 0, tables of up to four blocks, batches
- * that it reads in less time) or where its work list would pass 2^31.  The shared values' sums, over
+ * call is passed on where sharing does not pay (groups == 0, and S x width x heads x dim, times
+ * T x q_heads / heads, too small) or where its work list would pass 2^31.  The shared values' sums, over
  * a share of the blocks each, are in units of the row's largest weight x value scale; the weights
  * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer
  * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and

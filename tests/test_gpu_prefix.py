@@ -29,15 +29,19 @@ def _clean():
 
 
 class Shared(Cache):
-    """Sequences of which those of a group begin with the same blocks."""
+    """Sequences of which those of a group begin with the same blocks.  The table is wide
+    enough for the blocks to be shared (short ones are passed on to gemv_kv8_attention);
+    entries behind a sequence's own are -1."""
 
     def __init__(self, firsts, prefix, lens, heads, dim, seed, width=None):
+        if width is None:
+            width = 1 + max([320_000_000 // (len(lens) * BLOCK * heads * dim * 2)] + [-(-n // BLOCK) for n in lens])
         super().__init__(lens, heads, dim, seed, width)
         for i, p in enumerate(prefix):
             n = min(max(p, 0) // BLOCK, self.width)
-            for s in range(firsts[i], firsts[i + 1]):
-                if lens[s] >= n * BLOCK:
-                    self.table[s, :n] = self.table[firsts[i], :n]
+            long = [s for s in range(firsts[i], firsts[i + 1]) if lens[s] >= n * BLOCK]
+            for s in long:
+                self.table[s, :n] = self.table[long[0], :n]
         self.firsts = torch.tensor(firsts, dtype=torch.int32, device="cuda")
         self.prefix = torch.tensor(prefix, dtype=torch.int32, device="cuda")
 
@@ -128,8 +132,9 @@ def test_rows_of_one_and_more_tiles(S, T, group, dim):
 @pytest.mark.parametrize("prefix", [0, -5, 1, 63, 64, 65, 127, 128, 320, 321, 1000000])
 def test_prefix_lengths(prefix):
     lens = [prefix + 20 + i if 0 < prefix < 1000 else 400 + i for i in range(4)]
-    c = Shared([0, 4], [prefix], lens, 2, 128, seed=41, width=7).fill(42)
-    check(c, queries(c, 2, 4, 43), firsts=False)
+    for width in (None, 7):
+        c = Shared([0, 4], [prefix], lens, 2, 128, seed=41, width=width).fill(42)
+        check(c, queries(c, 2, 4, 43), firsts=False)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
@@ -140,6 +145,25 @@ def test_groups(dim):
     lens = [333, 302, 1003, 1100, 0, 960 + 2, 960 + 1, 50, 1024, 66, 65, 64, 0, 600, 40, 0]
     c = Shared(firsts, prefix, lens, 2, dim, seed=44 + dim).fill(45)
     check(c, queries(c, 2, 3, 46, torch.float16))
+    assert g.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("idle", [1, 5, 40])
+def test_idle_places_before_the_others(idle):
+    # the first places of a group are idle, and what their tables hold is no block
+    P = 1000
+    lens = [0] * idle + [P + 9, P + 80, P + 2] + [0] * idle + [P + 30]
+    n = idle + 3
+    c = Shared([0, n, 2 * idle + 4], [P, P], lens, 2, 128, seed=110).fill(111)
+    c.table[:idle] = c.pool + 5
+    c.table[n:n + idle] = -7
+    check(c, queries(c, 1, 4, 112))
+    assert g.device_status() == (0, 0)
+
+
+def test_no_one_shares():
+    c = Shared([0, 4], [100000], [300, 70, 0, 641], 2, 128, seed=113).fill(114)
+    check(c, queries(c, 3, 4, 115))
     assert g.device_status() == (0, 0)
 
 
@@ -282,21 +306,25 @@ def test_blocks_outside_the_pool():
     assert g.device_status() == (g.ERR_INVALID_VALUE, 64)
 
 
-def test_short_tables_are_passed_on():
-    c = Shared([0, 3], [128], [130, 200, 256], 2, 128, seed=89, width=4).fill(90)
-    n = g.launch_count()
-    check(c, queries(c, 1, 4, 91), again=False)
-    assert g.launch_count() - n == 1
-    c = Shared([0, 3], [128], [130, 200, 300], 2, 128, seed=92).fill(93)
-    n = g.launch_count()
-    check(c, queries(c, 1, 4, 94), again=False)
-    assert g.launch_count() - n == 3
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_what_is_passed_on(dim):
+    # the same results to rounding, from gemv_kv8_attention's kernels or from the shared ones
+    lens = [700, 800, 701]
+    narrow = Shared([0, 3], [640], lens, 2, dim, seed=89, width=13).fill(90)
+    wide = Shared([0, 3], [640], lens, 2, dim, seed=89).fill(90)
+    q = queries(narrow, 1, 4, 91)
+    for c, launches in ((narrow, 2), (wide, 3)):
+        n = g.launch_count()
+        call(c, q, 0.1)
+        assert g.launch_count() - n == launches
+        check(c, q)
 
 
 def test_lengths_beyond_the_table():
     c = Shared([0, 3], [640], [704, 704, 700], 2, 128, seed=95).fill(96)
-    c.lens[0] = 5000        # counts as the table's size
+    c.lens[0] = 64 * c.width + 5000        # counts as the table's size
     check(c, queries(c, 1, 4, 97), again=False)
+    assert g.device_status() == (g.ERR_INVALID_VALUE, 64)      # its table has no blocks there
 
 
 def test_alone_and_in_a_group_of_other_size():
@@ -307,7 +335,8 @@ def test_alone_and_in_a_group_of_other_size():
     check(c, q)
     for n in (1, 3):
         d = Shared([0, n], [P], [P + 5 + i for i in range(n)], 2, 128, seed=98)
-        d.k, d.v, d.ks, d.vs, d.table, d.pool = c.k, c.v, c.ks, c.vs, c.table[:n].contiguous(), c.pool
+        d.k, d.v, d.ks, d.vs, d.pool = c.k, c.v, c.ks, c.vs, c.pool
+        d.table[:, :20] = c.table[:n, :20]
         check(d, q[:n])
 
 
