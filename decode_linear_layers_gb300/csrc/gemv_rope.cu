@@ -77,6 +77,28 @@ __device__ __forceinline__ void rope_turn(float f, int32_t pos, float &c, float 
   sincospif((float)x * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
 }
 
+// Two fp32 values as one operand, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t rope_two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 rope_apart(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t rope_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t rope_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Eight values: loads that may be of what the kernel writes later (in place), stores.
 template <int DT>
 struct RopeRaw : F8Raw<DT> {
@@ -94,14 +116,15 @@ struct RopeRaw : F8Raw<DT> {
   }
 };
 template <int DT>
-__device__ __forceinline__ void rope_store8(void *p, int64_t i, const float *v) {
+__device__ __forceinline__ void rope_store8(void *p, int64_t i, const uint64_t (&o)[4]) {
+  const float2 a = rope_apart(o[0]), b = rope_apart(o[1]), c = rope_apart(o[2]), d = rope_apart(o[3]);
   if constexpr (DT == GEMV_DTYPE_F32) {
     float4 *q = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = make_float4(a.x, a.y, b.x, b.y);
+    q[1] = make_float4(c.x, c.y, d.x, d.y);
   } else {
     *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned short *>(p) + i) =
-        make_uint4(f8_pack16(v[0], v[1], DT), f8_pack16(v[2], v[3], DT), f8_pack16(v[4], v[5], DT), f8_pack16(v[6], v[7], DT));
+        make_uint4(f8_pack16(a.x, a.y, DT), f8_pack16(b.x, b.y, DT), f8_pack16(c.x, c.y, DT), f8_pack16(d.x, d.y, DT));
   }
 }
 
@@ -109,11 +132,15 @@ __device__ __forceinline__ void rope_store8(void *p, int64_t i, const float *v) 
 // its eight pairs lie (the eight channels of the first half and those rot / 2 further on;
 // or sixteen neighbours; behind the rotated channels sixteen others).  A warp takes
 // 32 / P heads of a row at a time, `per` times; its lanes work out the row's cosines
-// once, a few pairs each, and keep those of their own pairs in registers over the heads.
-// Bound by the bytes, in and out once each; a single token by its chain of dependent
-// reads (starts, lens, frequencies beside the heads).
-template <int DT, int P>
-__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a) {
+// once, a few pairs each, and keep those of their own pairs, times the weights, in registers
+// over the heads: an output is 1 / rms times a sum of two products, packed two by two.
+// Bound by the bytes, in and out once each, and by instructions (15 k tokens of 40 heads of
+// 128, us with weights and cosines apart / multiplied ahead and packed: 62 / 47, three CTAs an SM; with two
+// and two or three turns' reads on their way 49, 47); a single
+// token by its chain of dependent reads (starts, lens, frequencies beside the heads).
+// kFull: every channel turns.
+template <int DT, int P, bool kInter, bool kFull>
+__global__ void __launch_bounds__(kRopeThreads, 3) k_qk_norm_rope(const RopeArgs a) {
   constexpr int kHeads = 32 / P;                        // of a turn
   constexpr int kMine = kHeads >= 8 ? 1 : 8 / kHeads;   // cosines that a lane works out
   pdl_trigger();
@@ -128,25 +155,23 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a)
 
   const int half = a.rot / 2;
   const bool turned = 8 * u < half;  // this lane has rotated pairs
-  const int c0 = a.inter ? 16 * u : turned ? 8 * u : a.rot + (8 * u - half) * 2;
-  const int c1 = a.inter || !turned ? c0 + 8 : c0 + half;
+  const int c0 = kInter ? 16 * u : turned ? 8 * u : a.rot + (8 * u - half) * 2;
+  const int c1 = kInter || !turned ? c0 + 8 : c0 + half;
   const bool has0 = c0 < a.dim, has1 = c1 < a.dim;
 
-  RopeRaw<DT> next[2];
-  int which = 0;
-  int64_t head = 0;
-  auto begin = [&](int t) {  // the reads of a turn
-    const int h = t * kHeads + grp;
-    which = h < a.heads[0] ? 0 : 1;
-    head = (int64_t)(h - (which ? a.heads[0] : 0)) * a.dim;
-    next[0].zero();
-    next[1].zero();
-    if (h < all) {
-      if (has0) next[0].fetch(a.x[which], row * a.xs[which] + head + c0);
-      if (has1) next[1].fetch(a.x[which], row * a.xs[which] + head + c1);
+  RopeRaw<DT> next[2];  // the next turn's values, on their way
+  auto side = [&](int t) { return t * kHeads + grp < a.heads[0] ? 0 : 1; };  // queries, keys
+  auto start = [&](int t) { return (int64_t)(t * kHeads + grp - (side(t) ? a.heads[0] : 0)) * a.dim; };
+  auto begin = [&](int t, RopeRaw<DT> (&x)[2]) {  // the reads of a turn
+    x[0].zero();
+    x[1].zero();
+    if (t < end && t * kHeads + grp < all) {
+      const int64_t from = row * a.xs[side(t)] + start(t);
+      if (has0) x[0].fetch(a.x[side(t)], from + c0);
+      if (has1) x[1].fetch(a.x[side(t)], from + c1);
     }
   };
-  if (turn < end) begin(turn);
+  begin(turn, next);
 
   int32_t pos = 0;
   if (!rope_position(a, row, lane, pos)) return;
@@ -171,65 +196,84 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a)
     }
   }
 
-  F8Raw<DT> w[2];
-  int have = -1;  // whose weights the lane holds
+  // Of two channels at a time (x, y): their own factors, and those of their partners.  Half: the
+  // neighbours j, j + 1 of the first piece and of the second; else a pair.
+  uint64_t own[8], other[8];
+  int have = -1;  // whose weights are in them
   for (; turn < end; ++turn) {
-    RopeRaw<DT> x[2] = {next[0], next[1]};
-    const int k = which;
-    const int64_t at = row * a.ys[k] + head;
+    const int k = side(turn);
+    const int64_t at = row * a.ys[k] + start(turn);
     const bool on = turn * kHeads + grp < all;
-    if (turn + 1 < end) begin(turn + 1);
-    float v[16];
+    if (have != k) {
+      have = k;
+      F8Raw<DT> w[2];
+      const bool weighs = a.w[k] != nullptr;
+      w[0].zero();
+      w[1].zero();
+      if (weighs && has0) w[0].load(a.w[k], c0);
+      if (weighs && has1) w[1].load(a.w[k], c1);
+      auto weight = [&](int c) { return weighs ? w[c / 8].get(c % 8) : 1.f; };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = x[0].get(j);
-      v[8 + j] = x[1].get(j);
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (kInter) {
+          const float wa = weight(2 * j), wb = weight(2 * j + 1);
+          own[j] = rope_two(wa * cs[j], wb * cs[j]);
+          other[j] = rope_two(-wb * sn[j], wa * sn[j]);
+        } else {
+          const int i = 2 * j % 8;  // j < 4: channels i, i + 1 of the first piece, else of the second
+          const float x = weight(2 * j), y = weight(2 * j + 1), px = weight((2 * j + 8) % 16), py = weight((2 * j + 9) % 16);
+          own[j] = rope_two(x * cs[i], y * cs[i + 1]);
+          other[j] = j < 4 ? rope_two(-px * sn[i], -py * sn[i + 1]) : rope_two(px * sn[i], py * sn[i + 1]);
+        }
+      }
     }
-    if (a.w[0] != nullptr || a.w[1] != nullptr) {  // (the same for all lanes)
-      float sum = 0.f;
+    uint64_t v[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sum = fmaf(v[j], v[j], sum);
+    for (int j = 0; j < 4; ++j) {
+      v[j] = rope_two(next[0].get(2 * j), next[0].get(2 * j + 1));
+      v[4 + j] = rope_two(next[1].get(2 * j), next[1].get(2 * j + 1));
+    }
+    begin(turn + 1, next);
+    if (a.w[0] != nullptr || a.w[1] != nullptr) {  // (the same for all lanes)
+      uint64_t two = rope_mul(v[0], v[0]), more = rope_mul(v[1], v[1]);
+#pragma unroll
+      for (int j = 2; j < 8; j += 2) {
+        two = rope_fma(v[j], v[j], two);
+        more = rope_fma(v[j + 1], v[j + 1], more);
+      }
+      const float2 s0 = rope_apart(two), s1 = rope_apart(more);
+      float sum = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
       for (int d = 1; d < P; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (a.w[k] != nullptr) {
-        if (have != k) {
-          have = k;
-          w[0].zero();
-          w[1].zero();
-          if (has0) w[0].load(a.w[k], c0);
-          if (has1) w[1].load(a.w[k], c1);
-        }
         const float inv = rsqrtf(sum / (float)a.dim + a.eps);
+        const uint64_t inv2 = rope_two(inv, inv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] *= inv * w[0].get(j);
-          v[8 + j] *= inv * w[1].get(j);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = rope_mul(v[j], inv2);
       }
     }
-    float o[16];
+    uint64_t o[2][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // (chosen, not multiplied by 0: a channel beyond the rotated ones may be anything)
-      const bool r = 8 * u + j < half;
-      if (a.inter) {
-        const float x0 = v[2 * j], x1 = v[2 * j + 1];
-        o[2 * j] = r ? x0 * cs[j] - x1 * sn[j] : x0;
-        o[2 * j + 1] = r ? x1 * cs[j] + x0 * sn[j] : x1;
-      } else {
-        const float x0 = v[j], x1 = v[8 + j];
-        o[j] = r ? x0 * cs[j] - x1 * sn[j] : x0;
-        o[8 + j] = r ? x1 * cs[j] + x0 * sn[j] : x1;
+      const uint64_t kept = rope_mul(v[j], own[j]);
+      uint64_t partner = v[j ^ 4];
+      if constexpr (kInter) {
+        const float2 p = rope_apart(v[j]);
+        partner = rope_two(p.y, p.x);
       }
+      uint64_t r = rope_fma(partner, other[j], kept);
+      // (chosen, not multiplied by 0: a channel beyond the rotated ones may be anything)
+      if constexpr (!kFull) r = (kInter ? 8 * u + j < half : turned) ? r : kept;
+      o[j / 4][j % 4] = r;
     }
     if (on) {
-      if (has0) rope_store8<DT>(a.y[k], at + c0, o);
-      if (has1) rope_store8<DT>(a.y[k], at + c1, o + 8);
+      if (has0) rope_store8<DT>(a.y[k], at + c0, o[0]);
+      if (has1) rope_store8<DT>(a.y[k], at + c1, o[1]);
     }
   }
 }
 
-// Any number of channels, any alignment: a warp for each head of a row, a pair to a lane.
+// Wider heads, any number of channels, any alignment: a warp for each head of a row, a pair to a lane.
 template <int DT>
 __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_any(const RopeArgs a) {
   pdl_trigger();
@@ -309,21 +353,24 @@ bool meet(const Rows &a, const Rows &b) {
 template <int DT, int P>
 cudaError_t rope_launch(RopeArgs a, int sms, cudaStream_t s) {
   const int turns = (a.heads[0] + a.heads[1] + 32 / P - 1) / (32 / P);
-  // turns of a warp: one while the SMs hold all warps at once, else up to eight, over which
+  // turns of a warp: one while the SMs hold all warps at once, else up to sixteen, over which
   // the row's cosines are kept
-  a.per = a.N * turns <= (int64_t)sms * 32 ? 1 : turns < 8 ? turns : (turns + (turns + 7) / 8 - 1) / ((turns + 7) / 8);
+  constexpr int kMost = 16;
+  a.per = a.N * turns <= (int64_t)sms * 16 ? 1 : turns < kMost ? turns : (turns + (turns + kMost - 1) / kMost - 1) / ((turns + kMost - 1) / kMost);
   a.chunks = (turns + a.per - 1) / a.per;
   const int64_t ctas = (a.N * a.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_k(k_qk_norm_rope<DT, P>, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
+  const bool full = a.rot == a.dim && a.dim % 16 == 0;
+  auto kern = a.inter ? (full ? k_qk_norm_rope<DT, P, true, true> : k_qk_norm_rope<DT, P, true, false>)
+                      : (full ? k_qk_norm_rope<DT, P, false, true> : k_qk_norm_rope<DT, P, false, false>);
+  return launch_k(kern, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
 }
 template <int DT>
 cudaError_t rope(const RopeArgs &a, bool vec, int sms, cudaStream_t s) {
-  if (vec)
+  if (vec && a.dim <= 256)
     return a.dim <= 64    ? rope_launch<DT, 4>(a, sms, s)
            : a.dim <= 128 ? rope_launch<DT, 8>(a, sms, s)
-           : a.dim <= 256 ? rope_launch<DT, 16>(a, sms, s)
-                          : rope_launch<DT, 32>(a, sms, s);
+                          : rope_launch<DT, 16>(a, sms, s);
   const int64_t ctas = (a.N * (a.heads[0] + a.heads[1]) + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
   return launch_k(k_qk_norm_rope_any<DT>, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
