@@ -47,10 +47,10 @@ struct PxForm {
 constexpr int kPxMeta = 32;
 constexpr int kPxCost1 = 2, kPxCost2 = 3;  // places of a block: of an item of up to 128 rows, of more
 constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
-// The weights leave with a factor of 2^8 and may outgrow their reference by 2^7 before O is
-// scaled anew (a warp takes some 1000 cycles for that): fp16 holds them up to 2^15, and in
-// full down to 2^-22 of the reference.
-constexpr float kPxLift = 8.f, kPxSlack = 7.f;
+// The weights leave with a factor of 2^8, and O is scaled anew (a warp takes some 1000 cycles
+// for that) once those of a row and block come to 2^15: fp16 holds them, and in full down to
+// 2^-22 of the reference.
+constexpr float kPxLift = 8.f, kPxFull = 32768.f;
 
 // A group's part of the work list: its tiles of kRows rows, of each the heads, of each the
 // shared blocks.  (The host limits all groups' places to 31 bits: the first thing that a CTA
@@ -263,10 +263,8 @@ static __device__ __noinline__ uint4 px_load8(const unsigned short *p) {
 //                one: P has columns of its own
 //   softmax      four warps a set, a row to a thread: Q to tensor memory at an item's start, S to P
 //                for each step, O out at its end
-// O is scaled anew only where a row's largest weight (times its block's values' scale, which
-// goes into P) outgrows the reference by 2^7: as a rule in the first blocks only.  Weights and
-// their sums refer to the running maximum of the logits alone: a block of tiny values still counts
-// in full in the sum.
+// O is scaled anew only where a row's weights (times their block's value scale, which goes
+// into P) come to 2^15 of its units: as a rule in the first blocks only.
 template <int D, int DT>
 __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvArgs a) {
   using F = PxForm<D>;
@@ -632,7 +630,10 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       __syncwarp();
       if (lane == 0 && (both || x == 0)) tc_mbar_arrive(&qf[x]);
 
-      float m = -INFINITY, l = 0.f, ref = -INFINITY;  // largest logit, sum of weights, O's reference
+      // O's reference: a logit plus the log2 of its block's value scale (lvr); the sum of weights, in
+      // units of 2^(ref - lvr - kPxLift)
+      float ref = 0.f, lvr = 0.f, l = 0.f;
+      bool begun = false;
       const int by = F::kSets > 1 && !both ? 2 : 1;  // from one of its blocks to the next
 #pragma unroll 1
       for (int blk = c0 + (by == 2 ? x : 0); blk < c0 + nb; blk += by) {
@@ -647,65 +648,75 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           f8_ld<32>(ts + 32, r[1]);
         }
         // (S is there, so its keys were converted, so the block's scales had come)
-        const float ff = f * meta[slot][0], lv = px_log2(meta[slot][1]);
         const bool bad = meta_bad[slot] != 0;
+        // (a scale of 0, and of a block that is none, far below any other)
+        const float ff = f * meta[slot][0], lv = bad ? -INFINITY : fmaxf(px_log2(meta[slot][1]), -200.f);
         if (any) {
           f8_ld_wait<32>(r[0]);
           f8_ld_wait<32>(r[1]);
         }
+        // P = 2^(logit + up): the weight times the value scale, in units of 2^(ref - kPxLift).  Whether
+        // a weight has outgrown the reference its row's sum tells: no largest logit is looked for
+        // where all is as expected.
+        bool grow = false;
+        float shrink = 1.f;
+        if (any) {
+          float up = lv - ref + kPxLift, sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+            px_fma2(u, v, ff, up);
+            u = kv_exp2(u);
+            v = kv_exp2(v);
+            px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
+            r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
+          }
+          float total = (sum[0] + sum[2]) + (sum[1] + sum[3]);
+          // no reference yet; too large for fp16; or value scales so far below the reference's that P
+          // loses weights that count
+          if (__any_sync(0xffffffffu, !begun || total > kPxFull || lv - lvr < -96.f)) {
+            if (!bad) {
+              f8_ld<32>(ts, r[0]);
+              f8_ld<32>(ts + 32, r[1]);
+              f8_ld_wait<32>(r[0]);
+              f8_ld_wait<32>(r[1]);
+              float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                mx = fmaxf(mx, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[0][j + 1])));
+                my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
+              }
+              const float bm = fmaxf(mx, my) * ff;
+              grow = !begun || bm + lv > ref;
+              if (grow) {
+                const float was = ref - lvr;
+                shrink = begun ? kv_exp2(ref - (bm + lv)) : 0.f;
+                l = begun ? l * kv_exp2(was - bm) : 0.f;
+                ref = bm + lv;
+                lvr = lv;
+              }
+              begun = true;
+              up = lv - ref + kPxLift;
+              const float unit = kPxLift - (ref - lvr);  // weights by themselves, in l's units
+              total = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
+                total += kv_exp2(fmaf(u, ff, unit)) + kv_exp2(fmaf(v, ff, unit));
+                r[0][j] = kv_pack_half(kv_exp2(fmaf(u, ff, up)), kv_exp2(fmaf(v, ff, up)));
+              }
+              l += total;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[0][j] = 0;
+            }
+          } else {
+            l = fmaf(total, kv_exp2(lvr - lv), l);
+          }
+        }
         px_fence_before();
         __syncwarp();
         if (lane == 0) tc_mbar_arrive(&sr[x]);
-        bool grow = false;
-        float shrink = 1.f;
-        if (any && !bad) {
-          float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            mx = fmaxf(mx, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[0][j + 1])));
-            my = fmaxf(my, fmaxf(__uint_as_float(r[1][j]), __uint_as_float(r[1][j + 1])));
-          }
-          const float bm = fmaxf(mx, my) * ff, cand = bm + lv;
-          const float top = fmaxf(m, bm);  // (of a NaN and a number, the number)
-          l *= kv_exp2(m - (top == -INFINITY ? 0.f : top));
-          m = top;
-          grow = first || cand > ref + kPxSlack;
-          if (grow) {
-            shrink = kv_exp2(ref - cand);
-            ref = cand;
-          }
-          // P = 2^(logit + up): the weight 2^(logit - m) times 2^(m + up)
-          const float z = m == -INFINITY ? 0.f : m, up = lv - (ref == -INFINITY ? 0.f : ref) + kPxLift;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          if (!__any_sync(0xffffffffu, z + up < -80.f)) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-              px_fma2(u, v, ff, up);
-              u = kv_exp2(u);
-              v = kv_exp2(v);
-              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
-              r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
-            }
-            l = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), kv_exp2(-(z + up)), l);
-          } else {  // values so small that the weights would be lost in P: their sum apart
-            const float g = kv_exp2(z + up);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-              px_fma2(u, v, ff, -z);
-              u = kv_exp2(u);
-              v = kv_exp2(v);
-              px_add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], u, v);
-              px_mul2(u, v, g);
-              r[0][j] = kv_pack_half(u, v);
-            }
-            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[0][j] = 0;
-        }
         // the product before this one: done with P, with its values, with O
         if (!first) {
           ok = wait(&of[x], ph ^ 1, 1);
@@ -747,7 +758,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         }
       }
       if (any) {
-        const float units = kv_exp2(ref - kPxLift - m);  // O in units of the largest weight
+        const float units = kv_exp2(lvr);  // O in the weights' units
         float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -762,7 +773,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           }
         }
         if (alive) {
-          part[128 * D + in_tile] = m;
+          part[128 * D + in_tile] = begun ? ref - lvr - kPxLift : -INFINITY;
           part[128 * (D + 1) + in_tile] = l * kKvLifted;
         }
       }
