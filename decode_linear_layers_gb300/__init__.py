@@ -569,6 +569,8 @@ def gemv_kv8_prefix_attention(dtype, k_cache, v_cache, k_scale, v_scale, table, 
     S, T, q_heads = int(S), int(T), int(q_heads)
     cache, _, dim = _kv8_cache(k_cache, v_cache, k_scale, v_scale, table, S)
     size, rows, row = _ESIZE[dtype][1], max(0, S * T), max(0, q_heads * dim)
+    if isinstance(prefix, int):
+        raise ValueError("prefix must be a tensor: it has a value for each group")
     groups = prefix.numel()
     qa, qs = _rows(q, size, rows, row, "q")
     _check(_fn("gemv_kv8_prefix_attention")(DTYPE_CODES[dtype], cache, qa, qs, _addr(lens, 4, max(S, 0), "lens"),

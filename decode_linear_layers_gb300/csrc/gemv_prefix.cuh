@@ -630,9 +630,9 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       __syncwarp();
       if (lane == 0 && (both || x == 0)) tc_mbar_arrive(&qf[x]);
 
-      // O's reference: a logit plus the log2 of its block's value scale (lvr); the sum of weights, in
-      // units of 2^(ref - lvr - kPxLift)
-      float ref = 0.f, lvr = 0.f, l = 0.f;
+      // O's reference, a logit plus the log2 of its block's value scale; the weights' own, the
+      // largest logit of those looked for; the weights' sum, in units of 2^own
+      float ref = 0.f, own = 0.f, l = 0.f;
       bool begun = false;
       const int by = F::kSets > 1 && !both ? 2 : 1;  // from one of its blocks to the next
 #pragma unroll 1
@@ -672,9 +672,11 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
             r[0][j] = kv_pack_half(u, v);  // (in the place of values that are used up)
           }
           float total = (sum[0] + sum[2]) + (sum[1] + sum[3]);
-          // no reference yet; too large for fp16; or value scales so far below the reference's that P
-          // loses weights that count
-          if (__any_sync(0xffffffffu, !begun || total > kPxFull || lv - lvr < -96.f)) {
+          // P's unit, as a weight.  Far above the weights' own (value scales far below the reference's)
+          // P loses weights that count
+          const float unit = -up - own;
+          // (or no reference yet, or too large for fp16)
+          if (__any_sync(0xffffffffu, !begun || total > kPxFull || unit > 80.f)) {
             if (!bad) {
               f8_ld<32>(ts, r[0]);
               f8_ld<32>(ts + 32, r[1]);
@@ -689,20 +691,19 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
               const float bm = fmaxf(mx, my) * ff;
               grow = !begun || bm + lv > ref;
               if (grow) {
-                const float was = ref - lvr;
                 shrink = begun ? kv_exp2(ref - (bm + lv)) : 0.f;
-                l = begun ? l * kv_exp2(was - bm) : 0.f;
                 ref = bm + lv;
-                lvr = lv;
               }
+              const float top = begun ? fmaxf(own, bm) : bm;
+              l *= kv_exp2(own - top);
+              own = top;
               begun = true;
               up = lv - ref + kPxLift;
-              const float unit = kPxLift - (ref - lvr);  // weights by themselves, in l's units
               total = 0.f;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 float u = __uint_as_float(r[j >> 4][2 * (j & 15)]), v = __uint_as_float(r[j >> 4][2 * (j & 15) + 1]);
-                total += kv_exp2(fmaf(u, ff, unit)) + kv_exp2(fmaf(v, ff, unit));
+                total += kv_exp2(fmaf(u, ff, -own)) + kv_exp2(fmaf(v, ff, -own));
                 r[0][j] = kv_pack_half(kv_exp2(fmaf(u, ff, up)), kv_exp2(fmaf(v, ff, up)));
               }
               l += total;
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
               for (int j = 0; j < 32; ++j) r[0][j] = 0;
             }
           } else {
-            l = fmaf(total, kv_exp2(lvr - lv), l);
+            l = fmaf(total, kv_exp2(unit), l);
           }
         }
         px_fence_before();
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         }
       }
       if (any) {
-        const float units = kv_exp2(lvr);  // O in the weights' units
+        const float units = kv_exp2(ref - kPxLift - own);  // O in the weights' units
         float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           }
         }
         if (alive) {
-          part[128 * D + in_tile] = begun ? ref - lvr - kPxLift : -INFINITY;
+          part[128 * D + in_tile] = begun ? own : -INFINITY;
           part[128 * (D + 1) + in_tile] = l * kKvLifted;
         }
       }

@@ -273,20 +273,21 @@ __global__ void __launch_bounds__(kRopeThreads, 3) k_qk_norm_rope(const RopeArgs
   }
 }
 
-// Wider heads, any number of channels, any alignment: a warp for each head of a row, a pair to a lane.
-template <int DT>
+// Wider heads, any number of channels, any alignment: a warp has a head at a time, a lane every
+// 32nd pair (behind the rotated channels, of two neighbours), up to kPairs of them, value by
+// value; it keeps its pairs' cosines over the heads, as above (bf16, 41 k heads of 128 channels,
+// 36 of them rotated: 24 us, bound by instructions).
+template <int DT, int kPairs>
 __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_any(const RopeArgs a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, all = a.heads[0] + a.heads[1], half = a.rot / 2;
   const int64_t warp = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = warp / all;
+  const int64_t row = warp / a.chunks;
   if (row >= a.N) return;
   int32_t pos = 0;
   if (!rope_position(a, row, lane, pos)) return;
-  const int h = (int)(warp - row * all), k = h < a.heads[0] ? 0 : 1;
-  const int64_t head = (int64_t)(h - (k ? a.heads[0] : 0)) * a.dim;
-  const int64_t from = row * a.xs[k] + head, to = row * a.ys[k] + head;
+  // (reads that the kernel's own writes may follow, in place)
   auto get = [](const void *p, int64_t i) {
     if constexpr (DT == GEMV_DTYPE_F32) return reinterpret_cast<const volatile float *>(p)[i];
     const unsigned short b = reinterpret_cast<const volatile unsigned short *>(p)[i];
@@ -298,33 +299,60 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_any(const RopeArg
     else
       reinterpret_cast<unsigned short *>(p)[i] = f8_round16(v, DT);
   };
-  float inv = 1.f;
-  const bool norm = a.w[k] != nullptr;
-  if (norm) {
-    float sum = 0.f;
-    for (int c = lane; c < a.dim; c += 32) {
-      const float v = get(a.x[k], from + c);
-      sum = fmaf(v, v, sum);
+  float cs[kPairs], sn[kPairs], w0[kPairs], w1[kPairs];
+  auto pair = [&](int j) { return lane + 32 * j; };
+  auto c0 = [&](int j) { return pair(j) < half ? (a.inter ? 2 * pair(j) : pair(j)) : a.rot + 2 * (pair(j) - half); };
+  auto c1 = [&](int j) { return pair(j) < half && !a.inter ? pair(j) + half : c0(j) + 1; };
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    cs[j] = sn[j] = 0.f;
+    if (pair(j) < half) {
+      rope_turn(__ldg(a.inv_freq + pair(j)), pos, cs[j], sn[j]);
+      cs[j] *= a.factor;
+      sn[j] *= a.factor;
+    }
+  }
+  int have = -1;
+  int h = (int)(warp - row * a.chunks) * a.per;
+  const int end = h + a.per < all ? h + a.per : all;
+  for (; h < end; ++h) {
+    const int k = h < a.heads[0] ? 0 : 1;
+    const int64_t head = (int64_t)(h - (k ? a.heads[0] : 0)) * a.dim;
+    const int64_t from = row * a.xs[k] + head, to = row * a.ys[k] + head;
+    const bool norm = a.w[k] != nullptr;
+    if (have != k) {
+      have = k;
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        w0[j] = norm && c0(j) < a.dim ? get(a.w[k], c0(j)) : 1.f;
+        w1[j] = norm && c1(j) < a.dim ? get(a.w[k], c1(j)) : 1.f;
+      }
+    }
+    float x0[kPairs], x1[kPairs], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      x0[j] = c0(j) < a.dim ? get(a.x[k], from + c0(j)) : 0.f;
+      x1[j] = c1(j) < a.dim ? get(a.x[k], from + c1(j)) : 0.f;
+    }
+    if (norm) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) sum = fmaf(x0[j], x0[j], fmaf(x1[j], x1[j], sum));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const float inv = rsqrtf(sum / (float)a.dim + a.eps);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        x0[j] *= inv * w0[j];
+        x1[j] *= inv * w1[j];
+      }
     }
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    inv = rsqrtf(sum / (float)a.dim + a.eps);
+    for (int j = 0; j < kPairs; ++j) {
+      const bool turned = pair(j) < half;
+      if (c0(j) < a.dim) put(a.y[k], to + c0(j), turned ? x0[j] * cs[j] - x1[j] * sn[j] : x0[j]);
+      if (c1(j) < a.dim) put(a.y[k], to + c1(j), turned ? x1[j] * cs[j] + x0[j] * sn[j] : x1[j]);
+    }
   }
-  auto normed = [&](int c) {
-    const float v = get(a.x[k], from + c);
-    return norm ? v * (inv * get(a.w[k], c)) : v;
-  };
-  for (int i = lane; i < half; i += 32) {
-    const int c0 = a.inter ? 2 * i : i, c1 = a.inter ? 2 * i + 1 : i + half;
-    float c, s;
-    rope_turn(__ldg(a.inv_freq + i), pos, c, s);
-    c *= a.factor;
-    s *= a.factor;
-    const float x0 = normed(c0), x1 = normed(c1);
-    put(a.y[k], to + c0, x0 * c - x1 * s);
-    put(a.y[k], to + c1, x1 * c + x0 * s);
-  }
-  for (int c = a.rot + lane; c < a.dim; c += 32) put(a.y[k], to + c, normed(c));
 }
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
@@ -350,13 +378,18 @@ bool meet(const Rows &a, const Rows &b) {
   return d < a.row || a.stride - d < b.row;
 }
 
+// Turns (of a row's `most`) that a warp takes one after the other: one while the SMs hold all
+// warps at once, 24 each, else as many as keep those busy, up to sixteen, over which the row's
+// cosines are kept.
+int share(int64_t turns, int most, int sms) {
+  const int64_t n = turns / ((int64_t)sms * 24), cap = most < 16 ? most : 16;
+  return (int)(n < 1 ? 1 : n < cap ? n : cap);
+}
+
 template <int DT, int P>
 cudaError_t rope_launch(RopeArgs a, int sms, cudaStream_t s) {
   const int turns = (a.heads[0] + a.heads[1] + 32 / P - 1) / (32 / P);
-  // turns of a warp: one while the SMs hold all warps at once, else up to sixteen, over which
-  // the row's cosines are kept
-  constexpr int kMost = 16;
-  a.per = a.N * turns <= (int64_t)sms * 16 ? 1 : turns < kMost ? turns : (turns + (turns + kMost - 1) / kMost - 1) / ((turns + kMost - 1) / kMost);
+  a.per = share(a.N * turns, turns, sms);
   a.chunks = (turns + a.per - 1) / a.per;
   const int64_t ctas = (a.N * a.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -365,15 +398,27 @@ cudaError_t rope_launch(RopeArgs a, int sms, cudaStream_t s) {
                       : (full ? k_qk_norm_rope<DT, P, false, true> : k_qk_norm_rope<DT, P, false, false>);
   return launch_k(kern, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
 }
+template <int DT, int kPairs>
+cudaError_t rope_any(RopeArgs a, int sms, cudaStream_t s) {
+  const int all = a.heads[0] + a.heads[1];
+  a.per = share(a.N * all, all, sms);
+  a.chunks = (all + a.per - 1) / a.per;
+  const int64_t ctas = (a.N * a.chunks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  return launch_k(k_qk_norm_rope_any<DT, kPairs>, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
+}
 template <int DT>
 cudaError_t rope(const RopeArgs &a, bool vec, int sms, cudaStream_t s) {
   if (vec && a.dim <= 256)
     return a.dim <= 64    ? rope_launch<DT, 4>(a, sms, s)
            : a.dim <= 128 ? rope_launch<DT, 8>(a, sms, s)
                           : rope_launch<DT, 16>(a, sms, s);
-  const int64_t ctas = (a.N * (a.heads[0] + a.heads[1]) + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_k(k_qk_norm_rope_any<DT>, dim3((unsigned)ctas), dim3(kRopeThreads), 0, s, launch_overlap(), a);
+  // pairs of a lane: the rotated ones, and two by two the other channels
+  const int pairs = (a.rot / 2 + (a.dim - a.rot + 1) / 2 + 31) / 32;
+  return pairs <= 1   ? rope_any<DT, 1>(a, sms, s)
+         : pairs == 2 ? rope_any<DT, 2>(a, sms, s)
+         : pairs <= 4 ? rope_any<DT, 4>(a, sms, s)
+                      : rope_any<DT, 8>(a, sms, s);
 }
 
 }  // namespace

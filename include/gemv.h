@@ -418,10 +418,11 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, to which the
  * call is passed on where sharing does not pay (groups == 0, and S x width x heads x dim, times
  * T x q_heads / heads, too small) or where its work list would pass 2^31.  The shared values' sums, over
- * a share of the blocks each, are in units of the row's largest weight x value scale; the weights
+ * a share of the blocks each, are in units of about the row's largest weight x value scale; the weights
  * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer
  * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and
- * 4 (dim + 2) bytes twice for each row of out. */
+ * 4 (dim + 4) bytes twice for each row of out, counted in tiles of 8 to 32 rows for each sequence and
+ * head, and of 128 or 256 for each group and head. */
 gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
                                         const int32_t *lens, const int32_t *firsts, const int32_t *prefix, int groups, void *out,
                                         float *lse, int S, int T, int q_heads, float scale, gemv_stream_t stream);

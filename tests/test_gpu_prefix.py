@@ -212,6 +212,23 @@ def test_scales_of_very_different_size(dim):
         check(c, queries(c, 1, 4, 63))
 
 
+def test_large_logits_with_values_of_zero():
+    # a block of zeros (the smallest scale) has the largest logits by far: its weights are all that
+    # counts in the sums, and P cannot hold them beside the other values'
+    P = 1280
+    c = Shared([0, 3], [P], [P + 70] * 3, 2, 128, seed=116).fill(117)
+    q = queries(c, 1, 4, 118)
+    q[...] = q[:1, :, :1]
+    for at, far in ((0, 60.0), (0, 140.0), (5, 60.0), (5, 140.0), (19, 300.0)):
+        d = Shared([0, 3], [P], [P + 70] * 3, 2, 128, seed=116).fill(117)
+        b = d.table[0, at].long()
+        d.v[b], d.vs[b] = 0, 2.0 ** -126
+        norm = float(q[0, 0, 0].float().square().sum())
+        d.k[b] = (q[0, 0, 0].float() * 64).clamp(-448, 448).to(E4M3).view(torch.uint8)   # all 64 tokens alike
+        d.ks[b] = 2.0 ** -6
+        check(d, q, scale=far / norm * math.log(2.0))
+
+
 def test_a_sink_and_a_long_flat_rest():
     # one token far above all others, whose weights of 2^-20 count by their number
     P = 32768

@@ -136,6 +136,30 @@ def test_many_rows():
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_many_rows_of_odd_channels(layout):
+    # heads that do not come in pieces of eight: several of a row to a warp
+    check("bf16", [9000] * 2, [700] * 2, 12, 3, 128, 36, layout, even=True, seed=16, gap=3)
+    check("f32", [9000], [900], 10, 5, 200, 34, layout, even=True, seed=17)
+    check("f16", [9000], [400], 30, 7, 65, 20, layout, even=True, seed=18)
+
+
+@pytest.mark.parametrize("gap", [8, 3])
+def test_one_side_normed(gap):
+    # weights for the queries alone, or for the keys alone
+    x = torch.randn(6, 3 * 128 + gap, generator=gen(19), device="cuda").to(torch.bfloat16)
+    q, k = x[:, :256].unflatten(1, (2, 128)), x[:, 256:384].unflatten(1, (1, 128))
+    w = (1 + torch.randn(128, generator=gen(20), device="cuda")).to(torch.bfloat16)
+    lens = torch.tensor([77], dtype=torch.int32, device="cuda")
+    freq, _ = frequencies(128)
+    pos = positions([77], [6])
+    for qw, kw in ((w, None), (None, w)):
+        qo, ko = torch.empty(6, 2, 128, dtype=x.dtype, device="cuda"), torch.empty(6, 1, 128, dtype=x.dtype, device="cuda")
+        g.gemv_qk_norm_rope("bf16", q, k, qo, ko, qw, kw, freq, lens, None, 1, 6, 2, 1, 128, 128)
+        close("bf16", qo, *reference(q, qw, pos, freq, 128, "half", 1e-6, 1.0))
+        close("bf16", ko, *reference(k, kw, pos, freq, 128, "half", 1e-6, 1.0))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_far_positions(layout):
     # an angle's product in fp32 would be off by whole radians here
     check("f32", [131072, 1 << 20, (1 << 31) - 1, 5], [3, 2, 4, 5], 2, 1, 128, 128, layout, norm=False, factor=1.0, seed=10)
