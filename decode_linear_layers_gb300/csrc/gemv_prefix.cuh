@@ -7,8 +7,8 @@
 //     S = Q K^T          128 rows x 64 tokens, tcgen05 kind::f16
 //     P = 2^(S f - ..)   fp32, rounded to fp16
 //     O += P V           128 rows x D channels, in tensor memory over all blocks
-// The cached values become fp16 (exact) in shared memory once for all rows of the CTA; Q, S,
-// P and O stay in tensor memory, so that shared memory only feeds K and V.
+// The cached values become fp16 (exact) in shared memory once for all rows of the CTA; S, P and
+// O, and Q where it fits, stay in tensor memory, so that shared memory only feeds K and V.
 #pragma once
 
 #include <type_traits>
@@ -39,13 +39,13 @@ struct PxForm {
   static constexpr int kSmem = 1024 + kQBytes + 2 * (kStages * kStage + kSlots * kRaw);
   // one CTA an SM (each takes all of the tensor memory)
   static_assert(kSmem > 114 * 1024 && kSmem <= 226 * 1024);
-  // floats of a partial result's set: O as [D / 4][128 rows][4], largest logits, sums
+  // floats of a partial result's set: O as [D / 4][128 rows][4], the weights' references, their sums
   static constexpr int64_t kPart = 128 * (D + 2);
 };
 // Blocks whose scales are kept.  While the softmax is at block j, the converters are at
 // j + kStages + 1 at most, and the copies kSlots + 1 further on.
 constexpr int kPxMeta = 32;
-constexpr int kPxCost1 = 2, kPxCost2 = 3;  // places of a block: of an item of up to 128 rows, of more
+constexpr int kPxCost1 = 1, kPxCost2 = 2;  // places of a block: of an item of up to 128 rows, of more
 constexpr int kPxLeast = 4;       // blocks that a CTA takes at least
 // The weights leave with a factor of 2^8, and O is scaled anew (a warp takes some 1000 cycles
 // for that) once those of a row and block come to 2^15: fp16 holds them, and in full down to
@@ -224,17 +224,12 @@ __device__ __forceinline__ float px_log2(float v) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// (x, y) = (x, y) f + c;  (x, y) *= f;  (x, y) += (u, v)
+// (x, y) = (x, y) f + c;  (x, y) += (u, v)
 __device__ __forceinline__ void px_fma2(float &x, float &y, float f, float c) {
   asm("{\n\t.reg .b64 a, f, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
       "fma.rn.f32x2 a, a, f, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(f), "f"(c));
-}
-__device__ __forceinline__ void px_mul2(float &x, float &y, float f) {
-  asm("{\n\t.reg .b64 a, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmul.rn.f32x2 a, a, f;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(f));
 }
 __device__ __forceinline__ void px_add2(float &x, float &y, float u, float v) {
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
@@ -252,8 +247,8 @@ static __device__ __noinline__ uint4 px_load8(const unsigned short *p) {
 
 // ------------------------------------------------------------------ the shared blocks
 // One CTA per SM over its share of the work list.  Warps:
-//   copies       finds the share's segments and tells the others; a block's keys, then its values, by the bulk copy engine into a ring of raw
-//                slots, its scales beside them
+//   copies       finds the share's segments and tells the others; a block's keys and values by the
+//                bulk copy engine into a ring of raw slots, its scales beside them
 //   converters   raw e4m3 to fp16, in the 128-byte swizzle that the MMA reads: keys as 64 rows of
 //                tokens, values as D rows of channels, both along the product's k
 //   scores, sums the two products, a warp each: the queue between it and the tensor cores is
@@ -265,13 +260,20 @@ static __device__ __noinline__ uint4 px_load8(const unsigned short *p) {
 //                for each step, O out at its end
 // O is scaled anew only where a row's weights (times their block's value scale, which goes
 // into P) come to 2^15 of its units: as a rule in the first blocks only.
+// 16 x 64 queries of 4 heads behind 16384 tokens, 8 key heads of 128 (275 GFLOP): 250 us, 1100
+// TFLOP/s; 64 queries behind 32768 (67 MB, 34 GFLOP) 56 us.  A block of 64 tokens takes some 2000
+// cycles for 256 rows, where the products take 1150, exp2 512 and shared memory 1250: bound by
+// the softmax warps' chains of dependent instructions (39 % of the issue slots, 25 % of the tensor
+// cycles in use); the registers hold no more of them.  Some 13 us pass until the first weights
+// (share, queries, blocks, instructions, one after the other), 4 at the end.
 template <int D, int DT>
 __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvArgs a) {
   using F = PxForm<D>;
   constexpr int R = F::kSlots, NS = F::kStages;
   static_assert(NS + R + 3 < kPxMeta);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t rawf[R], rawe[R], wf[NS], we[NS], ql, qf[F::kSets], sf[F::kSets], sr[F::kSets], pf[F::kSets], of[F::kSets], gf[kPxSegs], ge[kPxSegs], fin;
+  __shared__ __align__(8) uint64_t rawf[R], rawe[R], wf[NS], we[NS], gf[kPxSegs], ge[kPxSegs], ql, fin;
+  __shared__ __align__(8) uint64_t qf[F::kSets], sf[F::kSets], sr[F::kSets], pf[F::kSets], of[F::kSets];
   __shared__ PxSeg segs[kPxSegs];
   __shared__ float meta[kPxMeta][2];  // of a block: the keys' and the values' scale
   __shared__ int meta_bad[kPxMeta];
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
       tc_mbar_init(&wf[i], F::kConv);
       tc_mbar_init(&we[i], 2 * F::kSets);  // both products of each set
     }
-    tc_mbar_init(&ql, F::kSoft);
+    tc_mbar_init(&ql, F::kSoft);  // the first queries have been read
     for (int i = 0; i < F::kSets; ++i) {
       tc_mbar_init(&qf[i], 4);  // Q is there
       tc_mbar_init(&sf[i], 1);  // S is

@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(kRopeThreads, 3) k_qk_norm_rope(const RopeArgs
   }
 }
 
-// Wider heads, any number of channels, any alignment: a warp has a head at a time, a lane every
+// Any number of channels, any alignment: a warp has a head at a time, a lane every
 // 32nd pair (behind the rotated channels, of two neighbours), up to kPairs of them, value by
 // value; it keeps its pairs' cosines over the heads, as above (bf16, 41 k heads of 128 channels,
-// 36 of them rotated: 24 us, bound by instructions).
+// 36 of them rotated: 26 us, bound by instructions; with the cosines worked out for each
+// head 71).
 template <int DT, int kPairs>
 __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_any(const RopeArgs a) {
   pdl_trigger();
@@ -409,10 +410,11 @@ cudaError_t rope_any(RopeArgs a, int sms, cudaStream_t s) {
 }
 template <int DT>
 cudaError_t rope(const RopeArgs &a, bool vec, int sms, cudaStream_t s) {
-  if (vec && a.dim <= 256)
+  if (vec)
     return a.dim <= 64    ? rope_launch<DT, 4>(a, sms, s)
            : a.dim <= 128 ? rope_launch<DT, 8>(a, sms, s)
-                          : rope_launch<DT, 16>(a, sms, s);
+           : a.dim <= 256 ? rope_launch<DT, 16>(a, sms, s)
+                          : rope_launch<DT, 32>(a, sms, s);
   // pairs of a lane: the rotated ones, and two by two the other channels
   const int pairs = (a.rot / 2 + (a.dim - a.rot + 1) / 2 + 31) / 32;
   return pairs <= 1   ? rope_any<DT, 1>(a, sms, s)
