@@ -634,7 +634,10 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
   __shared__ float meta[W * R][2];  // of the slot's block: the keys' and the values' scale
   __shared__ int meta_bad[W * R];
   __shared__ int abort_flag;
-  pdl_wait();
+  // (kOwn: the kernel before is k_kv8_prefix, which writes nothing that this one reads and lets it
+  // start after its own wait: an SM that is done there begins here.  The wait at the end is for
+  // the join, which needs both.)
+  if constexpr (!kOwn) pdl_wait();
   pdl_trigger();  // after the wait: the join reads lens before its own
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   unsigned char *smem = smem_raw + ((128u - (tc_smem_u32(smem_raw) & 127u)) & 127u);
@@ -1153,6 +1156,7 @@ __global__ void __launch_bounds__(KvForm<D, NT>::kThreads, 1) k_kv8_attention(co
       if (!drained && a.status != nullptr) atomicOr(a.status, kTcStatusDrain);
     }
   }
+  if constexpr (kOwn) pdl_wait();
 }
 
 // Items that several warps of k_kv8_attention share: their partial results, merged in the
