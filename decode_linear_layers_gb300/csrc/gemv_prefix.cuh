@@ -875,13 +875,14 @@ __global__ void __launch_bounds__(kPxJoinThreads) k_kv8_prefix_join(const KvArgs
       v[j].w = v[j].w * x + f[j].w * y;
     }
   };
+  constexpr int kOnWay = kGroups > 1 ? 4 : 2;  // parts whose reads are on their way (many parts: 84 us with two, 83)
   if (on) {
     const int total = of.y + w.y * sets;
-    for (int i0 = grp; i0 < total; i0 += 2 * kGroups) {
-      float fm[2], fden[2];
-      float4 f[2][4];
+    for (int i0 = grp; i0 < total; i0 += kOnWay * kGroups) {
+      float fm[kOnWay], fden[kOnWay];
+      float4 f[kOnWay][4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < kOnWay; ++k) {
         const int i = i0 + k * kGroups;
         if (i < total) {
           const bool mine = i < of.y;
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(kPxJoinThreads) k_kv8_prefix_join(const KvArgs
         }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < kOnWay; ++k)
         if (i0 + k * kGroups < total) add(fm[k], fden[k], f[k]);
     }
   }
