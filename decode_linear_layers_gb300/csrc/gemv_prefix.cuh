@@ -280,7 +280,6 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   pdl_wait();
-  pdl_trigger();  // after the wait: the next kernels read the batch's lengths before theirs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *smem = smem_raw + ((1024u - (tc_smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char *qst = smem, *kst = smem + F::kQBytes, *vst = kst + NS * F::kStage, *raw = vst + NS * F::kStage;
@@ -317,6 +316,9 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
   px_fence_before();
   __syncwarp();
   __syncthreads();
+  // After the wait: the next kernels read the batch's lengths before theirs.  With the tensor memory
+  // at hand: one that takes some and waits for this one cannot keep it from it.
+  pdl_trigger();
   px_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int *abort = &abort_flag;
