@@ -51,6 +51,8 @@ def call(c, q, scale, firsts=True, stream=None, want_lse=True, fill=5.0):
     name = "bf16" if q.dtype == torch.bfloat16 else "f16"
     out = torch.full((S, T, Hq, D), fill, dtype=q.dtype, device="cuda")
     lse = torch.full((S, T, Hq), fill, device="cuda") if want_lse else None
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
     g.gemv_kv8_prefix_attention(name, *c.args(), q, c.lens, c.firsts if firsts else None, c.prefix, out, lse, S, T, Hq, scale,
                                 stream=stream)
     return out, lse
@@ -397,6 +399,35 @@ def test_on_two_streams():
     torch.cuda.synchronize()
     for out, lse in got:
         assert same(out, want[0]) and same(lse, want[1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_calls_one_behind_the_other(dim):
+    # calls of different work lists, back to back: each kernel may begin before the one ahead of it
+    # is done, and the scratch memory is the same
+    c = Shared([0, 5, 9], [1500, 3000], [1600 + 30 * i for i in range(5)] + [3001 + 70 * i for i in range(4)], 2, dim, seed=108).fill(109)
+    kinds = [queries(c, 1, 4, 110), queries(c, 8, 4, 111), queries(c, 2, 8, 112)]
+    try:
+        g.set_launch_overlap("off")
+        want = []
+        for q in kinds:
+            want.append(call(c, q, 0.1))
+            torch.cuda.synchronize()
+        for mode in ("launch", "weights"):
+            g.set_launch_overlap(mode)
+            got = [call(c, kinds[i % 3], 0.1) for i in range(30)]
+            torch.cuda.synchronize()
+            for i, (out, lse) in enumerate(got):
+                assert same(out, want[i % 3][0]) and same(lse, want[i % 3][1]), (mode, i)
+    finally:
+        g.set_launch_overlap("launch")
+
+
+def test_a_block_that_stands_in_a_table_twice():
+    c = Shared([0, 4], [700], [705 + 40 * i for i in range(4)], 2, 128, seed=113).fill(114)
+    c.table[:, 3] = c.table[0, 1]      # among the shared blocks
+    c.table[2, 11] = c.table[2, 0]     # a shared one among a sequence's own
+    check(c, queries(c, 2, 4, 115), firsts=False)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 192, 256])
