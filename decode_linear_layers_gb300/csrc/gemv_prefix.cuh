@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
                 ref = bm + lv;
               }
               const float top = begun ? fmaxf(own, bm) : bm;
-              l *= kv_exp2(own - top);
+              // (chosen, not multiplied by 0: a first block far below 0 makes the factor infinite)
+              l = begun ? l * kv_exp2(own - top) : 0.f;
               own = top;
               begun = true;
               up = lv - ref + kPxLift;
