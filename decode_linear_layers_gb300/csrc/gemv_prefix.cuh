@@ -764,7 +764,9 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
         }
       }
       if (any) {
-        const float units = kv_exp2(ref - kPxLift - own);  // O in the weights' units
+        // O in the weights' units: 2^(ref - own), a value scale as a rule and down to 2^-126, less what
+        // rounding takes, and 2^-kPxLift.  (In one exponent the two would be flushed to 0.)
+        const float units = kv_exp2(ref - own + 0.5f), down = kv_exp2(-kPxLift - 0.5f);
         float4 *out = reinterpret_cast<float4 *>(part) + in_tile;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -774,8 +776,8 @@ __global__ void __launch_bounds__(PxForm<D>::kThreads, 1) k_kv8_prefix(const KvA
           if (alive) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              out[(c + j) / 4 * 128] = make_float4(__uint_as_float(o[j]) * units, __uint_as_float(o[j + 1]) * units,
-                                                   __uint_as_float(o[j + 2]) * units, __uint_as_float(o[j + 3]) * units);
+              out[(c + j) / 4 * 128] = make_float4(__uint_as_float(o[j]) * down * units, __uint_as_float(o[j + 1]) * down * units,
+                                                   __uint_as_float(o[j + 2]) * down * units, __uint_as_float(o[j + 3]) * down * units);
           }
         }
         if (alive) {

@@ -1,15 +1,18 @@
-"""gemv_kv8_prefix_attention at the ends of its ranges: logits far below zero.
+"""gemv_kv8_prefix_attention at the ends of its ranges: logits far below zero, values of
+the smallest scales.
 
 Tolerances: those of tests/test_gpu_prefix.py.
 """
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
 import decode_linear_layers_gb300 as g
-from tests.test_gpu_kv8 import BLOCK, E4M3
-from tests.test_gpu_prefix import Shared, check, queries
+from tests.test_gpu_kv8 import BLOCK, E4M3, ROUND, attend, attention_reference
+from tests.test_gpu_prefix import Shared, call, check, queries, small_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +58,23 @@ def test_blocks_far_below(dim, S, T, group, far):
         c.ks[blocks] = 2.0 ** -6
         out, lse = check(c, q, scale=far / float(q0.square().sum()))
         assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+@pytest.mark.parametrize("power", [-126, -123, -118])
+def test_the_smallest_value_scales(dim, power):
+    # values that bf16 holds, 2^-120 and below: nothing on the way may flush them to zero.  To the
+    # bounds of the other tests half of bf16's smallest step, 2^-134
+    P = 1280
+    c = finite(Shared([0, 4], [P], [P + 5, P + 70, P + 1, P + 130], 2, dim, seed=123).fill(124))
+    c.vs[:] = 2.0 ** power
+    q = queries(c, 2, 4, 125)
+    scale = 1 / math.sqrt(dim)
+    if dim % 128:      # logits whose rounding shows
+        scale *= 30
+    ref, _, tol = attention_reference(c, q, scale, 0, 0)
+    tol = tol + small_weights(c, q, scale) + ROUND["bf16"] * ref.abs() + 2.0 ** -134
+    assert float(ref.abs().amax()) > 2.0 ** (power + 3)
+    for out in (call(c, q, scale)[0], attend(c, q, scale)[0]):
+        err = (out.double() - ref).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
