@@ -63,13 +63,15 @@ __device__ __forceinline__ bool rope_position(const RopeArgs &a, int64_t row, in
 // cos and sin of pos x f.  The product is formed in turns, as a whole number of 2^-64
 // turns, whose overflow drops whole turns; its top 32 bits, as fp32, are good to 2^-23
 // radians at any position (a product in fp32 would be off by 2^-24 of the angle itself,
-// 0.008 at 131072).
+// 0.008 at 131072).  Turns a radian to 96 bits: 64 are off by 2^-65 of a turn for each
+// radian, of which there may be 2^55 (3.8e-4 radians for f = 2^20 at the last position).
 __device__ __forceinline__ void rope_turn(float f, int32_t pos, float &c, float &s) {
-  constexpr uint64_t kPerRadian = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+  constexpr uint64_t kPerRadian = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi), and 32 bits more
+  constexpr uint32_t kRest = 0x7F09D5F4u;
   const uint32_t bits = __float_as_uint(f), e = (bits >> 23) & 0xff;
   const uint64_t m = (bits & 0x7fffff) | (e != 0 ? 0x800000u : 0u);  // |f| = m 2^-sh
   const int sh = 150 - (int)(e != 0 ? e : 1);
-  const uint64_t lo = m * kPerRadian, hi = __umul64hi(m, kPerRadian);
+  const uint64_t rest = __umulhi((uint32_t)m, kRest), lo = m * kPerRadian + rest, hi = __umul64hi(m, kPerRadian) + (lo < rest ? 1 : 0);
   uint64_t t = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : sh > 0 ? (lo >> sh) | (hi << (64 - sh)) : sh > -64 ? lo << -sh : 0;
   t *= (uint64_t)(int64_t)pos;
   if ((bits >> 31) != 0) t = 0 - t;

@@ -251,3 +251,34 @@ def test_another_stream_and_a_replayed_graph():
         graph.replay()
         torch.cuda.synchronize()
         close("bf16", out, *reference(x, w, pos + 100 * step, freq, 128, "half", 1e-6, 1.0))
+
+
+def two_pi(bits):
+    """2 pi x 2^bits, a whole number: 32 atan(1/5) - 8 atan(1/239)."""
+    def atan(n):
+        total, term, k = 0, (1 << bits + 32) // n, 0
+        while term:
+            total += (-1) ** k * term // (2 * k + 1)
+            term //= n * n
+            k += 1
+        return total
+    return 32 * atan(5) - 8 * atan(239) >> 32
+
+
+def test_angles_to_the_last_position():
+    # Angles good to 2^-23 for any frequency below 2^24 at any position, against whole numbers: a
+    # pair (1, 0) becomes (cos, sin), each of which sincospif gives to one unit in the last place,
+    # 2^-23 of it at most
+    f = torch.tensor([0.75, 1.0, -3.5, 513.0625, 1000.25, 2.0 ** 20 + 0.5, -(2.0 ** 23 - 0.5), 2.0 ** 24 - 1], device="cuda")
+    for last in ((1 << 31) - 1, (1 << 30) + 77, (1 << 22) + 6):
+        x = torch.zeros(9, 1, 16, device="cuda")
+        x[..., 0::2] = 1
+        lens = torch.tensor([last], dtype=torch.int32, device="cuda")
+        g.gemv_qk_norm_rope("f32", x, None, None, None, None, None, f, lens, None, 1, 9, 1, 0, 16, 16, layout="interleaved")
+        for r, row in enumerate(x[:, 0].tolist()):
+            for i, v in enumerate(f.tolist()):
+                num, den = v.as_integer_ratio()
+                turns = ((last - 9 + r) * num << 400) // (den * two_pi(200))     # x 2^200
+                t = (turns & (1 << 200) - 1) / (1 << 200) * 2 * math.pi
+                for got, want in ((row[2 * i], math.cos(t)), (row[2 * i + 1], math.sin(t))):
+                    assert abs(got - want) <= 2.0 ** -23 * (1 + abs(want)), (v, last, r, got - want)
