@@ -1,5 +1,5 @@
 """gemv_kv8_prefix_attention at the ends of its ranges: logits far below zero, values of
-the smallest scales.
+the smallest scales, many groups.
 
 Tolerances: those of tests/test_gpu_prefix.py.
 """
@@ -78,3 +78,56 @@ def test_the_smallest_value_scales(dim, power):
     for out in (call(c, q, scale)[0], attend(c, q, scale)[0]):
         err = (out.double() - ref).abs()
         assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_hundreds_of_groups():
+    # most of them share nothing, in long runs: a CTA's share begins behind any number of groups
+    G, n = 320, 3
+    prefix = [64 * (1 + i % 5) + 9 if i % 40 in (0, 7, 39) or i > 300 else (0, 63, -1)[i % 3] for i in range(G)]
+    lens = [max(prefix[i // n], 0) + 1 + i % 70 for i in range(n * G)]
+    c = finite(Shared([n * i for i in range(G + 1)], prefix, lens, 1, 64, seed=129).fill(130))
+    q = queries(c, 1, 16, 131)
+    k = g.launch_count()
+    call(c, q, 0.1)
+    assert g.launch_count() - k == 3
+    check(c, q)
+
+
+def us(run, calls=5):
+    """Least time of a call, of a few rounds of captured ones."""
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(calls):
+            run()
+    best = math.inf
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / calls * 1e3)
+    return best
+
+
+def test_a_thousand_groups_take_no_walk():
+    # a CTA finds its share 32 groups at a time: one after the other they took 0.7 us each, three times
+    # what gemv_kv8_attention takes for all of it
+    G, n, P = 1024, 8, 512
+    c = Shared([n * i for i in range(G + 1)], [P] * G, [0] * (n * G), 1, 64, seed=132, width=16)
+    c.pool = G * 8 + n * G * 2
+    c.k = torch.randint(0, 120, (c.pool, 1, BLOCK, 64), device="cuda", dtype=torch.uint8)
+    c.v = torch.randint(0, 120, (c.pool, 1, 64, BLOCK), device="cuda", dtype=torch.uint8)
+    c.ks = c.vs = torch.full((c.pool, 1), 2.0 ** -9, device="cuda")
+    s = torch.arange(n * G, device="cuda")[:, None]
+    c.table[:, :8] = (s // n * 8 + torch.arange(8, device="cuda")).int()
+    c.table[:, 8:10] = (G * 8 + s * 2 + torch.arange(2, device="cuda")).int()
+    c.lens.fill_(P + 100)
+    q = torch.randn(n * G, 1, 16, 64, device="cuda").to(torch.bfloat16)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    args = ("bf16", *c.args(), q, c.lens)
+    shared = us(lambda: g.gemv_kv8_prefix_attention(*args, c.firsts, c.prefix, out, None, n * G, 1, 16, 0.125))
+    apart = us(lambda: g.gemv_kv8_attention(*args, want, None, n * G, 1, 16, 0.125))
+    assert bool(((out.float() - want.float()).abs() <= 2.0 ** -6 * want.float().abs() + 2.0 ** -8).all())
+    assert shared < 2 * apart, (shared, apart)
