@@ -1,5 +1,5 @@
 """gemv_kv8_prefix_attention at the ends of its ranges: logits far below zero, values of
-the smallest scales, many groups.
+the smallest scales, many groups, groups that share little.
 
 Tolerances: those of tests/test_gpu_prefix.py.
 """
@@ -12,7 +12,7 @@ import torch
 
 import decode_linear_layers_gb300 as g
 from tests.test_gpu_kv8 import BLOCK, E4M3, ROUND, attend, attention_reference
-from tests.test_gpu_prefix import Shared, call, check, queries, small_weights
+from tests.test_gpu_prefix import Shared, call, check, queries, same, small_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -85,7 +85,7 @@ def test_hundreds_of_groups():
     G, n = 320, 3
     prefix = [64 * (1 + i % 5) + 9 if i % 40 in (0, 7, 39) or i > 300 else (0, 63, -1)[i % 3] for i in range(G)]
     lens = [max(prefix[i // n], 0) + 1 + i % 70 for i in range(n * G)]
-    c = finite(Shared([n * i for i in range(G + 1)], prefix, lens, 1, 64, seed=129).fill(130))
+    c = finite(Shared([n * i for i in range(G + 1)], prefix, lens, 1, 64, seed=129, width=200).fill(130))
     q = queries(c, 1, 16, 131)
     k = g.launch_count()
     call(c, q, 0.1)
@@ -131,3 +131,82 @@ def test_a_thousand_groups_take_no_walk():
     apart = us(lambda: g.gemv_kv8_attention(*args, want, None, n * G, 1, 16, 0.125))
     assert bool(((out.float() - want.float()).abs() <= 2.0 ** -6 * want.float().abs() + 2.0 ** -8).all())
     assert shared < 2 * apart, (shared, apart)
+
+
+@pytest.mark.parametrize("firsts", [[0, 1], [0, 1, 2, 3, 4], [0, 0, 0, 2, 4]])
+def test_as_many_groups_as_sequences(firsts):
+    # nothing is shared, or (groups without sequences) little: the call is passed on, with equal bits
+    S = firsts[-1]
+    c = Shared(firsts, [640] * S, [650 + 40 * i for i in range(S)], 2, 128, seed=126).fill(127)
+    q = queries(c, 1, 4, 128)
+    n = g.launch_count()
+    out, lse = call(c, q, 0.1)
+    assert g.launch_count() - n == 2
+    want, want_lse = attend(c, q, 0.1)
+    assert same(out, want) and same(lse, want_lse)
+
+
+def wide(firsts, prefix, lens, heads, dim, seed):
+    """Tables so wide that any groups of three sequences are shared."""
+    return Shared(firsts, prefix, lens, heads, dim, seed, width=1 + 4_000_000_000 // (len(lens) * BLOCK * heads * dim * 2))
+
+
+def shared(c, q, **k):
+    """Checked, and not passed on."""
+    n = g.launch_count()
+    call(c, q, 0.1)
+    assert g.launch_count() - n == 3
+    return check(c, q, **k)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_groups_of_every_kind(dim):
+    # groups of one and many sequences, an empty one, sequences before the first and behind the last,
+    # idle places, sequences shorter than the prefix, or by one token too short to see it whole
+    firsts, prefix = [1, 2, 2, 9, 13, 14], [300, 640, 1000, 64, 500]
+    lens = [333, 302, 1003, 1100, 0, 960 + 2, 960 + 1, 50, 1024, 66, 65, 64, 0, 600, 40, 0]
+    c = wide(firsts, prefix, lens, 2, dim, seed=133).fill(134)
+    shared(c, queries(c, 2, 3, 135, torch.float16))
+
+
+def test_seventy_groups():
+    n, G = 3, 70
+    prefix = [64 * (i % 7) + 5 for i in range(G)]
+    c = wide([n * i for i in range(G + 1)], prefix, [prefix[i // n] + 3 + i % 90 for i in range(n * G)], 1, 64, seed=136).fill(137)
+    shared(c, queries(c, 1, 4, 138), again=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_groups_one_behind_the_other(dim):
+    # calls of different work lists, back to back, as in tests/test_gpu_prefix.py
+    c = wide([0, 5, 9], [1500, 3000], [1600 + 30 * i for i in range(5)] + [3001 + 70 * i for i in range(4)], 2, dim, seed=139).fill(140)
+    kinds = [queries(c, 1, 4, 141), queries(c, 8, 4, 142), queries(c, 2, 8, 143)]
+    try:
+        g.set_launch_overlap("off")
+        want = []
+        for q in kinds:
+            want.append(call(c, q, 0.1))
+            torch.cuda.synchronize()
+        for mode in ("launch", "weights"):
+            g.set_launch_overlap(mode)
+            n = g.launch_count()
+            got = [call(c, kinds[i % 3], 0.1) for i in range(30)]
+            assert g.launch_count() - n == 90
+            torch.cuda.synchronize()
+            for i, (out, lse) in enumerate(got):
+                assert same(out, want[i % 3][0]) and same(lse, want[i % 3][1]), (mode, i)
+    finally:
+        g.set_launch_overlap("launch")
+
+
+def test_a_sink_and_a_long_flat_rest():
+    # one token far above all others, whose weights of 2^-20 count by their number
+    P = 32768
+    c = finite(Shared([0, 4], [P], [P + 5, P + 9, P + 1, P + 70], 1, 128, seed=144).fill(145))
+    c.ks[:] = 2.0 ** -12
+    b = int(c.table[0, 0])
+    q = queries(c, 1, 4, 146)
+    q[...] = q[:1, :, :1]                       # all alike, so that one key suits all
+    c.k[b, 0, 7] = (q[0, 0, 0].float() * 100).clamp(-448, 448).to(E4M3).view(torch.uint8)
+    c.ks[b, 0] = 2.0 ** -6
+    shared(c, q)
