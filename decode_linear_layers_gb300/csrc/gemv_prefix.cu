@@ -30,15 +30,21 @@ bool px_pays(int64_t S, int64_t groups, int64_t width, int64_t heads, int64_t di
   return mb * ((double)S * (double)((rows + 7) / 8) - 2.5 * (double)(groups - 1)) > (dim <= 128 ? 230.0 : 300.0);
 }
 
-template <int D, int NT>
-gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
+// Scratch memory that a call takes at most, by the size of its output; `otherwise` is the call
+// passed on.  Full tiles take some 4 times the output, one row to a tile of eight up to 20 times;
+// hundreds of groups of a few rows, each with whole tiles for every head (66 to 133 KB), any number
+// of times (512 groups of three sequences with 32 heads of 128: 620 MB for 13).
+bool px_fits(int64_t bytes, int64_t out) { return bytes <= (64 << 20) + 24 * out; }
+
+template <int D, int NT, class Else>
+gemv_status_t attend(KvArgs a, int sms, cudaStream_t s, Else otherwise) {
   using F = KvForm<D, NT>;
   using P = PxForm<D>;
   a.row_tiles = (a.T * a.group + NT * 8 - 1) / (NT * 8);
   if ((int64_t)a.heads * a.row_tiles > 65535) return GEMV_ERR_UNSUPPORTED;
   const int items = a.heads * a.row_tiles;
   const int64_t px_items = ((int64_t)a.S * a.T * a.group / P::kRows + a.groups + 1) * a.heads;
-  if (px_items + sms > 0x7fffffff) return GEMV_ERR_UNSUPPORTED;
+  if (px_items + sms > 0x7fffffff) return otherwise();
   const int pdl = launch_overlap();
   a.workers = sms * F::kWarps;
   // partial results of the sequences' own blocks, where they are, those of the shared ones, where
@@ -46,8 +52,9 @@ gemv_status_t attend(KvArgs a, int sms, cudaStream_t s) {
   int64_t own, px, bytes;
   const int64_t own_items = (int64_t)a.S * items;
   if (!mul_ok(a.workers + own_items, kv_part<D, NT>() * 4, &own) || !mul_ok(sms + px_items, P::kSets * P::kPart * 4, &px) ||
-      __builtin_add_overflow(own, px, &bytes) || __builtin_add_overflow(bytes, (own_items + px_items) * 16, &bytes))
-    return GEMV_ERR_INVALID_VALUE;
+      __builtin_add_overflow(own, px, &bytes) || __builtin_add_overflow(bytes, (own_items + px_items) * 16, &bytes) ||
+      !px_fits(bytes, (int64_t)a.S * a.T * a.heads * a.group * D * 2))
+    return otherwise();
   void *ws = nullptr;
   cudaError_t e = workspace(&ws, (size_t)bytes, s);
   if (e != cudaSuccess) return fail((int)e);
@@ -122,8 +129,8 @@ gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache
   for (int i = 0; i < 2; ++i)
     for (int j = i + 1; j < 11; ++j)
       if (overlaps(part[i].p, part[i].n, part[j].p, part[j].n)) return GEMV_ERR_INVALID_VALUE;
-  if (pass_on)
-    return gemv_kv8_attention(dtype, cache, q, q_stride, lens, out, lse, S, T, q_heads, scale, 0, 0, stream);
+  auto otherwise = [&]() { return gemv_kv8_attention(dtype, cache, q, q_stride, lens, out, lse, S, T, q_heads, scale, 0, 0, stream); };
+  if (pass_on) return otherwise();
   int sms = 0;
   if ((st = device_sms(&sms)) != GEMV_SUCCESS) return st;
   KvArgs a = cache_args(cache);
@@ -146,14 +153,14 @@ gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache
   // rows of queries of one sequence that meet a block of its own at once, as in gemv_kv8_attention
   switch (cache->dim) {
     case 64:
-      return rows <= 8 ? attend<64, 1>(a, sms, s) : rows <= 16 ? attend<64, 2>(a, sms, s)
-             : rows <= 24 ? attend<64, 3>(a, sms, s) : attend<64, 4>(a, sms, s);
+      return rows <= 8 ? attend<64, 1>(a, sms, s, otherwise) : rows <= 16 ? attend<64, 2>(a, sms, s, otherwise)
+             : rows <= 24 ? attend<64, 3>(a, sms, s, otherwise) : attend<64, 4>(a, sms, s, otherwise);
     case 128:
-      return rows <= 8 ? attend<128, 1>(a, sms, s) : attend<128, 2>(a, sms, s);
+      return rows <= 8 ? attend<128, 1>(a, sms, s, otherwise) : attend<128, 2>(a, sms, s, otherwise);
     case 192:
-      return rows <= 8 ? attend<192, 1>(a, sms, s) : attend<192, 2>(a, sms, s);
+      return rows <= 8 ? attend<192, 1>(a, sms, s, otherwise) : attend<192, 2>(a, sms, s, otherwise);
     default:
-      return rows <= 8 ? attend<256, 1>(a, sms, s) : attend<256, 2>(a, sms, s);
+      return rows <= 8 ? attend<256, 1>(a, sms, s, otherwise) : attend<256, 2>(a, sms, s, otherwise);
   }
 }
 

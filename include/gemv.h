@@ -417,8 +417,8 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  * (lens[s] - T below them; an idle place of the batch with lens[s] == 0) is attended to by
  * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, to which the
  * call is passed on where sharing does not pay (groups == 0 or S; S x T x q_heads / heads query
- * rows, less those that further groups cost, times width x heads x dim too few) or where its work
- * list would pass 2^31.  The host knows the tables' width and not the lengths: for short sequences
+ * rows, less those that further groups cost, times width x heads x dim too few), where its work
+ * list would pass 2^31 or its scratch buffer 64 MB and 24 times the size of out.  The host knows the tables' width and not the lengths: for short sequences
  * in wide tables gemv_kv8_attention takes less.  The shared values' sums, over
  * a share of the blocks each, are in units of about the row's largest weight x value scale; the weights
  * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer

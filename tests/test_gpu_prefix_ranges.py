@@ -210,3 +210,19 @@ def test_a_sink_and_a_long_flat_rest():
     c.k[b, 0, 7] = (q[0, 0, 0].float() * 100).clamp(-448, 448).to(E4M3).view(torch.uint8)
     c.ks[b, 0] = 2.0 ** -6
     shared(c, q)
+
+
+def test_scratch_memory_has_a_limit():
+    # 512 groups of three sequences: a whole tile for each group and head would take 620 MB, the output
+    # takes 13 MB.  Forty groups stay below the limit
+    c = wide([3 * i for i in range(513)], [64] * 512, [65 + i % 5 for i in range(3 * 512)], 8, 128, seed=147)
+    c.k[:], c.v[:] = 0x30, 0x38
+    q = queries(c, 1, 4, 148)
+    want = attend(c, q, 0.1)
+    n = g.launch_count()
+    out, lse = call(c, q, 0.1)
+    assert g.launch_count() - n == 2
+    assert same(out, want[0]) and same(lse, want[1])
+    few = wide([3 * i for i in range(41)], [64] * 40, [65 + i % 5 for i in range(3 * 40)], 8, 128, seed=149)
+    few.k[:], few.v[:] = 0x30, 0x38
+    shared(few, queries(few, 1, 4, 150), again=False)
