@@ -54,6 +54,11 @@ class Layer:
     """Weights, cache and buffers of a batch of S sequences of up to `longest` tokens."""
 
     def __init__(self, S, hidden, heads, group, dim, longest, window=0, sinks=0, seed=0, rotate=False, shared=0):
+        # (the rest of a block would be in the first sequence's table alone; the shared blocks have no window)
+        if shared < 0 or shared % g.KV8_BLOCK:
+            raise ValueError(f"{shared} shared tokens are no whole number of blocks of {g.KV8_BLOCK}")
+        if shared and window:
+            raise ValueError("a window does not go with shared tokens")
         r = torch.Generator(device="cuda").manual_seed(seed)
         self.S, self.hidden, self.heads, self.q_heads, self.dim = S, hidden, heads, heads * group, dim
         self.window, self.sinks = window, sinks
@@ -186,7 +191,7 @@ if __name__ == "__main__":
     ap.add_argument("--window", type=int, default=0)
     ap.add_argument("--sinks", type=int, default=0)
     ap.add_argument("--rotate", action="store_true")
-    ap.add_argument("--shared", type=int, default=0)
+    ap.add_argument("--shared", type=int, default=0, help=f"tokens that all sequences begin with: a multiple of {g.KV8_BLOCK}, no --window")
     a = ap.parse_args()
     run(2)
     error, us = run(a.steps, window=a.window, sinks=a.sinks, rotate=a.rotate, shared=a.shared)
