@@ -110,3 +110,28 @@ def test_decode_layer_with_positions_and_a_shared_prompt(rotate, shared, prompt)
     error, us = m.run(steps=4, S=S, hidden=512, heads=heads, group=4, dim=128 if shared > 1000 else 64, prompt=prompt, rotate=rotate, shared=shared)
     assert 0 < error <= BOUND and us > 0
     assert g.launch_count() - n >= 12
+
+
+@pytest.mark.parametrize("rotate,shared,prompt", [(True, 0, 300), (True, 256, 300), (False, 8192, 100), (True, 8192, 100)])
+def test_decode_layer_launches_what_it_is_asked_for(monkeypatch, rotate, shared, prompt):
+    from examples import f8_decode_layer as m
+    wide = shared > 1000
+    launched = {}
+
+    def counted(name):
+        call = getattr(g, name)
+
+        def run(*a, **k):
+            n = g.launch_count()
+            call(*a, **k)
+            launched.setdefault(name, []).append(g.launch_count() - n)
+        return run
+
+    for name in ("gemv_qk_norm_rope", "gemv_kv8_attention", "gemv_kv8_prefix_attention"):
+        monkeypatch.setattr(m.g, name, counted(name))
+    m.run(steps=4, S=40 if wide else 5, hidden=512, heads=4 if wide else 2, group=4, dim=128 if wide else 64, prompt=prompt, rotate=rotate,
+          shared=shared)
+    # the shared tokens, the prompts, an eager step and a captured one; tables of five blocks or more
+    # take two kernels, the shared form three
+    assert launched.pop("gemv_qk_norm_rope", []) == [1] * ((3 + (shared > 0)) if rotate else 0)
+    assert launched == ({"gemv_kv8_prefix_attention": [3 if wide else 2] * 2} if shared else {"gemv_kv8_attention": [2] * 2})
