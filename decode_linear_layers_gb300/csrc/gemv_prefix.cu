@@ -19,15 +19,17 @@ namespace {
 // 32768 (538) 65 / 54; 16 queries each (eight times eight rows), 2 behind 2048 (9 x 8) 20 / 39, 8
 // behind 2048 (36 x 8) 36 / 37, 32 behind 512 (42 x 8) 57 / 44; 256 channels: 8 behind 8192
 // (272) 46 / 43, 32 behind 2048 (285) 50 / 48.
-// A further group's blocks take the shared kernel what two or three sequences' take apart, and
-// a group for each sequence shares nothing: 32 groups of one, two, three and four behind 8192
-// tokens 95 / 174, 123 / 175, 255 / 179, 306 / 183; 4 groups of four 38 / 50, of six 52 / 49.  (Over
-// 1268 batches of up to 64 groups the choice costs 0.9 % against the better form each time, 3 %
-// without the groups in it; the worst 1.4 times as long and 2.6.)
+// A group's blocks take the shared kernel what two or three times eight rows take apart: 32 groups of
+// one, two, three and four sequences behind 8192 tokens 95 / 174, 123 / 175, 255 / 179, 306 / 183; 4
+// groups of four 38 / 50, of six 52 / 49.  A group may be a single sequence, whose queries share its
+// blocks: one of 64 behind 65536 tokens, 4 heads of 256, 8 query heads each 891 / 176.  (Over 3858
+// batches of up to 64 groups the choice costs 0.7 % against the better form each time, 3.7 % by the
+// rows alone; the worst 1.5 times as long and 2.6.)
 bool px_pays(int64_t S, int64_t groups, int64_t width, int64_t heads, int64_t dim, int64_t rows) {
-  if (groups == 0 || groups == S) return false;
   const double mb = (double)width * kKvBlock * (double)heads * (double)dim * 2e-6;  // of a sequence
-  return mb * ((double)S * (double)((rows + 7) / 8) - 2.5 * (double)(groups - 1)) > (dim <= 128 ? 230.0 : 300.0);
+  const double eights = (double)S * (double)((rows + 7) / 8);
+  if (groups == 0 || eights < 3.0 * (double)groups) return false;
+  return mb * (eights - 2.5 * (double)(groups == S ? groups : groups - 1)) > (dim <= 128 ? 230.0 : 300.0);
 }
 
 // Scratch memory that a call takes at most, by the size of its output; `otherwise` is the call

@@ -416,15 +416,15 @@ gemv_status_t gemv_kv8_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cac
  * the new tokens as ever.  A sequence some of whose queries do not see all of the shared blocks
  * (lens[s] - T below them; an idle place of the batch with lens[s] == 0) is attended to by
  * itself, from its own table.  Limits and errors are those of gemv_kv8_attention, to which the
- * call is passed on where sharing does not pay (groups == 0 or S; S x T x q_heads / heads query
- * rows, less those that further groups cost, times width x heads x dim too few), where its work
- * list would pass 2^31 or its scratch buffer 64 MB and 24 times the size of out.  The host knows the tables' width and not the lengths: for short sequences
- * in wide tables gemv_kv8_attention takes less.  The shared values' sums, over
- * a share of the blocks each, are in units of about the row's largest weight x value scale; the weights
- * are rounded to 11 bits as there, those below 2^-22 of that largest to fewer.  A scratch buffer
- * from the library's stream-ordered pool holds partial results: about 40 MB with 152 SMs, and
- * 4 (dim + 4) bytes twice for each row of out, counted in tiles of 8 to 32 rows for each sequence and
- * head, and of 128 or 256 for each group and head. */
+ * call is passed on where sharing does not pay (no groups, too few rows of queries to a group, or
+ * too few times the tables' width x heads x dim, less what each group costs), where its work list
+ * would pass 2^31 or its scratch buffer 64 MB and 24 times the size of out.  The host knows the
+ * tables' width and not the lengths: for short sequences in wide tables gemv_kv8_attention takes
+ * less.  The shared values' sums, over a share of the blocks each, are in units of about the row's
+ * largest weight x value scale; the weights are rounded to 11 bits as there, those below 2^-22 of
+ * that largest to fewer.  A scratch buffer from the library's stream-ordered pool holds partial
+ * results: about 40 MB with 152 SMs, and 4 (dim + 4) bytes twice for each row of out, counted in
+ * tiles of 8 to 32 rows for each sequence and head, and of 128 or 256 for each group and head. */
 gemv_status_t gemv_kv8_prefix_attention(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, const void *q, int64_t q_stride,
                                         const int32_t *lens, const int32_t *firsts, const int32_t *prefix, int groups, void *out,
                                         float *lse, int S, int T, int q_heads, float scale, gemv_stream_t stream);

@@ -160,6 +160,15 @@ def shared(c, q, **k):
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_sequence_to_a_group(dim):
+    # its own queries share a sequence's blocks, where they are many
+    for S, T in ((1, 64), (3, 17)):
+        P = 2000
+        c = wide(list(range(S + 1)), [P + 100 * i for i in range(S)], [P + 100 * i + T + 30 for i in range(S)], 1, dim, seed=151).fill(152)
+        shared(c, queries(c, T, 4, 153), again=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
 def test_groups_of_every_kind(dim):
     # groups of one and many sequences, an empty one, sequences before the first and behind the last,
     # idle places, sequences shorter than the prefix, or by one token too short to see it whole
