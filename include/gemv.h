@@ -359,9 +359,10 @@ gemv_status_t gemv_kv8_append(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache,
 /* Cached tokens back as rows, the mirror of gemv_kv8_append: with the same lens, starts, S
  * and N, row i of k and v becomes the key and value that the cache holds at the position
  * to which gemv_kv8_append would write row i, k * k_scale rounded once to `dtype` (F32, F16,
- * BF16; NaN stays NaN).  So a sequence's rows are the last starts[s + 1] - starts[s] of its
- * lens[s] tokens; a range that ends earlier is read with that end as lens[s].  k or v may be
- * NULL: it is not read.  Both may be columns of one matrix; they overlap nothing else.
+ * BF16; NaN stays NaN; with scales that are no powers of two the product is rounded to F32
+ * first).  So a sequence's rows are the last starts[s + 1] - starts[s] of its lens[s] tokens; a
+ * range that ends earlier is read with that end as lens[s].  k or v may be NULL: it is not
+ * read.  Both may be columns of one matrix; they overlap nothing else.
  * Rows that no sequence has are left as they were.  So are those of a sequence with fewer
  * tokens than rows and of a position that has no block of the pool, and
  * gemv_get_device_status then returns GEMV_ERR_INVALID_VALUE with bit 64.  Blocks without
@@ -390,7 +391,7 @@ gemv_status_t gemv_kv8_read(gemv_dtype_t dtype, const gemv_kv8_cache_t *cache, v
  * more than 65535.
  * Sums, maxima and logits are fp32; the products' operands are fp16: q scaled by a
  * power of two per row, the 8-bit values exactly, and the softmax weights, rounded to
- * 11 bits.  The values' sum, weighted relative to the largest weight, has to stay in
+ * 11 bits (those below 2^-28 of the row's largest to fewer).  The values' sum, weighted relative to the largest weight, has to stay in
  * fp32's range (any value does alone, n equally weighted ones up to 3.4e38 / n).  The
  * result does not depend on the run: partial results are merged in a fixed order.  lens beyond the table count as the table's size.  A table entry outside
  * the pool counts as a block that no query sees, and gemv_get_device_status then
